@@ -63,6 +63,16 @@ class LowbitMatrix(ctypes.Structure):
                 ("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p)]
 
 
+class RowShape(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("dtype", "tokens", "top_k", "hidden", "rows")]
+
+
+class LoraSet(ctypes.Structure):
+    _fields_ = [("n_adapters", ctypes.c_int32), ("max_rank", ctypes.c_int32),
+                ("n", ctypes.c_int32), ("k", ctypes.c_int32), ("a", ctypes.c_void_p),
+                ("b", ctypes.c_void_p), ("rank", ctypes.c_void_p), ("scale", ctypes.c_void_p)]
+
+
 _LIB = None
 
 
@@ -105,6 +115,25 @@ def lib():
         L.lowbit_gemv.restype = ctypes.c_int
         L.lowbit_gemv.argtypes = [ctypes.POINTER(LowbitMatrix), ctypes.c_void_p, ctypes.c_int32,
                                   ctypes.c_void_p, ctypes.c_void_p]
+        p, i32, size = ctypes.c_void_p, ctypes.c_int32, ctypes.c_size_t
+        shape = ctypes.POINTER(RowShape)
+        lora = ctypes.POINTER(LoraSet)
+        for name, restype, args in (
+                ("moe_sort_workspace_size", size, [i32, i32, i32]),
+                ("moe_sort", ctypes.c_int, [p, i32, i32, i32, p, p, p, p, size, p]),
+                ("moe_gather", ctypes.c_int, [shape, p, p, p, p]),
+                ("moe_gather_backward", ctypes.c_int, [shape, p, p, p, p]),
+                ("moe_combine", ctypes.c_int, [shape, p, p, p, p, p, p]),
+                ("moe_combine_backward", ctypes.c_int, [shape, p, p, p, p, p, p, p]),
+                ("moe_wide_workspace_size", size, [ctypes.POINTER(Config), i32]),
+                ("moe_wide_step", ctypes.c_int, [ctypes.POINTER(Config), p, i32, p, p,
+                                                 ctypes.POINTER(Weights), p, p, size, p]),
+                ("lora_workspace_size", size, [lora, i32]),
+                ("lora_apply", ctypes.c_int, [lora, p, p, i32, p, p, p, size, p]),
+                ("lowbit_gemv_lora", ctypes.c_int, [ctypes.POINTER(LowbitMatrix), lora, p, p, i32,
+                                                    p, p, size, p])):
+            f = getattr(L, name)
+            f.restype, f.argtypes = restype, args
         _LIB = L
     return _LIB
 
@@ -230,10 +259,11 @@ def step_noalloc_status(cfg: Config, x, rows, weights: Weights, out, stream=None
 
 def make_weights(gamma, router_w, routed, shared=None) -> Weights:
     """Weights struct from device tensors: routed/shared are (gate, up, down)
-    tuples of (codes, scales) tensors in canonical layout."""
+    tuples of (codes, scales) tensors in canonical layout; router_w may be None
+    for moe_wide_step."""
     w = Weights()
     w.rms_gamma = gamma.data_ptr()
-    w.router_w = router_w.data_ptr()
+    w.router_w = None if router_w is None else router_w.data_ptr()
     for name, (c, s) in zip(("gate", "up", "down"), routed):
         setattr(w, name, Tensor(c.data_ptr(), None if s is None else s.data_ptr()))
     if shared is not None:
@@ -279,6 +309,192 @@ def gemv_bf16_status(w, x, y, n, k, rows=1, stream=None):
 def lowbit_gemv_status(blocks, x, y, n, k, rows=1, stream=None, fmt=FMT_Q1):
     m = LowbitMatrix(fmt, int(n), int(k), blocks.data_ptr() if blocks is not None else None, None)
     return lib().lowbit_gemv(ctypes.byref(m), _ptr(x), int(rows), _ptr(y), _stream(stream))
+
+
+def make_matrix(fmt, n, k, codes, scales=None) -> LowbitMatrix:
+    """LowbitMatrix struct of a weight [n, k] in one of lowbit_gemv's formats."""
+    return LowbitMatrix(int(fmt), int(n), int(k), codes.data_ptr(),
+                        None if scales is None else scales.data_ptr())
+
+
+# ------------------------------------------------ tokens sorted by expert and back
+MAX_TOP_K = 16             # MOE_MAX_TOP_K
+WIDE_MAX_TOKENS = 65536    # MOE_WIDE_MAX_TOKENS
+LORA_MAX_ROWS = 1 << 20    # MOE_LORA_MAX_ROWS
+_ROW_DTYPES = {"torch.bfloat16": 0, "torch.float32": 1}  # moe_dtype
+
+
+def _refuse(what, why):
+    e = MoeError(MOE_ERR_INVALID_ARG, what)
+    e.args = (f"{e.args[0]}: {why}",)
+    raise e
+
+
+def _check(what, device, **tensors):
+    """Every tensor (name=(tensor, dtype, shape), None allowed) is contiguous,
+    on `device` and of that dtype and shape; `device` is the current one."""
+    import torch
+    if device < 0 or device != torch.cuda.current_device():
+        _refuse(what, "the tensors are not on the current device")
+    for name, (t, dtype, shape) in tensors.items():
+        if t is None:
+            continue
+        if t.get_device() != device:
+            _refuse(what, f"{name} is on another device")
+        if t.dtype is not dtype:
+            _refuse(what, f"{name} is {t.dtype}, not {dtype}")
+        if tuple(t.shape) != shape:
+            _refuse(what, f"{name} is {tuple(t.shape)}, not {shape}")
+        if not t.is_contiguous():
+            _refuse(what, f"{name} is not contiguous")
+
+
+def _done(st, what):
+    if st != MOE_OK:
+        raise MoeError(st, what)
+
+
+def _address(t):
+    return None if t is None else t.data_ptr()
+
+
+def _space(t):
+    return (None, 0) if t is None else (t.data_ptr(), t.numel() * t.element_size())
+
+
+def moe_sort_workspace_size(tokens, top_k, n_experts) -> int:
+    return lib().moe_sort_workspace_size(int(tokens), int(top_k), int(n_experts))
+
+
+def moe_sort(ids, n_experts, offsets, order, pos, workspace=None, stream=None):
+    """Stable sort of the picks ids int32 [T, k] by expert: offsets int32
+    [n_experts + 1], order int32 [T k], pos int32 [T, k]; workspace: a device
+    tensor of moe_sort_workspace_size bytes (None where that is 0)."""
+    import torch
+    i32, (t, k) = torch.int32, ids.shape
+    _check("moe_sort", ids.get_device(), ids=(ids, i32, (t, k)), offsets=(offsets, i32, (n_experts + 1,)),
+           order=(order, i32, (t * k,)), pos=(pos, i32, (t, k)))
+    ws, n = _space(workspace)
+    _done(lib().moe_sort(ids.data_ptr(), t, k, int(n_experts), offsets.data_ptr(), order.data_ptr(),
+                         pos.data_ptr(), ws, n, _stream(stream)), "moe_sort")
+
+
+def _row_shape(what, rows, pos):
+    dtype = _ROW_DTYPES.get(str(rows.dtype))
+    if dtype is None:
+        _refuse(what, f"rows of {rows.dtype}")
+    t, k = pos.shape
+    return t, k, rows.shape[1], ctypes.byref(RowShape(dtype, t, k, rows.shape[1], rows.shape[0]))
+
+
+def moe_gather(x, pos, xs, stream=None):
+    """xs[pos[t, j]] = x[t]: x [T, H], pos int32 [T, k] (moe_sort's), xs [rows, H]."""
+    import torch
+    t, k, h, shape = _row_shape("moe_gather", xs, pos)
+    _check("moe_gather", xs.get_device(), x=(x, xs.dtype, (t, h)), pos=(pos, torch.int32, (t, k)),
+           xs=(xs, xs.dtype, (xs.shape[0], h)))
+    _done(lib().moe_gather(shape, x.data_ptr(), pos.data_ptr(), xs.data_ptr(), _stream(stream)),
+          "moe_gather")
+
+
+def moe_gather_backward(dxs, pos, dx, stream=None):
+    """dx[t] = sum_j dxs[pos[t, j]]: dxs [rows, H], dx [T, H]."""
+    import torch
+    t, k, h, shape = _row_shape("moe_gather_backward", dxs, pos)
+    _check("moe_gather_backward", dxs.get_device(), dx=(dx, dxs.dtype, (t, h)),
+           pos=(pos, torch.int32, (t, k)), dxs=(dxs, dxs.dtype, (dxs.shape[0], h)))
+    _done(lib().moe_gather_backward(shape, dxs.data_ptr(), pos.data_ptr(), dx.data_ptr(),
+                                    _stream(stream)), "moe_gather_backward")
+
+
+def moe_combine(y, pos, gates, out, add=None, stream=None):
+    """out[t] = sum_j gates[t, j] y[pos[t, j]] (+ add[t]): y [rows, H], gates
+    float32 [T, k], out and add [T, H]."""
+    import torch
+    t, k, h, shape = _row_shape("moe_combine", y, pos)
+    _check("moe_combine", y.get_device(), y=(y, y.dtype, (y.shape[0], h)),
+           pos=(pos, torch.int32, (t, k)), gates=(gates, torch.float32, (t, k)),
+           out=(out, y.dtype, (t, h)), add=(add, y.dtype, (t, h)))
+    _done(lib().moe_combine(shape, y.data_ptr(), pos.data_ptr(), gates.data_ptr(), _address(add),
+                            out.data_ptr(), _stream(stream)), "moe_combine")
+
+
+def moe_combine_backward(dout, y, pos, gates, dy, dgates, stream=None):
+    """dy[pos[t, j]] = gates[t, j] dout[t] and dgates[t, j] = dout[t] . y[pos[t, j]]:
+    dout [T, H], y and dy [rows, H], gates and dgates float32 [T, k]."""
+    import torch
+    t, k, h, shape = _row_shape("moe_combine_backward", y, pos)
+    _check("moe_combine_backward", y.get_device(), dout=(dout, y.dtype, (t, h)),
+           y=(y, y.dtype, (y.shape[0], h)), pos=(pos, torch.int32, (t, k)),
+           gates=(gates, torch.float32, (t, k)), dy=(dy, y.dtype, (y.shape[0], h)),
+           dgates=(dgates, torch.float32, (t, k)))
+    _done(lib().moe_combine_backward(shape, dout.data_ptr(), y.data_ptr(), pos.data_ptr(),
+                                     gates.data_ptr(), dy.data_ptr(), dgates.data_ptr(),
+                                     _stream(stream)), "moe_combine_backward")
+
+
+def moe_wide_workspace_size(cfg: Config, tokens) -> int:
+    return lib().moe_wide_workspace_size(ctypes.byref(cfg), int(tokens))
+
+
+def moe_wide_step(cfg: Config, x, ids, gates, weights: Weights, out, workspace, stream=None):
+    """The experts' step for any number of rows with given routing: x and out
+    bf16 [T, H], ids int32 [T, 8], gates float32 [T, 8]."""
+    import torch
+    t = x.shape[0]
+    _check("moe_wide_step", x.get_device(), x=(x, torch.bfloat16, (t, cfg.hidden)),
+           ids=(ids, torch.int32, (t, 8)), gates=(gates, torch.float32, (t, 8)),
+           out=(out, torch.bfloat16, (t, cfg.hidden)))
+    ws, n = _space(workspace)
+    _done(lib().moe_wide_step(ctypes.byref(cfg), x.data_ptr(), t, ids.data_ptr(), gates.data_ptr(),
+                              ctypes.byref(weights), out.data_ptr(), ws, n, _stream(stream)),
+          "moe_wide_step")
+
+
+# ----------------------------------------------------------- low-rank adapters
+def make_lora(a, b, scale, rank=None) -> LoraSet:
+    """LoraSet struct of adapters a bf16 [n_adapters, max_rank, k], b bf16
+    [n_adapters, n, max_rank], scale float32 [n_adapters], rank int32
+    [n_adapters] or None.  The struct keeps the tensors alive."""
+    import torch
+    n_adapters, max_rank, k = a.shape
+    n = b.shape[1]
+    _check("make_lora", a.get_device(), a=(a, torch.bfloat16, (n_adapters, max_rank, k)),
+           b=(b, torch.bfloat16, (n_adapters, n, max_rank)),
+           scale=(scale, torch.float32, (n_adapters,)), rank=(rank, torch.int32, (n_adapters,)))
+    s = LoraSet(n_adapters, max_rank, n, k, a.data_ptr(), b.data_ptr(), _address(rank),
+                scale.data_ptr())
+    s.tensors = (a, b, scale, rank)
+    return s
+
+
+def lora_workspace_size(lora: LoraSet, rows) -> int:
+    return lib().lora_workspace_size(ctypes.byref(lora), int(rows))
+
+
+def lora_apply(lora: LoraSet, x, ids, base, y, workspace, stream=None):
+    """y[r] = base[r] + scale_i B_i (A_i x[r]), i = ids[r]: x bf16 [rows, k], ids
+    int32 [rows], base and y bf16 [rows, n] (y may be base)."""
+    import torch
+    r, bf = x.shape[0], torch.bfloat16
+    _check("lora_apply", x.get_device(), x=(x, bf, (r, lora.k)), ids=(ids, torch.int32, (r,)),
+           base=(base, bf, (r, lora.n)), y=(y, bf, (r, lora.n)))
+    ws, n = _space(workspace)
+    _done(lib().lora_apply(ctypes.byref(lora), x.data_ptr(), ids.data_ptr(), r, base.data_ptr(),
+                           y.data_ptr(), ws, n, _stream(stream)), "lora_apply")
+
+
+def lowbit_gemv_lora(matrix: LowbitMatrix, lora: LoraSet, x, ids, y, workspace, stream=None):
+    """lowbit_gemv of 0..8 rows with the rows' adapters added before the
+    rounding: x bf16 [rows, k], ids int32 [rows], y bf16 [rows, n]."""
+    import torch
+    r, bf = x.shape[0], torch.bfloat16
+    _check("lowbit_gemv_lora", x.get_device(), x=(x, bf, (r, matrix.k)), ids=(ids, torch.int32, (r,)),
+           y=(y, bf, (r, matrix.n)))
+    ws, n = _space(workspace)
+    _done(lib().lowbit_gemv_lora(ctypes.byref(matrix), ctypes.byref(lora), x.data_ptr(),
+                                 ids.data_ptr(), r, y.data_ptr(), ws, n, _stream(stream)),
+          "lowbit_gemv_lora")
 
 
 class LayerRunner:

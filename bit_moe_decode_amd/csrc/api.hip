@@ -7,6 +7,9 @@
 #include <new>
 
 #include "device_common.h"
+#include "lora.h"
+#include "token_rows.h"
+#include "wide.h"
 
 namespace moe {
 hipError_t launch_router(const uint16_t* x, const Weights& w, const Ws& ws, const Dims& d,
@@ -21,11 +24,12 @@ hipError_t launch_down(int rfmt, int max_groups, const Weights& w, const Ws& ws,
 hipError_t launch_combine(const Ws& ws, const Dims& d, uint16_t* out, hipStream_t stream);
 int upgate_k_parts(int hidden, int routed_fmt);
 hipError_t launch_lowbit_q1(const uint8_t* blocks, const uint16_t* x, uint16_t* y, int rows,
-                            int n, int k, hipStream_t stream);
+                            int n, int k, const LoraArgs* lora, hipStream_t stream);
 hipError_t launch_gemv_fp8(const uint8_t* codes, const float* scales, const uint16_t* x,
-                           uint16_t* y, int rows, int n, int k, hipStream_t stream);
+                           uint16_t* y, int rows, int n, int k, const LoraArgs* lora,
+                           hipStream_t stream);
 hipError_t launch_gemv_bf16(const uint16_t* w, const uint16_t* x, uint16_t* y, int rows, int n,
-                            int k, hipStream_t stream);
+                            int k, const LoraArgs* lora, hipStream_t stream);
 
 __global__ void moe_fill_u32_kernel(uint32_t* p, size_t n, uint32_t v) {
   for (size_t i = blockIdx.x * (size_t)blockDim.x + threadIdx.x; i < n;
@@ -459,60 +463,374 @@ const char* moe_status_string(moe_status s) {
   return "unknown status";
 }
 
-moe_status lowbit_gemv(const lowbit_matrix* w, const uint16_t* x, int32_t rows, uint16_t* y,
-                       hipStream_t stream) {
+namespace {
+bool overlap(const void* a, size_t an, const void* b, size_t bn) {
+  const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
+  return x < y + bn && y < x + an;
+}
+
+// Checks of a GEMV call; *go is set when there is work to launch.
+moe_status check_gemv(const lowbit_matrix* w, const uint16_t* x, int32_t rows, const uint16_t* y,
+                      bool* go) {
+  *go = false;
   if (!w) return MOE_ERR_INVALID_ARG;
-  if (w->fmt == MOE_FMT_FP8_E4M3_B128) {
-    // FP8 weights in 128x128 blocks, 1 to 8 bf16 input rows
-    if (w->n < 0 || w->k <= 0) return MOE_ERR_INVALID_ARG;
-    if (w->n % 128 || w->k % 128) return MOE_ERR_UNSUPPORTED;
-    if (rows < 0) return MOE_ERR_INVALID_ARG;
-    if (rows == 0 || w->n == 0) return MOE_OK;
-    if (rows > 8) return MOE_ERR_UNSUPPORTED;
-    if (!w->codes || !w->scales || !x || !y || !aligned16(w->codes) || !aligned16(x) ||
-        ((uintptr_t)w->scales & 3u) || ((uintptr_t)y & 1u))
-      return MOE_ERR_INVALID_ARG;
-    const uintptr_t xa = (uintptr_t)x, ya = (uintptr_t)y;
-    if (xa < ya + (size_t)rows * w->n * 2 && ya < xa + (size_t)rows * w->k * 2)
-      return MOE_ERR_INVALID_ARG;
-    if (launch_gemv_fp8(static_cast<const uint8_t*>(w->codes), static_cast<const float*>(w->scales),
-                        x, y, rows, w->n, w->k, stream) != hipSuccess)
-      return MOE_ERR_DEVICE;
-    return MOE_OK;
-  }
-  if (w->fmt == MOE_FMT_BF16) {
-    // bf16 weights, 1 to 8 bf16 input rows
-    if (w->n < 0 || w->k <= 0) return MOE_ERR_INVALID_ARG;
-    if (w->n % 128 || w->k % 64) return MOE_ERR_UNSUPPORTED;
-    if (rows < 0) return MOE_ERR_INVALID_ARG;
-    if (rows == 0 || w->n == 0) return MOE_OK;
-    if (rows > 8) return MOE_ERR_UNSUPPORTED;
-    if (!w->codes || !x || !y || !aligned16(w->codes) || !aligned16(x) || ((uintptr_t)y & 1u))
-      return MOE_ERR_INVALID_ARG;
-    const uintptr_t xa = (uintptr_t)x, ya = (uintptr_t)y;
-    if (xa < ya + (size_t)rows * w->n * 2 && ya < xa + (size_t)rows * w->k * 2)
-      return MOE_ERR_INVALID_ARG;
-    if (launch_gemv_bf16(static_cast<const uint16_t*>(w->codes), x, y, rows, w->n, w->k,
-                         stream) != hipSuccess)
-      return MOE_ERR_DEVICE;
-    return MOE_OK;
-  }
-  if (w->fmt != MOE_FMT_Q1_G128) return MOE_ERR_UNSUPPORTED;
+  if (w->fmt != MOE_FMT_FP8_E4M3_B128 && w->fmt != MOE_FMT_BF16 && w->fmt != MOE_FMT_Q1_G128)
+    return MOE_ERR_UNSUPPORTED;
   if (w->n < 0 || w->k <= 0) return MOE_ERR_INVALID_ARG;
-  if (w->k % 128 || w->k > 16384) return MOE_ERR_UNSUPPORTED;
+  const bool q1 = w->fmt == MOE_FMT_Q1_G128;
+  if (q1) {
+    if (w->k % 128 || w->k > 16384) return MOE_ERR_UNSUPPORTED;
+  } else if (w->n % 128 || w->k % (w->fmt == MOE_FMT_BF16 ? 64 : 128)) {
+    return MOE_ERR_UNSUPPORTED;
+  }
   if (rows < 0) return MOE_ERR_INVALID_ARG;
   if (rows == 0 || w->n == 0) return MOE_OK;
-  // several rows: the MFMA form, which takes K in chunks of 256
-  if (rows > 8 || (rows > 1 && w->k % 256)) return MOE_ERR_UNSUPPORTED;
-  if (!w->codes || !x || !y || !aligned16(w->codes) || !aligned16(x) || !aligned16(y))
+  // 1-bit, several rows: the MFMA form, which takes K in chunks of 256
+  if (rows > 8 || (q1 && rows > 1 && w->k % 256)) return MOE_ERR_UNSUPPORTED;
+  if (!w->codes || !x || !y || !aligned16(w->codes) || !aligned16(x)) return MOE_ERR_INVALID_ARG;
+  if (q1 ? !aligned16(y) : ((uintptr_t)y & 1u) != 0) return MOE_ERR_INVALID_ARG;
+  if (w->fmt == MOE_FMT_FP8_E4M3_B128 && (!w->scales || ((uintptr_t)w->scales & 3u)))
     return MOE_ERR_INVALID_ARG;
-  const uintptr_t xa = (uintptr_t)x, ya = (uintptr_t)y;
-  if (xa < ya + (size_t)rows * w->n * 2 && ya < xa + (size_t)rows * w->k * 2)
-    return MOE_ERR_INVALID_ARG;
-  if (launch_lowbit_q1(static_cast<const uint8_t*>(w->codes), x, y, rows, w->n, w->k, stream) !=
-      hipSuccess)
-    return MOE_ERR_DEVICE;
+  if (overlap(x, (size_t)rows * w->k * 2, y, (size_t)rows * w->n * 2)) return MOE_ERR_INVALID_ARG;
+  *go = true;
   return MOE_OK;
+}
+
+moe_status enqueue_gemv(const lowbit_matrix* w, const uint16_t* x, int32_t rows, uint16_t* y,
+                        const LoraArgs* lora, hipStream_t stream) {
+  hipError_t e;
+  if (w->fmt == MOE_FMT_FP8_E4M3_B128)
+    e = launch_gemv_fp8(static_cast<const uint8_t*>(w->codes), static_cast<const float*>(w->scales),
+                        x, y, rows, w->n, w->k, lora, stream);
+  else if (w->fmt == MOE_FMT_BF16)
+    e = launch_gemv_bf16(static_cast<const uint16_t*>(w->codes), x, y, rows, w->n, w->k, lora, stream);
+  else
+    e = launch_lowbit_q1(static_cast<const uint8_t*>(w->codes), x, y, rows, w->n, w->k, lora, stream);
+  return e == hipSuccess ? MOE_OK : MOE_ERR_DEVICE;
+}
+
+// ---- rows grouped by expert
+
+bool sort_shape_ok(int64_t tokens, int top_k, int groups) {
+  return tokens >= 0 && top_k >= 1 && top_k <= MOE_MAX_TOP_K && groups >= 1 &&
+         groups <= kSortMaxGroups && tokens * top_k <= kSortMaxPicks;
+}
+
+bool aligned4(const void* p) { return ((uintptr_t)p & 3u) == 0; }
+
+// Checks of a row movement; *a is filled when there is work.
+moe_status row_args(const moe_row_shape* s, const int32_t* pos, RowArgs* a) {
+  if (!s) return MOE_ERR_INVALID_ARG;
+  if (s->dtype != MOE_BF16 && s->dtype != MOE_F32) return MOE_ERR_UNSUPPORTED;
+  if (s->tokens < 0 || s->top_k < 1 || s->hidden < 1 || s->rows < 0) return MOE_ERR_INVALID_ARG;
+  if (s->top_k > MOE_MAX_TOP_K || (int64_t)s->tokens * s->top_k > kSortMaxPicks ||
+      s->hidden > MOE_MAX_ROW)
+    return MOE_ERR_UNSUPPORTED;
+  if (s->tokens > 0 && (!pos || !aligned4(pos))) return MOE_ERR_INVALID_ARG;
+  a->pos = pos;
+  a->tokens = s->tokens;
+  a->top_k = s->top_k;
+  a->hidden = s->hidden;
+  a->rows = s->rows;
+  return MOE_OK;
+}
+
+struct RowBytes {
+  size_t tokens, sorted, picks;  // [tokens, hidden], [rows, hidden], [tokens, top_k] of 4 bytes
+};
+RowBytes row_bytes(const moe_row_shape* s) {
+  const size_t e = (size_t)s->hidden * (s->dtype == MOE_F32 ? 4 : 2);
+  return {s->tokens * e, s->rows * e, (size_t)s->tokens * s->top_k * 4};
+}
+
+// ---- the experts' step of any number of rows
+
+struct WidePlan {
+  size_t actq, acts, order, pos, offsets, counts, tiles, ntiles, midq, mids, y, total;
+  int64_t picks;
+  int tile_rows, max_tiles;
+};
+
+moe_status plan_wide(const moe_decode_config* cfg, int32_t tokens, Plan* p, WidePlan* q) {
+  const moe_status st = plan_config(cfg, p);
+  if (st != MOE_OK) return st;
+  if (cfg->routed_fmt != MOE_FMT_FP8_E4M3_B128 || cfg->act_fmt != MOE_ACT_FP8_B128)
+    return MOE_ERR_UNSUPPORTED;
+  if (tokens < 0) return MOE_ERR_INVALID_ARG;
+  if (tokens > MOE_WIDE_MAX_TOKENS) return MOE_ERR_UNSUPPORTED;
+  const size_t T = tokens, S = 8 * T, R = S + (p->Is ? T : 0);
+  q->picks = (int64_t)S;
+  q->tile_rows = wide_tile_rows(q->picks, p->E);
+  q->max_tiles = wide_max_tiles(q->picks, p->E, p->Is ? tokens : 0, q->tile_rows);
+  size_t o = 0;
+  auto take = [&](size_t bytes) {
+    const size_t at = o;
+    o = align_up(o + bytes, 256);
+    return at;
+  };
+  q->actq = take(T * p->H);
+  q->acts = take(T * (p->H / 128) * 4);
+  q->order = take(S * 4);
+  q->pos = take(S * 4);
+  q->offsets = take((p->E + 1) * 4);
+  q->counts = take(sort_workspace(q->picks, p->E));
+  q->tiles = take((size_t)q->max_tiles * sizeof(RowTile));
+  q->ntiles = take(4);
+  q->midq = take(R * p->I);
+  q->mids = take(R * (p->I / 128) * 4);
+  q->y = take(R * p->H * 4);
+  q->total = o;
+  return MOE_OK;
+}
+
+// ---- adapters
+
+moe_status check_lora_set(const lora_set* l) {
+  if (!l) return MOE_ERR_INVALID_ARG;
+  if (l->n_adapters < 0 || l->n < 0 || l->k <= 0) return MOE_ERR_INVALID_ARG;
+  if (l->n_adapters > kLoraMaxAdapters || l->max_rank < 8 || l->max_rank > kLoraMaxRank ||
+      l->max_rank % 8 || l->n % 8 || l->k % 64 || l->k > 32768)
+    return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+// Pointers of a call with rows >= 1, n >= 1.
+moe_status lora_args(const lora_set* l, const uint16_t* x, const int32_t* ids, int32_t rows,
+                     const uint16_t* y, void* ws, size_t ws_bytes, LoraArgs* a) {
+  if (!x || !ids || !y || !aligned16(x) || !aligned4(ids) || !aligned16(y)) return MOE_ERR_INVALID_ARG;
+  if (l->n_adapters > 0 && (!l->a || !l->b || !l->scale || !aligned16(l->a) || !aligned16(l->b) ||
+                            !aligned4(l->scale) || !aligned4(l->rank)))
+    return MOE_ERR_INVALID_ARG;
+  const size_t need = lora_workspace(l->n_adapters, l->max_rank, l->n, l->k, rows);
+  if (!ws || ws_bytes < need || !aligned16(ws)) return MOE_ERR_WORKSPACE;
+  const size_t yb = (size_t)rows * l->n * 2;
+  if (overlap(x, (size_t)rows * l->k * 2, y, yb) || overlap(ids, (size_t)rows * 4, y, yb) ||
+      overlap(ws, need, y, yb) || overlap(ws, need, x, (size_t)rows * l->k * 2))
+    return MOE_ERR_INVALID_ARG;
+  a->a = l->a;
+  a->b = l->b;
+  a->rank = l->rank;
+  a->scale = l->scale;
+  a->ids = ids;
+  a->adapters = l->n_adapters;
+  a->max_rank = l->max_rank;
+  a->n = l->n;
+  a->k = l->k;
+  a->rows = rows;
+  a->v = static_cast<float*>(ws);
+  a->k_parts = lora_k_parts(rows, l->k);
+  return MOE_OK;
+}
+}  // namespace
+
+moe_status lowbit_gemv(const lowbit_matrix* w, const uint16_t* x, int32_t rows, uint16_t* y,
+                       hipStream_t stream) {
+  bool go;
+  const moe_status st = check_gemv(w, x, rows, y, &go);
+  if (st != MOE_OK || !go) return st;
+  return enqueue_gemv(w, x, rows, y, nullptr, stream);
+}
+
+size_t moe_sort_workspace_size(int32_t tokens, int32_t top_k, int32_t n_experts) {
+  return sort_shape_ok(tokens, top_k, n_experts) ? sort_workspace((int64_t)tokens * top_k, n_experts) : 0;
+}
+
+moe_status moe_sort(const int32_t* ids, int32_t tokens, int32_t top_k, int32_t n_experts,
+                    int32_t* offsets, int32_t* order, int32_t* pos, void* workspace,
+                    size_t ws_bytes, hipStream_t stream) {
+  if (tokens < 0 || top_k < 1 || n_experts < 1) return MOE_ERR_INVALID_ARG;
+  if (!sort_shape_ok(tokens, top_k, n_experts)) return MOE_ERR_UNSUPPORTED;
+  const int64_t picks = (int64_t)tokens * top_k;
+  if (!offsets || !aligned4(offsets)) return MOE_ERR_INVALID_ARG;
+  if (picks > 0 && (!ids || !order || !pos || !aligned4(ids) || !aligned4(order) || !aligned4(pos)))
+    return MOE_ERR_INVALID_ARG;
+  const size_t pb = (size_t)picks * 4, ob = ((size_t)n_experts + 1) * 4;
+  const size_t need = sort_workspace(picks, n_experts);
+  if (need && (!workspace || ws_bytes < need || !aligned4(workspace))) return MOE_ERR_WORKSPACE;
+  const void* buf[] = {ids, offsets, order, pos, workspace};
+  const size_t len[] = {pb, ob, pb, pb, need};
+  for (int i = 0; i < 5; i++)
+    for (int j = i + 1; j < 5; j++)
+      if (len[i] && len[j] && overlap(buf[i], len[i], buf[j], len[j])) return MOE_ERR_INVALID_ARG;
+  SortArgs a = {};
+  a.ids = ids;
+  a.picks = picks;
+  a.groups = n_experts;
+  a.offsets = offsets;
+  a.order = order;
+  a.pos = pos;
+  a.counts = static_cast<int32_t*>(workspace);
+  return launch_sort(a, stream) == hipSuccess ? MOE_OK : MOE_ERR_DEVICE;
+}
+
+moe_status moe_gather(const moe_row_shape* shape, const void* x, const int32_t* pos, void* xs,
+                      hipStream_t stream) {
+  RowArgs a;
+  const moe_status st = row_args(shape, pos, &a);
+  if (st != MOE_OK) return st;
+  if (a.tokens == 0 || a.rows == 0) return MOE_OK;
+  const RowBytes n = row_bytes(shape);
+  if (!x || !xs || !aligned16(x) || !aligned16(xs)) return MOE_ERR_INVALID_ARG;
+  if (overlap(x, n.tokens, xs, n.sorted) || overlap(pos, n.picks, xs, n.sorted))
+    return MOE_ERR_INVALID_ARG;
+  return launch_gather(a, shape->dtype == MOE_F32, x, xs, stream) == hipSuccess ? MOE_OK
+                                                                               : MOE_ERR_DEVICE;
+}
+
+moe_status moe_gather_backward(const moe_row_shape* shape, const void* dxs, const int32_t* pos,
+                               void* dx, hipStream_t stream) {
+  RowArgs a;
+  const moe_status st = row_args(shape, pos, &a);
+  if (st != MOE_OK) return st;
+  if (a.tokens == 0) return MOE_OK;
+  const RowBytes n = row_bytes(shape);
+  if (!dx || !aligned16(dx) || (a.rows > 0 && (!dxs || !aligned16(dxs)))) return MOE_ERR_INVALID_ARG;
+  if (overlap(dxs, n.sorted, dx, n.tokens) || overlap(pos, n.picks, dx, n.tokens))
+    return MOE_ERR_INVALID_ARG;
+  return launch_combine_rows(a, shape->dtype == MOE_F32, dxs, nullptr, nullptr, dx, stream) ==
+                 hipSuccess
+             ? MOE_OK
+             : MOE_ERR_DEVICE;
+}
+
+moe_status moe_combine(const moe_row_shape* shape, const void* y, const int32_t* pos,
+                       const float* gates, const void* add, void* out, hipStream_t stream) {
+  RowArgs a;
+  const moe_status st = row_args(shape, pos, &a);
+  if (st != MOE_OK) return st;
+  if (a.tokens == 0) return MOE_OK;
+  const RowBytes n = row_bytes(shape);
+  if (!gates || !aligned4(gates) || !out || !aligned16(out) || !aligned16(add) ||
+      (a.rows > 0 && (!y || !aligned16(y))))
+    return MOE_ERR_INVALID_ARG;
+  // out may be add itself: each element is read before it is written
+  if (overlap(y, n.sorted, out, n.tokens) || overlap(pos, n.picks, out, n.tokens) ||
+      overlap(gates, n.picks, out, n.tokens) ||
+      (add && add != out && overlap(add, n.tokens, out, n.tokens)))
+    return MOE_ERR_INVALID_ARG;
+  return launch_combine_rows(a, shape->dtype == MOE_F32, y, gates, add, out, stream) == hipSuccess
+             ? MOE_OK
+             : MOE_ERR_DEVICE;
+}
+
+moe_status moe_combine_backward(const moe_row_shape* shape, const void* dout, const void* y,
+                                const int32_t* pos, const float* gates, void* dy, float* dgates,
+                                hipStream_t stream) {
+  RowArgs a;
+  const moe_status st = row_args(shape, pos, &a);
+  if (st != MOE_OK) return st;
+  if (a.tokens == 0) return MOE_OK;
+  const RowBytes n = row_bytes(shape);
+  if (!dout || !aligned16(dout) || !gates || !aligned4(gates) || !dgates || !aligned4(dgates) ||
+      (a.rows > 0 && (!y || !dy || !aligned16(y) || !aligned16(dy))))
+    return MOE_ERR_INVALID_ARG;
+  const void* in[] = {dout, y, pos, gates};
+  const size_t inb[] = {n.tokens, n.sorted, n.picks, n.picks};
+  for (int i = 0; i < 4; i++)
+    if (overlap(in[i], inb[i], dy, n.sorted) || overlap(in[i], inb[i], dgates, n.picks))
+      return MOE_ERR_INVALID_ARG;
+  if (overlap(dy, n.sorted, dgates, n.picks)) return MOE_ERR_INVALID_ARG;
+  return launch_combine_bwd(a, shape->dtype == MOE_F32, dout, y, gates, dy, dgates, stream) ==
+                 hipSuccess
+             ? MOE_OK
+             : MOE_ERR_DEVICE;
+}
+
+size_t moe_wide_workspace_size(const moe_decode_config* cfg, int32_t tokens) {
+  Plan p;
+  WidePlan q;
+  return plan_wide(cfg, tokens, &p, &q) == MOE_OK ? q.total : 0;
+}
+
+moe_status moe_wide_step(const moe_decode_config* cfg, const uint16_t* x, int32_t tokens,
+                         const int32_t* ids, const float* gates, const moe_decode_weights* w,
+                         uint16_t* out, void* workspace, size_t ws_bytes, hipStream_t stream) {
+  Plan p;
+  WidePlan q;
+  moe_status st = plan_wide(cfg, tokens, &p, &q);
+  if (st != MOE_OK) return st;
+  if (tokens == 0) return MOE_OK;
+  st = check_io(p, x, tokens, w, out);
+  if (st != MOE_OK) return st;
+  moe_decode_weights ww = *w;
+  ww.router_w = ww.rms_gamma;  // not read: the routing is given
+  Weights wt;
+  Dims d;
+  st = step_args(*cfg, p, 1, &ww, &wt, &d);
+  if (st != MOE_OK) return st;
+  if (!ids || !gates || !aligned4(ids) || !aligned4(gates)) return MOE_ERR_INVALID_ARG;
+  if (!workspace || ((uintptr_t)workspace & 255u) || ws_bytes < q.total) return MOE_ERR_WORKSPACE;
+  const size_t xb = (size_t)tokens * p.H * 2, rb = (size_t)q.picks * 4;
+  if (overlap(workspace, q.total, x, xb) || overlap(workspace, q.total, out, xb) ||
+      overlap(workspace, q.total, ids, rb) || overlap(workspace, q.total, gates, rb) ||
+      overlap(out, xb, ids, rb) || overlap(out, xb, gates, rb))
+    return MOE_ERR_INVALID_ARG;
+  char* b = static_cast<char*>(workspace);
+  WideArgs a;
+  a.H = p.H;
+  a.I = p.I;
+  a.E = p.E;
+  a.shared = p.Is > 0;
+  a.tokens = tokens;
+  a.picks = q.picks;
+  a.eps = cfg->rms_eps;
+  a.act_q = reinterpret_cast<uint8_t*>(b + q.actq);
+  a.act_s = reinterpret_cast<float*>(b + q.acts);
+  a.order = reinterpret_cast<int32_t*>(b + q.order);
+  a.mid_q = reinterpret_cast<uint8_t*>(b + q.midq);
+  a.mid_s = reinterpret_cast<float*>(b + q.mids);
+  a.y = reinterpret_cast<float*>(b + q.y);
+  a.pos = reinterpret_cast<int32_t*>(b + q.pos);
+  a.offsets = reinterpret_cast<int32_t*>(b + q.offsets);
+  a.counts = reinterpret_cast<int32_t*>(b + q.counts);
+  a.tiles = reinterpret_cast<RowTile*>(b + q.tiles);
+  a.n_tiles = reinterpret_cast<int32_t*>(b + q.ntiles);
+  a.tile_rows = q.tile_rows;
+  a.max_tiles = q.max_tiles;
+  const WideWeights v = {wt.gamma, wt.gate_c, wt.up_c, wt.down_c, (const float*)wt.gate_s,
+                         (const float*)wt.up_s, (const float*)wt.down_s, wt.sg_c, wt.su_c, wt.sd_c,
+                         wt.sg_s, wt.su_s, wt.sd_s};
+  return launch_wide(a, v, x, ids, gates, out, stream) == hipSuccess ? MOE_OK : MOE_ERR_DEVICE;
+}
+
+size_t lora_workspace_size(const lora_set* l, int32_t rows) {
+  if (check_lora_set(l) != MOE_OK || rows <= 0 || rows > MOE_LORA_MAX_ROWS) return 0;
+  return lora_workspace(l->n_adapters, l->max_rank, l->n, l->k, rows);
+}
+
+moe_status lora_apply(const lora_set* l, const uint16_t* x, const int32_t* ids, int32_t rows,
+                      const uint16_t* base, uint16_t* y, void* workspace, size_t ws_bytes,
+                      hipStream_t stream) {
+  moe_status st = check_lora_set(l);
+  if (st != MOE_OK) return st;
+  if (rows < 0) return MOE_ERR_INVALID_ARG;
+  if (rows > MOE_LORA_MAX_ROWS) return MOE_ERR_UNSUPPORTED;
+  if (rows == 0 || l->n == 0) return MOE_OK;
+  LoraArgs a;
+  st = lora_args(l, x, ids, rows, y, workspace, ws_bytes, &a);
+  if (st != MOE_OK) return st;
+  const size_t yb = (size_t)rows * l->n * 2;
+  if (!base || !aligned16(base) || (base != y && overlap(base, yb, y, yb)) ||
+      overlap(workspace, lora_workspace(l->n_adapters, l->max_rank, l->n, l->k, rows), base, yb))
+    return MOE_ERR_INVALID_ARG;
+  return launch_lora(a, x, base, y, stream) == hipSuccess ? MOE_OK : MOE_ERR_DEVICE;
+}
+
+moe_status lowbit_gemv_lora(const lowbit_matrix* w, const lora_set* l, const uint16_t* x,
+                            const int32_t* ids, int32_t rows, uint16_t* y, void* workspace,
+                            size_t ws_bytes, hipStream_t stream) {
+  bool go;
+  moe_status st = check_gemv(w, x, rows, y, &go);
+  if (st != MOE_OK) return st;
+  st = check_lora_set(l);
+  if (st != MOE_OK) return st;
+  if (l->n != w->n || l->k != w->k) return MOE_ERR_INVALID_ARG;
+  if (!go) return MOE_OK;
+  LoraArgs a;
+  st = lora_args(l, x, ids, rows, y, workspace, ws_bytes, &a);
+  if (st != MOE_OK) return st;
+  if (launch_lora_shrink(a, x, stream) != hipSuccess) return MOE_ERR_DEVICE;
+  return enqueue_gemv(w, x, rows, y, &a, stream);
 }
 
 }  // extern "C"

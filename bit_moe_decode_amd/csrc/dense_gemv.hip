@@ -22,8 +22,10 @@
 // against the input rows at the same inputs (the MFMA's columns are the input
 // rows; columns past them repeat row 0 and are not stored).  The K block's
 // fp32 result is scaled by its weight scale and accumulated.  The block then
-// adds its K parts in part order through LDS and stores y as bf16.
+// adds its K parts in part order through LDS and stores y as bf16, with the
+// rows' adapter terms (lora.h) added before that rounding where there are any.
 #include "device_common.h"
+#include "lora.h"
 
 namespace moe {
 
@@ -39,13 +41,16 @@ struct DgStage {
 
 // BF: bf16 weights (no scales), else FP8 codes with block scales.  T = 16-row
 // tiles a wave.
-template <bool BF, int P, int T>
+template <bool BF, int P, int T, bool LORA>
 __global__ __launch_bounds__(256) void dense_gemv_kernel(
     const uint8_t* __restrict__ codes, const float* __restrict__ scales,
-    const uint16_t* __restrict__ x, uint16_t* __restrict__ y, int rows, int n, int k, int ks) {
+    const uint16_t* __restrict__ x, uint16_t* __restrict__ y, int rows, int n, int k, int ks,
+    GemvTail<LORA> tail) {
   constexpr int S = DgStage<BF, T>::S, EPB = 32 * S;  // MFMA steps, inputs per K block
   __shared__ __align__(16) uint8_t s_tile[4][T][kTileBytes];
+  __shared__ float sv[GemvTail<LORA>::kSv];
   const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
+  tail.load(rows, sv, tid, 256);
   const int col = lane & 15, g = lane >> 4;
   const int spb = 4 / ks;  // wave groups (of T slabs) per block
   const int grp = blockIdx.x * spb + wv / ks, kp = wv % ks;
@@ -131,25 +136,26 @@ __global__ __launch_bounds__(256) void dense_gemv_kernel(
     for (int t = 0; t < T; t++) {
       float v = reinterpret_cast<const float*>(s_tile[s * ks][t])[c * 16 + i];
       for (int q = 1; q < ks; q++) v += reinterpret_cast<const float*>(s_tile[s * ks + q][t])[c * 16 + i];
-      y[(size_t)c * n + ((blockIdx.x * spb + s) * T + t) * 16 + i] = f32_to_bf16(v);
+      const int nr = ((blockIdx.x * spb + s) * T + t) * 16 + i;
+      y[(size_t)c * n + nr] = f32_to_bf16(tail.add(v, c, nr, sv));
     }
   }
 }
 
-template <bool BF, int T>
+template <bool BF, int T, bool LORA>
 static void launch_gemv_t(const uint8_t* codes, const float* scales, const uint16_t* x,
                           uint16_t* y, int rows, int n, int k, int ks, int nk,
-                          hipStream_t stream) {
+                          const GemvTail<LORA>& tail, hipStream_t stream) {
   const dim3 grid(n / (16 * T * (4 / ks)));  // n is a multiple of 128 >= 16 * T * (4 / ks)
   if (nk % 4 == 0)
-    hipLaunchKernelGGL((dense_gemv_kernel<BF, 4, T>), grid, dim3(256), 0, stream, codes, scales,
-                       x, y, rows, n, k, ks);
+    hipLaunchKernelGGL((dense_gemv_kernel<BF, 4, T, LORA>), grid, dim3(256), 0, stream, codes,
+                       scales, x, y, rows, n, k, ks, tail);
   else if (nk % 2 == 0)
-    hipLaunchKernelGGL((dense_gemv_kernel<BF, 2, T>), grid, dim3(256), 0, stream, codes, scales,
-                       x, y, rows, n, k, ks);
+    hipLaunchKernelGGL((dense_gemv_kernel<BF, 2, T, LORA>), grid, dim3(256), 0, stream, codes,
+                       scales, x, y, rows, n, k, ks, tail);
   else
-    hipLaunchKernelGGL((dense_gemv_kernel<BF, 1, T>), grid, dim3(256), 0, stream, codes, scales,
-                       x, y, rows, n, k, ks);
+    hipLaunchKernelGGL((dense_gemv_kernel<BF, 1, T, LORA>), grid, dim3(256), 0, stream, codes,
+                       scales, x, y, rows, n, k, ks, tail);
 }
 
 // K parts of a wave group: the largest of 4, 2, 1 dividing K/128; ring depth:
@@ -158,23 +164,30 @@ static void launch_gemv_t(const uint8_t* codes, const float* scales, const uint1
 // tile: 149.8 -> 132.8 us at one row, 187.3 -> 147.4 us at 8; four tiles
 // with a 2-deep ring: 141.6 us at one row, and 148.1 against 147.2 us at 8).
 hipError_t launch_gemv_fp8(const uint8_t* codes, const float* scales, const uint16_t* x,
-                           uint16_t* y, int rows, int n, int k, hipStream_t stream) {
+                           uint16_t* y, int rows, int n, int k, const LoraArgs* lora,
+                           hipStream_t stream) {
   const int nkb = k / 128;
   const int ks = nkb % 4 == 0 ? 4 : (nkb % 2 == 0 ? 2 : 1);
   const int nk = nkb / ks;
-  launch_gemv_t<false, 2>(codes, scales, x, y, rows, n, k, ks, nk, stream);
+  if (lora)
+    launch_gemv_t<false, 2, true>(codes, scales, x, y, rows, n, k, ks, nk, {*lora}, stream);
+  else
+    launch_gemv_t<false, 2, false>(codes, scales, x, y, rows, n, k, ks, nk, {}, stream);
   return hipGetLastError();
 }
 
 // bf16 weights [n, k]: K blocks of 64 inputs (128 bytes a row), the same K
 // parts, ring and tiles as the FP8 form.  n a multiple of 128, k of 64.
 hipError_t launch_gemv_bf16(const uint16_t* w, const uint16_t* x, uint16_t* y, int rows, int n,
-                            int k, hipStream_t stream) {
+                            int k, const LoraArgs* lora, hipStream_t stream) {
   const int nkb = k / 64;
   const int ks = nkb % 4 == 0 ? 4 : (nkb % 2 == 0 ? 2 : 1);
   const int nk = nkb / ks;
-  launch_gemv_t<true, 2>(reinterpret_cast<const uint8_t*>(w), nullptr, x, y, rows, n, k, ks, nk,
-                         stream);
+  const uint8_t* wb = reinterpret_cast<const uint8_t*>(w);
+  if (lora)
+    launch_gemv_t<true, 2, true>(wb, nullptr, x, y, rows, n, k, ks, nk, {*lora}, stream);
+  else
+    launch_gemv_t<true, 2, false>(wb, nullptr, x, y, rows, n, k, ks, nk, {}, stream);
   return hipGetLastError();
 }
 

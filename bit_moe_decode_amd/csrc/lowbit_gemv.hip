@@ -15,17 +15,22 @@
 // are scaled by d, summed over the row's groups per lane, then across the
 // wave.
 #include "device_common.h"
+#include "lora.h"
 
 namespace moe {
 
 constexpr int kQ1KMax = 16384;
 
+template <bool LORA>
 __global__ __launch_bounds__(256) void lowbit_gemv_q1_kernel(const uint8_t* __restrict__ blocks,
                                                              const uint16_t* __restrict__ x,
-                                                             uint16_t* __restrict__ y, int n, int k) {
+                                                             uint16_t* __restrict__ y, int n, int k,
+                                                             GemvTail<LORA> tail) {
   __shared__ float xs[kQ1KMax];
   __shared__ float s8[kQ1KMax / 8];
+  __shared__ float sv[GemvTail<LORA>::kSv];
   const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
+  tail.load(1, sv, tid, 256);
   for (int i = tid; i < k / 8; i += 256) {
     float s = 0.f;
 #pragma unroll
@@ -59,7 +64,7 @@ __global__ __launch_bounds__(256) void lowbit_gemv_q1_kernel(const uint8_t* __re
     }
 #pragma unroll
     for (int o = 32; o > 0; o >>= 1) acc += __shfl_xor(acc, o, kWave);
-    if (lane == 0) y[row] = f32_to_bf16(acc);
+    if (lane == 0) y[row] = f32_to_bf16(tail.add(acc, 0, row, sv));
   }
 }
 
@@ -198,10 +203,10 @@ __device__ __forceinline__ void lb_fill_pos(uint8_t* smem, uint32_t a, uint2 xv)
 }
 
 // (its LDS allows 3 blocks a CU, so the compiler may schedule for 3 waves a SIMD)
-template <int RB, int M>
+template <int RB, int M, bool LORA>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 3))) void lowbit_gemv_q1_nib_kernel(
     const uint8_t* __restrict__ blocks, const uint16_t* __restrict__ x,
-    uint16_t* __restrict__ y, int n, int k) {
+    uint16_t* __restrict__ y, int n, int k, GemvTail<LORA> tail) {
   constexpr int KP = 256 / RB;
   constexpr int CH = KP * M;  // chunks a round: part q takes q, q + KP, ..
   constexpr uint32_t kSlotB = 4 * lb_slot<KP>();
@@ -219,6 +224,8 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 3))) voi
     return;
   }
 
+  float* sv = reinterpret_cast<float*>(smem + kRed + 256 * 4);  // behind the part sums
+  tail.load(1, sv, tid, 256);
   const int rl = tid % RB, part = tid / RB;
   const int rowl = rl < nr ? rl : nr - 1;  // threads past n decode the last row
   const uint32_t* myrow = reinterpret_cast<const uint32_t*>(blocks + (size_t)(r0 + rowl) * rb);
@@ -271,7 +278,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 3))) voi
     float v = lds_ld(kRed + 4u * (uint32_t)tid);
 #pragma unroll
     for (int q = 1; q < KP; q++) v += lds_ld(kRed + 4u * (uint32_t)(q * RB + tid));
-    y[r0 + tid] = f32_to_bf16(v);
+    y[r0 + tid] = f32_to_bf16(tail.add(v, 0, r0 + tid, sv));
   }
 }
 
@@ -279,17 +286,23 @@ static size_t lb_nib_lds(int rbk, int m) {
   return (size_t)64 * m * 4 * (16 * (256 / rbk) + 4) + 256 * 4;  // tables + part sums
 }
 
-template <int RB, int M>
-static hipError_t lb_nib_launch(const uint8_t* blocks, const uint16_t* x, uint16_t* y, int n,
-                                int k, hipStream_t stream) {
-  const size_t sh = lb_nib_lds(RB, M);
+template <int RB, int M, bool LORA>
+static hipError_t lb_nib_tail(const uint8_t* blocks, const uint16_t* x, uint16_t* y, int n, int k,
+                              const GemvTail<LORA>& tail, hipStream_t stream) {
+  const size_t sh = lb_nib_lds(RB, M) + (LORA ? kLoraMaxRank * 4 : 0);  // + the adapter's v
   static size_t raised[kLdsDevices] = {};  // the limit set per device
-  if (ensure_dyn_lds(reinterpret_cast<const void*>(lowbit_gemv_q1_nib_kernel<RB, M>), sh,
+  if (ensure_dyn_lds(reinterpret_cast<const void*>(lowbit_gemv_q1_nib_kernel<RB, M, LORA>), sh,
                      raised) != hipSuccess)
     return hipErrorInvalidValue;
-  hipLaunchKernelGGL((lowbit_gemv_q1_nib_kernel<RB, M>), dim3((n + RB - 1) / RB), dim3(256), sh,
-                     stream, blocks, x, y, n, k);
+  hipLaunchKernelGGL((lowbit_gemv_q1_nib_kernel<RB, M, LORA>), dim3((n + RB - 1) / RB), dim3(256),
+                     sh, stream, blocks, x, y, n, k, tail);
   return hipGetLastError();
+}
+template <int RB, int M>
+static hipError_t lb_nib_launch(const uint8_t* blocks, const uint16_t* x, uint16_t* y, int n,
+                                int k, const LoraArgs* lora, hipStream_t stream) {
+  return lora ? lb_nib_tail<RB, M, true>(blocks, x, y, n, k, {*lora}, stream)
+              : lb_nib_tail<RB, M, false>(blocks, x, y, n, k, {}, stream);
 }
 
 // MFMA form, for 1 to 8 input rows (K a multiple of 256): y[r][n] for every
@@ -348,12 +361,14 @@ struct QmStage {
   u32x4 xb[8];    // the lane's input row at inputs 128h + 32s + 8(l/16) .. +8
 };
 
-template <int P, int WPB>
+template <int P, int WPB, bool LORA>
 __global__ __launch_bounds__(64 * WPB) void lowbit_gemv_q1_mfma_kernel(
     const uint8_t* __restrict__ blocks, const uint16_t* __restrict__ x,
-    uint16_t* __restrict__ y, int rows, int n, int k, int ks, SignK sk) {
+    uint16_t* __restrict__ y, int rows, int n, int k, int ks, SignK sk, GemvTail<LORA> tail) {
   __shared__ __align__(16) float s_part[WPB][256];  // per wave 16 x 16 sums, column-major
+  __shared__ float sv[GemvTail<LORA>::kSv];
   const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
+  tail.load(rows, sv, tid, 64 * WPB);
   const int col = lane & 15, g = lane >> 4;
   const int spb = WPB / ks;
   const int slab = blockIdx.x * spb + wv / ks, kp = wv % ks;
@@ -421,7 +436,7 @@ __global__ __launch_bounds__(64 * WPB) void lowbit_gemv_q1_mfma_kernel(
     float v = s_part[s2 * ks][cc * 16 + i];
     for (int q = 1; q < ks; q++) v += s_part[s2 * ks + q][cc * 16 + i];
     const int r = (blockIdx.x * spb + s2) * 16 + i;
-    if (r < n) y[(size_t)cc * n + r] = f32_to_bf16(v);
+    if (r < n) y[(size_t)cc * n + r] = f32_to_bf16(tail.add(v, cc, r, sv));
   }
 }
 
@@ -448,11 +463,12 @@ struct Q4Stage {
   uint32_t w[9];  // this lane's row, one chunk: d0, 16 bit-bytes, d1, 16 bit-bytes
 };
 
-template <int P>
+template <int P, bool LORA>
 __global__ __launch_bounds__(256) void lowbit_gemv_q1_mfma4_kernel(
     const uint8_t* __restrict__ blocks, const uint16_t* __restrict__ x,
-    uint16_t* __restrict__ y, int rows, int n, int k, int ks, SignK sk) {
+    uint16_t* __restrict__ y, int rows, int n, int k, int ks, SignK sk, GemvTail<LORA> tail) {
   constexpr int T = 4;
+  __shared__ float sv[GemvTail<LORA>::kSv];
   extern __shared__ __align__(16) uint8_t q4_dyn[];           // input rows, [rows][k + 8] bf16
   __shared__ __align__(16) uint32_t s_u[4][64 * kQ4Stride];  // per wave: sign dwords by row
   __shared__ __align__(16) uint32_t s_d[4][64];               // per wave: d0 | d1 << 16 by row
@@ -460,6 +476,7 @@ __global__ __launch_bounds__(256) void lowbit_gemv_q1_mfma4_kernel(
   const int col = lane & 15, g = lane >> 4;
   const int xs = k + 8;  // LDS row stride of the input rows (elements)
   uint16_t* sx = reinterpret_cast<uint16_t*>(q4_dyn);
+  tail.load(rows, sv, tid, 256);
   for (int i = tid; i < rows * (k / 8); i += 256) {
     const int r = i / (k / 8), e = 8 * (i - r * (k / 8));
     *reinterpret_cast<u32x4*>(sx + r * xs + e) = ld16(x + (size_t)r * k + e);
@@ -570,7 +587,7 @@ __global__ __launch_bounds__(256) void lowbit_gemv_q1_mfma4_kernel(
       float v = s_part[s2 * ks][t][cc * 16 + i];
       for (int q = 1; q < ks; q++) v += s_part[s2 * ks + q][t][cc * 16 + i];
       const int rr = (blockIdx.x * spb + s2) * 64 + 16 * t + i;
-      if (rr < n) y[(size_t)cc * n + rr] = f32_to_bf16(v);
+      if (rr < n) y[(size_t)cc * n + rr] = f32_to_bf16(tail.add(v, cc, rr, sv));
     }
   }
 }
@@ -579,19 +596,23 @@ __global__ __launch_bounds__(256) void lowbit_gemv_q1_mfma4_kernel(
 // that gives at least 4096 waves, else the most that divide; ring depth the
 // largest divisor of a part's chunks up to 8 (a whole part of 8 chunks or
 // fewer is loaded at once).
-template <int P>
+template <int P, bool LORA>
 static void lb_mfma4_one(dim3 grid, size_t lds, const uint8_t* blocks, const uint16_t* x,
-                         uint16_t* y, int rows, int n, int k, int ks, hipStream_t stream) {
-  hipLaunchKernelGGL(lowbit_gemv_q1_mfma4_kernel<P>, grid, dim3(256), lds, stream, blocks, x, y,
-                     rows, n, k, ks, kSignK);
+                         uint16_t* y, int rows, int n, int k, int ks, const GemvTail<LORA>& tail,
+                         hipStream_t stream) {
+  hipLaunchKernelGGL((lowbit_gemv_q1_mfma4_kernel<P, LORA>), grid, dim3(256), lds, stream, blocks,
+                     x, y, rows, n, k, ks, kSignK, tail);
 }
-template <int P>
+template <int P, bool LORA>
 static hipError_t lb_mfma4_lds(size_t lds) {
   static size_t raised[kLdsDevices] = {};
-  return ensure_dyn_lds(reinterpret_cast<const void*>(lowbit_gemv_q1_mfma4_kernel<P>), lds, raised);
+  return ensure_dyn_lds(reinterpret_cast<const void*>(lowbit_gemv_q1_mfma4_kernel<P, LORA>), lds,
+                        raised);
 }
+template <bool LORA>
 static hipError_t lb_mfma4_launch(const uint8_t* blocks, const uint16_t* x, uint16_t* y,
-                                  int rows, int n, int k, hipStream_t stream) {
+                                  int rows, int n, int k, const GemvTail<LORA>& tail,
+                                  hipStream_t stream) {
   const int nch = k / 256, slabs = (n + 63) / 64;
   int ks = 1;
   for (int c : {1, 2, 4}) {
@@ -614,8 +635,9 @@ static hipError_t lb_mfma4_launch(const uint8_t* blocks, const uint16_t* x, uint
   switch (p) {
 #define Q4_CASE(P)                                                          \
   case P:                                                                   \
-    e = lb_mfma4_lds<P>(lds);                                               \
-    if (e == hipSuccess) lb_mfma4_one<P>(grid, lds, blocks, x, y, rows, n, k, ks, stream); \
+    e = lb_mfma4_lds<P, LORA>(lds);                                         \
+    if (e == hipSuccess)                                                    \
+      lb_mfma4_one<P, LORA>(grid, lds, blocks, x, y, rows, n, k, ks, tail, stream); \
     break;
     Q4_CASE(8)
     Q4_CASE(7)
@@ -634,8 +656,9 @@ static hipError_t lb_mfma4_launch(const uint8_t* blocks, const uint16_t* x, uint
 // The MFMA form's launch: K parts the fewest of 1, 2, 4 dividing the chunks
 // that gives at least 512 blocks, else the most that divide (more parts, more
 // blocks); ring depth 2 where it divides a part's chunks, else 1.
+template <bool LORA>
 static hipError_t lb_mfma_launch(const uint8_t* blocks, const uint16_t* x, uint16_t* y, int rows,
-                                 int n, int k, hipStream_t stream) {
+                                 int n, int k, const GemvTail<LORA>& tail, hipStream_t stream) {
   const int nch = k / 256, slabs = (n + 15) / 16;
   // K parts a block (4 waves: 4 / ks slabs of ks parts): the fewest of 1 and
   // 2 that give 512 blocks, else 4 (more waves for few weight rows), at most
@@ -656,17 +679,17 @@ static hipError_t lb_mfma_launch(const uint8_t* blocks, const uint16_t* x, uint1
   const bool p2 = nch % ks == 0 && (nch / ks) % 2 == 0;
   if (w8) {
     if (p2)
-      hipLaunchKernelGGL((lowbit_gemv_q1_mfma_kernel<2, 8>), grid, dim3(512), 0, stream, blocks,
-                         x, y, rows, n, k, ks, kSignK);
+      hipLaunchKernelGGL((lowbit_gemv_q1_mfma_kernel<2, 8, LORA>), grid, dim3(512), 0, stream, blocks,
+                         x, y, rows, n, k, ks, kSignK, tail);
     else
-      hipLaunchKernelGGL((lowbit_gemv_q1_mfma_kernel<1, 8>), grid, dim3(512), 0, stream, blocks,
-                         x, y, rows, n, k, ks, kSignK);
+      hipLaunchKernelGGL((lowbit_gemv_q1_mfma_kernel<1, 8, LORA>), grid, dim3(512), 0, stream, blocks,
+                         x, y, rows, n, k, ks, kSignK, tail);
   } else if (p2) {
-    hipLaunchKernelGGL((lowbit_gemv_q1_mfma_kernel<2, 4>), grid, dim3(256), 0, stream, blocks, x,
-                       y, rows, n, k, ks, kSignK);
+    hipLaunchKernelGGL((lowbit_gemv_q1_mfma_kernel<2, 4, LORA>), grid, dim3(256), 0, stream, blocks, x,
+                       y, rows, n, k, ks, kSignK, tail);
   } else {
-    hipLaunchKernelGGL((lowbit_gemv_q1_mfma_kernel<1, 4>), grid, dim3(256), 0, stream, blocks, x,
-                       y, rows, n, k, ks, kSignK);
+    hipLaunchKernelGGL((lowbit_gemv_q1_mfma_kernel<1, 4, LORA>), grid, dim3(256), 0, stream, blocks, x,
+                       y, rows, n, k, ks, kSignK, tail);
   }
   return hipGetLastError();
 }
@@ -675,13 +698,19 @@ static hipError_t lb_mfma_launch(const uint8_t* blocks, const uint16_t* x, uint1
 // wave): below it there are too few waves to spread over the CUs.
 constexpr int kQ4MinRows = 32768;
 
+template <bool LORA>
+static hipError_t lb_rows_launch(const uint8_t* blocks, const uint16_t* x, uint16_t* y, int rows,
+                                 int n, int k, const GemvTail<LORA>& tail, hipStream_t stream) {
+  if (n >= kQ4MinRows && (size_t)rows * (k + 8) * 2 <= kQ4XBytes)
+    return lb_mfma4_launch<LORA>(blocks, x, y, rows, n, k, tail, stream);
+  return lb_mfma_launch<LORA>(blocks, x, y, rows, n, k, tail, stream);
+}
+
 hipError_t launch_lowbit_q1(const uint8_t* blocks, const uint16_t* x, uint16_t* y, int rows,
-                            int n, int k, hipStream_t stream) {
-  if (rows > 1) {  // K % 256 == 0
-    if (n >= kQ4MinRows && (size_t)rows * (k + 8) * 2 <= kQ4XBytes)
-      return lb_mfma4_launch(blocks, x, y, rows, n, k, stream);
-    return lb_mfma_launch(blocks, x, y, rows, n, k, stream);
-  }
+                            int n, int k, const LoraArgs* lora, hipStream_t stream) {
+  if (rows > 1)  // K % 256 == 0
+    return lora ? lb_rows_launch<true>(blocks, x, y, rows, n, k, {*lora}, stream)
+                : lb_rows_launch<false>(blocks, x, y, rows, n, k, {}, stream);
   // the nibble-table form: rows per block RB the largest of 128, 64, 32 that
   // gives 2048 blocks, else the largest that gives 256, else 16; chunks per
   // thread and round M the fewest (up to 5) that take all of K in one round,
@@ -702,11 +731,11 @@ hipError_t launch_lowbit_q1(const uint8_t* blocks, const uint16_t* x, uint16_t* 
 #define LB_CASE(R)                                                           \
   case R:                                                                    \
     switch (m) {                                                             \
-      case 5: return lb_nib_launch<R, 5>(blocks, x, y, n, k, stream);        \
-      case 4: return lb_nib_launch<R, 4>(blocks, x, y, n, k, stream);        \
-      case 3: return lb_nib_launch<R, 3>(blocks, x, y, n, k, stream);        \
-      case 2: return lb_nib_launch<R, 2>(blocks, x, y, n, k, stream);        \
-      default: return lb_nib_launch<R, 1>(blocks, x, y, n, k, stream);       \
+      case 5: return lb_nib_launch<R, 5>(blocks, x, y, n, k, lora, stream);  \
+      case 4: return lb_nib_launch<R, 4>(blocks, x, y, n, k, lora, stream);  \
+      case 3: return lb_nib_launch<R, 3>(blocks, x, y, n, k, lora, stream);  \
+      case 2: return lb_nib_launch<R, 2>(blocks, x, y, n, k, lora, stream);  \
+      default: return lb_nib_launch<R, 1>(blocks, x, y, n, k, lora, stream); \
     }
     switch (rbk) {
       LB_CASE(128)
@@ -718,7 +747,12 @@ hipError_t launch_lowbit_q1(const uint8_t* blocks, const uint16_t* x, uint16_t* 
   }
   int rows_blocks = (n + 3) / 4;
   int grid = rows_blocks < 1024 ? rows_blocks : 1024;
-  hipLaunchKernelGGL(lowbit_gemv_q1_kernel, dim3(grid), dim3(256), 0, stream, blocks, x, y, n, k);
+  if (lora)
+    hipLaunchKernelGGL((lowbit_gemv_q1_kernel<true>), dim3(grid), dim3(256), 0, stream, blocks, x, y,
+                       n, k, GemvTail<true>{*lora});
+  else
+    hipLaunchKernelGGL((lowbit_gemv_q1_kernel<false>), dim3(grid), dim3(256), 0, stream, blocks, x,
+                       y, n, k, GemvTail<false>{});
   return hipGetLastError();
 }
 

@@ -1,0 +1,467 @@
+// token_rows.hip -- tokens sorted by expert and back: the stable sort of a
+// batch's picks, the gather of the tokens' rows into sorted order, the
+// weighted combination of the sorted rows back into token order, and the
+// gradients of both movements.
+//
+// With ids [T, k] (the picks; flat pick i = t k + j) and E groups:
+//   sort      order = the flat picks with 0 <= id < E by (id, i), offsets[e] =
+//             the picks with an id below e, pos = order's inverse (-1 for a
+//             pick that is in no group)
+//   gather    xs[pos[t,j]] = x[t]
+//     its gradient     dx[t] = sum_j dxs[pos[t,j]]
+//   combine   out[t] = sum_j g[t,j] y[pos[t,j]] (+ add[t])
+//     its gradients    dy[pos[t,j]] = g[t,j] dout[t],
+//                      dg[t,j] = sum_h dout[t,h] y[pos[t,j],h]
+// All sums run in fp32 in pick order, and are rounded once.
+#include "token_rows.h"
+
+#include "device_common.h"
+
+namespace moe {
+
+// ---------------------------------------------------------------------- sort
+// A block takes a chunk of kSortChunk picks, its 16 waves 64 x kSortSteps
+// consecutive ones each.  A wave ranks 64 picks at a time: ballots over the
+// id's bits give each lane the lanes with its id, so the lanes below it are
+// its rank among them, and the lowest of them adds their number to the wave's
+// count of that id in LDS (one wave's own row: its LDS operations complete in
+// order).  The exclusive sums over the waves' counts, group by group, then
+// turn the ranks into places.
+constexpr int kSortWaves = kSortThreads / kWave;
+constexpr int kSortSteps = kSortChunk / kSortThreads;
+
+struct SortShared {
+  int32_t scan[kSortWaves];
+  int32_t total;
+};
+
+// Exclusive sum of v over the block's threads.
+__device__ __forceinline__ int block_scan(int v, SortShared& sh, int tid) {
+  const int lane = tid & 63, wv = tid >> 6;
+  int s = v;
+#pragma unroll
+  for (int o = 1; o < kWave; o <<= 1) {
+    const int u = __shfl_up(s, o, kWave);
+    if (lane >= o) s += u;
+  }
+  if (lane == 63) sh.scan[wv] = s;
+  __syncthreads();
+  int before = 0;
+#pragma unroll
+  for (int w = 0; w < kSortWaves; w++) before += w < wv ? sh.scan[w] : 0;
+  __syncthreads();
+  return before + s - v;
+}
+
+// The block's picks: id (or -1) and rank among the wave's picks of that id;
+// cnt [waves][groups] ends as the waves' counts.
+__device__ __forceinline__ void rank_chunk(const SortArgs& a, int chunk, uint16_t* cnt, int tid,
+                                           int (&id)[kSortSteps], int (&rk)[kSortSteps]) {
+  const int lane = tid & 63, wv = tid >> 6;
+  const int64_t i0 = (int64_t)chunk * kSortChunk + (int64_t)wv * (kWave * kSortSteps) + lane;
+#pragma unroll
+  for (int s = 0; s < kSortSteps; s++) {
+    const int64_t i = i0 + 64 * s;
+    const int e = i < a.picks ? a.ids[i] : -1;
+    id[s] = (uint32_t)e < (uint32_t)a.groups ? e : -1;
+  }
+  for (int i = tid; i < kSortWaves * a.groups; i += kSortThreads) cnt[i] = 0;
+  __syncthreads();
+  uint16_t* mine = cnt + wv * a.groups;
+#pragma unroll
+  for (int s = 0; s < kSortSteps; s++) {
+    const int e = id[s];
+    uint64_t same = __ballot(e >= 0);
+    for (int b = 0; b < a.bits; b++) {
+      const uint64_t m = __ballot((e >> b) & 1);
+      same &= ((e >> b) & 1) ? m : ~m;
+    }
+    if (e >= 0) {
+      const int below = lanes_below(same);
+      rk[s] = mine[e] + below;
+      // every lane of the id has read the count before the lowest adds to it
+      asm volatile("" ::: "memory");
+      if (below == 0) mine[e] = (uint16_t)(rk[s] + __popcll(same));
+      asm volatile("" ::: "memory");
+    }
+  }
+  __syncthreads();
+}
+
+// The tiles of `m` rows that cover every group's rows, in group order, and
+// behind them those of the extra rows [picks, picks + extra): (group, first
+// row, end).  Threads below `groups` hold their group's offsets.
+__device__ __forceinline__ void write_tiles(const SortArgs& a, int first, int count, SortShared& sh,
+                                            int tid) {
+  if (!a.tiles) return;
+  const int nt = tid < a.groups ? (count + a.tile_rows - 1) / a.tile_rows : 0;
+  const int at = block_scan(nt, sh, tid);
+  for (int i = 0; i < nt; i++)
+    a.tiles[at + i] = RowTile{tid, first + i * a.tile_rows, first + count};
+  if (tid == kSortThreads - 1) sh.total = at + nt;
+  __syncthreads();
+  const int routed = sh.total, more = (a.extra + a.tile_rows - 1) / a.tile_rows;
+  for (int i = tid; i < more; i += kSortThreads)
+    a.tiles[routed + i] = RowTile{a.groups, (int)a.picks + i * a.tile_rows, (int)a.picks + a.extra};
+  if (tid == 0) *a.n_tiles = routed + more;
+}
+
+// One chunk: the whole sort in one block (E <= 1024 = a group a thread).
+__global__ __launch_bounds__(kSortThreads) void moe_sort_one_kernel(SortArgs a) {
+  extern __shared__ uint16_t cnt[];
+  __shared__ SortShared sh;
+  __shared__ int32_t base[kSortMaxGroups];
+  const int tid = threadIdx.x;
+  int id[kSortSteps], rk[kSortSteps];
+  rank_chunk(a, 0, cnt, tid, id, rk);
+  int total = 0;
+  if (tid < a.groups) {
+#pragma unroll
+    for (int w = 0; w < kSortWaves; w++) {
+      const int c = cnt[w * a.groups + tid];
+      cnt[w * a.groups + tid] = (uint16_t)total;
+      total += c;
+    }
+  }
+  const int first = block_scan(total, sh, tid);
+  if (tid < a.groups) {
+    base[tid] = first;
+    a.offsets[tid] = first;
+    if (tid == a.groups - 1) a.offsets[a.groups] = first + total;
+  }
+  __syncthreads();
+  const int lane = tid & 63, wv = tid >> 6;
+#pragma unroll
+  for (int s = 0; s < kSortSteps; s++) {
+    const int64_t i = (int64_t)wv * (kWave * kSortSteps) + lane + 64 * s;
+    if (i < a.picks) {
+      const int p = id[s] >= 0 ? base[id[s]] + cnt[wv * a.groups + id[s]] + rk[s] : -1;
+      a.pos[i] = p;
+      if (p >= 0) a.order[p] = (int)i;
+    }
+  }
+  write_tiles(a, first, total, sh, tid);
+}
+
+// More chunks: each chunk's counts [chunk][group], ...
+__global__ __launch_bounds__(kSortThreads) void moe_sort_count_kernel(SortArgs a) {
+  extern __shared__ uint16_t cnt[];
+  const int tid = threadIdx.x;
+  int id[kSortSteps], rk[kSortSteps];
+  rank_chunk(a, blockIdx.x, cnt, tid, id, rk);
+  for (int g = tid; g < a.groups; g += kSortThreads) {
+    int total = 0;
+    for (int w = 0; w < kSortWaves; w++) total += cnt[w * a.groups + g];
+    a.counts[(size_t)blockIdx.x * a.groups + g] = total;
+  }
+}
+
+// ... and the places, every block summing the counts it needs: of its group
+// over the chunks before its own, and of the groups before over all chunks.
+__global__ __launch_bounds__(kSortThreads) void moe_sort_place_kernel(SortArgs a) {
+  extern __shared__ uint16_t cnt[];
+  __shared__ SortShared sh;
+  __shared__ int32_t base[kSortMaxGroups];
+  const int tid = threadIdx.x;
+  int id[kSortSteps], rk[kSortSteps];
+  rank_chunk(a, blockIdx.x, cnt, tid, id, rk);
+  int before = 0, total = 0;
+  if (tid < a.groups) {
+    for (int c = 0; c < a.chunks; c++) {
+      const int n = a.counts[(size_t)c * a.groups + tid];
+      before += c < (int)blockIdx.x ? n : 0;
+      total += n;
+    }
+    int w0 = 0;
+#pragma unroll
+    for (int w = 0; w < kSortWaves; w++) {
+      const int c = cnt[w * a.groups + tid];
+      cnt[w * a.groups + tid] = (uint16_t)w0;
+      w0 += c;
+    }
+  }
+  const int first = block_scan(total, sh, tid);
+  if (tid < a.groups) {
+    base[tid] = first + before;
+    if (blockIdx.x == 0) {
+      a.offsets[tid] = first;
+      if (tid == a.groups - 1) a.offsets[a.groups] = first + total;
+    }
+  }
+  __syncthreads();
+  const int lane = tid & 63, wv = tid >> 6;
+  const int64_t i0 = (int64_t)blockIdx.x * kSortChunk + (int64_t)wv * (kWave * kSortSteps) + lane;
+#pragma unroll
+  for (int s = 0; s < kSortSteps; s++) {
+    const int64_t i = i0 + 64 * s;
+    if (i < a.picks) {
+      const int p = id[s] >= 0 ? base[id[s]] + cnt[wv * a.groups + id[s]] + rk[s] : -1;
+      a.pos[i] = p;
+      if (p >= 0) a.order[p] = (int)i;
+    }
+  }
+  if (blockIdx.x == 0) write_tiles(a, first, total, sh, tid);
+}
+
+int sort_chunks(int64_t picks) { return (int)((picks + kSortChunk - 1) / kSortChunk); }
+
+size_t sort_workspace(int64_t picks, int groups) {
+  const int c = sort_chunks(picks);
+  return c > 1 ? (size_t)c * groups * sizeof(int32_t) : 0;
+}
+
+hipError_t launch_sort(SortArgs a, hipStream_t stream) {
+  a.chunks = sort_chunks(a.picks);
+  a.bits = 0;
+  while ((1 << a.bits) < a.groups) a.bits++;
+  const size_t lds = (size_t)kSortWaves * a.groups * sizeof(uint16_t);  // at most 32 KB
+  if (a.chunks <= 1) {
+    hipLaunchKernelGGL(moe_sort_one_kernel, dim3(1), dim3(kSortThreads), lds, stream, a);
+  } else {
+    hipLaunchKernelGGL(moe_sort_count_kernel, dim3(a.chunks), dim3(kSortThreads), lds, stream, a);
+    hipLaunchKernelGGL(moe_sort_place_kernel, dim3(a.chunks), dim3(kSortThreads), lds, stream, a);
+  }
+  return hipGetLastError();
+}
+
+// -------------------------------------------------------------- row movement
+// Rows are taken 16 bytes a lane where every row starts on a 4-byte boundary
+// (gfx950 loads and stores 16 bytes at any dword alignment), element by
+// element otherwise (an odd number of bf16).
+typedef uint32_t u32x4_a4 __attribute__((ext_vector_type(4), aligned(4)));
+
+template <typename T>
+constexpr int kVec = 16 / (int)sizeof(T);
+
+__device__ __forceinline__ float to_f32(float v) { return v; }
+__device__ __forceinline__ float to_f32(uint16_t v) { return bf16_to_f32(v); }
+__device__ __forceinline__ void from_f32(float v, float& o) { o = v; }
+__device__ __forceinline__ void from_f32(float v, uint16_t& o) { o = f32_to_bf16(v); }
+
+// Elements c .. c + V (those below n) of a row, as fp32.
+template <typename T, int V>
+__device__ __forceinline__ void load_row(const T* row, int c, int n, float (&f)[V]) {
+  if constexpr (V > 1) {
+    if (c + V <= n) {
+      const u32x4_a4 u = *reinterpret_cast<const u32x4_a4*>(row + c);
+#pragma unroll
+      for (int i = 0; i < V; i++) {
+        if constexpr (sizeof(T) == 4)
+          f[i] = __uint_as_float(u[i]);
+        else
+          f[i] = __uint_as_float(i & 1 ? u[i >> 1] & 0xFFFF0000u : u[i >> 1] << 16);
+      }
+      return;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < V; i++) f[i] = c + i < n ? to_f32(row[c + i]) : 0.f;
+}
+
+template <typename T, int V>
+__device__ __forceinline__ void store_row(T* row, int c, int n, const float (&f)[V]) {
+  if constexpr (V > 1) {
+    if (c + V <= n) {
+      u32x4_a4 u;
+#pragma unroll
+      for (int i = 0; i < 4; i++) {
+        if constexpr (sizeof(T) == 4)
+          u[i] = __float_as_uint(f[i]);
+        else
+          u[i] = (uint32_t)f32_to_bf16(f[2 * i]) | ((uint32_t)f32_to_bf16(f[2 * i + 1]) << 16);
+      }
+      *reinterpret_cast<u32x4_a4*>(row + c) = u;
+      return;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < V; i++)
+    if (c + i < n) from_f32(f[i], row[c + i]);
+}
+
+// The row of pick (t, j), or -1: a pick without one, or with one behind the
+// buffer.
+__device__ __forceinline__ int64_t pick_row(const RowArgs& a, int64_t t, int j) {
+  const int p = a.pos[t * a.top_k + j];
+  return (uint32_t)p < (uint32_t)a.rows ? (int64_t)p : -1;
+}
+
+// xs[pos[t,j]] = x[t]: a block reads its part of one token's row once and
+// writes it to the token's places.
+template <typename T, int V>
+__global__ void moe_gather_kernel(RowArgs a, const T* __restrict__ x, T* __restrict__ xs) {
+  const int64_t t = blockIdx.x;
+  const int c = (blockIdx.y * blockDim.x + threadIdx.x) * V;
+  if (c >= a.hidden) return;
+  const T* row = x + t * a.hidden;
+  if (V > 1 && c + V <= a.hidden) {
+    const u32x4_a4 u = *reinterpret_cast<const u32x4_a4*>(row + c);
+    for (int j = 0; j < a.top_k; j++) {
+      const int64_t p = pick_row(a, t, j);
+      if (p >= 0) *reinterpret_cast<u32x4_a4*>(xs + p * a.hidden + c) = u;
+    }
+    return;
+  }
+  for (int j = 0; j < a.top_k; j++) {
+    const int64_t p = pick_row(a, t, j);
+    if (p < 0) continue;
+    for (int i = c; i < c + V && i < a.hidden; i++) xs[p * a.hidden + i] = row[i];
+  }
+}
+
+// out[t] = sum_j w[t,j] y[pos[t,j]] (+ add[t]), w = 1 without gates.  The
+// rows of up to 8 picks are in flight at once; a pick without a row is not
+// read, nor is its gate.
+template <typename T, int V>
+__global__ void moe_combine_kernel_t(RowArgs a, const T* __restrict__ y,
+                                     const float* __restrict__ gates, const T* __restrict__ add,
+                                     T* __restrict__ out) {
+  const int64_t t = blockIdx.x;
+  const int c = (blockIdx.y * blockDim.x + threadIdx.x) * V;
+  if (c >= a.hidden) return;
+  float acc[V];
+#pragma unroll
+  for (int i = 0; i < V; i++) acc[i] = 0.f;
+  for (int j0 = 0; j0 < a.top_k; j0 += 8) {
+    float f[8][V], w[8];
+#pragma unroll
+    for (int j = 0; j < 8; j++) {
+      w[j] = 0.f;
+      if (j0 + j >= a.top_k) continue;
+      const int64_t p = pick_row(a, t, j0 + j);
+      if (p < 0) continue;
+      w[j] = gates ? gates[t * a.top_k + j0 + j] : 1.f;
+      load_row<T, V>(y + p * a.hidden, c, a.hidden, f[j]);
+    }
+#pragma unroll
+    for (int j = 0; j < 8; j++) {
+      if (j0 + j >= a.top_k || pick_row(a, t, j0 + j) < 0) continue;
+#pragma unroll
+      for (int i = 0; i < V; i++) acc[i] = fmaf(w[j], f[j][i], acc[i]);
+    }
+  }
+  if (add) {
+    float f[V];
+    load_row<T, V>(add + t * a.hidden, c, a.hidden, f);
+#pragma unroll
+    for (int i = 0; i < V; i++) acc[i] += f[i];
+  }
+  store_row<T, V>(out + t * a.hidden, c, a.hidden, acc);
+}
+
+// dy and dgates of one token a block: dout[t] is read once for up to 8 picks,
+// each lane keeps its part of their dots, which the waves then add.
+template <typename T, int V>
+__global__ __launch_bounds__(256) void moe_combine_bwd_kernel(
+    RowArgs a, const T* __restrict__ dout, const T* __restrict__ y,
+    const float* __restrict__ gates, T* __restrict__ dy, float* __restrict__ dgates) {
+  __shared__ float part[4][8];
+  const int64_t t = blockIdx.x;
+  const int tid = threadIdx.x;
+  const T* d = dout + t * a.hidden;
+  for (int j0 = 0; j0 < a.top_k; j0 += 8) {
+    float dot[8];
+#pragma unroll
+    for (int j = 0; j < 8; j++) dot[j] = 0.f;
+    for (int c = tid * V; c < a.hidden; c += 256 * V) {
+      float f[V];
+      load_row<T, V>(d, c, a.hidden, f);
+#pragma unroll
+      for (int j = 0; j < 8; j++) {
+        if (j0 + j >= a.top_k) continue;
+        const int64_t p = pick_row(a, t, j0 + j);
+        if (p < 0) continue;
+        const float w = gates[t * a.top_k + j0 + j];
+        float v[V], o[V];
+        load_row<T, V>(y + p * a.hidden, c, a.hidden, v);
+#pragma unroll
+        for (int i = 0; i < V; i++) {
+          dot[j] = fmaf(f[i], v[i], dot[j]);
+          o[i] = w * f[i];
+        }
+        store_row<T, V>(dy + p * a.hidden, c, a.hidden, o);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < 8; j++) {
+      float s = dot[j];
+#pragma unroll
+      for (int o = 32; o > 0; o >>= 1) s += __shfl_xor(s, o, kWave);
+      if ((tid & 63) == 0) part[tid >> 6][j] = s;
+    }
+    __syncthreads();
+    if (tid < 8 && j0 + tid < a.top_k) {
+      const float s = part[0][tid] + part[1][tid] + part[2][tid] + part[3][tid];
+      dgates[t * a.top_k + j0 + tid] = pick_row(a, t, j0 + tid) >= 0 ? s : 0.f;
+    }
+    __syncthreads();
+  }
+}
+
+// Threads a block, and its blocks along a row, for `lanes` lanes a row:
+// whole waves, at most 256 threads.
+static dim3 row_grid(const RowArgs& a, int vec, int* threads) {
+  const int lanes = (a.hidden + vec - 1) / vec;
+  *threads = lanes >= 256 ? 256 : (lanes + 63) / 64 * 64;
+  return dim3((uint32_t)a.tokens, (uint32_t)((lanes + *threads - 1) / *threads));
+}
+
+template <typename T>
+static bool rows_on_dwords(const RowArgs& a) {
+  return a.hidden * sizeof(T) % 4 == 0;
+}
+
+template <typename T>
+static hipError_t gather_t(const RowArgs& a, const void* x, void* xs, hipStream_t stream) {
+  int th;
+  if (rows_on_dwords<T>(a)) {
+    const dim3 g = row_grid(a, kVec<T>, &th);
+    hipLaunchKernelGGL((moe_gather_kernel<T, kVec<T>>), g, dim3(th), 0, stream, a, (const T*)x, (T*)xs);
+  } else {
+    const dim3 g = row_grid(a, 1, &th);
+    hipLaunchKernelGGL((moe_gather_kernel<T, 1>), g, dim3(th), 0, stream, a, (const T*)x, (T*)xs);
+  }
+  return hipGetLastError();
+}
+template <typename T>
+static hipError_t combine_t(const RowArgs& a, const void* y, const float* gates, const void* add,
+                            void* out, hipStream_t stream) {
+  int th;
+  if (rows_on_dwords<T>(a)) {
+    const dim3 g = row_grid(a, kVec<T>, &th);
+    hipLaunchKernelGGL((moe_combine_kernel_t<T, kVec<T>>), g, dim3(th), 0, stream, a, (const T*)y,
+                       gates, (const T*)add, (T*)out);
+  } else {
+    const dim3 g = row_grid(a, 1, &th);
+    hipLaunchKernelGGL((moe_combine_kernel_t<T, 1>), g, dim3(th), 0, stream, a, (const T*)y, gates,
+                       (const T*)add, (T*)out);
+  }
+  return hipGetLastError();
+}
+template <typename T>
+static hipError_t combine_bwd_t(const RowArgs& a, const void* dout, const void* y,
+                                const float* gates, void* dy, float* dgates, hipStream_t stream) {
+  if (rows_on_dwords<T>(a))
+    hipLaunchKernelGGL((moe_combine_bwd_kernel<T, kVec<T>>), dim3((uint32_t)a.tokens), dim3(256), 0,
+                       stream, a, (const T*)dout, (const T*)y, gates, (T*)dy, dgates);
+  else
+    hipLaunchKernelGGL((moe_combine_bwd_kernel<T, 1>), dim3((uint32_t)a.tokens), dim3(256), 0,
+                       stream, a, (const T*)dout, (const T*)y, gates, (T*)dy, dgates);
+  return hipGetLastError();
+}
+
+hipError_t launch_gather(const RowArgs& a, bool f32, const void* x, void* xs, hipStream_t stream) {
+  return f32 ? gather_t<float>(a, x, xs, stream) : gather_t<uint16_t>(a, x, xs, stream);
+}
+hipError_t launch_combine_rows(const RowArgs& a, bool f32, const void* y, const float* gates,
+                               const void* add, void* out, hipStream_t stream) {
+  return f32 ? combine_t<float>(a, y, gates, add, out, stream)
+             : combine_t<uint16_t>(a, y, gates, add, out, stream);
+}
+hipError_t launch_combine_bwd(const RowArgs& a, bool f32, const void* dout, const void* y,
+                              const float* gates, void* dy, float* dgates, hipStream_t stream) {
+  return f32 ? combine_bwd_t<float>(a, dout, y, gates, dy, dgates, stream)
+             : combine_bwd_t<uint16_t>(a, dout, y, gates, dy, dgates, stream);
+}
+
+}  // namespace moe

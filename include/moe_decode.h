@@ -297,6 +297,129 @@ typedef struct {
 moe_status lowbit_gemv(const lowbit_matrix* w, const uint16_t* x, int32_t rows, uint16_t* y,
                        hipStream_t stream);
 
+/* ---- Tokens sorted by expert and back, for batches of any width.
+ *
+ * ids [T, k] are the picks of T tokens (flat pick i = t k + j); an id outside
+ * [0, n_experts) puts its pick in no group (a padded token, an expert of
+ * another rank).  Work is enqueued on `stream` of the current device, where
+ * every pointer has to live; pointers are 16-byte aligned (int32 and gate
+ * pointers 4-byte). */
+#define MOE_MAX_TOP_K 16
+#define MOE_MAX_ROW (1 << 20) /* elements of a row */
+
+/* Bytes of workspace moe_sort needs (0 for small batches), or 0 when the
+ * shape is not supported. */
+size_t moe_sort_workspace_size(int32_t tokens, int32_t top_k, int32_t n_experts);
+
+/* The stable sort of the picks by expert:
+ *  offsets  int32 [n_experts + 1]: expert e's rows are offsets[e] ..
+ *           offsets[e+1] - 1 of the sorted order
+ *  order    int32 [T k]: the flat pick of each sorted row, ascending within
+ *           an expert; entries from offsets[n_experts] on are left as they were
+ *  pos      int32 [T, k]: the sorted row of each pick, -1 for one in no group
+ * top_k 1..16, n_experts 1..1024, tokens * top_k at most 2^24 (more:
+ * MOE_ERR_UNSUPPORTED).  tokens == 0 writes offsets only.  The buffers must
+ * not overlap.  `workspace` may be NULL where the size above is 0; it is
+ * scratch, and two sorts that overlap in time need one each. */
+moe_status moe_sort(const int32_t* ids, int32_t tokens, int32_t top_k, int32_t n_experts,
+                    int32_t* offsets, int32_t* order, int32_t* pos, void* workspace,
+                    size_t ws_bytes, hipStream_t stream);
+
+typedef enum { MOE_BF16 = 0, MOE_F32 = 1 } moe_dtype;
+
+/* Shapes of the row movements below.  `rows` is the number of rows of the
+ * sorted buffers (tokens * top_k holds every pick; fewer do where only that
+ * many picks are in a group); a pos outside [0, rows) is a pick without a
+ * row.  pos is as moe_sort writes it: no row occurs twice. */
+typedef struct {
+  int32_t dtype; /* moe_dtype of every row buffer */
+  int32_t tokens, top_k, hidden, rows;
+} moe_row_shape;
+
+/* xs[pos[t,j]] = x[t] for every pick with a row; x [tokens, hidden], xs
+ * [rows, hidden].  Rows that no pick has are left as they were. */
+moe_status moe_gather(const moe_row_shape* shape, const void* x, const int32_t* pos, void* xs,
+                      hipStream_t stream);
+
+/* Its gradient: dx[t] = sum_j dxs[pos[t,j]] over the picks with a row (0
+ * without any), in pick order in fp32, rounded once. */
+moe_status moe_gather_backward(const moe_row_shape* shape, const void* dxs, const int32_t* pos,
+                               void* dx, hipStream_t stream);
+
+/* out[t] = sum_j gates[t,j] y[pos[t,j]] (+ add[t] where add is not NULL), in
+ * pick order in fp32, rounded once; gates fp32 [tokens, top_k].  The gates of
+ * picks without a row are not read.  out may be add itself. */
+moe_status moe_combine(const moe_row_shape* shape, const void* y, const int32_t* pos,
+                       const float* gates, const void* add, void* out, hipStream_t stream);
+
+/* Its gradients: dy[pos[t,j]] = gates[t,j] dout[t] (rows that no pick has are
+ * left as they were) and dgates[t,j] = sum_h dout[t,h] y[pos[t,j],h] (fp32; 0
+ * for a pick without a row).  The gradient of add is dout itself. */
+moe_status moe_combine_backward(const moe_row_shape* shape, const void* dout, const void* y,
+                                const int32_t* pos, const float* gates, void* dy, float* dgates,
+                                hipStream_t stream);
+
+/* The experts' step for any number of token rows whose routing is given: what
+ * moe_decode_step computes after its top-8 (activation blocks, up/gate, mid,
+ * down, gate-weighted sum with the shared expert), for batches wider than 8
+ * rows.
+ *  cfg     as for moe_decode_init, with FP8 routed experts and FP8
+ *          activations (else MOE_ERR_UNSUPPORTED); max_rows and flags have no
+ *          effect
+ *  x       bf16 [tokens, H], 0..65536 tokens (0: nothing is enqueued)
+ *  ids     int32 [tokens, 8] picks, as moe_decode_debug's; an id outside
+ *          [0, n_experts) adds nothing to its token.  An expert may occur
+ *          twice in a token's picks.
+ *  gates   fp32 [tokens, 8]
+ *  w       as for moe_decode_step; router_w is not used and may be NULL
+ *  out     bf16 [tokens, H], overlapping no input
+ *  workspace  device memory of at least moe_wide_workspace_size bytes,
+ *          256-byte aligned; scratch of this call: steps that overlap in time
+ *          need one each
+ * The sums run in other groupings than the decode step's, so the two agree
+ * within rounding, not bitwise. */
+#define MOE_WIDE_MAX_TOKENS 65536
+size_t moe_wide_workspace_size(const moe_decode_config* cfg, int32_t tokens);
+moe_status moe_wide_step(const moe_decode_config* cfg, const uint16_t* x, int32_t tokens,
+                         const int32_t* ids, const float* gates, const moe_decode_weights* w,
+                         uint16_t* out, void* workspace, size_t ws_bytes, hipStream_t stream);
+
+/* ---- Low-rank adapters of many requests beside a projection they share.
+ *
+ * Row r with adapter i = ids[r] gets scale[i] * B_i (A_i x[r]) added to the
+ * projection's output; an id outside [0, n_adapters) is a row without one.
+ * A x is kept in fp32. */
+typedef struct {
+  int32_t n_adapters;   /* 0..1024 */
+  int32_t max_rank;     /* a multiple of 8, 8..128 */
+  int32_t n, k;         /* the projection's [n, k]; n a multiple of 8, k of 64, k <= 32768 */
+  const uint16_t* a;    /* bf16 [n_adapters, max_rank, k] (device) */
+  const uint16_t* b;    /* bf16 [n_adapters, n, max_rank] (device) */
+  const int32_t* rank;  /* [n_adapters] (device) ranks used of each adapter, 0..max_rank, the
+                           entries of a and b past them not used; NULL: all of max_rank */
+  const float* scale;   /* [n_adapters] (device) */
+} lora_set;
+
+#define MOE_LORA_MAX_ROWS (1 << 20)
+
+/* Bytes of workspace the two calls below need for `rows` rows, or 0 when the
+ * set or the row count is not supported. */
+size_t lora_workspace_size(const lora_set* l, int32_t rows);
+
+/* y[r] = bf16( base[r] + scale_i B_i (A_i x[r]) ): x bf16 [rows, k], ids int32
+ * [rows], base and y bf16 [rows, n]; y may be base itself.  rows == 0 or n ==
+ * 0 is a no-op.  The workspace is scratch of this call, 16-byte aligned. */
+moe_status lora_apply(const lora_set* l, const uint16_t* x, const int32_t* ids, int32_t rows,
+                      const uint16_t* base, uint16_t* y, void* workspace, size_t ws_bytes,
+                      hipStream_t stream);
+
+/* lowbit_gemv with the adapters' terms added in its epilogue, before the one
+ * rounding: y[r] = bf16( W x[r] + scale_i B_i (A_i x[r]) ), rows 0..8, every
+ * weight format of lowbit_gemv.  l->n and l->k must be w's. */
+moe_status lowbit_gemv_lora(const lowbit_matrix* w, const lora_set* l, const uint16_t* x,
+                            const int32_t* ids, int32_t rows, uint16_t* y, void* workspace,
+                            size_t ws_bytes, hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
