@@ -8,6 +8,8 @@ import ctypes
 import os
 import re
 
+import torch
+
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libbit_moe_decode.so")
 HEADER = os.path.join(os.path.dirname(HERE), "include", "moe_decode.h")
@@ -321,7 +323,12 @@ def make_matrix(fmt, n, k, codes, scales=None) -> LowbitMatrix:
 MAX_TOP_K = 16             # MOE_MAX_TOP_K
 WIDE_MAX_TOKENS = 65536    # MOE_WIDE_MAX_TOKENS
 LORA_MAX_ROWS = 1 << 20    # MOE_LORA_MAX_ROWS
-_ROW_DTYPES = {"torch.bfloat16": 0, "torch.float32": 1}  # moe_dtype
+_I32, _BF16, _F32 = torch.int32, torch.bfloat16, torch.float32
+_ROW_DTYPES = {_BF16: 0, _F32: 1}  # moe_dtype
+
+
+def _current_device():
+    return torch.cuda.current_device()
 
 
 def _refuse(what, why):
@@ -330,23 +337,19 @@ def _refuse(what, why):
     raise e
 
 
-def _check(what, device, **tensors):
-    """Every tensor (name=(tensor, dtype, shape), None allowed) is contiguous,
-    on `device` and of that dtype and shape; `device` is the current one."""
-    import torch
-    if device < 0 or device != torch.cuda.current_device():
+def _check(what, device, *tensors):
+    """Every (name, tensor, dtype, shape) -- a tensor may be None -- is
+    contiguous, on `device` and of that dtype and shape; `device` is the
+    current one."""
+    if device < 0 or device != _current_device():
         _refuse(what, "the tensors are not on the current device")
-    for name, (t, dtype, shape) in tensors.items():
+    for name, t, dtype, shape in tensors:
         if t is None:
             continue
-        if t.get_device() != device:
-            _refuse(what, f"{name} is on another device")
-        if t.dtype is not dtype:
-            _refuse(what, f"{name} is {t.dtype}, not {dtype}")
-        if tuple(t.shape) != shape:
-            _refuse(what, f"{name} is {tuple(t.shape)}, not {shape}")
-        if not t.is_contiguous():
-            _refuse(what, f"{name} is not contiguous")
+        if t.dtype is not dtype or t.shape != shape or t.get_device() != device \
+                or not t.is_contiguous():
+            _refuse(what, f"{name} is not a contiguous {dtype} {shape} on device {device}: "
+                          f"{t.dtype} {tuple(t.shape)} with strides {t.stride()} on {t.device}")
 
 
 def _done(st, what):
@@ -370,17 +373,16 @@ def moe_sort(ids, n_experts, offsets, order, pos, workspace=None, stream=None):
     """Stable sort of the picks ids int32 [T, k] by expert: offsets int32
     [n_experts + 1], order int32 [T k], pos int32 [T, k]; workspace: a device
     tensor of moe_sort_workspace_size bytes (None where that is 0)."""
-    import torch
-    i32, (t, k) = torch.int32, ids.shape
-    _check("moe_sort", ids.get_device(), ids=(ids, i32, (t, k)), offsets=(offsets, i32, (n_experts + 1,)),
-           order=(order, i32, (t * k,)), pos=(pos, i32, (t, k)))
+    t, k = ids.shape
+    _check("moe_sort", ids.get_device(), ("ids", ids, _I32, (t, k)), ("offsets", offsets, _I32, (n_experts + 1,)),
+           ("order", order, _I32, (t * k,)), ("pos", pos, _I32, (t, k)))
     ws, n = _space(workspace)
     _done(lib().moe_sort(ids.data_ptr(), t, k, int(n_experts), offsets.data_ptr(), order.data_ptr(),
                          pos.data_ptr(), ws, n, _stream(stream)), "moe_sort")
 
 
 def _row_shape(what, rows, pos):
-    dtype = _ROW_DTYPES.get(str(rows.dtype))
+    dtype = _ROW_DTYPES.get(rows.dtype)
     if dtype is None:
         _refuse(what, f"rows of {rows.dtype}")
     t, k = pos.shape
@@ -389,20 +391,18 @@ def _row_shape(what, rows, pos):
 
 def moe_gather(x, pos, xs, stream=None):
     """xs[pos[t, j]] = x[t]: x [T, H], pos int32 [T, k] (moe_sort's), xs [rows, H]."""
-    import torch
     t, k, h, shape = _row_shape("moe_gather", xs, pos)
-    _check("moe_gather", xs.get_device(), x=(x, xs.dtype, (t, h)), pos=(pos, torch.int32, (t, k)),
-           xs=(xs, xs.dtype, (xs.shape[0], h)))
+    _check("moe_gather", xs.get_device(), ("x", x, xs.dtype, (t, h)), ("pos", pos, _I32, (t, k)),
+           ("xs", xs, xs.dtype, (xs.shape[0], h)))
     _done(lib().moe_gather(shape, x.data_ptr(), pos.data_ptr(), xs.data_ptr(), _stream(stream)),
           "moe_gather")
 
 
 def moe_gather_backward(dxs, pos, dx, stream=None):
     """dx[t] = sum_j dxs[pos[t, j]]: dxs [rows, H], dx [T, H]."""
-    import torch
     t, k, h, shape = _row_shape("moe_gather_backward", dxs, pos)
-    _check("moe_gather_backward", dxs.get_device(), dx=(dx, dxs.dtype, (t, h)),
-           pos=(pos, torch.int32, (t, k)), dxs=(dxs, dxs.dtype, (dxs.shape[0], h)))
+    _check("moe_gather_backward", dxs.get_device(), ("dx", dx, dxs.dtype, (t, h)),
+           ("pos", pos, _I32, (t, k)), ("dxs", dxs, dxs.dtype, (dxs.shape[0], h)))
     _done(lib().moe_gather_backward(shape, dxs.data_ptr(), pos.data_ptr(), dx.data_ptr(),
                                     _stream(stream)), "moe_gather_backward")
 
@@ -410,11 +410,10 @@ def moe_gather_backward(dxs, pos, dx, stream=None):
 def moe_combine(y, pos, gates, out, add=None, stream=None):
     """out[t] = sum_j gates[t, j] y[pos[t, j]] (+ add[t]): y [rows, H], gates
     float32 [T, k], out and add [T, H]."""
-    import torch
     t, k, h, shape = _row_shape("moe_combine", y, pos)
-    _check("moe_combine", y.get_device(), y=(y, y.dtype, (y.shape[0], h)),
-           pos=(pos, torch.int32, (t, k)), gates=(gates, torch.float32, (t, k)),
-           out=(out, y.dtype, (t, h)), add=(add, y.dtype, (t, h)))
+    _check("moe_combine", y.get_device(), ("y", y, y.dtype, (y.shape[0], h)),
+           ("pos", pos, _I32, (t, k)), ("gates", gates, _F32, (t, k)),
+           ("out", out, y.dtype, (t, h)), ("add", add, y.dtype, (t, h)))
     _done(lib().moe_combine(shape, y.data_ptr(), pos.data_ptr(), gates.data_ptr(), _address(add),
                             out.data_ptr(), _stream(stream)), "moe_combine")
 
@@ -422,12 +421,11 @@ def moe_combine(y, pos, gates, out, add=None, stream=None):
 def moe_combine_backward(dout, y, pos, gates, dy, dgates, stream=None):
     """dy[pos[t, j]] = gates[t, j] dout[t] and dgates[t, j] = dout[t] . y[pos[t, j]]:
     dout [T, H], y and dy [rows, H], gates and dgates float32 [T, k]."""
-    import torch
     t, k, h, shape = _row_shape("moe_combine_backward", y, pos)
-    _check("moe_combine_backward", y.get_device(), dout=(dout, y.dtype, (t, h)),
-           y=(y, y.dtype, (y.shape[0], h)), pos=(pos, torch.int32, (t, k)),
-           gates=(gates, torch.float32, (t, k)), dy=(dy, y.dtype, (y.shape[0], h)),
-           dgates=(dgates, torch.float32, (t, k)))
+    _check("moe_combine_backward", y.get_device(), ("dout", dout, y.dtype, (t, h)),
+           ("y", y, y.dtype, (y.shape[0], h)), ("pos", pos, _I32, (t, k)),
+           ("gates", gates, _F32, (t, k)), ("dy", dy, y.dtype, (y.shape[0], h)),
+           ("dgates", dgates, _F32, (t, k)))
     _done(lib().moe_combine_backward(shape, dout.data_ptr(), y.data_ptr(), pos.data_ptr(),
                                      gates.data_ptr(), dy.data_ptr(), dgates.data_ptr(),
                                      _stream(stream)), "moe_combine_backward")
@@ -440,11 +438,10 @@ def moe_wide_workspace_size(cfg: Config, tokens) -> int:
 def moe_wide_step(cfg: Config, x, ids, gates, weights: Weights, out, workspace, stream=None):
     """The experts' step for any number of rows with given routing: x and out
     bf16 [T, H], ids int32 [T, 8], gates float32 [T, 8]."""
-    import torch
     t = x.shape[0]
-    _check("moe_wide_step", x.get_device(), x=(x, torch.bfloat16, (t, cfg.hidden)),
-           ids=(ids, torch.int32, (t, 8)), gates=(gates, torch.float32, (t, 8)),
-           out=(out, torch.bfloat16, (t, cfg.hidden)))
+    _check("moe_wide_step", x.get_device(), ("x", x, _BF16, (t, cfg.hidden)),
+           ("ids", ids, _I32, (t, 8)), ("gates", gates, _F32, (t, 8)),
+           ("out", out, _BF16, (t, cfg.hidden)))
     ws, n = _space(workspace)
     _done(lib().moe_wide_step(ctypes.byref(cfg), x.data_ptr(), t, ids.data_ptr(), gates.data_ptr(),
                               ctypes.byref(weights), out.data_ptr(), ws, n, _stream(stream)),
@@ -456,12 +453,11 @@ def make_lora(a, b, scale, rank=None) -> LoraSet:
     """LoraSet struct of adapters a bf16 [n_adapters, max_rank, k], b bf16
     [n_adapters, n, max_rank], scale float32 [n_adapters], rank int32
     [n_adapters] or None.  The struct keeps the tensors alive."""
-    import torch
     n_adapters, max_rank, k = a.shape
     n = b.shape[1]
-    _check("make_lora", a.get_device(), a=(a, torch.bfloat16, (n_adapters, max_rank, k)),
-           b=(b, torch.bfloat16, (n_adapters, n, max_rank)),
-           scale=(scale, torch.float32, (n_adapters,)), rank=(rank, torch.int32, (n_adapters,)))
+    _check("make_lora", a.get_device(), ("a", a, _BF16, (n_adapters, max_rank, k)),
+           ("b", b, _BF16, (n_adapters, n, max_rank)),
+           ("scale", scale, _F32, (n_adapters,)), ("rank", rank, _I32, (n_adapters,)))
     s = LoraSet(n_adapters, max_rank, n, k, a.data_ptr(), b.data_ptr(), _address(rank),
                 scale.data_ptr())
     s.tensors = (a, b, scale, rank)
@@ -475,10 +471,9 @@ def lora_workspace_size(lora: LoraSet, rows) -> int:
 def lora_apply(lora: LoraSet, x, ids, base, y, workspace, stream=None):
     """y[r] = base[r] + scale_i B_i (A_i x[r]), i = ids[r]: x bf16 [rows, k], ids
     int32 [rows], base and y bf16 [rows, n] (y may be base)."""
-    import torch
-    r, bf = x.shape[0], torch.bfloat16
-    _check("lora_apply", x.get_device(), x=(x, bf, (r, lora.k)), ids=(ids, torch.int32, (r,)),
-           base=(base, bf, (r, lora.n)), y=(y, bf, (r, lora.n)))
+    r, bf = x.shape[0], _BF16
+    _check("lora_apply", x.get_device(), ("x", x, bf, (r, lora.k)), ("ids", ids, _I32, (r,)),
+           ("base", base, bf, (r, lora.n)), ("y", y, bf, (r, lora.n)))
     ws, n = _space(workspace)
     _done(lib().lora_apply(ctypes.byref(lora), x.data_ptr(), ids.data_ptr(), r, base.data_ptr(),
                            y.data_ptr(), ws, n, _stream(stream)), "lora_apply")
@@ -487,10 +482,9 @@ def lora_apply(lora: LoraSet, x, ids, base, y, workspace, stream=None):
 def lowbit_gemv_lora(matrix: LowbitMatrix, lora: LoraSet, x, ids, y, workspace, stream=None):
     """lowbit_gemv of 0..8 rows with the rows' adapters added before the
     rounding: x bf16 [rows, k], ids int32 [rows], y bf16 [rows, n]."""
-    import torch
-    r, bf = x.shape[0], torch.bfloat16
-    _check("lowbit_gemv_lora", x.get_device(), x=(x, bf, (r, matrix.k)), ids=(ids, torch.int32, (r,)),
-           y=(y, bf, (r, matrix.n)))
+    r, bf = x.shape[0], _BF16
+    _check("lowbit_gemv_lora", x.get_device(), ("x", x, bf, (r, matrix.k)), ("ids", ids, _I32, (r,)),
+           ("y", y, bf, (r, matrix.n)))
     ws, n = _space(workspace)
     _done(lib().lowbit_gemv_lora(ctypes.byref(matrix), ctypes.byref(lora), x.data_ptr(),
                                  ids.data_ptr(), r, y.data_ptr(), ws, n, _stream(stream)),

@@ -601,7 +601,12 @@ moe_status lora_args(const lora_set* l, const uint16_t* x, const int32_t* ids, i
   if (l->n_adapters > 0 && (!l->a || !l->b || !l->scale || !aligned16(l->a) || !aligned16(l->b) ||
                             !aligned4(l->scale) || !aligned4(l->rank)))
     return MOE_ERR_INVALID_ARG;
-  const size_t need = lora_workspace(l->n_adapters, l->max_rank, l->n, l->k, rows);
+  a->adapters = l->n_adapters;
+  a->max_rank = l->max_rank;
+  a->n = l->n;
+  a->k = l->k;
+  a->rows = rows;
+  const size_t need = lora_plan(a, ws);
   if (!ws || ws_bytes < need || !aligned16(ws)) return MOE_ERR_WORKSPACE;
   const size_t yb = (size_t)rows * l->n * 2;
   if (overlap(x, (size_t)rows * l->k * 2, y, yb) || overlap(ids, (size_t)rows * 4, y, yb) ||
@@ -612,13 +617,6 @@ moe_status lora_args(const lora_set* l, const uint16_t* x, const int32_t* ids, i
   a->rank = l->rank;
   a->scale = l->scale;
   a->ids = ids;
-  a->adapters = l->n_adapters;
-  a->max_rank = l->max_rank;
-  a->n = l->n;
-  a->k = l->k;
-  a->rows = rows;
-  a->v = static_cast<float*>(ws);
-  a->k_parts = lora_k_parts(rows, l->k);
   return MOE_OK;
 }
 }  // namespace
@@ -795,7 +793,13 @@ moe_status moe_wide_step(const moe_decode_config* cfg, const uint16_t* x, int32_
 
 size_t lora_workspace_size(const lora_set* l, int32_t rows) {
   if (check_lora_set(l) != MOE_OK || rows <= 0 || rows > MOE_LORA_MAX_ROWS) return 0;
-  return lora_workspace(l->n_adapters, l->max_rank, l->n, l->k, rows);
+  LoraArgs a = {};
+  a.adapters = l->n_adapters;
+  a.max_rank = l->max_rank;
+  a.n = l->n;
+  a.k = l->k;
+  a.rows = rows;
+  return lora_plan(&a, nullptr);
 }
 
 moe_status lora_apply(const lora_set* l, const uint16_t* x, const int32_t* ids, int32_t rows,
@@ -806,12 +810,12 @@ moe_status lora_apply(const lora_set* l, const uint16_t* x, const int32_t* ids, 
   if (rows < 0) return MOE_ERR_INVALID_ARG;
   if (rows > MOE_LORA_MAX_ROWS) return MOE_ERR_UNSUPPORTED;
   if (rows == 0 || l->n == 0) return MOE_OK;
-  LoraArgs a;
+  LoraArgs a = {};
   st = lora_args(l, x, ids, rows, y, workspace, ws_bytes, &a);
   if (st != MOE_OK) return st;
   const size_t yb = (size_t)rows * l->n * 2;
   if (!base || !aligned16(base) || (base != y && overlap(base, yb, y, yb)) ||
-      overlap(workspace, lora_workspace(l->n_adapters, l->max_rank, l->n, l->k, rows), base, yb))
+      overlap(workspace, lora_plan(&a, workspace), base, yb))
     return MOE_ERR_INVALID_ARG;
   return launch_lora(a, x, base, y, stream) == hipSuccess ? MOE_OK : MOE_ERR_DEVICE;
 }
@@ -826,7 +830,7 @@ moe_status lowbit_gemv_lora(const lowbit_matrix* w, const lora_set* l, const uin
   if (st != MOE_OK) return st;
   if (l->n != w->n || l->k != w->k) return MOE_ERR_INVALID_ARG;
   if (!go) return MOE_OK;
-  LoraArgs a;
+  LoraArgs a = {};
   st = lora_args(l, x, ids, rows, y, workspace, ws_bytes, &a);
   if (st != MOE_OK) return st;
   if (launch_lora_shrink(a, x, stream) != hipSuccess) return MOE_ERR_DEVICE;

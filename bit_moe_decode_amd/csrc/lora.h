@@ -6,11 +6,13 @@
 #include <stdint.h>
 
 #include "device_common.h"
+#include "token_rows.h"
 
 namespace moe {
 
+constexpr int kLoraTile = 32;
 constexpr int kLoraMaxRank = 128;
-constexpr int kLoraMaxAdapters = 1024;
+constexpr int kLoraMaxAdapters = kSortMaxGroups - 1;  // and a group of the rows without one
 
 // Adapter i: A [max_rank, k] and B [n, max_rank] (bf16), its first rank[i]
 // ranks (all of max_rank without rank) used, times scale[i].
@@ -23,6 +25,10 @@ struct LoraArgs {
   int adapters, max_rank, n, k, rows;
   float* v;            // [k_parts][rows][max_rank] partial sums of A x
   int k_parts;
+  // many rows: grouped by adapter, in tiles of kLoraTile rows (v by sorted row)
+  int32_t *order, *pos, *offsets, *counts, *n_tiles;
+  RowTile* tiles;
+  int max_tiles;
 };
 
 __device__ __forceinline__ int lora_rank(const LoraArgs& l, int adapter) {
@@ -92,8 +98,9 @@ struct GemvTail<true> {
   }
 };
 
-int lora_k_parts(int rows, int k);
-size_t lora_workspace(int adapters, int max_rank, int n, int k, int rows);
+// The workspace of a call: its size, and its parts in *l at base (rows,
+// adapters, max_rank, n and k of *l set).
+size_t lora_plan(LoraArgs* l, void* base);
 hipError_t launch_lora_shrink(const LoraArgs& l, const uint16_t* x, hipStream_t stream);
 hipError_t launch_lora(LoraArgs l, const uint16_t* x, const uint16_t* base, uint16_t* y,
                        hipStream_t stream);

@@ -8,7 +8,7 @@
 namespace moe {
 
 constexpr int kSortThreads = 1024;
-constexpr int kSortChunk = 4096;       // picks a block ranks
+constexpr int kSortChunk = 8192;       // picks a block ranks
 constexpr int kSortMaxGroups = 1024;   // one thread a group
 constexpr int64_t kSortMaxPicks = (int64_t)1 << 24;
 
@@ -31,10 +31,16 @@ struct SortArgs {
   RowTile* tiles;
   int32_t* n_tiles;
   int tile_rows, extra;
-  int chunks, bits;  // set by launch_sort
+  int spill;  // 1: picks in no group go to the last one
+  int chunks, bits, steps;  // set by launch_sort
 };
 
 size_t sort_workspace(int64_t picks, int groups);
+// The most tiles of `tile_rows` rows that cover `picks` picks of `groups`
+// groups: every group has at most one tile that is not full.
+inline int64_t sort_max_tiles(int64_t picks, int groups, int tile_rows) {
+  return picks / tile_rows + (picks < groups ? picks : groups);
+}
 hipError_t launch_sort(SortArgs a, hipStream_t stream);
 
 struct RowArgs {

@@ -20,8 +20,8 @@
 namespace moe {
 
 // ---------------------------------------------------------------------- sort
-// A block takes a chunk of kSortChunk picks, its 16 waves 64 x kSortSteps
-// consecutive ones each.  A wave ranks 64 picks at a time: ballots over the
+// A block takes a chunk of kSortChunk picks, its 16 waves 64 x steps
+// consecutive ones each (as few steps as the picks of a single chunk need).  A wave ranks 64 picks at a time: ballots over the
 // id's bits give each lane the lanes with its id, so the lanes below it are
 // its rank among them, and the lowest of them adds their number to the wave's
 // count of that id in LDS (one wave's own row: its LDS operations complete in
@@ -31,26 +31,35 @@ constexpr int kSortWaves = kSortThreads / kWave;
 constexpr int kSortSteps = kSortChunk / kSortThreads;
 
 struct SortShared {
-  int32_t scan[kSortWaves];
-  int32_t total;
+  int2 scan[kSortWaves];
 };
 
-// Exclusive sum of v over the block's threads.
-__device__ __forceinline__ int block_scan(int v, SortShared& sh, int tid) {
+// Exclusive sums of v's parts over the block's threads, and the block's
+// totals.
+__device__ __forceinline__ int2 block_scan(int2 v, SortShared& sh, int tid, int2* total) {
   const int lane = tid & 63, wv = tid >> 6;
-  int s = v;
+  int2 s = v;
 #pragma unroll
   for (int o = 1; o < kWave; o <<= 1) {
-    const int u = __shfl_up(s, o, kWave);
-    if (lane >= o) s += u;
+    const int x = __shfl_up(s.x, o, kWave), y = __shfl_up(s.y, o, kWave);
+    if (lane >= o) {
+      s.x += x;
+      s.y += y;
+    }
   }
   if (lane == 63) sh.scan[wv] = s;
   __syncthreads();
-  int before = 0;
+  int2 before = {0, 0}, all = {0, 0};
 #pragma unroll
-  for (int w = 0; w < kSortWaves; w++) before += w < wv ? sh.scan[w] : 0;
-  __syncthreads();
-  return before + s - v;
+  for (int w = 0; w < kSortWaves; w++) {
+    const int2 t = sh.scan[w];
+    before.x += w < wv ? t.x : 0;
+    before.y += w < wv ? t.y : 0;
+    all.x += t.x;
+    all.y += t.y;
+  }
+  *total = all;
+  return int2{before.x + s.x - v.x, before.y + s.y - v.y};
 }
 
 // The block's picks: id (or -1) and rank among the wave's picks of that id;
@@ -58,18 +67,24 @@ __device__ __forceinline__ int block_scan(int v, SortShared& sh, int tid) {
 __device__ __forceinline__ void rank_chunk(const SortArgs& a, int chunk, uint16_t* cnt, int tid,
                                            int (&id)[kSortSteps], int (&rk)[kSortSteps]) {
   const int lane = tid & 63, wv = tid >> 6;
-  const int64_t i0 = (int64_t)chunk * kSortChunk + (int64_t)wv * (kWave * kSortSteps) + lane;
+  const int64_t i0 = (int64_t)chunk * kSortChunk + (int64_t)wv * (kWave * a.steps) + lane;
+  const int other = a.spill ? a.groups - 1 : -1;
 #pragma unroll
   for (int s = 0; s < kSortSteps; s++) {
+    id[s] = -1;
+    if (s >= a.steps) continue;
     const int64_t i = i0 + 64 * s;
-    const int e = i < a.picks ? a.ids[i] : -1;
-    id[s] = (uint32_t)e < (uint32_t)a.groups ? e : -1;
+    if (i < a.picks) {
+      const int e = a.ids[i];
+      id[s] = (uint32_t)e < (uint32_t)(a.groups - a.spill) ? e : other;
+    }
   }
   for (int i = tid; i < kSortWaves * a.groups; i += kSortThreads) cnt[i] = 0;
   __syncthreads();
   uint16_t* mine = cnt + wv * a.groups;
 #pragma unroll
   for (int s = 0; s < kSortSteps; s++) {
+    if (s >= a.steps) continue;
     const int e = id[s];
     uint64_t same = __ballot(e >= 0);
     for (int b = 0; b < a.bits; b++) {
@@ -88,19 +103,20 @@ __device__ __forceinline__ void rank_chunk(const SortArgs& a, int chunk, uint16_
   __syncthreads();
 }
 
-// The tiles of `m` rows that cover every group's rows, in group order, and
-// behind them those of the extra rows [picks, picks + extra): (group, first
-// row, end).  Threads below `groups` hold their group's offsets.
-__device__ __forceinline__ void write_tiles(const SortArgs& a, int first, int count, SortShared& sh,
-                                            int tid) {
+// Tiles of a group with `count` rows.
+__device__ __forceinline__ int tiles_of(const SortArgs& a, int count) {
+  return a.tiles ? (count + a.tile_rows - 1) / a.tile_rows : 0;
+}
+
+// The tiles covering every group's rows, in group order, and behind them those
+// of the extra rows [picks, picks + extra).  Threads below `groups` hold their
+// group's first row, rows and first tile; `routed` is the groups' tiles.
+__device__ __forceinline__ void write_tiles(const SortArgs& a, int first, int count, int at,
+                                            int routed, int tid) {
   if (!a.tiles) return;
-  const int nt = tid < a.groups ? (count + a.tile_rows - 1) / a.tile_rows : 0;
-  const int at = block_scan(nt, sh, tid);
-  for (int i = 0; i < nt; i++)
+  for (int i = 0; i * a.tile_rows < count; i++)
     a.tiles[at + i] = RowTile{tid, first + i * a.tile_rows, first + count};
-  if (tid == kSortThreads - 1) sh.total = at + nt;
-  __syncthreads();
-  const int routed = sh.total, more = (a.extra + a.tile_rows - 1) / a.tile_rows;
+  const int more = (a.extra + a.tile_rows - 1) / a.tile_rows;
   for (int i = tid; i < more; i += kSortThreads)
     a.tiles[routed + i] = RowTile{a.groups, (int)a.picks + i * a.tile_rows, (int)a.picks + a.extra};
   if (tid == 0) *a.n_tiles = routed + more;
@@ -123,7 +139,9 @@ __global__ __launch_bounds__(kSortThreads) void moe_sort_one_kernel(SortArgs a) 
       total += c;
     }
   }
-  const int first = block_scan(total, sh, tid);
+  int2 all;
+  const int2 at = block_scan(int2{total, tiles_of(a, total)}, sh, tid, &all);
+  const int first = at.x;
   if (tid < a.groups) {
     base[tid] = first;
     a.offsets[tid] = first;
@@ -133,14 +151,14 @@ __global__ __launch_bounds__(kSortThreads) void moe_sort_one_kernel(SortArgs a) 
   const int lane = tid & 63, wv = tid >> 6;
 #pragma unroll
   for (int s = 0; s < kSortSteps; s++) {
-    const int64_t i = (int64_t)wv * (kWave * kSortSteps) + lane + 64 * s;
-    if (i < a.picks) {
+    const int64_t i = (int64_t)wv * (kWave * a.steps) + lane + 64 * s;
+    if (s < a.steps && i < a.picks) {
       const int p = id[s] >= 0 ? base[id[s]] + cnt[wv * a.groups + id[s]] + rk[s] : -1;
       a.pos[i] = p;
       if (p >= 0) a.order[p] = (int)i;
     }
   }
-  write_tiles(a, first, total, sh, tid);
+  write_tiles(a, first, total, at.y, all.y, tid);
 }
 
 // More chunks: each chunk's counts [chunk][group], ...
@@ -180,7 +198,9 @@ __global__ __launch_bounds__(kSortThreads) void moe_sort_place_kernel(SortArgs a
       w0 += c;
     }
   }
-  const int first = block_scan(total, sh, tid);
+  int2 all;
+  const int2 at = block_scan(int2{total, tiles_of(a, total)}, sh, tid, &all);
+  const int first = at.x;
   if (tid < a.groups) {
     base[tid] = first + before;
     if (blockIdx.x == 0) {
@@ -190,7 +210,7 @@ __global__ __launch_bounds__(kSortThreads) void moe_sort_place_kernel(SortArgs a
   }
   __syncthreads();
   const int lane = tid & 63, wv = tid >> 6;
-  const int64_t i0 = (int64_t)blockIdx.x * kSortChunk + (int64_t)wv * (kWave * kSortSteps) + lane;
+  const int64_t i0 = (int64_t)blockIdx.x * kSortChunk + (int64_t)wv * (kWave * a.steps) + lane;
 #pragma unroll
   for (int s = 0; s < kSortSteps; s++) {
     const int64_t i = i0 + 64 * s;
@@ -200,7 +220,7 @@ __global__ __launch_bounds__(kSortThreads) void moe_sort_place_kernel(SortArgs a
       if (p >= 0) a.order[p] = (int)i;
     }
   }
-  if (blockIdx.x == 0) write_tiles(a, first, total, sh, tid);
+  if (blockIdx.x == 0) write_tiles(a, first, total, at.y, all.y, tid);
 }
 
 int sort_chunks(int64_t picks) { return (int)((picks + kSortChunk - 1) / kSortChunk); }
@@ -212,6 +232,7 @@ size_t sort_workspace(int64_t picks, int groups) {
 
 hipError_t launch_sort(SortArgs a, hipStream_t stream) {
   a.chunks = sort_chunks(a.picks);
+  a.steps = a.chunks > 1 ? kSortSteps : (int)((a.picks + kSortThreads - 1) / kSortThreads);
   a.bits = 0;
   while ((1 << a.bits) < a.groups) a.bits++;
   const size_t lds = (size_t)kSortWaves * a.groups * sizeof(uint16_t);  // at most 32 KB

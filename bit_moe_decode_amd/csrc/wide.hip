@@ -281,9 +281,7 @@ int wide_tile_rows(int64_t picks, int experts) {
 }
 
 int wide_max_tiles(int64_t picks, int experts, int shared_rows, int tile_rows) {
-  // every group has at most one tile that is not full
-  const int64_t most = picks / tile_rows + (picks < experts ? picks : experts);
-  return (int)(most + (shared_rows + tile_rows - 1) / tile_rows);
+  return (int)(sort_max_tiles(picks, experts, tile_rows) + (shared_rows + tile_rows - 1) / tile_rows);
 }
 
 template <int MT, int WM>

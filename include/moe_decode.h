@@ -390,7 +390,7 @@ moe_status moe_wide_step(const moe_decode_config* cfg, const uint16_t* x, int32_
  * projection's output; an id outside [0, n_adapters) is a row without one.
  * A x is kept in fp32. */
 typedef struct {
-  int32_t n_adapters;   /* 0..1024 */
+  int32_t n_adapters;   /* 0..1023 */
   int32_t max_rank;     /* a multiple of 8, 8..128 */
   int32_t n, k;         /* the projection's [n, k]; n a multiple of 8, k of 64, k <= 32768 */
   const uint16_t* a;    /* bf16 [n_adapters, max_rank, k] (device) */

@@ -26,16 +26,16 @@ def sort(tokens=4, top_k=8, n=16, ids=ptr(0), offsets=ptr(1), order=ptr(2), pos=
     (dict(order=None), B.MOE_ERR_INVALID_ARG), (dict(pos=None), B.MOE_ERR_INVALID_ARG),
     (dict(ids=ptr(0) + 2), B.MOE_ERR_INVALID_ARG), (dict(pos=ptr(2) + 64), B.MOE_ERR_INVALID_ARG),
     (dict(offsets=ptr(0) + 4), B.MOE_ERR_INVALID_ARG),
-    (dict(tokens=4096), B.MOE_ERR_WORKSPACE),
-    (dict(tokens=4096, ws=ptr(4), nb=16), B.MOE_ERR_WORKSPACE),
-    (dict(tokens=4096, ws=ptr(2) + 64, nb=1 << 20), B.MOE_ERR_INVALID_ARG)])
+    (dict(tokens=40960), B.MOE_ERR_WORKSPACE),
+    (dict(tokens=40960, ws=ptr(4), nb=16), B.MOE_ERR_WORKSPACE),
+    (dict(tokens=40960, ws=ptr(2) + 64, nb=1 << 20), B.MOE_ERR_INVALID_ARG)])
 def test_sort_refusals(kw, st):
     assert sort(**kw) == st
 
 
 def test_sort_workspace_size():
     assert B.moe_sort_workspace_size(16, 8, 256) == 0
-    assert B.moe_sort_workspace_size(4096, 8, 256) > 0
+    assert B.moe_sort_workspace_size(40960, 8, 256) > 0
     assert B.moe_sort_workspace_size(4096, 17, 256) == 0
     assert B.moe_sort_workspace_size(-1, 8, 256) == 0
 

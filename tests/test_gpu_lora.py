@@ -83,7 +83,8 @@ def _space(lora, rows):
 SHAPES = [(1, 8, 64, 8, 1, 1), (1, 6144, 6144, 16, 3, 1), (3, 264, 192, 24, 2, 1),
           (8, 1000, 1088, 8, 9, 1), (17, 520, 4160, 64, 40, 1), (64, 2048, 2560, 16, 128, 1),
           (65, 136, 640, 128, 5, 7), (200, 1024, 1024, 32, 3, 90), (777, 392, 704, 40, 11, 50),
-          (1025, 2056, 512, 128, 1000, 1), (2500, 512, 2048, 64, 6, 400), (130, 64, 32768, 16, 4, 1)]
+          (1025, 2056, 512, 128, 1000, 1), (2500, 512, 2048, 64, 6, 400), (130, 64, 32768, 16, 4, 1), (150, 128, 256, 16, 3, 1),
+          (70, 264, 64, 8, 3, 1), (300, 64, 576, 16, 2, 40)]
 
 
 @pytest.mark.parametrize("ragged", [False, True])

@@ -61,7 +61,7 @@ def _sort(ids, e, stream=None, ws=None):
 
 
 @pytest.mark.parametrize("t,k,e", [(1, 1, 1), (1, 8, 256), (3, 6, 16), (16, 8, 256), (61, 16, 1000),
-                                   (512, 8, 256), (513, 8, 256), (4097, 1, 1024), (5000, 7, 33),
+                                   (512, 8, 256), (1024, 8, 256), (1025, 8, 256), (8193, 1, 1024), (5000, 7, 33),
                                    (40001, 8, 256)])
 @pytest.mark.parametrize("mode", ["random", "outside", "same", "none"])
 def test_sort(t, k, e, mode):
