@@ -72,125 +72,142 @@ __global__ __launch_bounds__(256) void moe_wide_act_kernel(WideArgs a, const uin
 // sorted rows its B operand.  After each step the fp32 products are scaled by
 // weight scale times row scale and added.
 __device__ __forceinline__ int lds_at(int row, int chunk) {
-  return row * 128 + ((chunk ^ row ^ (row >> 3)) & 7) * 16;
+  return row * 128 + ((chunk ^ (row >> 1)) & 7) * 16;
 }
 
-template <int MT, int WM>
-struct WideTile {
-  static constexpr int BM = 16 * MT * WM;    // sorted rows
-  static constexpr int kThreads = 256 * WM;  // WM x 4 waves, MT x 4 MFMA tiles each
-  static constexpr int kChunksA = BM * 8, kChunksW = 256 * 8;  // 16-byte chunks a step
-  static constexpr int NA = (kChunksA + kThreads - 1) / kThreads, NW = kChunksW / kThreads;
-  static constexpr int kLds = (BM + 256) * 128;
+// Loads at a 32-bit offset from a block-uniform base: the base, the uniform
+// part of the offset and the bound stay in scalar registers (as 64-bit
+// addresses a lane's 12 loads a step took 24 vector registers).
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t uniform_base(const void* p, uint32_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, bytes, 0x00027000);
+}
+__device__ __forceinline__ u32x4 load_at(__amdgpu_buffer_rsrc_t r, uint32_t lane, uint32_t uniform) {
+  return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, lane, uniform, 0));
+}
+__device__ __forceinline__ float load_f32_at(__amdgpu_buffer_rsrc_t r, uint32_t lane, uint32_t uniform) {
+  return __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(r, lane, uniform, 0));
+}
+
+template <int MT>
+struct WideLds {
+  __align__(16) uint8_t codes[(16 * MT + 256) * 128];  // weight rows, then sorted rows
+  float as[16 * MT];
+  float mx[4][16 * MT];
 };
 
-template <int MT, int WM, bool UG>
-__global__ __launch_bounds__(256 * WM) void moe_wide_gemm_kernel(WideArgs a, WideWeights w) {
-  using C = WideTile<MT, WM>;
-  __shared__ __align__(16) uint8_t lds[C::kLds];
-  __shared__ float s_as[C::BM];
-  __shared__ float s_max[4][C::BM];
-  if ((int)blockIdx.y >= *a.n_tiles) return;
-  const RowTile tile = a.tiles[blockIdx.y];
-  const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
-  const int wn = wv & 3, wm = wv >> 2, col = lane & 15, g = lane >> 4;
-  const bool sh = tile.group == a.E;
+// The tile's products and their epilogue, U of its MT row tiles holding rows.
+template <int MT, int U, bool UG>
+__device__ __forceinline__ void wide_tile(const WideArgs& a, const WideWeights& w,
+                                          const RowTile& tile, int nb, WideLds<MT>& sh) {
+  constexpr int NA = (U + 1) / 2;  // 16-byte chunks of sorted rows a thread loads a step
+  const int tid = threadIdx.x, lane = tid & 63, wn = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int col = lane & 15, g = lane >> 4;
+  const bool shared = tile.group == a.E;
   const int K = UG ? a.H : a.I, N = UG ? a.I : a.H, nkb = K / 128;
-  const int nb = blockIdx.x;  // UG: 128 mid columns; down: 256 output columns
-  const int64_t ew = sh ? 0 : (int64_t)tile.group * N * K;
-  const int64_t es = sh ? 0 : (int64_t)tile.group * (N / 128) * nkb;
-  const uint8_t* w0 = (UG ? (sh ? w.sg_c : w.gate_c) : (sh ? w.sd_c : w.down_c)) + ew;
-  const uint8_t* w1 = UG ? (sh ? w.su_c : w.up_c) + ew : w0;
-  const float* s0 = (UG ? (sh ? w.sg_s : w.gate_s) : (sh ? w.sd_s : w.down_s)) + es;
-  const float* s1 = UG ? (sh ? w.su_s : w.up_s) + es : s0;
-  // weight rows of the block: half h (0, 1) starts at row n0[h]; a half past
+  const int64_t ew = shared ? 0 : (int64_t)tile.group * N * K;
+  const int64_t es = shared ? 0 : (int64_t)tile.group * (N / 128) * nkb;
+  const uint8_t* w0 = (UG ? (shared ? w.sg_c : w.gate_c) : (shared ? w.sd_c : w.down_c)) + ew;
+  const uint8_t* w1 = UG ? (shared ? w.su_c : w.up_c) + ew : w0;
+  const float* s0 = (UG ? (shared ? w.sg_s : w.gate_s) : (shared ? w.sd_s : w.down_s)) + es;
+  const float* s1 = UG ? (shared ? w.su_s : w.up_s) + es : s0;
+  // weight rows of the block: half h (0, 1) starts at row n0, n1; a half past
   // the end of the down matrix repeats its last and is not stored
   const int n0 = UG ? nb * 128 : nb * 256;
   const int n1 = UG ? n0 : (n0 + 128 < N ? n0 + 128 : n0);
   const float* ps0 = s0 + (int64_t)(n0 / 128) * nkb;
   const float* ps1 = s1 + (int64_t)(n1 / 128) * nkb;
 
-  // this thread's chunks of a step: weights, then sorted rows (those past the
-  // tile's end repeat its last row)
-  const uint8_t* pw[C::NW];
-#pragma unroll
-  for (int i = 0; i < C::NW; i++) {
-    const int q = tid + i * C::kThreads, r = q >> 3;
-    const uint8_t* base = r < 128 ? w0 + (int64_t)(n0 + r) * K : w1 + (int64_t)(n1 + r - 128) * K;
-    pw[i] = base + (q & 7) * 16;
-  }
-  const uint8_t* pa[C::NA];
-  auto source_row = [&](int i) -> int64_t {  // row of the activations for sorted row i of the tile
+  // this thread's chunks of a step: weight rows tid / 8 + 32 i (i < 4: half 0),
+  // then sorted rows (those past the tile's end repeat its last row)
+  const uint32_t ow = (uint32_t)(tid >> 3) * (uint32_t)K + (uint32_t)(tid & 7) * 16u;
+  const auto bw0 = uniform_base(w0 + (int64_t)n0 * K, 128u * K);
+  const auto bw1 = uniform_base(w1 + (int64_t)n1 * K, 128u * K);
+  const int rows = UG ? a.tokens : (tile.end - tile.row < 16 * U ? tile.end - tile.row : 16 * U);
+  const auto ba = uniform_base(UG ? a.act_q : a.mid_q + (int64_t)tile.row * K, (uint32_t)rows * K);
+  const auto bs = uniform_base(UG ? a.act_s : a.mid_s + (int64_t)tile.row * nkb, (uint32_t)rows * nkb * 4u);
+  auto source_row = [&](int i) -> uint32_t {  // row behind ba, bs of the tile's sorted row i
     int s = tile.row + i;
     if (s >= tile.end) s = tile.end - 1;
-    if (!UG) return s;
-    return s < a.picks ? a.order[s] >> 3 : s - a.picks;
+    if (!UG) return (uint32_t)(s - tile.row);
+    return (uint32_t)(s < a.picks ? a.order[s] >> 3 : s - a.picks);
   };
+  uint32_t oa[NA];
 #pragma unroll
-  for (int i = 0; i < C::NA; i++) {
-    const int q = tid + i * C::kThreads;
-    const int64_t r = q < C::kChunksA ? source_row(q >> 3) : 0;
-    pa[i] = (UG ? a.act_q : a.mid_q) + r * K + (q & 7) * 16;
-  }
-  const float* psa = (UG ? a.act_s : a.mid_s) + (tid < C::BM ? source_row(tid) : 0) * nkb;
+  for (int i = 0; i < NA; i++)
+    oa[i] = source_row((tid >> 3) + 32 * i) * (uint32_t)K + (uint32_t)(tid & 7) * 16u;
+  const uint32_t os = source_row(tid) * (uint32_t)nkb * 4u;
+  // an odd number of row tiles: the last 16 rows are loaded by the first two waves
+  auto loads = [&](int i) { return i + 1 < NA || U % 2 == 0 || wn < 2; };
 
-  u32x4 rw[C::NW], ra[C::NA];
+  u32x4 rw[8], ra[NA];
   float rs = 0.f;
-  auto issue = [&](int kb) {
+  auto issue = [&](uint32_t kb) {
 #pragma unroll
-    for (int i = 0; i < C::NW; i++) rw[i] = ld16(pw[i] + kb * 128);
+    for (int i = 0; i < 4; i++) rw[i] = load_at(bw0, ow, 32u * i * K + kb * 128u);
 #pragma unroll
-    for (int i = 0; i < C::NA; i++)
-      if (tid + i * C::kThreads < C::kChunksA) ra[i] = ld16(pa[i] + kb * 128);
-    if (tid < C::BM) rs = psa[kb];
+    for (int i = 0; i < 4; i++) rw[4 + i] = load_at(bw1, ow, 32u * i * K + kb * 128u);
+#pragma unroll
+    for (int i = 0; i < NA; i++)
+      if (loads(i)) ra[i] = load_at(ba, oa[i], kb * 128u);
+    if (64 * wn < 16 * U) rs = load_f32_at(bs, os, kb * 4u);
   };
-  float acc[MT][4][4];  // [sorted-row tile][weight tile: 2 of half 0, 2 of half 1][4 columns]
+  float acc[U][4][4];  // [sorted-row tile][weight tile: 2 of half 0, 2 of half 1][4 columns]
 #pragma unroll
-  for (int i = 0; i < MT; i++)
+  for (int i = 0; i < U; i++)
 #pragma unroll
     for (int j = 0; j < 4; j++)
 #pragma unroll
       for (int v = 0; v < 4; v++) acc[i][j][v] = 0.f;
 
+  // Places in LDS.  The permutation depends on a row's last 4 bits alone, so
+  // that 16 rows on (and 32, for the writes) are at a constant distance.
+  uint8_t* const put = sh.codes + lds_at(tid >> 3, tid & 7);
+  const uint8_t* const row0 = sh.codes + lds_at(col, g);      // K 16 g .. of row col
+  const uint8_t* const row1 = sh.codes + lds_at(col, g + 4);  // K 64 + 16 g ..
+  auto operand = [&](int row) { return cat8(ld16(row0 + row * 128), ld16(row1 + row * 128)); };
+
   issue(0);
   for (int kb = 0; kb < nkb; kb++) {
     __syncthreads();  // every wave is done with the last step's codes
 #pragma unroll
-    for (int i = 0; i < C::NW; i++) {
-      const int q = tid + i * C::kThreads;
-      *reinterpret_cast<u32x4*>(lds + lds_at(q >> 3, q & 7)) = rw[i];
-    }
+    for (int i = 0; i < 8; i++) *reinterpret_cast<u32x4*>(put + i * 4096) = rw[i];
 #pragma unroll
-    for (int i = 0; i < C::NA; i++) {
-      const int q = tid + i * C::kThreads;
-      if (q < C::kChunksA) *reinterpret_cast<u32x4*>(lds + lds_at(256 + (q >> 3), q & 7)) = ra[i];
-    }
-    if (tid < C::BM) s_as[tid] = rs;
+    for (int i = 0; i < NA; i++)
+      if (loads(i)) *reinterpret_cast<u32x4*>(put + 32768 + i * 4096) = ra[i];
+    if (tid < 16 * U) sh.as[tid] = rs;
     const float sw[2] = {ps0[kb], ps1[kb]};
     if (kb + 1 < nkb) issue(kb + 1);
     __syncthreads();
     v8i op[4];
 #pragma unroll
-    for (int j = 0; j < 4; j++) {
-      const int r = (j >> 1) * 128 + wn * 32 + (j & 1) * 16 + col;
-      op[j] = cat8(ld16(lds + lds_at(r, g)), ld16(lds + lds_at(r, g + 4)));
-    }
+    for (int j = 0; j < 4; j++) op[j] = operand((j >> 1) * 128 + wn * 32 + (j & 1) * 16);
+    // the scheduling barriers keep the compiler from hoisting every row tile's
+    // reads (71 spilled registers at 8 row tiles without them)
+    v8i b[2];
+    float as[2];
+    auto fetch = [&](int i) {
+      b[i & 1] = operand(256 + 16 * i);
+      as[i & 1] = sh.as[i * 16 + col];
+    };
+    fetch(0);
 #pragma unroll
-    for (int i = 0; i < MT; i++) {
-      const int m = (wm * MT + i) * 16 + col;
-      const v8i b = cat8(ld16(lds + lds_at(256 + m, g)), ld16(lds + lds_at(256 + m, g + 4)));
-      const float as = s_as[m];
+    for (int i = 0; i < U; i++) {
+      v4f c[4];
+#pragma unroll
+      for (int j = 0; j < 4; j++) c[j] = mfma_fp8(op[j], b[i & 1]);
+      const float ar = as[i & 1];
+      if (i + 1 < U) fetch(i + 1);
 #pragma unroll
       for (int j = 0; j < 4; j++) {
-        const v4f c = mfma_fp8(op[j], b);
-        const float s = as * sw[j >> 1];
+        const float s = ar * sw[j >> 1];
 #pragma unroll
-        for (int v = 0; v < 4; v++) acc[i][j][v] = fmaf(c[v], s, acc[i][j][v]);
+        for (int v = 0; v < 4; v++) acc[i][j][v] = fmaf(c[j][v], s, acc[i][j][v]);
       }
+      __builtin_amdgcn_sched_barrier(0);
     }
   }
 #pragma unroll
-  for (int i = 0; i < MT; i++)
+  for (int i = 0; i < U; i++)
 #pragma unroll
     for (int j = 0; j < 4; j++) pin4(acc[i][j]);
 
@@ -198,7 +215,7 @@ __global__ __launch_bounds__(256 * WM) void moe_wide_gemm_kernel(WideArgs a, Wid
     // mid of columns 32 wn + 16 j + 4 g + v, j < 2, then its 1x128 block's
     // largest value over the 4 waves of the row
 #pragma unroll
-    for (int i = 0; i < MT; i++) {
+    for (int i = 0; i < U; i++) {
       float mx = 0.f;
 #pragma unroll
       for (int j = 0; j < 2; j++)
@@ -211,39 +228,85 @@ __global__ __launch_bounds__(256 * WM) void moe_wide_gemm_kernel(WideArgs a, Wid
         }
       mx = fmaxf(mx, __shfl_xor(mx, 16, kWave));
       mx = fmaxf(mx, __shfl_xor(mx, 32, kWave));
-      if (g == 0) s_max[wn][(wm * MT + i) * 16 + col] = mx;
+      if (g == 0) sh.mx[wn][i * 16 + col] = mx;
     }
     __syncthreads();
+    // the codes through LDS, so that 8 lanes store a row's 128 bytes
 #pragma unroll
-    for (int i = 0; i < MT; i++) {
-      const int m = (wm * MT + i) * 16 + col;
-      const int row = tile.row + m;
-      if (row >= tile.end) continue;
-      const float s = fmaxf(fmaxf(s_max[0][m], s_max[1][m]), fmaxf(s_max[2][m], s_max[3][m])) / 448.0f;
+    for (int i = 0; i < U; i++) {
+      const int m = i * 16 + col;
+      const float s = fmaxf(fmaxf(sh.mx[0][m], sh.mx[1][m]), fmaxf(sh.mx[2][m], sh.mx[3][m])) / 448.0f;
 #pragma unroll
       for (int j = 0; j < 2; j++) {
         uint32_t q = 0u;
         if (s > 0.f)
           q = f32x2_to_e4m3(acc[i][j][0] / s, acc[i][j][1] / s) |
               (f32x2_to_e4m3(acc[i][j][2] / s, acc[i][j][3] / s) << 16);
-        *reinterpret_cast<uint32_t*>(a.mid_q + (int64_t)row * N + n0 + wn * 32 + j * 16 + 4 * g) = q;
+        *reinterpret_cast<uint32_t*>(sh.codes + m * 128 + wn * 32 + j * 16 + 4 * g) = q;
       }
-      if (wn == 0 && g == 0) a.mid_s[(int64_t)row * (N / 128) + nb] = s;
+      if (wn == 0 && g == 0 && tile.row + m < tile.end)
+        a.mid_s[(int64_t)(tile.row + m) * (N / 128) + nb] = s;
+    }
+    __syncthreads();
+    for (int q = tid; q < 16 * U * 8; q += 256) {
+      const int row = tile.row + (q >> 3);
+      if (row < tile.end)
+        *reinterpret_cast<u32x4*>(a.mid_q + (int64_t)row * N + n0 + (q & 7) * 16) = ld16(sh.codes + q * 16);
     }
   } else {
+    // through LDS, so that 8 lanes store 32 consecutive outputs of a row: the
+    // wave's 16 rows x 64 columns of one row tile at a time, in an area of its
+    // own (rows of 68 floats; one wave's LDS operations complete in order)
+    __syncthreads();  // every wave is done with the last step's codes
+    float* mine = reinterpret_cast<float*>(sh.codes) + wn * 16 * 68;
+    const int jn = lane & 15;  // columns 4 jn ..: half jn / 8
+    const int n = n0 + (jn >> 3) * 128 + wn * 32 + (jn & 7) * 4;
 #pragma unroll
-    for (int i = 0; i < MT; i++) {
-      const int row = tile.row + (wm * MT + i) * 16 + col;
-      if (row >= tile.end) continue;
+    for (int i = 0; i < U; i++) {
+      asm volatile("" ::: "memory");
 #pragma unroll
-      for (int j = 0; j < 4; j++) {
-        const int n = n0 + (j >> 1) * 128 + wn * 32 + (j & 1) * 16 + 4 * g;
-        if (n < N)
-          *reinterpret_cast<v4f*>(a.y + (int64_t)row * N + n) =
-              v4f{acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]};
+      for (int j = 0; j < 4; j++)
+        *reinterpret_cast<v4f*>(mine + col * 68 + j * 16 + 4 * g) =
+            v4f{acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]};
+      asm volatile("" ::: "memory");
+#pragma unroll
+      for (int q = 0; q < 4; q++) {
+        const int m = 4 * q + (lane >> 4), row = tile.row + i * 16 + m;
+        const v4f v = *reinterpret_cast<const v4f*>(mine + m * 68 + 4 * jn);
+        if (row < tile.end && n < N) *reinterpret_cast<v4f*>(a.y + (int64_t)row * N + n) = v;
       }
     }
   }
+}
+
+template <int MT, bool UG>
+__global__ __launch_bounds__(256, MT <= 2 ? 3 : 2) void moe_wide_gemm_kernel(WideArgs a, WideWeights w) {
+  __shared__ WideLds<MT> sh;
+  // Column blocks (UG: 128 mid columns; down: 256 outputs) first: consecutive
+  // blocks go to the 8 XCDs in turn, each with an L2 of its own, and where a
+  // multiple of 8 column blocks makes up a row tile, one XCD's L2 serves all
+  // the row tiles of a column block, so that an expert's tiles share its weights
+  const uint32_t nbs = UG ? a.I / 128 : (a.H + 255) / 256;
+  const int ti = (int)(blockIdx.x / nbs), nb = (int)(blockIdx.x % nbs);
+  if (ti >= *a.n_tiles) return;
+  const RowTile tile = a.tiles[ti];
+  int used = (tile.end - tile.row + 15) >> 4;
+  used = __builtin_amdgcn_readfirstlane(used < MT ? used : MT);
+  // a loop for each number of row tiles that hold rows
+  if constexpr (MT >= 8) {
+    if (used == 8) return wide_tile<MT, 8, UG>(a, w, tile, nb, sh);
+    if (used == 7) return wide_tile<MT, 7, UG>(a, w, tile, nb, sh);
+    if (used == 6) return wide_tile<MT, 6, UG>(a, w, tile, nb, sh);
+    if (used == 5) return wide_tile<MT, 5, UG>(a, w, tile, nb, sh);
+  }
+  if constexpr (MT >= 4) {
+    if (used == 4) return wide_tile<MT, 4, UG>(a, w, tile, nb, sh);
+    if (used == 3) return wide_tile<MT, 3, UG>(a, w, tile, nb, sh);
+  }
+  if constexpr (MT >= 2) {
+    if (used == 2) return wide_tile<MT, 2, UG>(a, w, tile, nb, sh);
+  }
+  wide_tile<MT, 1, UG>(a, w, tile, nb, sh);
 }
 
 // out[t] = bf16( sum_j g[t,j] y[pos[t,j]] + y[picks + t] ), in pick order.
@@ -277,19 +340,19 @@ __global__ __launch_bounds__(256) void moe_wide_combine_kernel(WideArgs a,
 
 int wide_tile_rows(int64_t picks, int experts) {
   const int64_t per = picks / experts;
-  return per <= 16 ? 16 : (per <= 48 ? 32 : (per <= 96 ? 64 : 128));
+  return per <= 16 ? 32 : (per <= 48 ? 64 : 128);
 }
 
 int wide_max_tiles(int64_t picks, int experts, int shared_rows, int tile_rows) {
   return (int)(sort_max_tiles(picks, experts, tile_rows) + (shared_rows + tile_rows - 1) / tile_rows);
 }
 
-template <int MT, int WM>
+template <int MT>
 static void launch_products(const WideArgs& a, const WideWeights& w, hipStream_t stream) {
-  hipLaunchKernelGGL((moe_wide_gemm_kernel<MT, WM, true>), dim3(a.I / 128, a.max_tiles),
-                     dim3(256 * WM), 0, stream, a, w);
-  hipLaunchKernelGGL((moe_wide_gemm_kernel<MT, WM, false>), dim3((a.H + 255) / 256, a.max_tiles),
-                     dim3(256 * WM), 0, stream, a, w);
+  hipLaunchKernelGGL((moe_wide_gemm_kernel<MT, true>), dim3(a.max_tiles * (a.I / 128)), dim3(256), 0,
+                     stream, a, w);
+  hipLaunchKernelGGL((moe_wide_gemm_kernel<MT, false>), dim3(a.max_tiles * ((a.H + 255) / 256)),
+                     dim3(256), 0, stream, a, w);
 }
 
 hipError_t launch_wide(const WideArgs& a, const WideWeights& w, const uint16_t* x,
@@ -310,10 +373,9 @@ hipError_t launch_wide(const WideArgs& a, const WideWeights& w, const uint16_t* 
   hipError_t e = launch_sort(s, stream);
   if (e != hipSuccess) return e;
   switch (a.tile_rows) {
-    case 16: launch_products<1, 1>(a, w, stream); break;
-    case 32: launch_products<2, 1>(a, w, stream); break;
-    case 64: launch_products<4, 1>(a, w, stream); break;
-    default: launch_products<4, 2>(a, w, stream); break;
+    case 32: launch_products<2>(a, w, stream); break;
+    case 64: launch_products<4>(a, w, stream); break;
+    default: launch_products<8>(a, w, stream); break;
   }
   hipLaunchKernelGGL(moe_wide_combine_kernel, dim3(a.tokens, (a.H + 1023) / 1024), dim3(256), 0,
                      stream, a, gates, out);
