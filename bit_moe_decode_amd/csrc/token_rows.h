@@ -8,7 +8,8 @@
 namespace moe {
 
 constexpr int kSortThreads = 1024;
-constexpr int kSortChunk = 8192;       // picks a block ranks
+constexpr int kSortSteps = 8;          // picks a thread ranks at most
+constexpr int kSortChunk = kSortSteps * kSortThreads;  // picks a block ranks at most
 constexpr int kSortMaxGroups = 1024;   // one thread a group
 constexpr int64_t kSortMaxPicks = (int64_t)1 << 24;
 
@@ -32,7 +33,7 @@ struct SortArgs {
   int32_t* n_tiles;
   int tile_rows, extra;
   int spill;  // 1: picks in no group go to the last one
-  int chunks, bits, steps;  // set by launch_sort
+  int chunks, bits, steps;  // set by launch_sort: blocks, bits of a group, picks a thread
 };
 
 size_t sort_workspace(int64_t picks, int groups);

@@ -20,15 +20,14 @@
 namespace moe {
 
 // ---------------------------------------------------------------------- sort
-// A block takes a chunk of kSortChunk picks, its 16 waves 64 x steps
-// consecutive ones each (as few steps as the picks of a single chunk need).  A wave ranks 64 picks at a time: ballots over the
+// A block takes a chunk of 1024 x steps picks, its 16 waves 64 x steps
+// consecutive ones each.  A wave ranks 64 picks at a time: ballots over the
 // id's bits give each lane the lanes with its id, so the lanes below it are
 // its rank among them, and the lowest of them adds their number to the wave's
 // count of that id in LDS (one wave's own row: its LDS operations complete in
 // order).  The exclusive sums over the waves' counts, group by group, then
 // turn the ranks into places.
 constexpr int kSortWaves = kSortThreads / kWave;
-constexpr int kSortSteps = kSortChunk / kSortThreads;
 
 struct SortShared {
   int2 scan[kSortWaves];
@@ -67,7 +66,7 @@ __device__ __forceinline__ int2 block_scan(int2 v, SortShared& sh, int tid, int2
 __device__ __forceinline__ void rank_chunk(const SortArgs& a, int chunk, uint16_t* cnt, int tid,
                                            int (&id)[kSortSteps], int (&rk)[kSortSteps]) {
   const int lane = tid & 63, wv = tid >> 6;
-  const int64_t i0 = (int64_t)chunk * kSortChunk + (int64_t)wv * (kWave * a.steps) + lane;
+  const int64_t i0 = (int64_t)chunk * (kSortThreads * a.steps) + (int64_t)wv * (kWave * a.steps) + lane;
   const int other = a.spill ? a.groups - 1 : -1;
 #pragma unroll
   for (int s = 0; s < kSortSteps; s++) {
@@ -210,11 +209,11 @@ __global__ __launch_bounds__(kSortThreads) void moe_sort_place_kernel(SortArgs a
   }
   __syncthreads();
   const int lane = tid & 63, wv = tid >> 6;
-  const int64_t i0 = (int64_t)blockIdx.x * kSortChunk + (int64_t)wv * (kWave * a.steps) + lane;
+  const int64_t i0 = (int64_t)blockIdx.x * (kSortThreads * a.steps) + (int64_t)wv * (kWave * a.steps) + lane;
 #pragma unroll
   for (int s = 0; s < kSortSteps; s++) {
     const int64_t i = i0 + 64 * s;
-    if (i < a.picks) {
+    if (s < a.steps && i < a.picks) {
       const int p = id[s] >= 0 ? base[id[s]] + cnt[wv * a.groups + id[s]] + rk[s] : -1;
       a.pos[i] = p;
       if (p >= 0) a.order[p] = (int)i;
@@ -223,7 +222,19 @@ __global__ __launch_bounds__(kSortThreads) void moe_sort_place_kernel(SortArgs a
   if (blockIdx.x == 0) write_tiles(a, first, total, at.y, all.y, tid);
 }
 
-int sort_chunks(int64_t picks) { return (int)((picks + kSortChunk - 1) / kSortChunk); }
+// Picks a thread: all of them in one block up to kSortChunk picks; above that
+// two launches, of at least 2 picks a thread and blocks enough that 32 of them
+// hold the picks, up to 8 a thread (32768 picks of 256 groups: 10.7 + 13.6 us
+// in 4 blocks of 8 a thread).
+static int sort_steps(int64_t picks) {
+  if (picks <= kSortChunk) return (int)((picks + kSortThreads - 1) / kSortThreads);
+  const int64_t s = picks / (32 * kSortThreads);
+  return s < 2 ? 2 : (s > kSortSteps ? kSortSteps : (int)s);
+}
+static int sort_chunks(int64_t picks) {
+  const int64_t per = (int64_t)kSortThreads * sort_steps(picks);
+  return picks > 0 ? (int)((picks + per - 1) / per) : 0;
+}
 
 size_t sort_workspace(int64_t picks, int groups) {
   const int c = sort_chunks(picks);
@@ -232,7 +243,7 @@ size_t sort_workspace(int64_t picks, int groups) {
 
 hipError_t launch_sort(SortArgs a, hipStream_t stream) {
   a.chunks = sort_chunks(a.picks);
-  a.steps = a.chunks > 1 ? kSortSteps : (int)((a.picks + kSortThreads - 1) / kSortThreads);
+  a.steps = sort_steps(a.picks);
   a.bits = 0;
   while ((1 << a.bits) < a.groups) a.bits++;
   const size_t lds = (size_t)kSortWaves * a.groups * sizeof(uint16_t);  // at most 32 KB

@@ -280,7 +280,7 @@ __device__ __forceinline__ void wide_tile(const WideArgs& a, const WideWeights& 
 }
 
 template <int MT, bool UG>
-__global__ __launch_bounds__(256, MT <= 2 ? 3 : 2) void moe_wide_gemm_kernel(WideArgs a, WideWeights w) {
+__global__ __launch_bounds__(256, 2) void moe_wide_gemm_kernel(WideArgs a, WideWeights w) {
   __shared__ WideLds<MT> sh;
   // Column blocks (UG: 128 mid columns; down: 256 outputs) first: consecutive
   // blocks go to the 8 XCDs in turn, each with an L2 of its own, and where a
@@ -340,7 +340,7 @@ __global__ __launch_bounds__(256) void moe_wide_combine_kernel(WideArgs a,
 
 int wide_tile_rows(int64_t picks, int experts) {
   const int64_t per = picks / experts;
-  return per <= 16 ? 32 : (per <= 48 ? 64 : 128);
+  return per <= 48 ? 64 : 128;
 }
 
 int wide_max_tiles(int64_t picks, int experts, int shared_rows, int tile_rows) {
@@ -373,7 +373,6 @@ hipError_t launch_wide(const WideArgs& a, const WideWeights& w, const uint16_t* 
   hipError_t e = launch_sort(s, stream);
   if (e != hipSuccess) return e;
   switch (a.tile_rows) {
-    case 32: launch_products<2>(a, w, stream); break;
     case 64: launch_products<4>(a, w, stream); break;
     default: launch_products<8>(a, w, stream); break;
   }
