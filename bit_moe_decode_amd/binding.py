@@ -327,10 +327,6 @@ _I32, _BF16, _F32 = torch.int32, torch.bfloat16, torch.float32
 _ROW_DTYPES = {_BF16: 0, _F32: 1}  # moe_dtype
 
 
-def _current_device():
-    return torch.cuda.current_device()
-
-
 def _refuse(what, why):
     e = MoeError(MOE_ERR_INVALID_ARG, what)
     e.args = (f"{e.args[0]}: {why}",)
@@ -341,14 +337,12 @@ def _check(what, device, *tensors):
     """Every (name, tensor, dtype, shape) -- a tensor may be None -- is
     contiguous, on `device` and of that dtype and shape; `device` is the
     current one."""
-    if device < 0 or device != _current_device():
+    if device < 0 or device != torch.cuda.current_device():
         _refuse(what, "the tensors are not on the current device")
     for name, t, dtype, shape in tensors:
-        if t is None:
-            continue
-        if t.dtype is not dtype or t.shape != shape or t.get_device() != device \
-                or not t.is_contiguous():
-            _refuse(what, f"{name} is not a contiguous {dtype} {shape} on device {device}: "
+        if t is not None and (t.dtype is not dtype or t.shape != shape or not t.is_contiguous()
+                              or t.get_device() != device):
+            _refuse(what, f"{name} is not a contiguous {dtype} {tuple(shape)} on device {device}: "
                           f"{t.dtype} {tuple(t.shape)} with strides {t.stride()} on {t.device}")
 
 

@@ -48,9 +48,8 @@ __global__ __launch_bounds__(256) void dense_gemv_kernel(
     GemvTail<LORA> tail) {
   constexpr int S = DgStage<BF, T>::S, EPB = 32 * S;  // MFMA steps, inputs per K block
   __shared__ __align__(16) uint8_t s_tile[4][T][kTileBytes];
-  __shared__ float sv[GemvTail<LORA>::kSv];
+  __shared__ typename GemvTail<LORA>::Rows ad;
   const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
-  tail.load(rows, sv, tid, 256);
   const int col = lane & 15, g = lane >> 4;
   const int spb = 4 / ks;  // wave groups (of T slabs) per block
   const int grp = blockIdx.x * spb + wv / ks, kp = wv % ks;
@@ -108,6 +107,7 @@ __global__ __launch_bounds__(256) void dense_gemv_kernel(
   DgStage<BF, T> st[P];
 #pragma unroll
   for (int p = 0; p < P; p++) issue(st[p], p);
+  tail.load(ad, rows, tid, 256);
   for (int k0 = 0; k0 < nk - P; k0 += P) {
 #pragma unroll
     for (int p = 0; p < P; p++) {
@@ -137,7 +137,7 @@ __global__ __launch_bounds__(256) void dense_gemv_kernel(
       float v = reinterpret_cast<const float*>(s_tile[s * ks][t])[c * 16 + i];
       for (int q = 1; q < ks; q++) v += reinterpret_cast<const float*>(s_tile[s * ks + q][t])[c * 16 + i];
       const int nr = ((blockIdx.x * spb + s) * T + t) * 16 + i;
-      y[(size_t)c * n + nr] = f32_to_bf16(tail.add(v, c, nr, sv));
+      y[(size_t)c * n + nr] = f32_to_bf16(tail.add(v, c, nr, ad));
     }
   }
 }

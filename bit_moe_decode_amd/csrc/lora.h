@@ -23,7 +23,9 @@ struct LoraArgs {
   const float* scale;
   const int32_t* ids;  // [rows] adapter of each row; outside [0, adapters): none
   int adapters, max_rank, n, k, rows;
-  float* v;            // [k_parts][rows][max_rank] partial sums of A x
+  // scale A x of each row [rows][max_rank] (0 past the adapter's rank); with
+  // rows grouped, A x by sorted row, [k_parts][rows][max_rank] partial sums
+  float* v;
   int k_parts;
   // many rows: grouped by adapter, in tiles of kLoraTile rows (v by sorted row)
   int32_t *order, *pos, *offsets, *counts, *n_tiles;
@@ -37,64 +39,59 @@ __device__ __forceinline__ int lora_rank(const LoraArgs& l, int adapter) {
   return r < 0 ? 0 : (r < l.max_rank ? r : l.max_rank);
 }
 
-// Rows and adapters of a block's epilogue: sv[row][j] = scale * (A x)_j, the
-// K parts added in part order, 0 past the adapter's rank and for rows without
-// an adapter.  Called by every thread of the block, which then synchronises.
-__device__ __forceinline__ void lora_load_v(const LoraArgs& l, int rows, float* sv, int tid,
-                                            int threads) {
-  for (int i = tid; i < rows * l.max_rank; i += threads) {
-    const int r = i / l.max_rank, j = i - r * l.max_rank;
-    const int id = l.ids[r];
+// What a block's epilogue needs of its rows' adapters, in LDS: id (-1: none),
+// ranks used, and v = scale A x (lora_shrink_kernel's).  load() is called by
+// every thread of the block, which then synchronises.
+struct LoraRows {
+  float v[kMaxRows * kLoraMaxRank];
+  int id[kMaxRows], rank[kMaxRows];
+  __device__ __forceinline__ void load(const LoraArgs& l, int rows, int tid, int threads) {
+    for (int i = tid; i < rows * l.max_rank; i += threads) v[i] = l.v[i];
+    if (tid < rows) {
+      const int i = l.ids[tid];
+      const bool on = (uint32_t)i < (uint32_t)l.adapters;
+      id[tid] = on ? i : -1;
+      rank[tid] = on ? lora_rank(l, i) : 0;
+    }
+  }
+  // What row r's adapter adds at output n: sum_j B[n, j] v[j] over the
+  // adapter's ranks, 8 at a time; B past them is not used, whatever it holds.
+  __device__ __forceinline__ float term(const LoraArgs& l, int r, int n) const {
+    const int i = id[r], rk = rank[r];
+    if (i < 0) return 0.f;
+    const uint16_t* b = l.b + ((size_t)i * l.n + n) * l.max_rank;
+    const float* vr = v + r * l.max_rank;
     float s = 0.f;
-    if ((uint32_t)id < (uint32_t)l.adapters && j < lora_rank(l, id)) {
-      for (int p = 0; p < l.k_parts; p++) s += l.v[((size_t)p * l.rows + r) * l.max_rank + j];
-      s *= l.scale[id];
-    }
-    sv[i] = s;
-  }
-}
-
-// sum_j B[n, j] v[j] over the adapter's ranks (8 at a time: the ranks past
-// the adapter's are masked, whatever they hold).
-__device__ __forceinline__ float lora_dot(const LoraArgs& l, int adapter, int rank, int n,
-                                          const float* v) {
-  const uint16_t* b = l.b + ((size_t)adapter * l.n + n) * l.max_rank;
-  float s = 0.f;
-  for (int j = 0; j < rank; j += 8) {
-    const u32x4 u = ld16(b + j);
+    for (int j = 0; j < rk; j += 8) {
+      const u32x4 u = ld16(b + j);
 #pragma unroll
-    for (int i = 0; i < 8; i++) {
-      const float f = __uint_as_float(i & 1 ? u[i >> 1] & 0xFFFF0000u : u[i >> 1] << 16);
-      s = j + i < rank ? fmaf(f, v[j + i], s) : s;
+      for (int q = 0; q < 8; q++) {
+        const float f = __uint_as_float(q & 1 ? u[q >> 1] & 0xFFFF0000u : u[q >> 1] << 16);
+        s = j + q < rk ? fmaf(f, vr[j + q], s) : s;
+      }
     }
+    return s;
   }
-  return s;
-}
+};
 
-// What row r's adapter adds at output n, from the block's sv.
-__device__ __forceinline__ float lora_term(const LoraArgs& l, int r, int n, const float* sv) {
-  const int id = l.ids[r];
-  if ((uint32_t)id >= (uint32_t)l.adapters) return 0.f;
-  return lora_dot(l, id, lora_rank(l, id), n, sv + r * l.max_rank);
-}
-
-// The GEMVs' epilogue beside adapters (LORA) or without: sv is kSv floats
-// of the block's LDS, filled by load() before a barrier.
+// The GEMVs' epilogue beside adapters (LORA) or without: Rows is its part of
+// the block's LDS, filled by load() before a barrier.
+struct NoLoraRows {};
 template <bool LORA>
 struct GemvTail {
-  static constexpr int kSv = 1;
-  __device__ __forceinline__ void load(int, float*, int, int) const {}
-  __device__ __forceinline__ float add(float v, int, int, const float*) const { return v; }
+  using Rows = NoLoraRows;
+  __device__ __forceinline__ void load(Rows&, int, int, int) const {}
+  __device__ __forceinline__ float add(float v, int, int, const Rows&) const { return v; }
 };
 template <>
 struct GemvTail<true> {
-  static constexpr int kSv = kMaxRows * kLoraMaxRank;
+  using Rows = LoraRows;
   LoraArgs l;
-  __device__ __forceinline__ void load(int rows, float* sv, int tid, int threads) const {
-    lora_load_v(l, rows, sv, tid, threads);
+  __device__ __forceinline__ void load(Rows& rows, int n_rows, int tid, int threads) const {
+    rows.load(l, n_rows, tid, threads);
   }
-  __device__ __forceinline__ float add(float v, int r, int n, const float* sv) const {
-    return v + lora_term(l, r, n, sv);
+  __device__ __forceinline__ float add(float v, int r, int n, const Rows& rows) const {
+    return v + rows.term(l, r, n);
   }
 };
 

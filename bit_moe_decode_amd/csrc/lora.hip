@@ -7,57 +7,65 @@
 
 namespace moe {
 
-// A x of one row over one part of K: lanes take 8 inputs each, kept in
-// registers for every rank; a wave takes the ranks wv, wv + 4, ...
-constexpr int kShrinkPart = 2048;  // inputs a part at most: 4 x 8 a lane
-
+// ------------------------------------------------------------- up to 64 rows
+// scale A x of one row at RPB ranks: the block's 4 waves split K, lanes take 8
+// inputs at a time; the waves' sums are added in wave order.
+template <int RPB>
 __global__ __launch_bounds__(256) void lora_shrink_kernel(LoraArgs l, const uint16_t* __restrict__ x) {
-  const int r = blockIdx.x, part = blockIdx.y, tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
+  __shared__ float part[4][RPB];
+  const int r = blockIdx.x, j0 = blockIdx.y * RPB, tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
   const int id = l.ids[r];
   if ((uint32_t)id >= (uint32_t)l.adapters) return;
   const int rank = lora_rank(l, id);
   const int chunks = l.k / 8;  // of 8 inputs
-  const int c0 = (int)((int64_t)chunks * part / l.k_parts), c1 = (int)((int64_t)chunks * (part + 1) / l.k_parts);
-  u32x4 xv[4];
+  const int c0 = chunks * wv / 4, c1 = chunks * (wv + 1) / 4;
+  const uint16_t* px = x + (size_t)r * l.k;
+  const uint16_t* pa = l.a + ((size_t)id * l.max_rank + j0) * l.k;
+  float s[RPB];
 #pragma unroll
-  for (int i = 0; i < 4; i++) {
-    const int c = c0 + i * 64 + lane;
-    xv[i] = c < c1 ? ld16(x + (size_t)r * l.k + 8 * c) : u32x4{0u, 0u, 0u, 0u};
-  }
-  for (int j = wv; j < rank; j += 4) {
-    const uint16_t* row = l.a + ((size_t)id * l.max_rank + j) * l.k;
-    float s = 0.f;
+  for (int j = 0; j < RPB; j++) s[j] = 0.f;
+  if (j0 < rank) {
+#pragma unroll 4
+    for (int c = c0 + lane; c < c1; c += 64) {
+      const u32x4 xv = ld16(px + 8 * c);
 #pragma unroll
-    for (int i = 0; i < 4; i++) {
-      const int c = c0 + i * 64 + lane;
-      if (c >= c1) continue;
-      const u32x4 av = ld16(row + 8 * c);
+      for (int j = 0; j < RPB; j++) {
+        const u32x4 av = ld16(pa + (size_t)j * l.k + 8 * c);
 #pragma unroll
-      for (int q = 0; q < 4; q++) {
-        s = fmaf(__uint_as_float(av[q] << 16), __uint_as_float(xv[i][q] << 16), s);
-        s = fmaf(__uint_as_float(av[q] & 0xFFFF0000u), __uint_as_float(xv[i][q] & 0xFFFF0000u), s);
+        for (int q = 0; q < 4; q++) {
+          s[j] = fmaf(__uint_as_float(av[q] << 16), __uint_as_float(xv[q] << 16), s[j]);
+          s[j] = fmaf(__uint_as_float(av[q] & 0xFFFF0000u), __uint_as_float(xv[q] & 0xFFFF0000u), s[j]);
+        }
       }
     }
-#pragma unroll
-    for (int o = 32; o > 0; o >>= 1) s += __shfl_xor(s, o, kWave);
-    if (lane == 0) l.v[((size_t)part * l.rows + r) * l.max_rank + j] = s;
   }
+#pragma unroll
+  for (int j = 0; j < RPB; j++) {
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) s[j] += __shfl_xor(s[j], o, kWave);
+    if (lane == 0) part[wv][j] = s[j];
+  }
+  __syncthreads();
+  if (tid < RPB)
+    l.v[(size_t)r * l.max_rank + j0 + tid] =
+        j0 + tid < rank ? (part[0][tid] + part[1][tid] + part[2][tid] + part[3][tid]) * l.scale[id] : 0.f;
 }
 
 // base + B v of one row, an output a thread.
 __global__ __launch_bounds__(256) void lora_expand_kernel(LoraArgs l, const uint16_t* base,
                                                           uint16_t* y) {
-  __shared__ float sv[kLoraMaxRank];
+  __shared__ LoraRows rows;
   const int r = blockIdx.x, tid = threadIdx.x;
   const int n = blockIdx.y * 256 + tid;
+  const size_t at = (size_t)r * l.n + n;
+  const float b = n < l.n ? bf16_to_f32(base[at]) : 0.f;
   LoraArgs one = l;
   one.ids = l.ids + r;
   one.v = l.v + (size_t)r * l.max_rank;
-  lora_load_v(one, 1, sv, tid, 256);
+  rows.load(one, 1, tid, 256);
   __syncthreads();
-  if (n >= l.n) return;
-  const size_t at = (size_t)r * l.n + n;
-  y[at] = f32_to_bf16(bf16_to_f32(base[at]) + lora_term(one, 0, n, sv));
+  if (n >= l.n || (rows.id[0] < 0 && y == base)) return;
+  y[at] = f32_to_bf16(b + rows.term(one, 0, n));
 }
 
 // ---------------------------------------------------------------- many rows
@@ -397,18 +405,18 @@ size_t lora_plan(LoraArgs* l, void* base) {
     l->n_tiles = (int32_t*)take(4);
     l->tiles = (RowTile*)take((size_t)l->max_tiles * sizeof(RowTile));
   } else {
-    const int least = (l->k + kShrinkPart - 1) / kShrinkPart;
-    int parts = (1024 + l->rows - 1) / l->rows;  // about four blocks a CU
-    const int most = (l->k + 511) / 512;
-    parts = parts < most ? parts : most;
-    l->k_parts = parts > least ? parts : least;
+    l->k_parts = 1;
   }
   l->v = (float*)take((size_t)l->k_parts * l->rows * l->max_rank * sizeof(float));
   return o;
 }
 
 hipError_t launch_lora_shrink(const LoraArgs& l, const uint16_t* x, hipStream_t stream) {
-  hipLaunchKernelGGL(lora_shrink_kernel, dim3(l.rows, l.k_parts), dim3(256), 0, stream, l, x);
+  // a rank a block up to 2048 blocks (the shortest chain of loads), else 8
+  if (l.rows * l.max_rank <= 2048)
+    hipLaunchKernelGGL(lora_shrink_kernel<1>, dim3(l.rows, l.max_rank), dim3(256), 0, stream, l, x);
+  else
+    hipLaunchKernelGGL(lora_shrink_kernel<8>, dim3(l.rows, l.max_rank / 8), dim3(256), 0, stream, l, x);
   return hipGetLastError();
 }
 

@@ -28,9 +28,9 @@ __global__ __launch_bounds__(256) void lowbit_gemv_q1_kernel(const uint8_t* __re
                                                              GemvTail<LORA> tail) {
   __shared__ float xs[kQ1KMax];
   __shared__ float s8[kQ1KMax / 8];
-  __shared__ float sv[GemvTail<LORA>::kSv];
+  __shared__ typename GemvTail<LORA>::Rows ad;
   const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
-  tail.load(1, sv, tid, 256);
+  tail.load(ad, 1, tid, 256);
   for (int i = tid; i < k / 8; i += 256) {
     float s = 0.f;
 #pragma unroll
@@ -64,7 +64,7 @@ __global__ __launch_bounds__(256) void lowbit_gemv_q1_kernel(const uint8_t* __re
     }
 #pragma unroll
     for (int o = 32; o > 0; o >>= 1) acc += __shfl_xor(acc, o, kWave);
-    if (lane == 0) y[row] = f32_to_bf16(tail.add(acc, 0, row, sv));
+    if (lane == 0) y[row] = f32_to_bf16(tail.add(acc, 0, row, ad));
   }
 }
 
@@ -224,8 +224,8 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 3))) voi
     return;
   }
 
-  float* sv = reinterpret_cast<float*>(smem + kRed + 256 * 4);  // behind the part sums
-  tail.load(1, sv, tid, 256);
+  // behind the part sums
+  auto& ad = *reinterpret_cast<typename GemvTail<LORA>::Rows*>(smem + kRed + 256 * 4);
   const int rl = tid % RB, part = tid / RB;
   const int rowl = rl < nr ? rl : nr - 1;  // threads past n decode the last row
   const uint32_t* myrow = reinterpret_cast<const uint32_t*>(blocks + (size_t)(r0 + rowl) * rb);
@@ -268,6 +268,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 3))) voi
       }
     }
     if (c0 + CH < nch) xload(c0 + CH);
+    if (c0 == 0) tail.load(ad, 1, tid, 256);
     __syncthreads();
     acc = lb_chunks<KP, M>(w9, pb, c0 + part, nch, acc);
     if (c0 + CH < nch) __syncthreads();
@@ -278,7 +279,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 3))) voi
     float v = lds_ld(kRed + 4u * (uint32_t)tid);
 #pragma unroll
     for (int q = 1; q < KP; q++) v += lds_ld(kRed + 4u * (uint32_t)(q * RB + tid));
-    y[r0 + tid] = f32_to_bf16(tail.add(v, 0, r0 + tid, sv));
+    y[r0 + tid] = f32_to_bf16(tail.add(v, 0, r0 + tid, ad));
   }
 }
 
@@ -289,7 +290,7 @@ static size_t lb_nib_lds(int rbk, int m) {
 template <int RB, int M, bool LORA>
 static hipError_t lb_nib_tail(const uint8_t* blocks, const uint16_t* x, uint16_t* y, int n, int k,
                               const GemvTail<LORA>& tail, hipStream_t stream) {
-  const size_t sh = lb_nib_lds(RB, M) + (LORA ? kLoraMaxRank * 4 : 0);  // + the adapter's v
+  const size_t sh = lb_nib_lds(RB, M) + (LORA ? sizeof(LoraRows) : 0);
   static size_t raised[kLdsDevices] = {};  // the limit set per device
   if (ensure_dyn_lds(reinterpret_cast<const void*>(lowbit_gemv_q1_nib_kernel<RB, M, LORA>), sh,
                      raised) != hipSuccess)
@@ -366,9 +367,8 @@ __global__ __launch_bounds__(64 * WPB) void lowbit_gemv_q1_mfma_kernel(
     const uint8_t* __restrict__ blocks, const uint16_t* __restrict__ x,
     uint16_t* __restrict__ y, int rows, int n, int k, int ks, SignK sk, GemvTail<LORA> tail) {
   __shared__ __align__(16) float s_part[WPB][256];  // per wave 16 x 16 sums, column-major
-  __shared__ float sv[GemvTail<LORA>::kSv];
+  __shared__ typename GemvTail<LORA>::Rows ad;
   const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
-  tail.load(rows, sv, tid, 64 * WPB);
   const int col = lane & 15, g = lane >> 4;
   const int spb = WPB / ks;
   const int slab = blockIdx.x * spb + wv / ks, kp = wv % ks;
@@ -417,6 +417,7 @@ __global__ __launch_bounds__(64 * WPB) void lowbit_gemv_q1_mfma_kernel(
   QmStage st[P];
 #pragma unroll
   for (int p = 0; p < P; p++) issue(st[p], c0 + p);
+  tail.load(ad, rows, tid, 64 * WPB);
   for (int i0 = 0; i0 < nc - P; i0 += P) {
 #pragma unroll
     for (int p = 0; p < P; p++) {
@@ -436,7 +437,7 @@ __global__ __launch_bounds__(64 * WPB) void lowbit_gemv_q1_mfma_kernel(
     float v = s_part[s2 * ks][cc * 16 + i];
     for (int q = 1; q < ks; q++) v += s_part[s2 * ks + q][cc * 16 + i];
     const int r = (blockIdx.x * spb + s2) * 16 + i;
-    if (r < n) y[(size_t)cc * n + r] = f32_to_bf16(tail.add(v, cc, r, sv));
+    if (r < n) y[(size_t)cc * n + r] = f32_to_bf16(tail.add(v, cc, r, ad));
   }
 }
 
@@ -468,7 +469,7 @@ __global__ __launch_bounds__(256) void lowbit_gemv_q1_mfma4_kernel(
     const uint8_t* __restrict__ blocks, const uint16_t* __restrict__ x,
     uint16_t* __restrict__ y, int rows, int n, int k, int ks, SignK sk, GemvTail<LORA> tail) {
   constexpr int T = 4;
-  __shared__ float sv[GemvTail<LORA>::kSv];
+  __shared__ typename GemvTail<LORA>::Rows ad;
   extern __shared__ __align__(16) uint8_t q4_dyn[];           // input rows, [rows][k + 8] bf16
   __shared__ __align__(16) uint32_t s_u[4][64 * kQ4Stride];  // per wave: sign dwords by row
   __shared__ __align__(16) uint32_t s_d[4][64];               // per wave: d0 | d1 << 16 by row
@@ -476,7 +477,7 @@ __global__ __launch_bounds__(256) void lowbit_gemv_q1_mfma4_kernel(
   const int col = lane & 15, g = lane >> 4;
   const int xs = k + 8;  // LDS row stride of the input rows (elements)
   uint16_t* sx = reinterpret_cast<uint16_t*>(q4_dyn);
-  tail.load(rows, sv, tid, 256);
+  tail.load(ad, rows, tid, 256);
   for (int i = tid; i < rows * (k / 8); i += 256) {
     const int r = i / (k / 8), e = 8 * (i - r * (k / 8));
     *reinterpret_cast<u32x4*>(sx + r * xs + e) = ld16(x + (size_t)r * k + e);
@@ -587,7 +588,7 @@ __global__ __launch_bounds__(256) void lowbit_gemv_q1_mfma4_kernel(
       float v = s_part[s2 * ks][t][cc * 16 + i];
       for (int q = 1; q < ks; q++) v += s_part[s2 * ks + q][t][cc * 16 + i];
       const int rr = (blockIdx.x * spb + s2) * 64 + 16 * t + i;
-      if (rr < n) y[(size_t)cc * n + rr] = f32_to_bf16(tail.add(v, cc, rr, sv));
+      if (rr < n) y[(size_t)cc * n + rr] = f32_to_bf16(tail.add(v, cc, rr, ad));
     }
   }
 }

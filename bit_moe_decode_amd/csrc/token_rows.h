@@ -49,6 +49,9 @@ struct RowArgs {
   int64_t tokens;
   int top_k, hidden;
   int rows;  // rows of the sorted buffer
+  // set by the launches: blocks a row, and the first token of one of several
+  uint32_t parts;
+  int64_t first;
 };
 
 hipError_t launch_gather(const RowArgs& a, bool f32, const void* x, void* xs, hipStream_t stream);

@@ -311,63 +311,72 @@ __device__ __forceinline__ void store_row(T* row, int c, int n, const float (&f)
     if (c + i < n) from_f32(f[i], row[c + i]);
 }
 
-// The row of pick (t, j), or -1: a pick without one, or with one behind the
-// buffer.
-__device__ __forceinline__ int64_t pick_row(const RowArgs& a, int64_t t, int j) {
-  const int p = a.pos[t * a.top_k + j];
-  return (uint32_t)p < (uint32_t)a.rows ? (int64_t)p : -1;
+// The rows of picks j0 .. j0 + 7 of token t: -1 for a pick without one, for
+// one behind the buffer and past the last pick.  The eight loads carry no
+// condition (past the last pick they repeat it), so they are under way at once.
+__device__ __forceinline__ void pick_rows(const RowArgs& a, int64_t t, int j0, int (&p)[8]) {
+#pragma unroll
+  for (int j = 0; j < 8; j++) p[j] = a.pos[t * a.top_k + (j0 + j < a.top_k ? j0 + j : a.top_k - 1)];
+#pragma unroll
+  for (int j = 0; j < 8; j++) p[j] = j0 + j < a.top_k && (uint32_t)p[j] < (uint32_t)a.rows ? p[j] : -1;
+}
+__device__ __forceinline__ void pick_gates(const RowArgs& a, const float* gates, int64_t t, int j0,
+                                           float (&w)[8]) {
+#pragma unroll
+  for (int j = 0; j < 8; j++)
+    w[j] = gates ? gates[t * a.top_k + (j0 + j < a.top_k ? j0 + j : a.top_k - 1)] : 1.f;
 }
 
 // xs[pos[t,j]] = x[t]: a block reads its part of one token's row once and
 // writes it to the token's places.
 template <typename T, int V>
 __global__ void moe_gather_kernel(RowArgs a, const T* __restrict__ x, T* __restrict__ xs) {
-  const int64_t t = blockIdx.x;
-  const int c = (blockIdx.y * blockDim.x + threadIdx.x) * V;
+  const int64_t t = a.first + blockIdx.x / a.parts;
+  const int c = ((int)(blockIdx.x % a.parts) * (int)blockDim.x + (int)threadIdx.x) * V;
   if (c >= a.hidden) return;
   const T* row = x + t * a.hidden;
-  if (V > 1 && c + V <= a.hidden) {
-    const u32x4_a4 u = *reinterpret_cast<const u32x4_a4*>(row + c);
-    for (int j = 0; j < a.top_k; j++) {
-      const int64_t p = pick_row(a, t, j);
-      if (p >= 0) *reinterpret_cast<u32x4_a4*>(xs + p * a.hidden + c) = u;
+  const bool whole = V > 1 && c + V <= a.hidden;
+  u32x4_a4 u = {0u, 0u, 0u, 0u};
+  if (whole) u = *reinterpret_cast<const u32x4_a4*>(row + c);
+  for (int j0 = 0; j0 < a.top_k; j0 += 8) {
+    int p[8];
+    pick_rows(a, t, j0, p);
+#pragma unroll
+    for (int j = 0; j < 8; j++) {
+      if (p[j] < 0) continue;
+      T* to = xs + (int64_t)p[j] * a.hidden;
+      if (whole)
+        *reinterpret_cast<u32x4_a4*>(to + c) = u;
+      else
+        for (int i = c; i < c + V && i < a.hidden; i++) to[i] = row[i];
     }
-    return;
-  }
-  for (int j = 0; j < a.top_k; j++) {
-    const int64_t p = pick_row(a, t, j);
-    if (p < 0) continue;
-    for (int i = c; i < c + V && i < a.hidden; i++) xs[p * a.hidden + i] = row[i];
   }
 }
 
 // out[t] = sum_j w[t,j] y[pos[t,j]] (+ add[t]), w = 1 without gates.  The
 // rows of up to 8 picks are in flight at once; a pick without a row is not
-// read, nor is its gate.
+// read, and its gate not used.
 template <typename T, int V>
 __global__ void moe_combine_kernel_t(RowArgs a, const T* __restrict__ y,
                                      const float* __restrict__ gates, const T* __restrict__ add,
                                      T* __restrict__ out) {
-  const int64_t t = blockIdx.x;
-  const int c = (blockIdx.y * blockDim.x + threadIdx.x) * V;
+  const int64_t t = a.first + blockIdx.x / a.parts;
+  const int c = ((int)(blockIdx.x % a.parts) * (int)blockDim.x + (int)threadIdx.x) * V;
   if (c >= a.hidden) return;
   float acc[V];
 #pragma unroll
   for (int i = 0; i < V; i++) acc[i] = 0.f;
   for (int j0 = 0; j0 < a.top_k; j0 += 8) {
-    float f[8][V], w[8];
+    int p[8];
+    float w[8], f[8][V];
+    pick_rows(a, t, j0, p);
+    pick_gates(a, gates, t, j0, w);
+#pragma unroll
+    for (int j = 0; j < 8; j++)
+      if (p[j] >= 0) load_row<T, V>(y + (int64_t)p[j] * a.hidden, c, a.hidden, f[j]);
 #pragma unroll
     for (int j = 0; j < 8; j++) {
-      w[j] = 0.f;
-      if (j0 + j >= a.top_k) continue;
-      const int64_t p = pick_row(a, t, j0 + j);
-      if (p < 0) continue;
-      w[j] = gates ? gates[t * a.top_k + j0 + j] : 1.f;
-      load_row<T, V>(y + p * a.hidden, c, a.hidden, f[j]);
-    }
-#pragma unroll
-    for (int j = 0; j < 8; j++) {
-      if (j0 + j >= a.top_k || pick_row(a, t, j0 + j) < 0) continue;
+      if (p[j] < 0) continue;
 #pragma unroll
       for (int i = 0; i < V; i++) acc[i] = fmaf(w[j], f[j][i], acc[i]);
     }
@@ -388,30 +397,32 @@ __global__ __launch_bounds__(256) void moe_combine_bwd_kernel(
     RowArgs a, const T* __restrict__ dout, const T* __restrict__ y,
     const float* __restrict__ gates, T* __restrict__ dy, float* __restrict__ dgates) {
   __shared__ float part[4][8];
-  const int64_t t = blockIdx.x;
+  const int64_t t = a.first + blockIdx.x;
   const int tid = threadIdx.x;
   const T* d = dout + t * a.hidden;
   for (int j0 = 0; j0 < a.top_k; j0 += 8) {
-    float dot[8];
+    int p[8];
+    float w[8], dot[8];
+    pick_rows(a, t, j0, p);
+    pick_gates(a, gates, t, j0, w);
 #pragma unroll
     for (int j = 0; j < 8; j++) dot[j] = 0.f;
     for (int c = tid * V; c < a.hidden; c += 256 * V) {
-      float f[V];
+      float f[V], v[8][V];
       load_row<T, V>(d, c, a.hidden, f);
 #pragma unroll
+      for (int j = 0; j < 8; j++)
+        if (p[j] >= 0) load_row<T, V>(y + (int64_t)p[j] * a.hidden, c, a.hidden, v[j]);
+#pragma unroll
       for (int j = 0; j < 8; j++) {
-        if (j0 + j >= a.top_k) continue;
-        const int64_t p = pick_row(a, t, j0 + j);
-        if (p < 0) continue;
-        const float w = gates[t * a.top_k + j0 + j];
-        float v[V], o[V];
-        load_row<T, V>(y + p * a.hidden, c, a.hidden, v);
+        if (p[j] < 0) continue;
+        float o[V];
 #pragma unroll
         for (int i = 0; i < V; i++) {
-          dot[j] = fmaf(f[i], v[i], dot[j]);
-          o[i] = w * f[i];
+          dot[j] = fmaf(f[i], v[j][i], dot[j]);
+          o[i] = w[j] * f[i];
         }
-        store_row<T, V>(dy + p * a.hidden, c, a.hidden, o);
+        store_row<T, V>(dy + (int64_t)p[j] * a.hidden, c, a.hidden, o);
       }
     }
 #pragma unroll
@@ -422,20 +433,34 @@ __global__ __launch_bounds__(256) void moe_combine_bwd_kernel(
       if ((tid & 63) == 0) part[tid >> 6][j] = s;
     }
     __syncthreads();
-    if (tid < 8 && j0 + tid < a.top_k) {
-      const float s = part[0][tid] + part[1][tid] + part[2][tid] + part[3][tid];
-      dgates[t * a.top_k + j0 + tid] = pick_row(a, t, j0 + tid) >= 0 ? s : 0.f;
+    if (tid < 8 && j0 + tid < a.top_k) {  // 0 for a pick without a row: its dots stayed 0
+      dgates[t * a.top_k + j0 + tid] = part[0][tid] + part[1][tid] + part[2][tid] + part[3][tid];
     }
     __syncthreads();
   }
 }
 
-// Threads a block, and its blocks along a row, for `lanes` lanes a row:
-// whole waves, at most 256 threads.
-static dim3 row_grid(const RowArgs& a, int vec, int* threads) {
-  const int lanes = (a.hidden + vec - 1) / vec;
-  *threads = lanes >= 256 ? 256 : (lanes + 63) / 64 * 64;
-  return dim3((uint32_t)a.tokens, (uint32_t)((lanes + *threads - 1) / *threads));
+// Threads of a block (whole waves, at most 256); sets the blocks a row
+// (consecutive ones, so that a row is read in one go) for `vec` elements a lane.
+static int row_threads(RowArgs* a, int vec) {
+  const int lanes = (a->hidden + vec - 1) / vec;
+  const int threads = lanes >= 256 ? 256 : (lanes + 63) / 64 * 64;
+  a->parts = (uint32_t)((lanes + threads - 1) / threads);
+  return threads;
+}
+
+// Calls launch(blocks) for tokens from a->first on: one launch, or several
+// where the grid would pass 2^32 threads.
+template <typename F>
+static hipError_t for_tokens(RowArgs* a, F launch) {
+  const int64_t most = ((int64_t)1 << 23) / a->parts > 0 ? ((int64_t)1 << 23) / a->parts : 1;
+  for (a->first = 0; a->first < a->tokens; a->first += most) {
+    const int64_t n = a->tokens - a->first < most ? a->tokens - a->first : most;
+    launch(dim3((uint32_t)(n * a->parts)));
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 template <typename T>
@@ -443,43 +468,47 @@ static bool rows_on_dwords(const RowArgs& a) {
   return a.hidden * sizeof(T) % 4 == 0;
 }
 
+template <typename T, int V>
+static hipError_t gather_v(RowArgs a, const void* x, void* xs, hipStream_t stream) {
+  const int th = row_threads(&a, V);
+  return for_tokens(&a, [&](dim3 g) {
+    hipLaunchKernelGGL((moe_gather_kernel<T, V>), g, dim3(th), 0, stream, a, (const T*)x, (T*)xs);
+  });
+}
+template <typename T, int V>
+static hipError_t combine_v(RowArgs a, const void* y, const float* gates, const void* add, void* out,
+                            hipStream_t stream) {
+  const int th = row_threads(&a, V);
+  return for_tokens(&a, [&](dim3 g) {
+    hipLaunchKernelGGL((moe_combine_kernel_t<T, V>), g, dim3(th), 0, stream, a, (const T*)y, gates,
+                       (const T*)add, (T*)out);
+  });
+}
+template <typename T, int V>
+static hipError_t combine_bwd_v(RowArgs a, const void* dout, const void* y, const float* gates,
+                                void* dy, float* dgates, hipStream_t stream) {
+  a.parts = 1;
+  return for_tokens(&a, [&](dim3 g) {
+    hipLaunchKernelGGL((moe_combine_bwd_kernel<T, V>), g, dim3(256), 0, stream, a, (const T*)dout,
+                       (const T*)y, gates, (T*)dy, dgates);
+  });
+}
+
 template <typename T>
 static hipError_t gather_t(const RowArgs& a, const void* x, void* xs, hipStream_t stream) {
-  int th;
-  if (rows_on_dwords<T>(a)) {
-    const dim3 g = row_grid(a, kVec<T>, &th);
-    hipLaunchKernelGGL((moe_gather_kernel<T, kVec<T>>), g, dim3(th), 0, stream, a, (const T*)x, (T*)xs);
-  } else {
-    const dim3 g = row_grid(a, 1, &th);
-    hipLaunchKernelGGL((moe_gather_kernel<T, 1>), g, dim3(th), 0, stream, a, (const T*)x, (T*)xs);
-  }
-  return hipGetLastError();
+  return rows_on_dwords<T>(a) ? gather_v<T, kVec<T>>(a, x, xs, stream) : gather_v<T, 1>(a, x, xs, stream);
 }
 template <typename T>
 static hipError_t combine_t(const RowArgs& a, const void* y, const float* gates, const void* add,
                             void* out, hipStream_t stream) {
-  int th;
-  if (rows_on_dwords<T>(a)) {
-    const dim3 g = row_grid(a, kVec<T>, &th);
-    hipLaunchKernelGGL((moe_combine_kernel_t<T, kVec<T>>), g, dim3(th), 0, stream, a, (const T*)y,
-                       gates, (const T*)add, (T*)out);
-  } else {
-    const dim3 g = row_grid(a, 1, &th);
-    hipLaunchKernelGGL((moe_combine_kernel_t<T, 1>), g, dim3(th), 0, stream, a, (const T*)y, gates,
-                       (const T*)add, (T*)out);
-  }
-  return hipGetLastError();
+  return rows_on_dwords<T>(a) ? combine_v<T, kVec<T>>(a, y, gates, add, out, stream)
+                              : combine_v<T, 1>(a, y, gates, add, out, stream);
 }
 template <typename T>
 static hipError_t combine_bwd_t(const RowArgs& a, const void* dout, const void* y,
                                 const float* gates, void* dy, float* dgates, hipStream_t stream) {
-  if (rows_on_dwords<T>(a))
-    hipLaunchKernelGGL((moe_combine_bwd_kernel<T, kVec<T>>), dim3((uint32_t)a.tokens), dim3(256), 0,
-                       stream, a, (const T*)dout, (const T*)y, gates, (T*)dy, dgates);
-  else
-    hipLaunchKernelGGL((moe_combine_bwd_kernel<T, 1>), dim3((uint32_t)a.tokens), dim3(256), 0,
-                       stream, a, (const T*)dout, (const T*)y, gates, (T*)dy, dgates);
-  return hipGetLastError();
+  return rows_on_dwords<T>(a) ? combine_bwd_v<T, kVec<T>>(a, dout, y, gates, dy, dgates, stream)
+                              : combine_bwd_v<T, 1>(a, dout, y, gates, dy, dgates, stream);
 }
 
 hipError_t launch_gather(const RowArgs& a, bool f32, const void* x, void* xs, hipStream_t stream) {

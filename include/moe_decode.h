@@ -348,7 +348,7 @@ moe_status moe_gather_backward(const moe_row_shape* shape, const void* dxs, cons
 
 /* out[t] = sum_j gates[t,j] y[pos[t,j]] (+ add[t] where add is not NULL), in
  * pick order in fp32, rounded once; gates fp32 [tokens, top_k].  The gates of
- * picks without a row are not read.  out may be add itself. */
+ * picks without a row are not used.  out may be add itself. */
 moe_status moe_combine(const moe_row_shape* shape, const void* y, const int32_t* pos,
                        const float* gates, const void* add, void* out, hipStream_t stream);
 
