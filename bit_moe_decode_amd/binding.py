@@ -314,9 +314,13 @@ def lowbit_gemv_status(blocks, x, y, n, k, rows=1, stream=None, fmt=FMT_Q1):
 
 
 def make_matrix(fmt, n, k, codes, scales=None) -> LowbitMatrix:
-    """LowbitMatrix struct of a weight [n, k] in one of lowbit_gemv's formats."""
-    return LowbitMatrix(int(fmt), int(n), int(k), codes.data_ptr(),
-                        None if scales is None else scales.data_ptr())
+    """LowbitMatrix struct of a weight [n, k] in one of lowbit_gemv's formats.
+    The struct keeps the tensors alive."""
+    if scales is not None and scales.get_device() != codes.get_device():
+        _refuse("make_matrix", "codes and scales are on different devices")
+    m = LowbitMatrix(int(fmt), int(n), int(k), codes.data_ptr(), _address(scales))
+    m.tensors, m.device = (codes, scales), codes.get_device()
+    return m
 
 
 # ------------------------------------------------ tokens sorted by expert and back
@@ -355,8 +359,19 @@ def _address(t):
     return None if t is None else t.data_ptr()
 
 
-def _space(t):
-    return (None, 0) if t is None else (t.data_ptr(), t.numel() * t.element_size())
+def _space(what, t, device):
+    """(address, bytes) of a workspace tensor, which lies on `device` in one piece."""
+    if t is None:
+        return None, 0
+    if t.get_device() != device or not t.is_contiguous():
+        _refuse(what, f"the workspace is not a contiguous tensor on device {device}")
+    return t.data_ptr(), t.numel() * t.element_size()
+
+
+def _on(what, name, struct, device):
+    """A struct made from tensors (make_matrix, make_lora) has them on `device`."""
+    if getattr(struct, "device", device) != device:
+        _refuse(what, f"{name} is not on device {device}")
 
 
 def moe_sort_workspace_size(tokens, top_k, n_experts) -> int:
@@ -370,7 +385,7 @@ def moe_sort(ids, n_experts, offsets, order, pos, workspace=None, stream=None):
     t, k = ids.shape
     _check("moe_sort", ids.get_device(), ("ids", ids, _I32, (t, k)), ("offsets", offsets, _I32, (n_experts + 1,)),
            ("order", order, _I32, (t * k,)), ("pos", pos, _I32, (t, k)))
-    ws, n = _space(workspace)
+    ws, n = _space("moe_sort", workspace, ids.get_device())
     _done(lib().moe_sort(ids.data_ptr(), t, k, int(n_experts), offsets.data_ptr(), order.data_ptr(),
                          pos.data_ptr(), ws, n, _stream(stream)), "moe_sort")
 
@@ -436,7 +451,7 @@ def moe_wide_step(cfg: Config, x, ids, gates, weights: Weights, out, workspace, 
     _check("moe_wide_step", x.get_device(), ("x", x, _BF16, (t, cfg.hidden)),
            ("ids", ids, _I32, (t, 8)), ("gates", gates, _F32, (t, 8)),
            ("out", out, _BF16, (t, cfg.hidden)))
-    ws, n = _space(workspace)
+    ws, n = _space("moe_wide_step", workspace, x.get_device())
     _done(lib().moe_wide_step(ctypes.byref(cfg), x.data_ptr(), t, ids.data_ptr(), gates.data_ptr(),
                               ctypes.byref(weights), out.data_ptr(), ws, n, _stream(stream)),
           "moe_wide_step")
@@ -454,7 +469,7 @@ def make_lora(a, b, scale, rank=None) -> LoraSet:
            ("scale", scale, _F32, (n_adapters,)), ("rank", rank, _I32, (n_adapters,)))
     s = LoraSet(n_adapters, max_rank, n, k, a.data_ptr(), b.data_ptr(), _address(rank),
                 scale.data_ptr())
-    s.tensors = (a, b, scale, rank)
+    s.tensors, s.device = (a, b, scale, rank), a.get_device()
     return s
 
 
@@ -468,7 +483,8 @@ def lora_apply(lora: LoraSet, x, ids, base, y, workspace, stream=None):
     r, bf = x.shape[0], _BF16
     _check("lora_apply", x.get_device(), ("x", x, bf, (r, lora.k)), ("ids", ids, _I32, (r,)),
            ("base", base, bf, (r, lora.n)), ("y", y, bf, (r, lora.n)))
-    ws, n = _space(workspace)
+    _on("lora_apply", "lora", lora, x.get_device())
+    ws, n = _space("lora_apply", workspace, x.get_device())
     _done(lib().lora_apply(ctypes.byref(lora), x.data_ptr(), ids.data_ptr(), r, base.data_ptr(),
                            y.data_ptr(), ws, n, _stream(stream)), "lora_apply")
 
@@ -479,7 +495,9 @@ def lowbit_gemv_lora(matrix: LowbitMatrix, lora: LoraSet, x, ids, y, workspace, 
     r, bf = x.shape[0], _BF16
     _check("lowbit_gemv_lora", x.get_device(), ("x", x, bf, (r, matrix.k)), ("ids", ids, _I32, (r,)),
            ("y", y, bf, (r, matrix.n)))
-    ws, n = _space(workspace)
+    _on("lowbit_gemv_lora", "lora", lora, x.get_device())
+    _on("lowbit_gemv_lora", "matrix", matrix, x.get_device())
+    ws, n = _space("lowbit_gemv_lora", workspace, x.get_device())
     _done(lib().lowbit_gemv_lora(ctypes.byref(matrix), ctypes.byref(lora), x.data_ptr(),
                                  ids.data_ptr(), r, y.data_ptr(), ws, n, _stream(stream)),
           "lowbit_gemv_lora")

@@ -589,7 +589,7 @@ moe_status check_lora_set(const lora_set* l) {
   if (!l) return MOE_ERR_INVALID_ARG;
   if (l->n_adapters < 0 || l->n < 0 || l->k <= 0) return MOE_ERR_INVALID_ARG;
   if (l->n_adapters > kLoraMaxAdapters || l->max_rank < 8 || l->max_rank > kLoraMaxRank ||
-      l->max_rank % 8 || l->n % 8 || l->k % 64 || l->k > 32768)
+      l->max_rank % 8 || l->n % 8 || l->n > MOE_MAX_ROW || l->k % 64 || l->k > 32768)
     return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }
@@ -610,7 +610,8 @@ moe_status lora_args(const lora_set* l, const uint16_t* x, const int32_t* ids, i
   if (!ws || ws_bytes < need || !aligned16(ws)) return MOE_ERR_WORKSPACE;
   const size_t yb = (size_t)rows * l->n * 2;
   if (overlap(x, (size_t)rows * l->k * 2, y, yb) || overlap(ids, (size_t)rows * 4, y, yb) ||
-      overlap(ws, need, y, yb) || overlap(ws, need, x, (size_t)rows * l->k * 2))
+      overlap(ws, need, y, yb) || overlap(ws, need, x, (size_t)rows * l->k * 2) ||
+      overlap(ws, need, ids, (size_t)rows * 4))
     return MOE_ERR_INVALID_ARG;
   a->a = l->a;
   a->b = l->b;

@@ -2,7 +2,7 @@
 // they share: row r with adapter i = ids[r] gets
 //   y[r] = bf16( base[r] + scale_i * B_i (A_i x[r]) )
 // with A_i [rank, K], B_i [N, rank].  Rows without an adapter keep base.  The
-// inner product A x is kept in fp32, never rounded.
+// inner product A x is summed and kept in fp32.
 #include "lora.h"
 
 namespace moe {
@@ -217,8 +217,8 @@ __global__ __launch_bounds__(256, 2) void lora_shrink_tile_kernel(
 
 // y = bf16(base + B v) of a tile's 32 rows over a part of N, 64 outputs a wave
 // at a time.  v (its K parts added in order, times scale) is split into two
-// bf16 parts, v = hi + lo within 2^-17: two MFMAs for one keep the inner
-// product's precision.  The products go back through the wave's LDS area to
+// bf16 parts, v = hi + lo within 2^-16 of it (one part alone: 2^-8, as much as
+// the result's own rounding): two MFMAs for one.  The products go back through the wave's LDS area to
 // lanes that hold 8 outputs of one row.  RS: K steps of 32 ranks; the ranks
 // past the adapter's are zero in both operands.
 constexpr int kOutStride = 68;  // floats of a row of products in LDS (64 used)

@@ -10,6 +10,10 @@
  *   per 1x128 block -> down GEMV -> gate-weighted combine with a shared expert.
  * A second entry point, lowbit_gemv, is a dense decode GEMV over 1-bit
  * group-128 weights or, for the LM head after the last layer, FP8 weights.
+ * Beside them stand the operators on rows grouped by an index: tokens sorted
+ * by expert and back, with gradients (moe_sort, moe_gather, moe_combine), the
+ * experts' step for any number of tokens (moe_wide_step), and low-rank
+ * adapters of many requests (lora_apply, lowbit_gemv_lora).
  *
  * Sources.  The operations follow the body of sgl-amd-mono PR #85 ("...MoE
  * expert dedup and weight loads, kernarg reload, LM-head loads"), quoted on the
@@ -388,11 +392,13 @@ moe_status moe_wide_step(const moe_decode_config* cfg, const uint16_t* x, int32_
  *
  * Row r with adapter i = ids[r] gets scale[i] * B_i (A_i x[r]) added to the
  * projection's output; an id outside [0, n_adapters) is a row without one.
- * A x is kept in fp32. */
+ * A x is summed and kept in fp32; past 64 rows it enters the second product
+ * as the sum of two bf16 parts, within 2^-16 of its value. */
 typedef struct {
   int32_t n_adapters;   /* 0..1023 */
   int32_t max_rank;     /* a multiple of 8, 8..128 */
-  int32_t n, k;         /* the projection's [n, k]; n a multiple of 8, k of 64, k <= 32768 */
+  int32_t n, k;         /* the projection's [n, k]; n a multiple of 8, at most MOE_MAX_ROW,
+                           k a multiple of 64, at most 32768 */
   const uint16_t* a;    /* bf16 [n_adapters, max_rank, k] (device) */
   const uint16_t* b;    /* bf16 [n_adapters, n, max_rank] (device) */
   const int32_t* rank;  /* [n_adapters] (device) ranks used of each adapter, 0..max_rank, the

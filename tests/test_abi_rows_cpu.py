@@ -222,6 +222,12 @@ def test_gemv_lora_refusals():
     assert call(nb=15) == B.MOE_ERR_WORKSPACE
 
 
+def test_lora_refuses_wide_outputs_and_a_workspace_on_the_ids():
+    assert apply(lora_set(n=(1 << 20) + 8)) == B.MOE_ERR_UNSUPPORTED
+    assert B.lora_workspace_size(lora_set(n=1 << 20), 5) > 0
+    assert apply(ids=ptr(4) + 16) == B.MOE_ERR_INVALID_ARG
+
+
 def test_binding_refuses_host_tensors():
     import torch
     ids = torch.zeros(4, 8, dtype=torch.int32)

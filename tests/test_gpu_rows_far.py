@@ -23,6 +23,30 @@ def _gen(seed):
     return g
 
 
+def test_refusal_of_a_workspace_in_host_memory():
+    """Refused before anything is enqueued; so is a part of a strided one."""
+    ids = torch.zeros(4000, 8, dtype=I32, device="cuda")
+    offsets = torch.zeros(17, dtype=I32, device="cuda")
+    order, pos = torch.zeros(32000, dtype=I32, device="cuda"), torch.zeros_like(ids)
+    n = B.moe_sort_workspace_size(4000, 8, 16)
+    for ws in (torch.zeros(n, dtype=torch.uint8),
+               torch.zeros(n, 2, dtype=torch.uint8, device="cuda")[:, 0]):
+        with pytest.raises(B.MoeError):
+            B.moe_sort(ids, 16, offsets, order, pos, ws)
+    a, b, scale, rank = L._adapters(2, 8, 64, 64, 1, False)
+    lora = B.make_lora(a, b, scale, rank)
+    x = torch.zeros(3, 64, dtype=torch.bfloat16, device="cuda")
+    some = torch.zeros(3, dtype=I32, device="cuda")
+    with pytest.raises(B.MoeError):
+        B.lora_apply(lora, x, some, x, torch.empty_like(x), torch.zeros(1 << 16, dtype=torch.uint8))
+    matrix = B.make_matrix(B.FMT_BF16, 128, 64, torch.zeros(128, 64, dtype=torch.bfloat16))
+    a, b, scale, rank = L._adapters(2, 8, 128, 64, 2, False)
+    with pytest.raises(B.MoeError):  # the matrix in host memory
+        B.lowbit_gemv_lora(matrix, B.make_lora(a, b, scale, rank), x, some,
+                           torch.zeros(3, 128, dtype=torch.bfloat16, device="cuda"),
+                           torch.zeros(1 << 16, dtype=torch.uint8, device="cuda"))
+
+
 @pytest.mark.parametrize("tokens,h,dtype", [
     (2 ** 23 + 5, 2, torch.bfloat16),    # more blocks than one launch
     (2 ** 23 + 5, 3, torch.float32),
