@@ -68,15 +68,19 @@ __device__ __forceinline__ void rank_chunk(const SortArgs& a, int chunk, uint16_
   const int lane = tid & 63, wv = tid >> 6;
   const int64_t i0 = (int64_t)chunk * (kSortThreads * a.steps) + (int64_t)wv * (kWave * a.steps) + lane;
   const int other = a.spill ? a.groups - 1 : -1;
+  // the loads carry no condition of the lane's (past the last pick they repeat
+  // it), so that all of them are under way at once
 #pragma unroll
   for (int s = 0; s < kSortSteps; s++) {
     id[s] = -1;
     if (s >= a.steps) continue;
     const int64_t i = i0 + 64 * s;
-    if (i < a.picks) {
-      const int e = a.ids[i];
-      id[s] = (uint32_t)e < (uint32_t)(a.groups - a.spill) ? e : other;
-    }
+    id[s] = a.ids[i < a.picks ? i : a.picks - 1];
+  }
+#pragma unroll
+  for (int s = 0; s < kSortSteps; s++) {
+    const int e = (uint32_t)id[s] < (uint32_t)(a.groups - a.spill) ? id[s] : other;
+    id[s] = s < a.steps && i0 + 64 * s < a.picks ? e : -1;
   }
   for (int i = tid; i < kSortWaves * a.groups; i += kSortThreads) cnt[i] = 0;
   __syncthreads();
@@ -184,10 +188,16 @@ __global__ __launch_bounds__(kSortThreads) void moe_sort_place_kernel(SortArgs a
   rank_chunk(a, blockIdx.x, cnt, tid, id, rk);
   int before = 0, total = 0;
   if (tid < a.groups) {
-    for (int c = 0; c < a.chunks; c++) {
-      const int n = a.counts[(size_t)c * a.groups + tid];
-      before += c < (int)blockIdx.x ? n : 0;
-      total += n;
+    for (int c0 = 0; c0 < a.chunks; c0 += 16) {  // 16 loads under way at once
+      int n[16];
+#pragma unroll
+      for (int c = 0; c < 16; c++)
+        n[c] = a.counts[(size_t)(c0 + c < a.chunks ? c0 + c : a.chunks - 1) * a.groups + tid];
+#pragma unroll
+      for (int c = 0; c < 16; c++) {
+        before += c0 + c < (int)blockIdx.x ? n[c] : 0;
+        total += c0 + c < a.chunks ? n[c] : 0;
+      }
     }
     int w0 = 0;
 #pragma unroll
