@@ -11,6 +11,19 @@
 // decode step multiplies the finished sum).  y stays in fp32 between the down
 // products and the sum: rounding it to bf16 would halve that traffic and add
 // an error as large as the output's own rounding.
+//
+// How 128 products are added.  The FP8 MFMA aligns each group of 8 to its
+// largest product and drops what lies 13 bits below (1.3e-5 of a result, rms).
+// That is nothing in y, but it moves some of mid's values across a border
+// between two FP8 codes, 2^-4 of the value apart: at 16 to 48 tokens of 6144
+// the outputs' error went from the 0.00166 of their bf16 rounding to 0.0018 ..
+// 0.0026.  Gate and up of the 64-row tiles therefore take the codes as bf16
+// numbers, which they are, through the bf16 MFMA, whose sums are fp32's: twice
+// the MFMA work and the conversions, for 558.7 -> 560.7 us at 16 tokens, 1598
+// -> 1611 us at 300 and 2102 -> 2182 us at 1536, where the weights' bytes set
+// the time.  In the 128-row tiles the products set it (4096 tokens: 2935 us
+// with FP8 MFMAs, 6076 us with bf16, its operands spilling): they keep the FP8
+// MFMA, and an error of 0.0020.
 #include "wide.h"
 
 #include "device_common.h"
@@ -99,6 +112,7 @@ struct WideLds {
 template <int MT, int U, bool UG>
 __device__ __forceinline__ void wide_tile(const WideArgs& a, const WideWeights& w,
                                           const RowTile& tile, int nb, WideLds<MT>& sh) {
+  constexpr bool kExact = UG && MT == 4;  // sums in fp32: see the top of the file
   constexpr int NA = (U + 1) / 2;  // 16-byte chunks of sorted rows a thread loads a step
   const int tid = threadIdx.x, lane = tid & 63, wn = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int col = lane & 15, g = lane >> 4;
@@ -179,8 +193,15 @@ __device__ __forceinline__ void wide_tile(const WideArgs& a, const WideWeights& 
     if (kb + 1 < nkb) issue(kb + 1);
     __syncthreads();
     v8i op[4];
+    v8bf opx[4][4];  // (kExact) as bf16: 8 codes of every lane an MFMA
 #pragma unroll
-    for (int j = 0; j < 4; j++) op[j] = operand((j >> 1) * 128 + wn * 32 + (j & 1) * 16);
+    for (int j = 0; j < 4; j++) {
+      op[j] = operand((j >> 1) * 128 + wn * 32 + (j & 1) * 16);
+      if constexpr (kExact) {
+#pragma unroll
+        for (int q = 0; q < 4; q++) opx[j][q] = fp8x8_to_bf16(uint2{(uint32_t)op[j][2 * q], (uint32_t)op[j][2 * q + 1]});
+      }
+    }
     // the scheduling barriers keep the compiler from hoisting every row tile's
     // reads (71 spilled registers at 8 row tiles without them)
     v8i b[2];
@@ -193,8 +214,19 @@ __device__ __forceinline__ void wide_tile(const WideArgs& a, const WideWeights& 
 #pragma unroll
     for (int i = 0; i < U; i++) {
       v4f c[4];
+      if constexpr (kExact) {
 #pragma unroll
-      for (int j = 0; j < 4; j++) c[j] = mfma_fp8(op[j], b[i & 1]);
+        for (int j = 0; j < 4; j++) c[j] = v4f{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int q = 0; q < 4; q++) {
+          const v8bf bx = fp8x8_to_bf16(uint2{(uint32_t)b[i & 1][2 * q], (uint32_t)b[i & 1][2 * q + 1]});
+#pragma unroll
+          for (int j = 0; j < 4; j++) c[j] = mfma_bf16(opx[j][q], bx, c[j]);
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; j++) c[j] = mfma_fp8(op[j], b[i & 1]);
+      }
       const float ar = as[i & 1];
       if (i + 1 < U) fetch(i + 1);
 #pragma unroll
@@ -293,19 +325,15 @@ __global__ __launch_bounds__(256, 2) void moe_wide_gemm_kernel(WideArgs a, WideW
   int used = (tile.end - tile.row + 15) >> 4;
   used = __builtin_amdgcn_readfirstlane(used < MT ? used : MT);
   // a loop for each number of row tiles that hold rows
-  if constexpr (MT >= 8) {
+  if constexpr (MT == 8) {
     if (used == 8) return wide_tile<MT, 8, UG>(a, w, tile, nb, sh);
     if (used == 7) return wide_tile<MT, 7, UG>(a, w, tile, nb, sh);
     if (used == 6) return wide_tile<MT, 6, UG>(a, w, tile, nb, sh);
     if (used == 5) return wide_tile<MT, 5, UG>(a, w, tile, nb, sh);
   }
-  if constexpr (MT >= 4) {
-    if (used == 4) return wide_tile<MT, 4, UG>(a, w, tile, nb, sh);
-    if (used == 3) return wide_tile<MT, 3, UG>(a, w, tile, nb, sh);
-  }
-  if constexpr (MT >= 2) {
-    if (used == 2) return wide_tile<MT, 2, UG>(a, w, tile, nb, sh);
-  }
+  if (used == 4) return wide_tile<MT, 4, UG>(a, w, tile, nb, sh);
+  if (used == 3) return wide_tile<MT, 3, UG>(a, w, tile, nb, sh);
+  if (used == 2) return wide_tile<MT, 2, UG>(a, w, tile, nb, sh);
   wide_tile<MT, 1, UG>(a, w, tile, nb, sh);
 }
 

@@ -138,7 +138,8 @@ def test_the_wide_steps_most_tokens():
     bound = tol + 2.0 ** -8 * (ref.abs() + tol)
     err = (out[some].double() - ref).abs()
     assert bool((err <= bound).all()), (int((err > bound).sum()), float((err - bound).max()))
-    # and each token as in a batch of its own
-    few = W._run(layer, x[some].contiguous(), ids[some].contiguous(), gates[some].contiguous())
+    # and each token as in another batch whose experts have as many rows (the
+    # products' tiles, and with them the order of the sums, go by that)
+    few = W._run(layer, x[-256:].contiguous(), ids[-256:].contiguous(), gates[-256:].contiguous())
     torch.cuda.synchronize()
-    assert torch.equal(few, out[some])
+    assert torch.equal(few, out[-256:])
