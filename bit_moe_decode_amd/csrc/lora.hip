@@ -7,51 +7,46 @@
 
 namespace moe {
 
-// ------------------------------------------------------------- up to 64 rows
-// scale A x of one row at RPB ranks: the block's 4 waves split K, lanes take 8
-// inputs at a time; the waves' sums are added in wave order.
-template <int RPB>
+// ------------------------------------------------------------------ few rows
+// scale A x of one row at one rank a block: its 4 waves split K, lanes take 8
+// inputs at a time; the waves' sums are added in wave order.  A few hundred KB
+// to a few MB: bound by the latency of one chain of loads, 3.5 us for 16 rows
+// of 6144 at rank 16, 4.8 for 64 (8 ranks a block, which read x once for them:
+// 5.6 and 7.1 us).
 __global__ __launch_bounds__(256) void lora_shrink_kernel(LoraArgs l, const uint16_t* __restrict__ x) {
-  __shared__ float part[4][RPB];
-  const int r = blockIdx.x, j0 = blockIdx.y * RPB, tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
+  __shared__ float part[4];
+  const int r = blockIdx.x, j = blockIdx.y, tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
   const int id = l.ids[r];
   if ((uint32_t)id >= (uint32_t)l.adapters) return;
   const int rank = lora_rank(l, id);
   const int chunks = l.k / 8;  // of 8 inputs
   const int c0 = chunks * wv / 4, c1 = chunks * (wv + 1) / 4;
   const uint16_t* px = x + (size_t)r * l.k;
-  const uint16_t* pa = l.a + ((size_t)id * l.max_rank + j0) * l.k;
-  float s[RPB];
-#pragma unroll
-  for (int j = 0; j < RPB; j++) s[j] = 0.f;
-  if (j0 < rank) {
+  const uint16_t* pa = l.a + ((size_t)id * l.max_rank + j) * l.k;
+  float s = 0.f;
+  if (j < rank) {
 #pragma unroll 4
     for (int c = c0 + lane; c < c1; c += 64) {
-      const u32x4 xv = ld16(px + 8 * c);
+      const u32x4 xv = ld16(px + 8 * c), av = ld16(pa + 8 * c);
 #pragma unroll
-      for (int j = 0; j < RPB; j++) {
-        const u32x4 av = ld16(pa + (size_t)j * l.k + 8 * c);
-#pragma unroll
-        for (int q = 0; q < 4; q++) {
-          s[j] = fmaf(__uint_as_float(av[q] << 16), __uint_as_float(xv[q] << 16), s[j]);
-          s[j] = fmaf(__uint_as_float(av[q] & 0xFFFF0000u), __uint_as_float(xv[q] & 0xFFFF0000u), s[j]);
-        }
+      for (int q = 0; q < 4; q++) {
+        s = fmaf(__uint_as_float(av[q] << 16), __uint_as_float(xv[q] << 16), s);
+        s = fmaf(__uint_as_float(av[q] & 0xFFFF0000u), __uint_as_float(xv[q] & 0xFFFF0000u), s);
       }
     }
   }
 #pragma unroll
-  for (int j = 0; j < RPB; j++) {
-#pragma unroll
-    for (int o = 32; o > 0; o >>= 1) s[j] += __shfl_xor(s[j], o, kWave);
-    if (lane == 0) part[wv][j] = s[j];
-  }
+  for (int o = 32; o > 0; o >>= 1) s += __shfl_xor(s, o, kWave);
+  if (lane == 0) part[wv] = s;
   __syncthreads();
-  if (tid < RPB)
-    l.v[(size_t)r * l.max_rank + j0 + tid] =
-        j0 + tid < rank ? (part[0][tid] + part[1][tid] + part[2][tid] + part[3][tid]) * l.scale[id] : 0.f;
+  if (tid == 0)
+    l.v[(size_t)r * l.max_rank + j] =
+        j < rank ? (part[0] + part[1] + part[2] + part[3]) * l.scale[id] : 0.f;
 }
 
-// base + B v of one row, an output a thread.
+// base + B v of one row, an output a thread: the adapter's row of B is the
+// thread's own 16 to 256 bytes.  3.7 us for 16 rows of 6144 at rank 16, 5.1 for
+// 64: latency.
 __global__ __launch_bounds__(256) void lora_expand_kernel(LoraArgs l, const uint16_t* base,
                                                           uint16_t* y) {
   __shared__ LoraRows rows;
@@ -71,10 +66,10 @@ __global__ __launch_bounds__(256) void lora_expand_kernel(LoraArgs l, const uint
 // ---------------------------------------------------------------- many rows
 // Rows grouped by adapter (token_rows.hip), in tiles of 32: a tile reads its
 // adapter once for 32 rows, in 16x16x32 bf16 MFMAs.  Memory is read and
-// written row by row, 4 or 8 neighbouring lanes to a line (lanes that take
-// their MFMA operand straight from memory, neighbours in different rows, cost
-// an access each: 12.7M against 3.7M cache accesses in the shrink of 6001 rows
-// of 6144 at rank 64, and 45 against 25 us), and each wave turns what it loaded
+// written row by row, 4 or 8 neighbouring lanes to a line (where lanes took
+// their MFMA operand straight from memory, neighbours in different rows, each
+// cost an access: the shrink of 6001 rows of 6144 at rank 64 45 against 36 us,
+// the expand 60 against 47), and each wave turns what it loaded
 // into operand order through an LDS area of its own.  LDS operations of one
 // wave complete in order, so these need no barrier, only the compiler's order.
 constexpr int kLoraM = kLoraTile / 16;
@@ -375,8 +370,12 @@ __global__ __launch_bounds__(256, 2) void lora_expand_tile_kernel(
   }
 }
 
-// From how many rows on the rows are grouped.
-constexpr int kLoraGroupRows = 65;
+// Above rows * max_rank = 2048 the rows are grouped.  Kernels of one call at n
+// = k = 6144, one by one and grouped, with 128 adapters and with 4: 16 rows at
+// rank 128 18.5 and 25.6, 18.1 and 21.2 us; 64 rows at rank 32 15.1 and 21.6,
+// 12.9 and 13.5; 128 at rank 16 15.0 and 23.4, 12.0 and 14.1; 256 at rank 16
+// 21.1 and 24.5, 16.0 and 14.9; 64 at rank 64 52 and 30, 25 and 17.
+constexpr int kLoraDirect = 2048;
 
 size_t lora_plan(LoraArgs* l, void* base) {
   char* b = static_cast<char*>(base);
@@ -386,7 +385,7 @@ size_t lora_plan(LoraArgs* l, void* base) {
     o = (o + bytes + 255) / 256 * 256;
     return p;
   };
-  const bool grouped = l->rows >= kLoraGroupRows;
+  const bool grouped = (int64_t)l->rows * l->max_rank > kLoraDirect;
   l->max_tiles = 0;
   if (grouped) {
     const int groups = l->adapters + 1;
@@ -412,11 +411,7 @@ size_t lora_plan(LoraArgs* l, void* base) {
 }
 
 hipError_t launch_lora_shrink(const LoraArgs& l, const uint16_t* x, hipStream_t stream) {
-  // a rank a block up to 2048 blocks (the shortest chain of loads), else 8
-  if (l.rows * l.max_rank <= 2048)
-    hipLaunchKernelGGL(lora_shrink_kernel<1>, dim3(l.rows, l.max_rank), dim3(256), 0, stream, l, x);
-  else
-    hipLaunchKernelGGL(lora_shrink_kernel<8>, dim3(l.rows, l.max_rank / 8), dim3(256), 0, stream, l, x);
+  hipLaunchKernelGGL(lora_shrink_kernel, dim3(l.rows, l.max_rank), dim3(256), 0, stream, l, x);
   return hipGetLastError();
 }
 

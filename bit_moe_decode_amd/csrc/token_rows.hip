@@ -26,7 +26,9 @@ namespace moe {
 // its rank among them, and the lowest of them adds their number to the wave's
 // count of that id in LDS (one wave's own row: its LDS operations complete in
 // order).  The exclusive sums over the waves' counts, group by group, then
-// turn the ranks into places.
+// turn the ranks into places.  Bound by the latency of that chain, not by its
+// bytes (4 read and 8 written a pick): 128 picks of 256 groups 3.8 us, 6001 of
+// 25 groups 7.6 us in one block, 65536 of 256 in two launches 4.8 + 8.1 us.
 constexpr int kSortWaves = kSortThreads / kWave;
 
 struct SortShared {
@@ -269,7 +271,13 @@ hipError_t launch_sort(SortArgs a, hipStream_t stream) {
 // -------------------------------------------------------------- row movement
 // Rows are taken 16 bytes a lane where every row starts on a 4-byte boundary
 // (gfx950 loads and stores 16 bytes at any dword alignment), element by
-// element otherwise (an odd number of bf16).
+// element otherwise (an odd number of bf16).  All of them are bound by memory:
+// a row is read once and written once, several rows under way a lane, a row's
+// blocks next to each other so that its lines are used while they are open.
+// At 6144 columns: gather of 8192 tokens to 65536 rows of bf16 170 us, 5.3
+// TB/s; combine of 8191 tokens' 4 of 8 picks in fp32 107 us; combine's gradient
+// of 4096 tokens in bf16 168 us, gather's 111 us.  A few rows take the launch
+// and one pass of latency: 16 tokens gathered 3.5 us, 32 combined 4.3 us.
 typedef uint32_t u32x4_a4 __attribute__((ext_vector_type(4), aligned(4)));
 
 template <typename T>

@@ -31,7 +31,9 @@
 namespace moe {
 
 // ------------------------------------------------------- activation blocks
-// A block takes one token: 8 columns a lane, a 1x128 block in 16 lanes.
+// A block takes one token: 8 columns a lane, a 1x128 block in 16 lanes.  Reads
+// and writes 18 KB a token of 6144: 4096 tokens 23 us (3.3 TB/s; 0.8% of the
+// step), 16 tokens 4.8 us, the latency of one pass.
 __global__ __launch_bounds__(256) void moe_wide_act_kernel(WideArgs a, const uint16_t* __restrict__ x,
                                                            const uint16_t* __restrict__ gamma) {
   __shared__ float s_ss[4];
@@ -338,6 +340,8 @@ __global__ __launch_bounds__(256, 2) void moe_wide_gemm_kernel(WideArgs a, WideW
 }
 
 // out[t] = bf16( sum_j g[t,j] y[pos[t,j]] + y[picks + t] ), in pick order.
+// Nine fp32 rows read for one bf16 row written, all loads under way at once:
+// 4096 tokens of 6144 196 us, 4.9 TB/s, bound by memory.
 __global__ __launch_bounds__(256) void moe_wide_combine_kernel(WideArgs a,
                                                                const float* __restrict__ gates,
                                                                uint16_t* __restrict__ out) {
@@ -366,6 +370,11 @@ __global__ __launch_bounds__(256) void moe_wide_combine_kernel(WideArgs a,
   *reinterpret_cast<uint2*>(out + t * a.H + c) = q;
 }
 
+// Rows of a tile, by the rows an expert has in the mean.  256 experts of 6144
+// x 2048, whole step in 64- and 128-row tiles: 1538 and 1616 us at 9 rows, 1990
+// and 1969 at 32, 2176 and 2048 at 48, 2495 and 2202 at 64.  From 32 to 48 rows
+// the 64-row tiles' sums in fp32 (top of the file) are taken for up to 6% of
+// the time.
 int wide_tile_rows(int64_t picks, int experts) {
   const int64_t per = picks / experts;
   return per <= 48 ? 64 : 128;

@@ -393,8 +393,8 @@ moe_status moe_wide_step(const moe_decode_config* cfg, const uint16_t* x, int32_
  *
  * Row r with adapter i = ids[r] gets scale[i] * B_i (A_i x[r]) added to the
  * projection's output; an id outside [0, n_adapters) is a row without one.
- * A x is summed and kept in fp32; past 64 rows it enters the second product
- * as the sum of two bf16 parts, within 2^-16 of its value. */
+ * A x is summed and kept in fp32; where rows * max_rank passes 2048 it enters the
+ * second product as the sum of two bf16 parts, within 2^-16 of its value. */
 typedef struct {
   int32_t n_adapters;   /* 0..1023 */
   int32_t max_rank;     /* a multiple of 8, 8..128 */

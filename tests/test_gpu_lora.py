@@ -183,6 +183,38 @@ def test_no_adapters_and_no_rows():
     B.lora_apply(lora, none, torch.empty(0, dtype=torch.int32, device="cuda"), out, out, _space(lora, 1))
 
 
+@pytest.mark.parametrize("ragged", [False, True])
+@pytest.mark.parametrize("rows,mr", [(256, 8), (257, 8), (128, 16), (129, 16), (32, 64), (33, 64),
+                                     (16, 128), (17, 128)])
+def test_few_and_many_rows(rows, mr, ragged):
+    """Either side of the row count from which rows are grouped."""
+    n, k, adapters = 520, 704, 5
+    _say("lora", rows, mr, ragged)
+    a, b, scale, rank = _adapters(adapters, mr, n, k, rows + mr, ragged)
+    ids = _ids(rows, adapters, rows)
+    x = S.make_x(rows, k, seed=rows).cuda()
+    base = S.make_x(rows, n, seed=rows + 1).cuda()
+    lora = B.make_lora(a, b, scale, rank)
+    y = torch.full_like(base, float("nan"))
+    B.lora_apply(lora, x, ids, base, y, _space(lora, rows))
+    torch.cuda.synchronize()
+    d, tol = _delta(a, b, scale, rank, x, ids)
+    _assert_close(y, base.double() + d, tol)
+
+
+def test_no_adapters_and_grouped_rows():
+    n, k, rows = 128, 128, 300
+    lora = B.make_lora(torch.empty(0, 8, k, dtype=torch.bfloat16, device="cuda"),
+                       torch.empty(0, n, 8, dtype=torch.bfloat16, device="cuda"),
+                       torch.empty(0, device="cuda"))
+    base = S.make_x(rows, n, seed=1).cuda()
+    y = torch.zeros_like(base)
+    B.lora_apply(lora, S.make_x(rows, k, seed=2).cuda(), torch.zeros(rows, dtype=torch.int32, device="cuda"),
+                 base, y, _space(lora, rows))
+    torch.cuda.synchronize()
+    assert torch.equal(y, base)
+
+
 def test_a_row_does_not_depend_on_the_batch_around_it():
     """NaN and infinities in other rows stay there."""
     rows, n, k, mr, adapters = 300, 256, 256, 16, 4
