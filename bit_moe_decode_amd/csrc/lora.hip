@@ -69,8 +69,8 @@ __global__ __launch_bounds__(256) void lora_expand_kernel(LoraArgs l, const uint
 // written row by row, 4 or 8 neighbouring lanes to a line (where lanes took
 // their MFMA operand straight from memory, neighbours in different rows, each
 // cost an access: the shrink of 6001 rows of 6144 at rank 64 45 against 36 us,
-// the expand 60 against 47), and each wave turns what it loaded
-// into operand order through an LDS area of its own.  LDS operations of one
+// the expand 60 against 47), and each wave turns what it loaded into operand
+// order through an LDS area of its own.  LDS operations of one
 // wave complete in order, so these need no barrier, only the compiler's order.
 constexpr int kLoraM = kLoraTile / 16;
 constexpr int kLoraParts = 8;  // parts of K at most
@@ -114,6 +114,10 @@ __device__ __forceinline__ void k_range(int k, int w, int waves, int* s0, int* s
 
 // A x of a tile over one part of K; the block's 4 waves split the part
 // further and add their sums through LDS in wave order.  RT: rank tiles of 16.
+// 6001 rows of 6144, 24 adapters: 22 us at rank 16, 32 at rank 64 (x alone is
+// 74 MB, 11 us of memory; every tile reads its adapter again, from L2).  Bound
+// by latency: a wave has 6 to 12 steps of 32, 4 of them under way.  Tiles of 64
+// rows halve A's traffic: 32 us here, but 85 against 48 in the expand.
 template <int RT>
 __global__ __launch_bounds__(256, 2) void lora_shrink_tile_kernel(
     LoraArgs l, const uint16_t* __restrict__ x) {
@@ -213,9 +217,11 @@ __global__ __launch_bounds__(256, 2) void lora_shrink_tile_kernel(
 // y = bf16(base + B v) of a tile's 32 rows over a part of N, 64 outputs a wave
 // at a time.  v (its K parts added in order, times scale) is split into two
 // bf16 parts, v = hi + lo within 2^-16 of it (one part alone: 2^-8, as much as
-// the result's own rounding): two MFMAs for one.  The products go back through the wave's LDS area to
-// lanes that hold 8 outputs of one row.  RS: K steps of 32 ranks; the ranks
+// the result's own rounding): two MFMAs for one.  The products go back through
+// the wave's LDS area to lanes that hold 8 outputs of one row.  RS: K steps of 32 ranks; the ranks
 // past the adapter's are zero in both operands.
+// 6001 rows of 6144, 24 adapters: 38 us at rank 16, 50 at rank 64; base and y
+// are 148 MB, 29 us of memory at the rate of a copy, which bounds it.
 constexpr int kOutStride = 68;  // floats of a row of products in LDS (64 used)
 
 template <int RS>
@@ -390,9 +396,10 @@ size_t lora_plan(LoraArgs* l, void* base) {
   if (grouped) {
     const int groups = l->adapters + 1;
     l->max_tiles = (int)sort_max_tiles(l->rows, groups, kLoraTile);
-    // K parts of at least 8 steps of 32, about 1024 blocks (512 where a rank
-    // above 64 takes twice the registers)
-    int parts = (l->max_rank <= 64 ? 1024 : 512) / l->max_tiles;
+    // K parts of at least 8 steps of 32, about 2048 blocks (512 where a rank
+    // above 64 takes more registers and longer sums): shrink and expand of 6001
+    // rows of 6144 61 us at rank 16 and 82 at rank 64, 64 and 83 with half as many
+    int parts = (l->max_rank <= 64 ? 2048 : 512) / l->max_tiles;
     if (parts < 1) parts = 1;
     int most = l->k / 256 > 1 ? l->k / 256 : 1;
     if (most > kLoraParts) most = kLoraParts;
@@ -439,7 +446,8 @@ static hipError_t launch_lora_grouped(const LoraArgs& l, const uint16_t* x, cons
     LORA_RT(1) LORA_RT(2) LORA_RT(3) LORA_RT(4) LORA_RT(5) LORA_RT(6) LORA_RT(7) LORA_RT(8)
 #undef LORA_RT
   }
-  // parts of N: about 1024 blocks, of 256 outputs or more
+  // parts of N: about 1024 blocks, of 256 outputs or more (6001 rows of 6144 at
+  // rank 16: 38.5 us with 5 parts, 42.6 with 4, 44.9 with 6)
   int parts = (1024 + l.max_tiles - 1) / l.max_tiles;
   const int steps = (l.n + 255) / 256;
   parts = parts < steps ? parts : steps;
