@@ -546,9 +546,9 @@ RowBytes row_bytes(const moe_row_shape* s) {
 // ---- the experts' step of any number of rows
 
 struct WidePlan {
-  size_t actq, acts, order, pos, offsets, counts, tiles, ntiles, midq, mids, y, total;
+  size_t actq, acts, actt, order, pos, offsets, counts, tiles, ntiles, midq, mids, y, total;
   int64_t picks;
-  int tile_rows, max_tiles;
+  int max_tiles;
 };
 
 moe_status plan_wide(const moe_decode_config* cfg, int32_t tokens, Plan* p, WidePlan* q) {
@@ -560,8 +560,7 @@ moe_status plan_wide(const moe_decode_config* cfg, int32_t tokens, Plan* p, Wide
   if (tokens > MOE_WIDE_MAX_TOKENS) return MOE_ERR_UNSUPPORTED;
   const size_t T = tokens, S = 8 * T, R = S + (p->Is ? T : 0);
   q->picks = (int64_t)S;
-  q->tile_rows = wide_tile_rows(q->picks, p->E);
-  q->max_tiles = wide_max_tiles(q->picks, p->E, p->Is ? tokens : 0, q->tile_rows);
+  q->max_tiles = wide_max_tiles(q->picks, p->E, p->Is ? tokens : 0);
   size_t o = 0;
   auto take = [&](size_t bytes) {
     const size_t at = o;
@@ -570,6 +569,7 @@ moe_status plan_wide(const moe_decode_config* cfg, int32_t tokens, Plan* p, Wide
   };
   q->actq = take(T * p->H);
   q->acts = take(T * (p->H / 128) * 4);
+  q->actt = take(R * (p->H / 128) * 4);
   q->order = take(S * 4);
   q->pos = take(S * 4);
   q->offsets = take((p->E + 1) * 4);
@@ -772,9 +772,11 @@ moe_status moe_wide_step(const moe_decode_config* cfg, const uint16_t* x, int32_
   a.shared = p.Is > 0;
   a.tokens = tokens;
   a.picks = q.picks;
+  a.rows = q.picks + (a.shared ? tokens : 0);
   a.eps = cfg->rms_eps;
   a.act_q = reinterpret_cast<uint8_t*>(b + q.actq);
   a.act_s = reinterpret_cast<float*>(b + q.acts);
+  a.act_t = reinterpret_cast<float*>(b + q.actt);
   a.order = reinterpret_cast<int32_t*>(b + q.order);
   a.mid_q = reinterpret_cast<uint8_t*>(b + q.midq);
   a.mid_s = reinterpret_cast<float*>(b + q.mids);
@@ -784,7 +786,6 @@ moe_status moe_wide_step(const moe_decode_config* cfg, const uint16_t* x, int32_
   a.counts = reinterpret_cast<int32_t*>(b + q.counts);
   a.tiles = reinterpret_cast<RowTile*>(b + q.tiles);
   a.n_tiles = reinterpret_cast<int32_t*>(b + q.ntiles);
-  a.tile_rows = q.tile_rows;
   a.max_tiles = q.max_tiles;
   const WideWeights v = {wt.gamma, wt.gate_c, wt.up_c, wt.down_c, (const float*)wt.gate_s,
                          (const float*)wt.up_s, (const float*)wt.down_s, wt.sg_c, wt.su_c, wt.sd_c,

@@ -75,7 +75,11 @@ struct LoraRows {
 };
 
 // The GEMVs' epilogue beside adapters (LORA) or without: Rows is its part of
-// the block's LDS, filled by load() before a barrier.
+// the block's LDS, filled by load() before a barrier.  The term reads B's row
+// after the sum it joins, one latency: at rank 16 [9728, 2560] of 1 bit takes
+// 5.8 us with it and 4.5 without at 1 row, 9.3 and 7.9 at 8; [6144, 6144] of
+// FP8 12.1 and 9.4, of bf16 17.6 and 14.6.  A pass of its own over y would
+// cost a launch and round twice.
 struct NoLoraRows {};
 template <bool LORA>
 struct GemvTail {

@@ -17,14 +17,16 @@
 // That is nothing in y, but it moves some of mid's values across a border
 // between two FP8 codes, 2^-4 of the value apart: at 16 to 48 tokens of 6144
 // the outputs' error went from the 0.00166 of their bf16 rounding to 0.0018 ..
-// 0.0026.  Gate and up of the 64-row tiles therefore take the codes as bf16
-// numbers, which they are, through the bf16 MFMA, whose sums are fp32's: twice
-// the MFMA work and the conversions, for 558.7 -> 560.7 us at 16 tokens, 1598
-// -> 1611 us at 300 and 2102 -> 2182 us at 1536, where the weights' bytes set
-// the time.  In the 128-row tiles the products set it (4096 tokens: 2935 us
-// with FP8 MFMAs, 6076 us with bf16, its operands spilling): they keep the FP8
-// MFMA, and an error of 0.0020.
+// 0.0026.  Where a block has up to 64 rows, gate and up therefore take the codes
+// as bf16 numbers, which they are, through the bf16 MFMA, whose sums are
+// fp32's: four times the MFMAs and the conversions, 524 -> 544 us at 16 tokens,
+// 1568 -> 1572 at 300, 1890 -> 1849 (within the run's spread) at 1024, where
+// the weights' bytes set the time.  Above 64 rows a block's products set it (all
+// of 4096 tokens' up/gate in bf16: 4950 us against 1830), and they keep the FP8
+// MFMA, with an error of 0.0020.
 #include "wide.h"
+
+#include <type_traits>
 
 #include "device_common.h"
 
@@ -77,182 +79,107 @@ __global__ __launch_bounds__(256) void moe_wide_act_kernel(WideArgs a, const uin
   }
 }
 
-// ------------------------------------------------------------ the products
-// A block computes BM sorted rows of one expert against 256 weight rows (the
-// gate and up rows of 128 mid columns, or 256 down rows), K in steps of 128.
-// Each step's codes go through LDS in rows of 128 bytes whose 16-byte chunks
-// are permuted by the row, so that the 16 rows a wave reads at one chunk fall
-// on distinct banks.  The weights are the MFMA's A operand (their 16 rows its
-// output rows: a lane holds 4 consecutive columns of one sorted row), the
-// sorted rows its B operand.  After each step the fp32 products are scaled by
-// weight scale times row scale and added.
-//
-// Measured at 256 experts of 6144 x 2048 and a shared one.  300 tokens: up/gate
-// 1012 us, down 544, the weights' 9.7 GB at 6.2 TB/s, which bounds it.  4096
-// tokens: 1805 .. 1870 and 911 .. 945 us, 1.0 PFLOP/s, bound by no single unit:
-// the loads of the next step are under way during one step's products, yet the
-// step's phases add up (MFMAs busy 24% of the cycles, LDS 25%; without any
-// loads the up/gate still takes 1115 us, without the weights' 1160, and a loop
-// of loads and LDS reads without any MFMA 1690).  Tried there: loads straight
-// into three LDS stages, the products of one row tile issued before the last
-// one's are scaled, in blocks of 4 waves and of 8 (1740 .. 1860 us, not taken:
-// 3% for a second kernel whose waits count its loads); rows of 256 in two
-// stages (2100); other orders of tiles over the XCDs, tiles of even size and
-// staggered K (1760 .. 1990).
-__device__ __forceinline__ int lds_at(int row, int chunk) {
-  return row * 128 + ((chunk ^ (row >> 1)) & 7) * 16;
+// The tokens' scales once more, by K block and sorted row: a step of a tile
+// reads 512 bytes in a row instead of 4 from each of 128 places, each of which
+// costs a request as a line of codes does (4096 tokens: 110 us of the up/gate
+// for the 7 that this takes).
+__global__ __launch_bounds__(256) void moe_wide_sorted_scales_kernel(WideArgs a) {
+  const int64_t s = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  // (sorted rows behind the last pick of a group: none)
+  if (s >= a.rows || (s < a.picks && s >= a.offsets[a.E])) return;
+  const int64_t t = s < a.picks ? a.order[s] >> 3 : s - a.picks;
+  const int nkb = a.H / 128, k0 = blockIdx.y * 4;
+  float v[4];
+#pragma unroll
+  for (int k = 0; k < 4; k++) v[k] = a.act_s[t * nkb + (k0 + k < nkb ? k0 + k : nkb - 1)];
+#pragma unroll
+  for (int k = 0; k < 4; k++)
+    if (k0 + k < nkb) a.act_t[(int64_t)(k0 + k) * a.rows + s] = v[k];
 }
 
+// ------------------------------------------------------------ the products
+// A block computes up to 128 sorted rows of one expert against 256 weight rows
+// (the gate and up rows of 128 mid columns, or 256 down rows), K in steps of
+// 128; one block holds a CU.  The weights are the MFMA's A operand (their 16
+// rows its output rows: a lane holds 4 consecutive columns of one sorted row),
+// the sorted rows its B operand; each of the 4 waves takes 64 weight rows and
+// all the sorted ones.  The fp32 products of a step are scaled by weight scale
+// times row scale and added.
+//
+// Codes are loaded straight into LDS, into a ring of three stages, and each
+// operand is replaced by the next one right after its last use, so that a
+// wave's loads, LDS reads, MFMAs and scaling run beside each other: the products
+// of one row tile are issued before the last one's are scaled, and the ring's
+// next loads are spread between the MFMAs (in one go they stall the wave that
+// issues them: up/gate of 4096 tokens 1790 against 1740 us).
+//
+// Measured at 256 experts of 6144 x 2048 and a shared one.  300 tokens: the
+// weights' 9.7 GB at 6.2 TB/s, which bounds it.  4096 tokens: up/gate 1630 us,
+// down 914, 1.1 PFLOP/s.  Without any loads the up/gate takes 955 us, with half
+// the weights' 1352, and a loop of the loads and LDS reads without any MFMA
+// 1690 (with row scales read from 128 places a step, 1740 instead of 1630 in
+// all): bound by the loads, 14 GB a launch from L2 to the CUs.  A form with the
+// next step in registers and two blocks a CU took 1830 and 920 us, and 4 to 10%
+// more time from 16 tokens on; other orders of tiles over the XCDs, tiles of
+// even size and K started at other places were no faster (1760 .. 1890 where
+// this order took 1760).
 // Loads at a 32-bit offset from a block-uniform base: the base, the uniform
-// part of the offset and the bound stay in scalar registers (as 64-bit
-// addresses a lane's 12 loads a step took 24 vector registers).
+// part of the offset and the bound stay in scalar registers.
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t uniform_base(const void* p, uint32_t bytes) {
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, bytes, 0x00027000);
 }
-__device__ __forceinline__ u32x4 load_at(__amdgpu_buffer_rsrc_t r, uint32_t lane, uint32_t uniform) {
-  return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, lane, uniform, 0));
-}
-__device__ __forceinline__ float load_f32_at(__amdgpu_buffer_rsrc_t r, uint32_t lane, uint32_t uniform) {
-  return __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(r, lane, uniform, 0));
-}
 
-template <int MT>
-struct WideLds {
-  __align__(16) uint8_t codes[(16 * MT + 256) * 128];  // weight rows, then sorted rows
-  float as[16 * MT];
-  float mx[4][16 * MT];
+// A block's weights and columns: half h (0, 1) of its 256 weight rows starts at
+// row n0, n1 of w0, w1, with scales from s0, s1 on; a half past the end of the
+// down matrix repeats its last and is not stored.
+struct WideBlock {
+  const uint8_t *w0, *w1;
+  const float *s0, *s1;
+  int K, N, nkb, n0;
 };
+template <bool UG>
+__device__ __forceinline__ WideBlock wide_block(const WideArgs& a, const WideWeights& w,
+                                                const RowTile& tile, int nb) {
+  const bool shared = tile.group == a.E;
+  WideBlock o;
+  o.K = UG ? a.H : a.I;
+  o.N = UG ? a.I : a.H;
+  o.nkb = o.K / 128;
+  const int64_t ew = shared ? 0 : (int64_t)tile.group * o.N * o.K;
+  const int64_t es = shared ? 0 : (int64_t)tile.group * (o.N / 128) * o.nkb;
+  o.w0 = (UG ? (shared ? w.sg_c : w.gate_c) : (shared ? w.sd_c : w.down_c)) + ew;
+  o.w1 = UG ? (shared ? w.su_c : w.up_c) + ew : o.w0;
+  o.s0 = (UG ? (shared ? w.sg_s : w.gate_s) : (shared ? w.sd_s : w.down_s)) + es;
+  o.s1 = UG ? (shared ? w.su_s : w.up_s) + es : o.s0;
+  o.n0 = UG ? nb * 128 : nb * 256;
+  const int n1 = UG ? o.n0 : (o.n0 + 128 < o.N ? o.n0 + 128 : o.n0);
+  o.w0 += (int64_t)o.n0 * o.K;
+  o.w1 += (int64_t)n1 * o.K;
+  o.s0 += (int64_t)(o.n0 / 128) * o.nkb;
+  o.s1 += (int64_t)(n1 / 128) * o.nkb;
+  return o;
+}
 
-// The tile's products and their epilogue, U of its MT row tiles holding rows.
-template <int MT, int U, bool UG>
-__device__ __forceinline__ void wide_tile(const WideArgs& a, const WideWeights& w,
-                                          const RowTile& tile, int nb, WideLds<MT>& sh) {
-  constexpr bool kExact = UG && MT == 4;  // sums in fp32: see the top of the file
-  constexpr int NA = (U + 1) / 2;  // 16-byte chunks of sorted rows a thread loads a step
+// The row behind act_q (UG: a token) or behind the tile's first of mid_q that
+// is the tile's sorted row i; rows past the tile's end repeat its last.
+template <bool UG>
+__device__ __forceinline__ uint32_t source_row(const WideArgs& a, const RowTile& tile, int i) {
+  int s = tile.row + i;
+  if (s >= tile.end) s = tile.end - 1;
+  if (!UG) return (uint32_t)(s - tile.row);
+  return (uint32_t)(s < a.picks ? a.order[s] >> 3 : s - a.picks);
+}
+
+// Stores a tile's sums.  codes: 17408 bytes of the block's LDS, mx: 4 floats a
+// row, neither in use by any wave once the block has met (down) or has met
+// after writing mx (up/gate: codes only).
+template <int U, bool UG>
+__device__ __forceinline__ void wide_store(const WideArgs& a, const RowTile& tile, int nb,
+                                           const WideBlock& bl, float (&acc)[U][4][4],
+                                           uint8_t* codes, float* mx) {
   const int tid = threadIdx.x, lane = tid & 63, wn = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int col = lane & 15, g = lane >> 4;
-  const bool shared = tile.group == a.E;
-  const int K = UG ? a.H : a.I, N = UG ? a.I : a.H, nkb = K / 128;
-  const int64_t ew = shared ? 0 : (int64_t)tile.group * N * K;
-  const int64_t es = shared ? 0 : (int64_t)tile.group * (N / 128) * nkb;
-  const uint8_t* w0 = (UG ? (shared ? w.sg_c : w.gate_c) : (shared ? w.sd_c : w.down_c)) + ew;
-  const uint8_t* w1 = UG ? (shared ? w.su_c : w.up_c) + ew : w0;
-  const float* s0 = (UG ? (shared ? w.sg_s : w.gate_s) : (shared ? w.sd_s : w.down_s)) + es;
-  const float* s1 = UG ? (shared ? w.su_s : w.up_s) + es : s0;
-  // weight rows of the block: half h (0, 1) starts at row n0, n1; a half past
-  // the end of the down matrix repeats its last and is not stored
-  const int n0 = UG ? nb * 128 : nb * 256;
-  const int n1 = UG ? n0 : (n0 + 128 < N ? n0 + 128 : n0);
-  const float* ps0 = s0 + (int64_t)(n0 / 128) * nkb;
-  const float* ps1 = s1 + (int64_t)(n1 / 128) * nkb;
-
-  // this thread's chunks of a step: weight rows tid / 8 + 32 i (i < 4: half 0),
-  // then sorted rows (those past the tile's end repeat its last row)
-  const uint32_t ow = (uint32_t)(tid >> 3) * (uint32_t)K + (uint32_t)(tid & 7) * 16u;
-  const auto bw0 = uniform_base(w0 + (int64_t)n0 * K, 128u * K);
-  const auto bw1 = uniform_base(w1 + (int64_t)n1 * K, 128u * K);
-  const int rows = UG ? a.tokens : (tile.end - tile.row < 16 * U ? tile.end - tile.row : 16 * U);
-  const auto ba = uniform_base(UG ? a.act_q : a.mid_q + (int64_t)tile.row * K, (uint32_t)rows * K);
-  const auto bs = uniform_base(UG ? a.act_s : a.mid_s + (int64_t)tile.row * nkb, (uint32_t)rows * nkb * 4u);
-  auto source_row = [&](int i) -> uint32_t {  // row behind ba, bs of the tile's sorted row i
-    int s = tile.row + i;
-    if (s >= tile.end) s = tile.end - 1;
-    if (!UG) return (uint32_t)(s - tile.row);
-    return (uint32_t)(s < a.picks ? a.order[s] >> 3 : s - a.picks);
-  };
-  uint32_t oa[NA];
-#pragma unroll
-  for (int i = 0; i < NA; i++)
-    oa[i] = source_row((tid >> 3) + 32 * i) * (uint32_t)K + (uint32_t)(tid & 7) * 16u;
-  const uint32_t os = source_row(tid) * (uint32_t)nkb * 4u;
-  // an odd number of row tiles: the last 16 rows are loaded by the first two waves
-  auto loads = [&](int i) { return i + 1 < NA || U % 2 == 0 || wn < 2; };
-
-  u32x4 rw[8], ra[NA];
-  float rs = 0.f;
-  auto issue = [&](uint32_t kb) {
-#pragma unroll
-    for (int i = 0; i < 4; i++) rw[i] = load_at(bw0, ow, 32u * i * K + kb * 128u);
-#pragma unroll
-    for (int i = 0; i < 4; i++) rw[4 + i] = load_at(bw1, ow, 32u * i * K + kb * 128u);
-#pragma unroll
-    for (int i = 0; i < NA; i++)
-      if (loads(i)) ra[i] = load_at(ba, oa[i], kb * 128u);
-    if (64 * wn < 16 * U) rs = load_f32_at(bs, os, kb * 4u);
-  };
-  float acc[U][4][4];  // [sorted-row tile][weight tile: 2 of half 0, 2 of half 1][4 columns]
-#pragma unroll
-  for (int i = 0; i < U; i++)
-#pragma unroll
-    for (int j = 0; j < 4; j++)
-#pragma unroll
-      for (int v = 0; v < 4; v++) acc[i][j][v] = 0.f;
-
-  // Places in LDS.  The permutation depends on a row's last 4 bits alone, so
-  // that 16 rows on (and 32, for the writes) are at a constant distance.
-  uint8_t* const put = sh.codes + lds_at(tid >> 3, tid & 7);
-  const uint8_t* const row0 = sh.codes + lds_at(col, g);      // K 16 g .. of row col
-  const uint8_t* const row1 = sh.codes + lds_at(col, g + 4);  // K 64 + 16 g ..
-  auto operand = [&](int row) { return cat8(ld16(row0 + row * 128), ld16(row1 + row * 128)); };
-
-  issue(0);
-  for (int kb = 0; kb < nkb; kb++) {
-    __syncthreads();  // every wave is done with the last step's codes
-#pragma unroll
-    for (int i = 0; i < 8; i++) *reinterpret_cast<u32x4*>(put + i * 4096) = rw[i];
-#pragma unroll
-    for (int i = 0; i < NA; i++)
-      if (loads(i)) *reinterpret_cast<u32x4*>(put + 32768 + i * 4096) = ra[i];
-    if (tid < 16 * U) sh.as[tid] = rs;
-    const float sw[2] = {ps0[kb], ps1[kb]};
-    if (kb + 1 < nkb) issue(kb + 1);
-    __syncthreads();
-    v8i op[4];
-    v8bf opx[4][4];  // (kExact) as bf16: 8 codes of every lane an MFMA
-#pragma unroll
-    for (int j = 0; j < 4; j++) {
-      op[j] = operand((j >> 1) * 128 + wn * 32 + (j & 1) * 16);
-      if constexpr (kExact) {
-#pragma unroll
-        for (int q = 0; q < 4; q++) opx[j][q] = fp8x8_to_bf16(uint2{(uint32_t)op[j][2 * q], (uint32_t)op[j][2 * q + 1]});
-      }
-    }
-    // the scheduling barriers keep the compiler from hoisting every row tile's
-    // reads (71 spilled registers at 8 row tiles without them)
-    v8i b[2];
-    float as[2];
-    auto fetch = [&](int i) {
-      b[i & 1] = operand(256 + 16 * i);
-      as[i & 1] = sh.as[i * 16 + col];
-    };
-    fetch(0);
-#pragma unroll
-    for (int i = 0; i < U; i++) {
-      v4f c[4];
-      if constexpr (kExact) {
-#pragma unroll
-        for (int j = 0; j < 4; j++) c[j] = v4f{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int q = 0; q < 4; q++) {
-          const v8bf bx = fp8x8_to_bf16(uint2{(uint32_t)b[i & 1][2 * q], (uint32_t)b[i & 1][2 * q + 1]});
-#pragma unroll
-          for (int j = 0; j < 4; j++) c[j] = mfma_bf16(opx[j][q], bx, c[j]);
-        }
-      } else {
-#pragma unroll
-        for (int j = 0; j < 4; j++) c[j] = mfma_fp8(op[j], b[i & 1]);
-      }
-      const float ar = as[i & 1];
-      if (i + 1 < U) fetch(i + 1);
-#pragma unroll
-      for (int j = 0; j < 4; j++) {
-        const float s = ar * sw[j >> 1];
-#pragma unroll
-        for (int v = 0; v < 4; v++) acc[i][j][v] = fmaf(c[j][v], s, acc[i][j][v]);
-      }
-      __builtin_amdgcn_sched_barrier(0);
-    }
-  }
+  const int N = bl.N, n0 = bl.n0;
 #pragma unroll
   for (int i = 0; i < U; i++)
 #pragma unroll
@@ -263,7 +190,7 @@ __device__ __forceinline__ void wide_tile(const WideArgs& a, const WideWeights& 
     // largest value over the 4 waves of the row
 #pragma unroll
     for (int i = 0; i < U; i++) {
-      float mx = 0.f;
+      float big = 0.f;
 #pragma unroll
       for (int j = 0; j < 2; j++)
 #pragma unroll
@@ -271,41 +198,41 @@ __device__ __forceinline__ void wide_tile(const WideArgs& a, const WideWeights& 
           const float gt = acc[i][j][v];
           const float mid = gt / (1.0f + __expf(-gt)) * acc[i][j + 2][v];
           acc[i][j][v] = mid;
-          mx = fmaxf(mx, fabsf(mid));
+          big = fmaxf(big, fabsf(mid));
         }
-      mx = fmaxf(mx, __shfl_xor(mx, 16, kWave));
-      mx = fmaxf(mx, __shfl_xor(mx, 32, kWave));
-      if (g == 0) sh.mx[wn][i * 16 + col] = mx;
+      big = fmaxf(big, __shfl_xor(big, 16, kWave));
+      big = fmaxf(big, __shfl_xor(big, 32, kWave));
+      if (g == 0) mx[wn * 16 * U + i * 16 + col] = big;
     }
     __syncthreads();
     // the codes through LDS, so that 8 lanes store a row's 128 bytes
 #pragma unroll
     for (int i = 0; i < U; i++) {
       const int m = i * 16 + col;
-      const float s = fmaxf(fmaxf(sh.mx[0][m], sh.mx[1][m]), fmaxf(sh.mx[2][m], sh.mx[3][m])) / 448.0f;
+      const float s = fmaxf(fmaxf(mx[m], mx[16 * U + m]), fmaxf(mx[32 * U + m], mx[48 * U + m])) / 448.0f;
 #pragma unroll
       for (int j = 0; j < 2; j++) {
         uint32_t q = 0u;
         if (s > 0.f)
           q = f32x2_to_e4m3(acc[i][j][0] / s, acc[i][j][1] / s) |
               (f32x2_to_e4m3(acc[i][j][2] / s, acc[i][j][3] / s) << 16);
-        *reinterpret_cast<uint32_t*>(sh.codes + m * 128 + wn * 32 + j * 16 + 4 * g) = q;
+        *reinterpret_cast<uint32_t*>(codes + m * 128 + wn * 32 + j * 16 + 4 * g) = q;
       }
       if (wn == 0 && g == 0 && tile.row + m < tile.end)
-        a.mid_s[(int64_t)(tile.row + m) * (N / 128) + nb] = s;
+        a.mid_s[(int64_t)nb * a.rows + tile.row + m] = s;
     }
     __syncthreads();
     for (int q = tid; q < 16 * U * 8; q += 256) {
       const int row = tile.row + (q >> 3);
       if (row < tile.end)
-        *reinterpret_cast<u32x4*>(a.mid_q + (int64_t)row * N + n0 + (q & 7) * 16) = ld16(sh.codes + q * 16);
+        *reinterpret_cast<u32x4*>(a.mid_q + (int64_t)row * N + n0 + (q & 7) * 16) = ld16(codes + q * 16);
     }
   } else {
     // through LDS, so that 8 lanes store 32 consecutive outputs of a row: the
     // wave's 16 rows x 64 columns of one row tile at a time, in an area of its
     // own (rows of 68 floats; one wave's LDS operations complete in order)
     __syncthreads();  // every wave is done with the last step's codes
-    float* mine = reinterpret_cast<float*>(sh.codes) + wn * 16 * 68;
+    float* mine = reinterpret_cast<float*>(codes) + wn * 16 * 68;
     const int jn = lane & 15;  // columns 4 jn ..: half jn / 8
     const int n = n0 + (jn >> 3) * 128 + wn * 32 + (jn & 7) * 4;
 #pragma unroll
@@ -326,30 +253,296 @@ __device__ __forceinline__ void wide_tile(const WideArgs& a, const WideWeights& 
   }
 }
 
-template <int MT, bool UG>
-__global__ __launch_bounds__(256, 2) void moe_wide_gemm_kernel(WideArgs a, WideWeights w) {
-  __shared__ WideLds<MT> sh;
-  // Column blocks (UG: 128 mid columns; down: 256 outputs) first: consecutive
-  // blocks go to the 8 XCDs in turn, each with an L2 of its own, and where a
-  // multiple of 8 column blocks makes up a row tile, one XCD's L2 serves all
-  // the row tiles of a column block, so that an expert's tiles share its weights
+// A block's tile, column block and number of row tiles that hold rows; false:
+// none.  Column blocks (UG: 128 mid columns; down: 256 outputs) first:
+// consecutive blocks go to the 8 XCDs in turn, each with an L2 of its own, and
+// where a multiple of 8 column blocks makes up a row tile, one XCD's L2 serves
+// all the row tiles of a column block, so that an expert's tiles share its
+// weights.
+template <bool UG>
+__device__ __forceinline__ bool wide_place(const WideArgs& a, RowTile* tile, int* nb, int* used) {
   const uint32_t nbs = UG ? a.I / 128 : (a.H + 255) / 256;
-  const int ti = (int)(blockIdx.x / nbs), nb = (int)(blockIdx.x % nbs);
-  if (ti >= *a.n_tiles) return;
-  const RowTile tile = a.tiles[ti];
-  int used = (tile.end - tile.row + 15) >> 4;
-  used = __builtin_amdgcn_readfirstlane(used < MT ? used : MT);
-  // a loop for each number of row tiles that hold rows
-  if constexpr (MT == 8) {
-    if (used == 8) return wide_tile<MT, 8, UG>(a, w, tile, nb, sh);
-    if (used == 7) return wide_tile<MT, 7, UG>(a, w, tile, nb, sh);
-    if (used == 6) return wide_tile<MT, 6, UG>(a, w, tile, nb, sh);
-    if (used == 5) return wide_tile<MT, 5, UG>(a, w, tile, nb, sh);
+  const int ti = (int)(blockIdx.x / nbs);
+  if (ti >= *a.n_tiles) return false;
+  *nb = (int)(blockIdx.x % nbs);
+  *tile = a.tiles[ti];
+  *used = __builtin_amdgcn_readfirstlane((tile->end - tile->row + 15) >> 4);
+  return true;
+}
+
+// A load to LDS puts 16 bytes a lane at consecutive places, 1 KB in all, and
+// reads memory a line at a time only where neighbouring lanes read ascending
+// addresses.  So a kilobyte holds 8 pieces of 128 bytes, each of another row,
+// and starts 1056 bytes behind the one before: 16 rows' chunks that lie in 8
+// kilobytes of different index mod 8, or in 4 and half a kilobyte apart, are
+// read from distinct banks (lanes 0-3, 12-15 and 20-27 of a wave go together).
+constexpr int kKilo = 1056;
+
+// A wave's own 64 weight rows: kilobyte 8 wn + 4 h + q holds rows 32 wn + 16 j +
+// 4 p + q of half h, its piece 4 j + p.
+struct RingWeights {
+  __align__(16) uint8_t b[32 * kKilo];
+};
+// Sorted rows: kilobyte i holds row i of each row tile.  Behind them their
+// scales, and a place for loads of nothing.
+struct RingRows {
+  static constexpr int kScales = 16 * kKilo, kNone = kScales + 512;
+  __align__(16) uint8_t b[kNone + 256];
+};
+// (one LDS object for each: while a load to an object is under way, the
+// compiler lets reads of that object wait for all loads)
+struct RingStage {
+  RingWeights& w;
+  RingRows& r;
+};
+
+typedef __attribute__((address_space(3))) void lds_void;
+__device__ __forceinline__ void load_to_lds(__amdgpu_buffer_rsrc_t r, uint8_t* lds, uint32_t lane,
+                                            uint32_t uniform) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)lds, 16, lane, uniform, 0, 0);
+}
+__device__ __forceinline__ void load_f32_to_lds(__amdgpu_buffer_rsrc_t r, uint8_t* lds, uint32_t lane,
+                                                uint32_t uniform) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)lds, 4, lane, uniform, 0, 0);
+}
+
+// Waits for this wave's LDS operations, and until at most VM of its loads are
+// under way.  No memory operation moves across.
+template <int VM>
+__device__ __forceinline__ void wait_own() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt((VM & 15) | (7 << 4) | ((VM >> 4) << 14));
+  asm volatile("" ::: "memory");
+}
+// The same, then for the other waves.
+template <int VM>
+__device__ __forceinline__ void wait_and_meet() {
+  wait_own<VM>();
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
+template <int U, bool UG>
+__device__ __forceinline__ void wide_tile(const WideArgs& a, const WideWeights& w, const RowTile& tile,
+                                          int nb, const RingStage& st0, const RingStage& st1,
+                                          const RingStage& st2) {
+  // a wave's loads of a step: 8 of weights, then 4 of sorted rows and 1 of their
+  // scales.  A wave (or lane) without any loads from past the buffer's end,
+  // which touches no memory: every step of every wave has as many loads.
+  constexpr int NW = 8, NR = 5, ND = NW + NR;
+  constexpr uint32_t kNothing = 0xFFFFFF00u;
+  const int tid = threadIdx.x, lane = tid & 63, wn = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int col = lane & 15, g = lane >> 4;
+  const WideBlock bl = wide_block<UG>(a, w, tile, nb);
+  const int K = bl.K, nkb = bl.nkb;
+  typedef const __attribute__((address_space(4))) float* scalar_ptr;
+  const scalar_ptr ps0 = (scalar_ptr)bl.s0, ps1 = (scalar_ptr)bl.s1;  // scalar loads
+  const int left = tile.end - tile.row < 16 * U ? tile.end - tile.row : 16 * U;
+  const auto bw0 = uniform_base(bl.w0, 128u * K);
+  const auto bw1 = uniform_base(bl.w1, 128u * K);
+  const auto ba = uniform_base(UG ? a.act_q : a.mid_q + (int64_t)tile.row * K, (uint32_t)(UG ? a.tokens : left) * K);
+  const uint32_t sb = 4u * (uint32_t)a.rows;  // bytes from one K block's scales to the next
+  const auto bs = uniform_base((UG ? a.act_t : a.mid_s) + tile.row, (uint32_t)(nkb - 1) * sb + 4u * (uint32_t)left);
+  const uint32_t ow = (uint32_t)(32 * wn + 16 * (lane >> 5) + 4 * ((lane >> 3) & 3)) * (uint32_t)K + 16u * (lane & 7);
+  uint32_t oa[4];
+#pragma unroll
+  for (int n = 0; n < 4; n++)
+    oa[n] = (lane >> 3) < U ? source_row<UG>(a, tile, 4 * wn + n + 16 * (lane >> 3)) * (uint32_t)K + 16u * (uint32_t)(lane & 7)
+                            : kNothing;
+  const int srow = 64 * wn + lane;  // whose scale this lane loads
+  const uint32_t os = srow < 16 * U ? 4u * (uint32_t)(srow < left ? srow : left - 1) : kNothing;
+  const int ls = wn < 2 ? RingRows::kScales + wn * 256 : RingRows::kNone;
+  // load n of step kb; wq, rq, sq: where the wave's parts of a stage start
+  auto issue = [&](const RingStage& st, int kb, int n, int wq, int rq, int sq) {
+    const uint32_t k0 = (uint32_t)kb * 128u;
+    if (n < NW)
+      load_to_lds(n < 4 ? bw0 : bw1, st.w.b + wq + n * kKilo, ow, k0 + (uint32_t)(n & 3) * K);
+    else if (n < NW + 4)
+      load_to_lds(ba, st.r.b + rq + (n - NW) * kKilo, oa[n - NW], k0);
+    else
+      load_f32_to_lds(bs, st.r.b + sq, os, (uint32_t)kb * sb);
+  };
+  const int wq0 = 8 * wn * kKilo, rq0 = 4 * wn * kKilo;
+
+  // operands: chunks g and g + 4 of weight row 16 j + col, of sorted row 16 i + col
+  const int ow0 = (8 * wn + (col & 3)) * kKilo + (col >> 2) * 128 + 16 * g, oa0 = col * kKilo + 16 * g;
+  auto weights = [&](const RingStage& st, int wo, int j) {
+    const uint8_t* p = st.w.b + (j >> 1) * (4 * kKilo) + (j & 1) * 512 + wo;
+    return cat8(ld16(p), ld16(p + 64));
+  };
+  auto rows_of = [&](const RingStage& st, int ro, int i) {
+    const uint8_t* p = st.r.b + i * 128 + ro;
+    return cat8(ld16(p), ld16(p + 64));
+  };
+  auto scale_of = [&](const RingStage& st, int so, int i) {
+    return *reinterpret_cast<const float*>(st.r.b + RingRows::kScales + i * 64 + so);
+  };
+
+  // Row tile i of a step uses slot (first + i) % 3 of b and as; the one D tiles
+  // on is read meanwhile.  At row tile M the wave meets the others: they have
+  // then read all of this step's rows, whose stage may be loaded again, and the
+  // next step's have arrived, from which the reads go on.
+  constexpr int D = U > 1 ? 2 : 1, M = U > 2 ? U - 2 : 0;
+  // The wave's own weights of this step are in registers from its first row
+  // tile on: with 4 row tiles or more their place is loaded again from the
+  // second on, before the meeting.
+  constexpr bool kAhead = U >= 4;
+  // kExact: sums in fp32 by the bf16 MFMA (top of the file)
+  constexpr bool kExact = UG && U <= 4;
+  v8i op[4], b[3];
+  v8bf opx[4][4], bx[4];  // (kExact) op and b as bf16, 8 codes of every lane an MFMA
+  float as[3] = {0.f, 0.f, 0.f}, sw[2], sw_last[2] = {0.f, 0.f};
+  v4f c[4] = {};  // the products not yet scaled: of the row tile before
+  float acc[U][4][4];
+#pragma unroll
+  for (int i = 0; i < U; i++)
+#pragma unroll
+    for (int j = 0; j < 4; j++)
+#pragma unroll
+      for (int v = 0; v < 4; v++) acc[i][j][v] = 0.f;
+  auto at = [&](int k) { return k < nkb ? k : nkb - 1; };  // (loads past the last step repeat it)
+  auto step = [&](auto first, const RingStage& cur, const RingStage& nx, int k) {
+    constexpr int P = decltype(first)::value;
+    const int kl = at(k + 3);
+    float sw_next[2];
+    // (opaque, or the addresses in all three stages are kept in registers)
+    int wq = wq0, rq = rq0, sq = ls, wo = ow0, ro = oa0, so = 4 * col;
+    asm volatile("" : "+s"(wq), "+s"(rq), "+s"(sq), "+v"(wo), "+v"(ro), "+v"(so));
+#pragma unroll
+    for (int i = 0; i < U; i++) {
+      const float ap = as[(P + i + 2) % 3];
+      const float s[2] = {ap * (i ? sw[0] : sw_last[0]), ap * (i ? sw[1] : sw_last[1])};
+      if (kAhead && i == 1) wait_own<63>();  // the operands read from cur's weights are here
+      if (i == M) {
+        // step k + 1 has arrived when at most these are under way: all of step
+        // k + 2, and the weights of k + 3 where they have been issued
+        wait_and_meet<kAhead ? ND + NW : ND>();
+        sw_next[0] = ps0[at(k + 1)];
+        sw_next[1] = ps1[at(k + 1)];
+      }
+      b[(P + i + D) % 3] = i + D < U ? rows_of(cur, ro, i + D) : rows_of(nx, ro, i + D - U);
+      as[(P + i + D) % 3] = i + D < U ? scale_of(cur, so, i + D) : scale_of(nx, so, i + D - U);
+      const int t = i ? i - 1 : U - 1;
+      auto scale = [&](int j) {  // the products of the row tile before
+#pragma unroll
+        for (int v = 0; v < 4; v++) acc[t][j][v] = fmaf(c[j][v], s[j >> 1], acc[t][j][v]);
+      };
+      if constexpr (kExact) {
+        auto bf16_of = [](const v8i& o, int q) {
+          return fp8x8_to_bf16(uint2{(uint32_t)o[2 * q], (uint32_t)o[2 * q + 1]});
+        };
+        if (i == 0) {
+#pragma unroll
+          for (int j = 0; j < 4; j++)
+#pragma unroll
+            for (int q = 0; q < 4; q++) opx[j][q] = bf16_of(op[j], q);
+        }
+#pragma unroll
+        for (int j = 0; j < 4; j++) {
+          bx[j] = bf16_of(b[(P + i) % 3], j);
+          scale(j);
+          c[j] = v4f{0.f, 0.f, 0.f, 0.f};
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < 4; j++) {
+        if constexpr (kExact) {
+#pragma unroll
+          for (int q = 0; q < 4; q++) c[q] = mfma_bf16(opx[q][j], bx[j], c[q]);
+        } else {
+          scale(j);
+          c[j] = mfma_fp8(op[j], b[(P + i) % 3]);
+        }
+        if (i == U - 1) op[j] = weights(nx, wo, j);
+        // step k + 3's loads, evenly over the MFMAs that they may follow
+        if constexpr (kAhead) {
+          constexpr int QW = 4 * (M - 1), QR = 4 * (U - M);
+          const int qw = (i - 1) * 4 + j, qr = (i - M) * 4 + j;
+          if (qw >= 0 && qw < QW) {
+#pragma unroll
+            for (int n = NW * qw / QW; n < NW * (qw + 1) / QW; n++) issue(cur, kl, n, wq, rq, sq);
+          }
+          if (qr >= 0) {
+#pragma unroll
+            for (int n = NW + NR * qr / QR; n < NW + NR * (qr + 1) / QR; n++) issue(cur, kl, n, wq, rq, sq);
+          }
+        } else {
+          constexpr int Q = 4 * (U - M);
+          const int q = (i - M) * 4 + j;
+          if (q >= 0) {
+#pragma unroll
+            for (int n = ND * q / Q; n < ND * (q + 1) / Q; n++) issue(cur, kl, n, wq, rq, sq);
+          }
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    }
+    sw_last[0] = sw[0];
+    sw_last[1] = sw[1];
+    sw[0] = sw_next[0];
+    sw[1] = sw_next[1];
+  };
+#pragma unroll
+  for (int n = 0; n < ND; n++) issue(st0, at(0), n, wq0, rq0, ls);
+#pragma unroll
+  for (int n = 0; n < ND; n++) issue(st1, at(1), n, wq0, rq0, ls);
+#pragma unroll
+  for (int n = 0; n < ND; n++) issue(st2, at(2), n, wq0, rq0, ls);
+  sw[0] = ps0[0];
+  sw[1] = ps1[0];
+  wait_and_meet<2 * ND>();  // step 0 has arrived
+#pragma unroll
+  for (int j = 0; j < 4; j++) op[j] = weights(st0, ow0, j);
+#pragma unroll
+  for (int i = 0; i < D; i++) {
+    b[i] = rows_of(st0, oa0, i);
+    as[i] = scale_of(st0, 4 * col, i);
   }
-  if (used == 4) return wide_tile<MT, 4, UG>(a, w, tile, nb, sh);
-  if (used == 3) return wide_tile<MT, 3, UG>(a, w, tile, nb, sh);
-  if (used == 2) return wide_tile<MT, 2, UG>(a, w, tile, nb, sh);
-  wide_tile<MT, 1, UG>(a, w, tile, nb, sh);
+  using p0 = std::integral_constant<int, 0>;
+  using p1 = std::integral_constant<int, U % 3>;
+  using p2 = std::integral_constant<int, 2 * U % 3>;
+  int k = 0, next = 0;  // next: the slot of the row tile behind the last
+  for (; k + 3 <= nkb; k += 3) {
+    step(p0{}, st0, st1, k);
+    step(p1{}, st1, st2, k + 1);
+    step(p2{}, st2, st0, k + 2);
+  }
+  if (k < nkb) {
+    step(p0{}, st0, st1, k);
+    next = p1::value;
+  }
+  if (k + 1 < nkb) {
+    step(p1{}, st1, st2, k + 1);
+    next = p2::value;
+  }
+  const float ap = next == 0 ? as[2] : next == 1 ? as[0] : as[1];
+#pragma unroll
+  for (int j = 0; j < 4; j++)
+#pragma unroll
+    for (int v = 0; v < 4; v++) acc[U - 1][j][v] = fmaf(c[j][v], ap * sw_last[j >> 1], acc[U - 1][j][v]);
+  wait_and_meet<0>();  // nothing under way into the LDS that the epilogue uses
+  wide_store<U, UG>(a, tile, nb, bl, acc, st0.w.b, reinterpret_cast<float*>(st1.w.b));
+}
+
+// (256 threads a block; the bound of 512 keeps the compiler at 256 registers a
+// thread.  With more it leaves the MFMAs' results in accumulation registers and
+// moves each one before it is scaled: 1857 against 1818 us up/gate)
+template <bool UG>
+__global__ __launch_bounds__(512) void moe_wide_gemm_kernel(WideArgs a, WideWeights w) {
+  __shared__ RingWeights w0, w1, w2;
+  __shared__ RingRows r0, r1, r2;
+  RowTile tile;
+  int nb, used;
+  if (!wide_place<UG>(a, &tile, &nb, &used)) return;
+  const RingStage s0{w0, r0}, s1{w1, r1}, s2{w2, r2};
+  if (used >= 8) return wide_tile<8, UG>(a, w, tile, nb, s0, s1, s2);
+  if (used == 7) return wide_tile<7, UG>(a, w, tile, nb, s0, s1, s2);
+  if (used == 6) return wide_tile<6, UG>(a, w, tile, nb, s0, s1, s2);
+  if (used == 5) return wide_tile<5, UG>(a, w, tile, nb, s0, s1, s2);
+  if (used == 4) return wide_tile<4, UG>(a, w, tile, nb, s0, s1, s2);
+  if (used == 3) return wide_tile<3, UG>(a, w, tile, nb, s0, s1, s2);
+  if (used == 2) return wide_tile<2, UG>(a, w, tile, nb, s0, s1, s2);
+  wide_tile<1, UG>(a, w, tile, nb, s0, s1, s2);
 }
 
 // out[t] = bf16( sum_j g[t,j] y[pos[t,j]] + y[picks + t] ), in pick order.
@@ -383,26 +576,8 @@ __global__ __launch_bounds__(256) void moe_wide_combine_kernel(WideArgs a,
   *reinterpret_cast<uint2*>(out + t * a.H + c) = q;
 }
 
-// Rows of a tile, by the rows an expert has in the mean.  256 experts of 6144
-// x 2048, whole step in 64- and 128-row tiles: 1538 and 1616 us at 9 rows, 1990
-// and 1969 at 32, 2176 and 2048 at 48, 2495 and 2202 at 64.  From 32 to 48 rows
-// the 64-row tiles' sums in fp32 (top of the file) are taken for up to 6% of
-// the time.
-int wide_tile_rows(int64_t picks, int experts) {
-  const int64_t per = picks / experts;
-  return per <= 48 ? 64 : 128;
-}
-
-int wide_max_tiles(int64_t picks, int experts, int shared_rows, int tile_rows) {
-  return (int)(sort_max_tiles(picks, experts, tile_rows) + (shared_rows + tile_rows - 1) / tile_rows);
-}
-
-template <int MT>
-static void launch_products(const WideArgs& a, const WideWeights& w, hipStream_t stream) {
-  hipLaunchKernelGGL((moe_wide_gemm_kernel<MT, true>), dim3(a.max_tiles * (a.I / 128)), dim3(256), 0,
-                     stream, a, w);
-  hipLaunchKernelGGL((moe_wide_gemm_kernel<MT, false>), dim3(a.max_tiles * ((a.H + 255) / 256)),
-                     dim3(256), 0, stream, a, w);
+int wide_max_tiles(int64_t picks, int experts, int shared_rows) {
+  return (int)(sort_max_tiles(picks, experts, kWideTile) + (shared_rows + kWideTile - 1) / kWideTile);
 }
 
 hipError_t launch_wide(const WideArgs& a, const WideWeights& w, const uint16_t* x,
@@ -418,14 +593,15 @@ hipError_t launch_wide(const WideArgs& a, const WideWeights& w, const uint16_t* 
   s.counts = a.counts;
   s.tiles = a.tiles;
   s.n_tiles = a.n_tiles;
-  s.tile_rows = a.tile_rows;
+  s.tile_rows = kWideTile;
   s.extra = a.shared ? a.tokens : 0;
   hipError_t e = launch_sort(s, stream);
   if (e != hipSuccess) return e;
-  switch (a.tile_rows) {
-    case 64: launch_products<4>(a, w, stream); break;
-    default: launch_products<8>(a, w, stream); break;
-  }
+  const dim3 gu(a.max_tiles * (a.I / 128)), gd(a.max_tiles * ((a.H + 255) / 256));
+  hipLaunchKernelGGL(moe_wide_sorted_scales_kernel,
+                     dim3((uint32_t)((a.rows + 255) / 256), (a.H / 128 + 3) / 4), dim3(256), 0, stream, a);
+  hipLaunchKernelGGL(moe_wide_gemm_kernel<true>, gu, dim3(256), 0, stream, a, w);
+  hipLaunchKernelGGL(moe_wide_gemm_kernel<false>, gd, dim3(256), 0, stream, a, w);
   hipLaunchKernelGGL(moe_wide_combine_kernel, dim3(a.tokens, (a.H + 1023) / 1024), dim3(256), 0,
                      stream, a, gates, out);
   return hipGetLastError();

@@ -380,9 +380,10 @@ moe_status moe_combine_backward(const moe_row_shape* shape, const void* dout, co
  *  workspace  device memory of at least moe_wide_workspace_size bytes,
  *          256-byte aligned; scratch of this call: steps that overlap in time
  *          need one each
- * The sums run in other groupings than the decode step's, and in batches of
- * up to 48 picks an expert in others than in wider ones, so that a token's
- * results in these agree within rounding, not bitwise. */
+ * The sums run in other groupings than the decode step's, and in others where
+ * more than 64 rows of an expert are taken together, so that a token's results
+ * in the decode step and in different batches agree within rounding, not
+ * bitwise. */
 #define MOE_WIDE_MAX_TOKENS 65536
 size_t moe_wide_workspace_size(const moe_decode_config* cfg, int32_t tokens);
 moe_status moe_wide_step(const moe_decode_config* cfg, const uint16_t* x, int32_t tokens,
