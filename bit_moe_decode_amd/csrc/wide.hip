@@ -21,9 +21,9 @@
 // as bf16 numbers, which they are, through the bf16 MFMA, whose sums are
 // fp32's: four times the MFMAs and the conversions, 524 -> 544 us at 16 tokens,
 // 1568 -> 1572 at 300, 1890 -> 1849 (within the run's spread) at 1024, where
-// the weights' bytes set the time.  Above 64 rows a block's products set it (all
-// of 4096 tokens' up/gate in bf16: 4950 us against 1830), and they keep the FP8
-// MFMA, with an error of 0.0020.
+// the weights' bytes set the time.  Above 64 rows the products tell (4096 tokens
+// with bf16 in every block, in a form whose operands spilled: 6076 us against
+// 2935), and they keep the FP8 MFMA, with an error of 0.0020.
 #include "wide.h"
 
 #include <type_traits>
@@ -123,6 +123,7 @@ __global__ __launch_bounds__(256) void moe_wide_sorted_scales_kernel(WideArgs a)
 // more time from 16 tokens on; other orders of tiles over the XCDs, tiles of
 // even size and K started at other places were no faster (1760 .. 1890 where
 // this order took 1760).
+
 // Loads at a 32-bit offset from a block-uniform base: the base, the uniform
 // part of the offset and the bound stay in scalar registers.
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t uniform_base(const void* p, uint32_t bytes) {
@@ -171,8 +172,7 @@ __device__ __forceinline__ uint32_t source_row(const WideArgs& a, const RowTile&
 }
 
 // Stores a tile's sums.  codes: 17408 bytes of the block's LDS, mx: 4 floats a
-// row, neither in use by any wave once the block has met (down) or has met
-// after writing mx (up/gate: codes only).
+// row, which no wave uses any more.
 template <int U, bool UG>
 __device__ __forceinline__ void wide_store(const WideArgs& a, const RowTile& tile, int nb,
                                            const WideBlock& bl, float (&acc)[U][4][4],
@@ -231,7 +231,6 @@ __device__ __forceinline__ void wide_store(const WideArgs& a, const RowTile& til
     // through LDS, so that 8 lanes store 32 consecutive outputs of a row: the
     // wave's 16 rows x 64 columns of one row tile at a time, in an area of its
     // own (rows of 68 floats; one wave's LDS operations complete in order)
-    __syncthreads();  // every wave is done with the last step's codes
     float* mine = reinterpret_cast<float*>(codes) + wn * 16 * 68;
     const int jn = lane & 15;  // columns 4 jn ..: half jn / 8
     const int n = n0 + (jn >> 3) * 128 + wn * 32 + (jn & 7) * 4;
