@@ -49,16 +49,17 @@ __global__ __launch_bounds__(256) void moe_wide_act_kernel(WideArgs a, const uin
     sc[it] = 0.f;
     if (c >= a.H) continue;  // whole rows of 16 lanes
     const u32x4 xv = ld16(row + c), gv = ld16(gamma + c);
-    float u[8], m = 0.f;
+    float u[8];
+    uint32_t m = 0u;  // largest |u| by its bits: a NaN is the largest, and stays one
 #pragma unroll
     for (int i = 0; i < 8; i++) {
       const float xf = __uint_as_float(i & 1 ? xv[i >> 1] & 0xFFFF0000u : xv[i >> 1] << 16);
       const float gf = __uint_as_float(i & 1 ? gv[i >> 1] & 0xFFFF0000u : gv[i >> 1] << 16);
       ss = fmaf(xf, xf, ss);
       u[i] = bf16_to_f32(f32_to_bf16(xf * gf));
-      m = fmaxf(m, fabsf(u[i]));
+      m = max(m, __float_as_uint(fabsf(u[i])));
     }
-    const float s = __uint_as_float(row16_umax(__float_as_uint(m))) / 448.0f;
+    const float s = __uint_as_float(row16_umax(m)) / 448.0f;
     sc[it] = s;
     uint2 q = {0u, 0u};
     if (s > 0.f) {
@@ -171,12 +172,12 @@ __device__ __forceinline__ uint32_t source_row(const WideArgs& a, const RowTile&
   return (uint32_t)(s < a.picks ? a.order[s] >> 3 : s - a.picks);
 }
 
-// Stores a tile's sums.  codes: 17408 bytes of the block's LDS, mx: 4 floats a
+// Stores a tile's sums.  codes: 17408 bytes of the block's LDS, mx: 4 words a
 // row, which no wave uses any more.
 template <int U, bool UG>
 __device__ __forceinline__ void wide_store(const WideArgs& a, const RowTile& tile, int nb,
                                            const WideBlock& bl, float (&acc)[U][4][4],
-                                           uint8_t* codes, float* mx) {
+                                           uint8_t* codes, uint32_t* mx) {
   const int tid = threadIdx.x, lane = tid & 63, wn = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int col = lane & 15, g = lane >> 4;
   const int N = bl.N, n0 = bl.n0;
@@ -190,7 +191,7 @@ __device__ __forceinline__ void wide_store(const WideArgs& a, const RowTile& til
     // largest value over the 4 waves of the row
 #pragma unroll
     for (int i = 0; i < U; i++) {
-      float big = 0.f;
+      uint32_t big = 0u;  // by its bits, as for the activations
 #pragma unroll
       for (int j = 0; j < 2; j++)
 #pragma unroll
@@ -198,10 +199,10 @@ __device__ __forceinline__ void wide_store(const WideArgs& a, const RowTile& til
           const float gt = acc[i][j][v];
           const float mid = gt / (1.0f + __expf(-gt)) * acc[i][j + 2][v];
           acc[i][j][v] = mid;
-          big = fmaxf(big, fabsf(mid));
+          big = max(big, __float_as_uint(fabsf(mid)));
         }
-      big = fmaxf(big, __shfl_xor(big, 16, kWave));
-      big = fmaxf(big, __shfl_xor(big, 32, kWave));
+      big = max(big, (uint32_t)__shfl_xor((int)big, 16, kWave));
+      big = max(big, (uint32_t)__shfl_xor((int)big, 32, kWave));
       if (g == 0) mx[wn * 16 * U + i * 16 + col] = big;
     }
     __syncthreads();
@@ -209,7 +210,7 @@ __device__ __forceinline__ void wide_store(const WideArgs& a, const RowTile& til
 #pragma unroll
     for (int i = 0; i < U; i++) {
       const int m = i * 16 + col;
-      const float s = fmaxf(fmaxf(mx[m], mx[16 * U + m]), fmaxf(mx[32 * U + m], mx[48 * U + m])) / 448.0f;
+      const float s = __uint_as_float(max(max(mx[m], mx[16 * U + m]), max(mx[32 * U + m], mx[48 * U + m]))) / 448.0f;
 #pragma unroll
       for (int j = 0; j < 2; j++) {
         uint32_t q = 0u;
@@ -520,7 +521,7 @@ __device__ __forceinline__ void wide_tile(const WideArgs& a, const WideWeights& 
 #pragma unroll
     for (int v = 0; v < 4; v++) acc[U - 1][j][v] = fmaf(c[j][v], ap * sw_last[j >> 1], acc[U - 1][j][v]);
   wait_and_meet<0>();  // nothing under way into the LDS that the epilogue uses
-  wide_store<U, UG>(a, tile, nb, bl, acc, st0.w.b, reinterpret_cast<float*>(st1.w.b));
+  wide_store<U, UG>(a, tile, nb, bl, acc, st0.w.b, reinterpret_cast<uint32_t*>(st1.w.b));
 }
 
 // (256 threads a block; the bound of 512 keeps the compiler at 256 registers a

@@ -178,6 +178,65 @@ def test_against_the_definition(t, hidden, inter, experts, shared, mode):
     assert torch.equal(_run(layer, x, ids, gates), out)  # the same bits again
 
 
+def _check_definition(layer, x, ids, gates):
+    out = _run(layer, x, ids, gates)
+    torch.cuda.synchronize()
+    ref, tol = _reference(layer, x, ids, gates)
+    bound = tol + 2.0 ** -8 * (ref.abs() + tol)
+    err = (out.double() - ref).abs()
+    assert bool((err <= bound).all()), (int((err > bound).sum()), float((err - bound).max()))
+    assert float(err.norm()) <= P.OUT_TOL * float(ref.norm())
+
+
+# rows of an expert: every number of row tiles of 16, full, one short and one over
+COUNTS = [1, 15, 16, 17, 31, 32, 33, 47, 48, 49, 63, 64, 65, 79, 80, 81, 95, 96, 97, 111, 112, 113,
+          126, 127, 128, 129, 144, 191, 192, 193, 255, 257]
+
+
+@pytest.mark.parametrize("hidden,inter,shared", [(128, 128, False), (256, 256, True), (384, 640, False),
+                                                 (640, 384, True)])
+def test_every_number_of_rows_an_expert(hidden, inter, shared):
+    _say("wide rows", hidden, inter, shared)
+    experts = len(COUNTS)
+    flat = torch.repeat_interleave(torch.arange(experts), torch.tensor(COUNTS))
+    flat = torch.cat([flat, torch.full((-flat.numel() % 8,), -1)])
+    flat = flat[torch.randperm(flat.numel(), generator=torch.Generator().manual_seed(hidden))]
+    ids = flat.view(-1, 8).to(torch.int32).cuda()
+    layer = _layer(hidden, inter, experts, shared, seed=inter)
+    x = S.make_x(ids.shape[0], hidden, seed=inter + 1).cuda()
+    gates = torch.softmax(torch.randn(ids.shape, device="cuda", generator=torch.Generator("cuda").manual_seed(3)), 1)
+    _check_definition(layer, x, ids, torch.where(ids >= 0, gates, torch.zeros_like(gates)))
+
+
+@pytest.mark.parametrize("t,hidden,inter", [(20, 16384, 128), (20, 128, 16384), (160, 16384, 128),
+                                            (160, 128, 16384)])
+def test_the_longest_rows(t, hidden, inter):
+    _say("wide long", t, hidden, inter)
+    layer = _layer(hidden, inter, 16, True, seed=t)
+    x = S.make_x(t, hidden, seed=t + 1).cuda()
+    ids, gates = _routing(t, 16, "top", t + 2)
+    _check_definition(layer, x, ids, gates)
+
+
+@pytest.mark.parametrize("mode", ["top", "one"])
+def test_a_token_does_not_touch_the_others(mode):
+    """NaN and infinities of some tokens stay in their outputs."""
+    t, experts = 90, 16
+    layer = _layer(256, 256, experts, True, 31)
+    x = S.make_x(t, 256, seed=32).cuda()
+    ids, gates = _routing(t, experts, mode, 33)
+    out = _run(layer, x, ids, gates)
+    bad = x.clone()
+    bad[::7] = float("nan")
+    bad[1::7, 5] = float("inf")
+    got = _run(layer, bad, ids, gates)
+    torch.cuda.synchronize()
+    clean = torch.ones(t, dtype=torch.bool, device="cuda")
+    clean[::7] = clean[1::7] = False
+    assert torch.equal(got[clean], out[clean])
+    assert bool(torch.isnan(got[~clean]).all())
+
+
 def test_no_picks_and_no_shared_expert():
     layer = _layer(256, 128, 16, False, 3)
     x = S.make_x(33, 256, seed=4).cuda()
