@@ -273,9 +273,10 @@ __device__ __forceinline__ bool wide_place(const WideArgs& a, RowTile* tile, int
 // A load to LDS puts 16 bytes a lane at consecutive places, 1 KB in all, and
 // reads memory a line at a time only where neighbouring lanes read ascending
 // addresses.  So a kilobyte holds 8 pieces of 128 bytes, each of another row,
-// and starts 1056 bytes behind the one before: 16 rows' chunks that lie in 8
-// kilobytes of different index mod 8, or in 4 and half a kilobyte apart, are
-// read from distinct banks (lanes 0-3, 12-15 and 20-27 of a wave go together).
+// and starts 1056 bytes behind the one before.  The LDS reads lanes 0-3, 12-15
+// and 20-27 of a wave together (and so on): the chunks that these take, of rows
+// in 8 kilobytes in turn, or in 4 kilobytes and neighbouring pieces, lie in
+// distinct banks (1040 bytes apart, two and two shared one: 5% of the up/gate).
 constexpr int kKilo = 1056;
 
 // A wave's own 64 weight rows: kilobyte 8 wn + 4 h + q holds rows 32 wn + 16 j +
