@@ -276,7 +276,8 @@ __device__ __forceinline__ bool wide_place(const WideArgs& a, RowTile* tile, int
 // and starts 1056 bytes behind the one before.  The LDS reads lanes 0-3, 12-15
 // and 20-27 of a wave together (and so on): the chunks that these take, of rows
 // in 8 kilobytes in turn, or in 4 kilobytes and neighbouring pieces, lie in
-// distinct banks (1040 bytes apart, two and two shared one: 5% of the up/gate).
+// distinct banks (1040 bytes apart, two and two shared one: up/gate 1817 against
+// 1774 us).
 constexpr int kKilo = 1056;
 
 // A wave's own 64 weight rows: kilobyte 8 wn + 4 h + q holds rows 32 wn + 16 j +
