@@ -1,0 +1,130 @@
+"""How the experts' step of many rows (moe_wide_step) adds: in fp32 up to 24
+picks an expert, and for the shared expert's gate and up in every batch; by the
+FP8 MFMA for the rest of wider batches.
+
+The measure is rms(out - bf16(definition)) / rms(definition).  Rounding the
+definition as the kernel rounds its result takes that rounding out of it, and
+what is left are values that lie on the other side of a border between two
+codes: a relative error d of a sum moves the share 2 d / step of the quotients
+across one, by `step` of their value each, an rms of sqrt(2 d step), step <=
+2^-3 for E4M3 and <= 2^-7 for bf16.
+
+Limit of fp32 sums: d = 2^-21, eight fp32 roundings of 2^-24 (the sums' own, the
+scales, the row's rstd, SiLU): sqrt(2 * 2^-21 * 2^-3) = 3.5e-4 from mid and
+sqrt(2 * 2^-21 * 2^-7) = 0.9e-4 from the output; 7e-4 allows each twice.
+Limit of the FP8 MFMA: it drops 1.33e-5 of a sum (rms, measured on N(0, 1)
+blocks), gate and up together 1.9e-5: sqrt(2 * 1.9e-5 * 2^-3) = 2.2e-3; 2.5e-3
+with the output's sqrt(2 * 1.9e-5 * 2^-7) = 0.6e-3 in quadrature, and no factor.
+
+The bounds of single elements are tests/test_gpu_wide.py's, with the fp32 sums'
+own model in place of the FP8 MFMA's: 128 products in fp32 with truncation,
+128 * 2^-23 of their size.
+"""
+import pytest
+import torch
+
+from tests import test_gpu_wide as W
+
+pytestmark = pytest.mark.gpu
+
+U32 = 2.0 ** -24
+FP32_LIMIT, FP8_LIMIT = 7e-4, 2.5e-3
+
+
+def _power(e):
+    """2^e exactly, from the bits of a double."""
+    return ((e.long() + 1023) << 52).view(torch.float64)
+
+
+def _e4m3(v):
+    """Nearest E4M3 value, ties to the even mantissa (float64)."""
+    _, e = torch.frexp(v.abs())
+    step = _power((e - 1).clamp(min=-6) - 3)
+    return (torch.round(v / step) * step).clamp(-448.0, 448.0)
+
+
+def _fp32_product(h, w, nkb):
+    ref, terms = h @ w.t(), h.abs() @ w.abs().t()
+    return ref, (128 * 2.0 ** -23 + (nkb + 7) * U32) * terms
+
+
+@pytest.fixture
+def exact_codes(monkeypatch):
+    monkeypatch.setattr(W, "_e4m3", _e4m3)
+
+
+def _case(t, hidden, inter, experts, shared, mode, seed):
+    layer = W._layer(hidden, inter, experts, shared, seed)
+    x = W.S.make_x(t, hidden, seed=seed + 1).cuda()
+    ids, gates = W._routing(t, experts, "top" if mode == "skewed" else mode, seed + 2)
+    if mode == "skewed":  # most tokens pick expert 0, whose rows pass a half tile
+        ids[: (4 * t) // 5, 0] = 0
+    return layer, x, ids, gates
+
+
+def _apart(out, ref):
+    return float((out.double() - ref.to(torch.bfloat16).double()).norm() / ref.norm())
+
+
+@pytest.mark.parametrize("t,hidden,inter,experts,shared,mode", [
+    (16, 2048, 1024, 32, True, "top"), (96, 2048, 1024, 32, True, "skewed"),
+    (96, 1024, 512, 32, False, "skewed"), (48, 512, 256, 16, True, "dropped")])
+def test_few_picks_an_expert(exact_codes, monkeypatch, t, hidden, inter, experts, shared, mode):
+    print("wide sums", t, hidden, inter, experts, shared, mode, flush=True)
+    assert t * 8 <= 24 * experts
+    monkeypatch.setattr(W, "_product", _fp32_product)
+    layer, x, ids, gates = _case(t, hidden, inter, experts, shared, mode, t + hidden)
+    out = W._run(layer, x, ids, gates)
+    torch.cuda.synchronize()
+    safe = torch.where((ids >= 0) & (ids < experts), gates, torch.zeros_like(gates))
+    ref, tol = W._reference(layer, x, ids, safe)
+    bound = tol + 2.0 ** -8 * (ref.abs() + tol)
+    err = (out.double() - ref).abs()
+    assert bool((err <= bound).all()), (int((err > bound).sum()), float((err - bound).max()))
+    apart = _apart(out, ref)
+    print("apart", apart, flush=True)
+    assert apart <= FP32_LIMIT
+
+
+@pytest.mark.parametrize("t", [130, 300])
+def test_the_shared_expert_of_any_batch(exact_codes, t):
+    """No pick is in a group: the outputs are the shared expert's, whose gate
+    and up are summed in fp32 in batches of more than 24 picks an expert too.
+    Its down is the FP8 MFMA's, 1.33e-5 off: sqrt(2 * 1.33e-5 * 2^-7) = 4.6e-4
+    from the output's rounding instead of 0.9e-4, twice that in quadrature with
+    twice 3.5e-4."""
+    assert t * 8 > 24 * 16
+    layer, x, ids, gates = _case(t, 2048, 1024, 16, True, "none", t)
+    out = W._run(layer, x, ids, gates)
+    torch.cuda.synchronize()
+    ref, _ = W._reference(layer, x, ids, gates)
+    apart = _apart(out, ref)
+    print("apart", apart, flush=True)
+    assert apart <= 1.16e-3
+
+
+@pytest.mark.parametrize("t,shared", [(200, False), (300, True)])
+def test_many_picks_an_expert(exact_codes, t, shared):
+    layer, x, ids, gates = _case(t, 1024, 512, 16, shared, "top", t)
+    out = W._run(layer, x, ids, gates)
+    torch.cuda.synchronize()
+    ref, _ = W._reference(layer, x, ids, gates)
+    apart = _apart(out, ref)
+    print("apart", apart, flush=True)
+    assert apart <= FP8_LIMIT
+
+
+@pytest.mark.parametrize("t,more,experts", [(20, 37, 32), (150, 333, 16)])
+def test_a_tokens_bits_in_two_batches(t, more, experts):
+    """Batches on the same side of 24 picks an expert: the first tokens' results
+    are the same bits alone and among others, at other places in the sorted
+    order and in tiles of other sizes."""
+    layer, x, ids, gates = _case(t + more, 512, 384, experts, True, "top", 7 * t)
+    both = W._run(layer, x, ids, gates)
+    alone = W._run(layer, x[:t].contiguous(), ids[:t].contiguous(), gates[:t].contiguous())
+    at = torch.randperm(t + more, generator=torch.Generator().manual_seed(t)).cuda()
+    moved = W._run(layer, x[at].contiguous(), ids[at].contiguous(), gates[at].contiguous())
+    torch.cuda.synchronize()
+    as_bits = lambda v: v.view(torch.int16)  # noqa: E731
+    assert torch.equal(as_bits(both[:t]), as_bits(alone))
+    assert torch.equal(as_bits(both[at]), as_bits(moved))
