@@ -214,10 +214,21 @@ __global__ __launch_bounds__(256, 2) void lora_shrink_tile_kernel(
   }
 }
 
+// v as two bf16 parts of its sign, v = hi + lo within 2^-16 of it: hi is v's
+// leading 8 bits.  An infinity in B has to give v's infinity, so where nothing
+// is left for lo (inf * 0 is a NaN) it is 2^-24 of hi, less than a rounding of
+// v (0 for a v below 2^-102 at most, and for 0), and 1 beside an infinity.
+__device__ __forceinline__ void split_bf16(float v, uint16_t* hi, uint16_t* lo) {
+  *hi = (uint16_t)(__float_as_uint(v) >> 16);
+  const float h = bf16_to_f32(*hi), left = v - h;
+  *lo = f32_to_bf16(left == 0.f ? h * 0x1p-24f : left);
+  if ((*hi & 0x7F80u) == 0x7F80u) *lo = (*hi & 0x8000u) | 0x3F80u;
+}
+
 // y = bf16(base + B v) of a tile's 32 rows over a part of N, 64 outputs a wave
 // at a time.  v (its K parts added in order, times scale) is split into two
-// bf16 parts, v = hi + lo within 2^-16 of it (one part alone: 2^-8, as much as
-// the result's own rounding): two MFMAs for one.  The products go back through
+// bf16 parts (one part alone: 2^-8, as much as the result's own rounding): two
+// MFMAs for one.  The products go back through
 // the wave's LDS area to lanes that hold 8 outputs of one row.  RS: K steps of 32 ranks; the ranks
 // past the adapter's are zero in both operands.
 // 6001 rows of 6144, 24 adapters: 38 us at rank 16, 50 at rank 64; base and y
@@ -299,9 +310,7 @@ __global__ __launch_bounds__(256, 2) void lora_expand_tile_kernel(
 #pragma unroll
     for (int c = 0; c < 4; c++) {
       const float v = r + c < rank ? s[c] * scale : 0.f;
-      hi[c] = f32_to_bf16(v);
-      // nothing is left of an infinity or a NaN (inf - inf would be a NaN)
-      lo[c] = (hi[c] & 0x7F80u) == 0x7F80u ? 0 : f32_to_bf16(v - bf16_to_f32(hi[c]));
+      split_bf16(v, &hi[c], &lo[c]);
     }
     *reinterpret_cast<uint2*>(&sv[0][m][r]) =
         uint2{hi[0] | (uint32_t)hi[1] << 16, hi[2] | (uint32_t)hi[3] << 16};
