@@ -54,11 +54,10 @@ struct LoraRows {
       rank[tid] = on ? lora_rank(l, i) : 0;
     }
   }
-  // What row r's adapter adds at output n: sum_j B[n, j] v[j] over the
-  // adapter's ranks, 8 at a time; B past them is not used, whatever it holds.
+  // What the adapter of row r, which has one, adds at output n: sum_j B[n, j]
+  // v[j] over its ranks, 8 at a time; B past them is not used, whatever it holds.
   __device__ __forceinline__ float term(const LoraArgs& l, int r, int n) const {
     const int i = id[r], rk = rank[r];
-    if (i < 0) return 0.f;
     const uint16_t* b = l.b + ((size_t)i * l.n + n) * l.max_rank;
     const float* vr = v + r * l.max_rank;
     float s = 0.f;
@@ -95,7 +94,7 @@ struct GemvTail<true> {
     rows.load(l, n_rows, tid, threads);
   }
   __device__ __forceinline__ float add(float v, int r, int n, const Rows& rows) const {
-    return v + rows.term(l, r, n);
+    return rows.id[r] < 0 ? v : v + rows.term(l, r, n);  // (-0 + 0 would be 0)
   }
 };
 

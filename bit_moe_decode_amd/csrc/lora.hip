@@ -53,14 +53,17 @@ __global__ __launch_bounds__(256) void lora_expand_kernel(LoraArgs l, const uint
   const int r = blockIdx.x, tid = threadIdx.x;
   const int n = blockIdx.y * 256 + tid;
   const size_t at = (size_t)r * l.n + n;
-  const float b = n < l.n ? bf16_to_f32(base[at]) : 0.f;
+  const uint16_t b = n < l.n ? base[at] : 0;
   LoraArgs one = l;
   one.ids = l.ids + r;
   one.v = l.v + (size_t)r * l.max_rank;
   rows.load(one, 1, tid, 256);
   __syncthreads();
-  if (n >= l.n || (rows.id[0] < 0 && y == base)) return;
-  y[at] = f32_to_bf16(b + rows.term(one, 0, n));
+  if (n >= l.n) return;
+  if (rows.id[0] >= 0)
+    y[at] = f32_to_bf16(bf16_to_f32(b) + rows.term(one, 0, n));
+  else if (y != base)
+    y[at] = b;
 }
 
 // ---------------------------------------------------------------- many rows
