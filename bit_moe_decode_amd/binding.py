@@ -313,21 +313,12 @@ def lowbit_gemv_status(blocks, x, y, n, k, rows=1, stream=None, fmt=FMT_Q1):
     return lib().lowbit_gemv(ctypes.byref(m), _ptr(x), int(rows), _ptr(y), _stream(stream))
 
 
-def make_matrix(fmt, n, k, codes, scales=None) -> LowbitMatrix:
-    """LowbitMatrix struct of a weight [n, k] in one of lowbit_gemv's formats.
-    The struct keeps the tensors alive."""
-    if scales is not None and scales.get_device() != codes.get_device():
-        _refuse("make_matrix", "codes and scales are on different devices")
-    m = LowbitMatrix(int(fmt), int(n), int(k), codes.data_ptr(), _address(scales))
-    m.tensors, m.device = (codes, scales), codes.get_device()
-    return m
-
-
 # ------------------------------------------------ tokens sorted by expert and back
 MAX_TOP_K = 16             # MOE_MAX_TOP_K
 WIDE_MAX_TOKENS = 65536    # MOE_WIDE_MAX_TOKENS
 LORA_MAX_ROWS = 1 << 20    # MOE_LORA_MAX_ROWS
 _I32, _BF16, _F32 = torch.int32, torch.bfloat16, torch.float32
+_BYTES = (torch.uint8, torch.float8_e4m3fn)  # FP8 codes, as either
 _ROW_DTYPES = {_BF16: 0, _F32: 1}  # moe_dtype
 
 
@@ -348,6 +339,16 @@ def _check(what, device, *tensors):
                               or t.get_device() != device):
             _refuse(what, f"{name} is not a contiguous {dtype} {tuple(shape)} on device {device}: "
                           f"{t.dtype} {tuple(t.shape)} with strides {t.stride()} on {t.device}")
+
+
+def _laid_out(what, *tensors):
+    """Every (name, tensor, dtype or dtypes, shape) is a contiguous tensor of
+    that dtype and shape, on whatever device."""
+    for name, t, dtype, shape in tensors:
+        if t is None or (t.dtype not in dtype if isinstance(dtype, tuple) else t.dtype is not dtype) \
+                or t.shape != shape or not t.is_contiguous():
+            is_ = "missing" if t is None else f"{t.dtype} {tuple(t.shape)} with strides {t.stride()}"
+            _refuse(what, f"{name} is not a contiguous {dtype} {tuple(shape)}: {is_}")
 
 
 def _done(st, what):
@@ -372,6 +373,25 @@ def _on(what, name, struct, device):
     """A struct made from tensors (make_matrix, make_lora) has them on `device`."""
     if getattr(struct, "device", device) != device:
         _refuse(what, f"{name} is not on device {device}")
+
+
+def make_matrix(fmt, n, k, codes, scales=None) -> LowbitMatrix:
+    """LowbitMatrix struct of a weight [n, k] in one of lowbit_gemv's formats:
+    codes uint8 [n, k/128, 18] (1-bit), uint8 or float8_e4m3fn [n, k] with scales
+    float32 [n/128, k/128] (FP8), or bfloat16 [n, k].  The struct keeps the
+    tensors alive."""
+    if fmt == FMT_Q1:
+        _laid_out("make_matrix", ("codes", codes, _BYTES, (n, k // 128, 18)))
+    elif fmt == FMT_FP8:
+        _laid_out("make_matrix", ("codes", codes, _BYTES, (n, k)),
+                  ("scales", scales, _F32, (n // 128, k // 128)))
+    elif fmt == FMT_BF16:
+        _laid_out("make_matrix", ("codes", codes, _BF16, (n, k)))
+    if scales is not None and scales.get_device() != codes.get_device():
+        _refuse("make_matrix", "codes and scales are on different devices")
+    m = LowbitMatrix(int(fmt), int(n), int(k), codes.data_ptr(), _address(scales))
+    m.tensors, m.device = (codes, scales), codes.get_device()
+    return m
 
 
 def moe_sort_workspace_size(tokens, top_k, n_experts) -> int:
