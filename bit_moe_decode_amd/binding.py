@@ -262,8 +262,9 @@ def step_noalloc_status(cfg: Config, x, rows, weights: Weights, out, stream=None
 def make_weights(gamma, router_w, routed, shared=None) -> Weights:
     """Weights struct from device tensors: routed/shared are (gate, up, down)
     tuples of (codes, scales) tensors in canonical layout; router_w may be None
-    for moe_wide_step."""
+    for moe_wide_step.  The struct keeps the tensors alive."""
     w = Weights()
+    w.tensors = (gamma, router_w, tuple(routed), None if shared is None else tuple(shared))
     w.rms_gamma = gamma.data_ptr()
     w.router_w = None if router_w is None else router_w.data_ptr()
     for name, (c, s) in zip(("gate", "up", "down"), routed):
@@ -464,10 +465,36 @@ def moe_wide_workspace_size(cfg: Config, tokens) -> int:
     return lib().moe_wide_workspace_size(ctypes.byref(cfg), int(tokens))
 
 
+def _wide_weights(cfg: Config, weights: Weights, device):
+    """Weights from make_weights are cfg's FP8 matrices, on `device`."""
+    if not hasattr(weights, "tensors") or cfg.routed_fmt != FMT_FP8:
+        return
+    gamma, _, routed, shared = weights.tensors
+    h = cfg.hidden
+    _laid_out("moe_wide_step", ("gamma", gamma, _BF16, (h,)))
+    if cfg.shared_inter > 0 and shared is None:
+        _refuse("moe_wide_step", "the weights have no shared expert")
+    sets = [("", routed, cfg.n_experts, cfg.inter)]
+    if cfg.shared_inter > 0:
+        sets.append(("shared ", shared, 1, cfg.shared_inter))
+    tensors = [gamma]
+    for kind, mats, experts, inter in sets:
+        for name, (c, s), (n, k) in zip(("gate", "up", "down"), mats, ((inter, h), (inter, h), (h, inter))):
+            for part, t, dtype, shape in (("codes", c, _BYTES, (n, k)), ("scales", s, _F32, (n // 128, k // 128))):
+                # (the shared expert's may lack the leading dimension of 1)
+                one = kind and t is not None and t.dim() == 2
+                _laid_out("moe_wide_step", (f"{kind}{name} {part}", t, dtype, shape if one else (experts, *shape)))
+                tensors.append(t)
+    if any(t.get_device() != device for t in tensors):
+        _refuse("moe_wide_step", f"the weights are not on device {device}")
+
+
 def moe_wide_step(cfg: Config, x, ids, gates, weights: Weights, out, workspace, stream=None):
     """The experts' step for any number of rows with given routing: x and out
-    bf16 [T, H], ids int32 [T, 8], gates float32 [T, 8]."""
+    bf16 [T, H], ids int32 [T, 8], gates float32 [T, 8]; weights from
+    make_weights have to be cfg's."""
     t = x.shape[0]
+    _wide_weights(cfg, weights, x.get_device())
     _check("moe_wide_step", x.get_device(), ("x", x, _BF16, (t, cfg.hidden)),
            ("ids", ids, _I32, (t, 8)), ("gates", gates, _F32, (t, 8)),
            ("out", out, _BF16, (t, cfg.hidden)))

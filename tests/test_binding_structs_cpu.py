@@ -1,5 +1,9 @@
 """The binding's structs of weights refuse tensors that the kernels would read
-past or misread: make_matrix.  No kernel runs."""
+past or misread: make_matrix, and moe_wide_step for make_weights'.  No kernel
+runs."""
+import gc
+import weakref
+
 import pytest
 import torch
 
@@ -39,3 +43,76 @@ def test_matrices_that_are_refused(fmt, codes, scales):
     with pytest.raises(B.MoeError) as e:
         B.make_matrix(fmt, 256, 384, codes, scales)
     assert e.value.status == B.MOE_ERR_INVALID_ARG
+
+
+H, I, E, SHARED = 256, 384, 16, 384
+
+
+def weights(shared=True, **kw):
+    """make_weights of a small layer; kw replaces tensors: gamma, gate_c, sh_down_s, .."""
+    def mats(pre, lead):
+        out = []
+        for name, n, k in (("gate", I, H), ("up", I, H), ("down", H, I)):
+            out.append((kw.get(f"{pre}{name}_c", z(U8, *lead, n, k)),
+                        kw.get(f"{pre}{name}_s", z(F32, *lead, n // 128, k // 128))))
+        return out
+    return B.make_weights(kw.get("gamma", z(BF, H)), None, mats("", (E,)), mats("sh_", (1,)) if shared else None)
+
+
+def wide(w, shared=SHARED, **kw):
+    """The error of a call on the CPU, where every call is refused."""
+    c = dict(hidden=H, inter=I, n_experts=E, top_k=8, shared_inter=shared, max_rows=8, rms_eps=1e-6,
+             routed_fmt=B.FMT_FP8, shared_fmt=B.FMT_FP8, flags=0, act_fmt=B.ACT_FP8)
+    c.update(kw)
+    x = z(BF, 20, c["hidden"])
+    with pytest.raises(B.MoeError) as e:
+        B.moe_wide_step(B.Config(*c.values()), x, z(torch.int32, 20, 8), z(F32, 20, 8), w, z(BF, 20, c["hidden"]), None)
+    assert e.value.status == B.MOE_ERR_INVALID_ARG
+    return str(e.value)
+
+
+ONLY_DEVICE = "not on the current device"  # all that is wrong with a call on the CPU
+
+
+def test_wide_weights():
+    assert ONLY_DEVICE in wide(weights())
+    assert ONLY_DEVICE in wide(weights(shared=False), shared=0)
+    assert ONLY_DEVICE in wide(weights(gate_c=z(F8, E, I, H)))
+    one = dict(sh_gate_c=z(U8, I, H), sh_up_c=z(U8, I, H), sh_down_c=z(U8, H, I), sh_gate_s=z(F32, 3, 2),
+               sh_up_s=z(F32, 3, 2), sh_down_s=z(F32, 2, 3))
+    assert ONLY_DEVICE in wide(weights(**one))
+    assert ONLY_DEVICE in wide(B.Weights())  # addresses alone: the caller's word
+
+
+@pytest.mark.parametrize("name,t", [
+    ("gamma", z(BF, H - 8)), ("gamma", z(F32, H)), ("gate_c", z(U8, E, H, I)), ("gate_c", z(U8, E - 1, I, H)),
+    ("gate_c", z(U8, E * I, H)), ("up_c", z(U8, E, H, I).transpose(1, 2)), ("up_c", z(BF, E, I, H)),
+    ("down_c", z(U8, E, H, I + 128)[..., :I]), ("gate_s", None), ("up_s", z(F32, E, 2, 3)),
+    ("down_s", z(torch.float64, E, 2, 3)), ("sh_gate_c", z(U8, 1, H, I)), ("sh_up_s", None),
+    ("sh_down_c", z(U8, H, I - 128)), ("sh_down_s", z(F32, 2, 2))])
+def test_wide_weights_that_are_refused(name, t):
+    e = wide(weights(**{name: t})) if t is not None or "sh_" not in name else None
+    if e is None:  # make_weights itself takes no shared matrix without scales
+        with pytest.raises(AttributeError):
+            weights(**{name: t})
+    else:
+        assert ONLY_DEVICE not in e and "is not a contiguous" in e
+
+
+def test_wide_weights_of_another_layer():
+    assert ONLY_DEVICE not in wide(weights(), n_experts=32)
+    assert ONLY_DEVICE not in wide(weights(), hidden=512)
+    assert ONLY_DEVICE not in wide(weights(), inter=256, shared=256)
+    assert "no shared expert" in wide(weights(shared=False))
+
+
+def test_structs_keep_their_tensors():
+    codes = z(U8, E, I, H)
+    gone = weakref.ref(codes)
+    w = weights(gate_c=codes)
+    del codes
+    gc.collect()
+    assert gone() is not None and w.gate.codes == gone().data_ptr()
+    del w
+    gc.collect()
+    assert gone() is None
