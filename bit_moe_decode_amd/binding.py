@@ -8,8 +8,6 @@ import ctypes
 import os
 import re
 
-import torch
-
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libbit_moe_decode.so")
 HEADER = os.path.join(os.path.dirname(HERE), "include", "moe_decode.h")
@@ -24,6 +22,19 @@ F_NO_DEDUP = 1 << 1
 N_KERNELS = 5
 K_UPGATE, K_DOWN = 2, 3  # kernels moe_decode_relaunch repeats
 KERNEL_NAMES = ("router", "route", "upgate", "down", "combine")  # launch order
+
+
+class _Torch:
+    """torch's attributes, looked up when first used: this module loads without
+    torch."""
+
+    def __getattr__(self, name):
+        import torch
+        setattr(self, name, getattr(torch, name))
+        return getattr(self, name)
+
+
+_torch = _Torch()
 
 
 class MoeError(RuntimeError):
@@ -318,9 +329,6 @@ def lowbit_gemv_status(blocks, x, y, n, k, rows=1, stream=None, fmt=FMT_Q1):
 MAX_TOP_K = 16             # MOE_MAX_TOP_K
 WIDE_MAX_TOKENS = 65536    # MOE_WIDE_MAX_TOKENS
 LORA_MAX_ROWS = 1 << 20    # MOE_LORA_MAX_ROWS
-_I32, _BF16, _F32 = torch.int32, torch.bfloat16, torch.float32
-_BYTES = (torch.uint8, torch.float8_e4m3fn)  # FP8 codes, as either
-_ROW_DTYPES = {_BF16: 0, _F32: 1}  # moe_dtype
 
 
 def _refuse(what, why):
@@ -333,13 +341,17 @@ def _check(what, device, *tensors):
     """Every (name, tensor, dtype, shape) -- a tensor may be None -- is
     contiguous, on `device` and of that dtype and shape; `device` is the
     current one."""
-    if device < 0 or device != torch.cuda.current_device():
+    if device < 0 or device != _torch.cuda.current_device():
         _refuse(what, "the tensors are not on the current device")
     for name, t, dtype, shape in tensors:
         if t is not None and (t.dtype is not dtype or t.shape != shape or not t.is_contiguous()
                               or t.get_device() != device):
             _refuse(what, f"{name} is not a contiguous {dtype} {tuple(shape)} on device {device}: "
                           f"{t.dtype} {tuple(t.shape)} with strides {t.stride()} on {t.device}")
+
+
+def _byte_types():
+    return _torch.uint8, _torch.float8_e4m3fn  # FP8 codes, as either
 
 
 def _laid_out(what, *tensors):
@@ -382,12 +394,12 @@ def make_matrix(fmt, n, k, codes, scales=None) -> LowbitMatrix:
     float32 [n/128, k/128] (FP8), or bfloat16 [n, k].  The struct keeps the
     tensors alive."""
     if fmt == FMT_Q1:
-        _laid_out("make_matrix", ("codes", codes, _BYTES, (n, k // 128, 18)))
+        _laid_out("make_matrix", ("codes", codes, _byte_types(), (n, k // 128, 18)))
     elif fmt == FMT_FP8:
-        _laid_out("make_matrix", ("codes", codes, _BYTES, (n, k)),
-                  ("scales", scales, _F32, (n // 128, k // 128)))
+        _laid_out("make_matrix", ("codes", codes, _byte_types(), (n, k)),
+                  ("scales", scales, _torch.float32, (n // 128, k // 128)))
     elif fmt == FMT_BF16:
-        _laid_out("make_matrix", ("codes", codes, _BF16, (n, k)))
+        _laid_out("make_matrix", ("codes", codes, _torch.bfloat16, (n, k)))
     if scales is not None and scales.get_device() != codes.get_device():
         _refuse("make_matrix", "codes and scales are on different devices")
     m = LowbitMatrix(int(fmt), int(n), int(k), codes.data_ptr(), _address(scales))
@@ -404,15 +416,16 @@ def moe_sort(ids, n_experts, offsets, order, pos, workspace=None, stream=None):
     [n_experts + 1], order int32 [T k], pos int32 [T, k]; workspace: a device
     tensor of moe_sort_workspace_size bytes (None where that is 0)."""
     t, k = ids.shape
-    _check("moe_sort", ids.get_device(), ("ids", ids, _I32, (t, k)), ("offsets", offsets, _I32, (n_experts + 1,)),
-           ("order", order, _I32, (t * k,)), ("pos", pos, _I32, (t, k)))
+    _check("moe_sort", ids.get_device(), ("ids", ids, _torch.int32, (t, k)),
+           ("offsets", offsets, _torch.int32, (n_experts + 1,)),
+           ("order", order, _torch.int32, (t * k,)), ("pos", pos, _torch.int32, (t, k)))
     ws, n = _space("moe_sort", workspace, ids.get_device())
     _done(lib().moe_sort(ids.data_ptr(), t, k, int(n_experts), offsets.data_ptr(), order.data_ptr(),
                          pos.data_ptr(), ws, n, _stream(stream)), "moe_sort")
 
 
 def _row_shape(what, rows, pos):
-    dtype = _ROW_DTYPES.get(rows.dtype)
+    dtype = {_torch.bfloat16: 0, _torch.float32: 1}.get(rows.dtype)  # moe_dtype
     if dtype is None:
         _refuse(what, f"rows of {rows.dtype}")
     t, k = pos.shape
@@ -422,7 +435,7 @@ def _row_shape(what, rows, pos):
 def moe_gather(x, pos, xs, stream=None):
     """xs[pos[t, j]] = x[t]: x [T, H], pos int32 [T, k] (moe_sort's), xs [rows, H]."""
     t, k, h, shape = _row_shape("moe_gather", xs, pos)
-    _check("moe_gather", xs.get_device(), ("x", x, xs.dtype, (t, h)), ("pos", pos, _I32, (t, k)),
+    _check("moe_gather", xs.get_device(), ("x", x, xs.dtype, (t, h)), ("pos", pos, _torch.int32, (t, k)),
            ("xs", xs, xs.dtype, (xs.shape[0], h)))
     _done(lib().moe_gather(shape, x.data_ptr(), pos.data_ptr(), xs.data_ptr(), _stream(stream)),
           "moe_gather")
@@ -432,7 +445,7 @@ def moe_gather_backward(dxs, pos, dx, stream=None):
     """dx[t] = sum_j dxs[pos[t, j]]: dxs [rows, H], dx [T, H]."""
     t, k, h, shape = _row_shape("moe_gather_backward", dxs, pos)
     _check("moe_gather_backward", dxs.get_device(), ("dx", dx, dxs.dtype, (t, h)),
-           ("pos", pos, _I32, (t, k)), ("dxs", dxs, dxs.dtype, (dxs.shape[0], h)))
+           ("pos", pos, _torch.int32, (t, k)), ("dxs", dxs, dxs.dtype, (dxs.shape[0], h)))
     _done(lib().moe_gather_backward(shape, dxs.data_ptr(), pos.data_ptr(), dx.data_ptr(),
                                     _stream(stream)), "moe_gather_backward")
 
@@ -442,7 +455,7 @@ def moe_combine(y, pos, gates, out, add=None, stream=None):
     float32 [T, k], out and add [T, H]."""
     t, k, h, shape = _row_shape("moe_combine", y, pos)
     _check("moe_combine", y.get_device(), ("y", y, y.dtype, (y.shape[0], h)),
-           ("pos", pos, _I32, (t, k)), ("gates", gates, _F32, (t, k)),
+           ("pos", pos, _torch.int32, (t, k)), ("gates", gates, _torch.float32, (t, k)),
            ("out", out, y.dtype, (t, h)), ("add", add, y.dtype, (t, h)))
     _done(lib().moe_combine(shape, y.data_ptr(), pos.data_ptr(), gates.data_ptr(), _address(add),
                             out.data_ptr(), _stream(stream)), "moe_combine")
@@ -453,9 +466,9 @@ def moe_combine_backward(dout, y, pos, gates, dy, dgates, stream=None):
     dout [T, H], y and dy [rows, H], gates and dgates float32 [T, k]."""
     t, k, h, shape = _row_shape("moe_combine_backward", y, pos)
     _check("moe_combine_backward", y.get_device(), ("dout", dout, y.dtype, (t, h)),
-           ("y", y, y.dtype, (y.shape[0], h)), ("pos", pos, _I32, (t, k)),
-           ("gates", gates, _F32, (t, k)), ("dy", dy, y.dtype, (y.shape[0], h)),
-           ("dgates", dgates, _F32, (t, k)))
+           ("y", y, y.dtype, (y.shape[0], h)), ("pos", pos, _torch.int32, (t, k)),
+           ("gates", gates, _torch.float32, (t, k)), ("dy", dy, y.dtype, (y.shape[0], h)),
+           ("dgates", dgates, _torch.float32, (t, k)))
     _done(lib().moe_combine_backward(shape, dout.data_ptr(), y.data_ptr(), pos.data_ptr(),
                                      gates.data_ptr(), dy.data_ptr(), dgates.data_ptr(),
                                      _stream(stream)), "moe_combine_backward")
@@ -471,7 +484,7 @@ def _wide_weights(cfg: Config, weights: Weights, device):
         return
     gamma, _, routed, shared = weights.tensors
     h = cfg.hidden
-    _laid_out("moe_wide_step", ("gamma", gamma, _BF16, (h,)))
+    _laid_out("moe_wide_step", ("gamma", gamma, _torch.bfloat16, (h,)))
     if cfg.shared_inter > 0 and shared is None:
         _refuse("moe_wide_step", "the weights have no shared expert")
     sets = [("", routed, cfg.n_experts, cfg.inter)]
@@ -480,7 +493,8 @@ def _wide_weights(cfg: Config, weights: Weights, device):
     tensors = [gamma]
     for kind, mats, experts, inter in sets:
         for name, (c, s), (n, k) in zip(("gate", "up", "down"), mats, ((inter, h), (inter, h), (h, inter))):
-            for part, t, dtype, shape in (("codes", c, _BYTES, (n, k)), ("scales", s, _F32, (n // 128, k // 128))):
+            for part, t, dtype, shape in (("codes", c, _byte_types(), (n, k)),
+                                          ("scales", s, _torch.float32, (n // 128, k // 128))):
                 # (the shared expert's may lack the leading dimension of 1)
                 one = kind and t is not None and t.dim() == 2
                 _laid_out("moe_wide_step", (f"{kind}{name} {part}", t, dtype, shape if one else (experts, *shape)))
@@ -495,9 +509,9 @@ def moe_wide_step(cfg: Config, x, ids, gates, weights: Weights, out, workspace, 
     make_weights have to be cfg's."""
     t = x.shape[0]
     _wide_weights(cfg, weights, x.get_device())
-    _check("moe_wide_step", x.get_device(), ("x", x, _BF16, (t, cfg.hidden)),
-           ("ids", ids, _I32, (t, 8)), ("gates", gates, _F32, (t, 8)),
-           ("out", out, _BF16, (t, cfg.hidden)))
+    _check("moe_wide_step", x.get_device(), ("x", x, _torch.bfloat16, (t, cfg.hidden)),
+           ("ids", ids, _torch.int32, (t, 8)), ("gates", gates, _torch.float32, (t, 8)),
+           ("out", out, _torch.bfloat16, (t, cfg.hidden)))
     ws, n = _space("moe_wide_step", workspace, x.get_device())
     _done(lib().moe_wide_step(ctypes.byref(cfg), x.data_ptr(), t, ids.data_ptr(), gates.data_ptr(),
                               ctypes.byref(weights), out.data_ptr(), ws, n, _stream(stream)),
@@ -511,9 +525,9 @@ def make_lora(a, b, scale, rank=None) -> LoraSet:
     [n_adapters] or None.  The struct keeps the tensors alive."""
     n_adapters, max_rank, k = a.shape
     n = b.shape[1]
-    _check("make_lora", a.get_device(), ("a", a, _BF16, (n_adapters, max_rank, k)),
-           ("b", b, _BF16, (n_adapters, n, max_rank)),
-           ("scale", scale, _F32, (n_adapters,)), ("rank", rank, _I32, (n_adapters,)))
+    _check("make_lora", a.get_device(), ("a", a, _torch.bfloat16, (n_adapters, max_rank, k)),
+           ("b", b, _torch.bfloat16, (n_adapters, n, max_rank)),
+           ("scale", scale, _torch.float32, (n_adapters,)), ("rank", rank, _torch.int32, (n_adapters,)))
     s = LoraSet(n_adapters, max_rank, n, k, a.data_ptr(), b.data_ptr(), _address(rank),
                 scale.data_ptr())
     s.tensors, s.device = (a, b, scale, rank), a.get_device()
@@ -527,8 +541,8 @@ def lora_workspace_size(lora: LoraSet, rows) -> int:
 def lora_apply(lora: LoraSet, x, ids, base, y, workspace, stream=None):
     """y[r] = base[r] + scale_i B_i (A_i x[r]), i = ids[r]: x bf16 [rows, k], ids
     int32 [rows], base and y bf16 [rows, n] (y may be base)."""
-    r, bf = x.shape[0], _BF16
-    _check("lora_apply", x.get_device(), ("x", x, bf, (r, lora.k)), ("ids", ids, _I32, (r,)),
+    r, bf = x.shape[0], _torch.bfloat16
+    _check("lora_apply", x.get_device(), ("x", x, bf, (r, lora.k)), ("ids", ids, _torch.int32, (r,)),
            ("base", base, bf, (r, lora.n)), ("y", y, bf, (r, lora.n)))
     _on("lora_apply", "lora", lora, x.get_device())
     ws, n = _space("lora_apply", workspace, x.get_device())
@@ -539,8 +553,8 @@ def lora_apply(lora: LoraSet, x, ids, base, y, workspace, stream=None):
 def lowbit_gemv_lora(matrix: LowbitMatrix, lora: LoraSet, x, ids, y, workspace, stream=None):
     """lowbit_gemv of 0..8 rows with the rows' adapters added before the
     rounding: x bf16 [rows, k], ids int32 [rows], y bf16 [rows, n]."""
-    r, bf = x.shape[0], _BF16
-    _check("lowbit_gemv_lora", x.get_device(), ("x", x, bf, (r, matrix.k)), ("ids", ids, _I32, (r,)),
+    r, bf = x.shape[0], _torch.bfloat16
+    _check("lowbit_gemv_lora", x.get_device(), ("x", x, bf, (r, matrix.k)), ("ids", ids, _torch.int32, (r,)),
            ("y", y, bf, (r, matrix.n)))
     _on("lowbit_gemv_lora", "lora", lora, x.get_device())
     _on("lowbit_gemv_lora", "matrix", matrix, x.get_device())

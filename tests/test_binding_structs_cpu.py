@@ -2,6 +2,9 @@
 past or misread: make_matrix, and moe_wide_step for make_weights'.  No kernel
 runs."""
 import gc
+import os
+import subprocess
+import sys
 import weakref
 
 import pytest
@@ -116,3 +119,16 @@ def test_structs_keep_their_tensors():
     del w
     gc.collect()
     assert gone() is None
+
+
+def test_the_binding_loads_without_torch():
+    """As far as it takes no tensors: the library, its sizes, its statuses."""
+    code = ("import sys; sys.modules['torch'] = None\n"
+            "from bit_moe_decode_amd import binding as B\n"
+            "c = B.Config(256, 128, 32, 8, 0, 8, 1e-6, B.FMT_FP8, B.FMT_FP8, 0, B.ACT_FP8)\n"
+            "assert B.workspace_size(c) > 0 and B.moe_wide_workspace_size(c, 20) > 0\n"
+            "assert 'ok' in B.status_string(B.MOE_OK)\n"
+            "assert 'moe_sort' in B.declared_functions()\n")
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=120,
+                       cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+    assert r.returncode == 0, r.stderr[-500:]
