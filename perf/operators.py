@@ -231,14 +231,14 @@ def _prepare_own(case, s):
         t, k, h, e = case["tokens"], case["top_k"], case["hidden"], case["local"]
         if op == "dispatch":
             s["offsets"] = torch.empty(e + 1, dtype=torch.int32, device="cuda")
-            s["order"] = torch.full((t * k,), -1, dtype=torch.int32, device="cuda")
+            s["order"] = torch.empty(t * k, dtype=torch.int32, device="cuda")
             s["pos"] = torch.empty(t, k, dtype=torch.int32, device="cuda")
-            s["xs"] = torch.zeros(t * k, h, dtype=_dtype(case), device="cuda")
+            s["xs"] = torch.empty(t * k, h, dtype=_dtype(case), device="cuda")
             s["ws"] = space(B.moe_sort_workspace_size(t, k, e))
         elif op == "combine":
             s["out"] = torch.empty(t, h, dtype=_dtype(case), device="cuda")
         else:
-            s["dy"] = torch.zeros(t * k, h, dtype=_dtype(case), device="cuda")
+            s["dy"] = torch.empty(t * k, h, dtype=_dtype(case), device="cuda")
             s["dgates"] = torch.empty(t, k, device="cuda")
             s["dx"] = torch.empty(t, h, dtype=_dtype(case), device="cuda")
     elif op == "wide":
@@ -268,7 +268,13 @@ def run(state):
 def _run_own(case, s):
     from bit_moe_decode_amd import binding as B
     op = case["op"]
+    # rows that no pick has are left as they were: where there are such, the pass
+    # clears the buffers
+    some = case.get("local", 0) < case.get("experts", 0)
     if op == "dispatch":
+        if some:
+            s["order"].fill_(-1)
+            s["xs"].zero_()
         B.moe_sort(s["ids"], case["local"], s["offsets"], s["order"], s["pos"], s["ws"])
         B.moe_gather(s["x"], s["pos"], s["xs"])
         return {n: s[n] for n in ("offsets", "order", "pos", "xs")}
@@ -276,6 +282,8 @@ def _run_own(case, s):
         B.moe_combine(s["y"], s["pos"], s["gates"], s["out"], s["add"])
         return s["out"]
     if op == "backward":
+        if some:
+            s["dy"].zero_()
         B.moe_combine_backward(s["dout"], s["y"], s["pos"], s["gates"], s["dy"], s["dgates"])
         B.moe_gather_backward(s["dxs"], s["pos"], s["dx"])
         return {n: s[n] for n in ("dy", "dgates", "dx")}
