@@ -13,8 +13,8 @@ constexpr int kSortChunk = kSortSteps * kSortThreads;  // picks a block ranks at
 constexpr int kSortMaxGroups = 1024;   // one thread a group
 constexpr int64_t kSortMaxPicks = (int64_t)1 << 24;
 
-// Rows [row, end) of the sorted order, at most the sort's tile_rows of them
-// taken by one tile, all of group `group`.
+// Rows [row, end) of the sorted order, all of group `group`, of which one tile
+// takes at most the sort's tile_rows (extra_rows for the rows behind the picks).
 struct RowTile {
   int32_t group, row, end;
 };
@@ -28,10 +28,11 @@ struct SortArgs {
   int32_t* pos;      // [picks]
   int32_t* counts;   // [chunks][groups], workspace of more than one chunk
   // Optional: the tiles of tile_rows rows covering every group's rows, then
-  // those covering `extra` more rows behind the picks as group `groups`.
+  // those of extra_rows covering `extra` more rows behind the picks as group
+  // `groups`.
   RowTile* tiles;
   int32_t* n_tiles;
-  int tile_rows, extra;
+  int tile_rows, extra, extra_rows;
   int spill;  // 1: picks in no group go to the last one
   int chunks, bits, steps;  // set by launch_sort: blocks, bits of a group, picks a thread
 };

@@ -121,9 +121,9 @@ __device__ __forceinline__ void write_tiles(const SortArgs& a, int first, int co
   if (!a.tiles) return;
   for (int i = 0; i * a.tile_rows < count; i++)
     a.tiles[at + i] = RowTile{tid, first + i * a.tile_rows, first + count};
-  const int more = (a.extra + a.tile_rows - 1) / a.tile_rows;
+  const int more = a.extra > 0 ? (a.extra + a.extra_rows - 1) / a.extra_rows : 0;
   for (int i = tid; i < more; i += kSortThreads)
-    a.tiles[routed + i] = RowTile{a.groups, (int)a.picks + i * a.tile_rows, (int)a.picks + a.extra};
+    a.tiles[routed + i] = RowTile{a.groups, (int)a.picks + i * a.extra_rows, (int)a.picks + a.extra};
   if (tid == 0) *a.n_tiles = routed + more;
 }
 

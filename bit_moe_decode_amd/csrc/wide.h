@@ -9,7 +9,9 @@
 
 namespace moe {
 
-constexpr int kWideTile = 128;  // sorted rows of a tile of the products, at most
+// sorted rows of a tile of the products, at most: by the FP8 MFMA, and summed in
+// fp32 (and the shared expert's)
+constexpr int kWideTile = 128, kWideExactTile = 80;
 
 // One step's shapes and workspace.  Sorted rows: the picks by expert in rows
 // [0, picks), then one row a token for the shared expert.

@@ -19,16 +19,16 @@
 // the definition is 0.00166 of their size where all sums are fp32's, which is
 // their bf16 rounding, and 0.0020 where gate and up take the FP8 MFMA, with
 // single tokens at 0.014.  The bf16 MFMA, which takes the codes as the bf16
-// numbers they are, sums in fp32, for four MFMAs and the conversions where the
-// FP8 MFMA is one.  While the weights' bytes set the time that costs little:
-// of 256 experts and a shared one of 6144 x 2048, everything in fp32 against
-// everything by the FP8 MFMA takes 533 and 530 us at 16 tokens, 1547 .. 1568
-// and 1502 .. 1571 at 300, 1700 .. 1709 and 1672 .. 1711 at 512, 1807 .. 1845 and
-// 1695 .. 1807 at 768, 1895 .. 1955 and 1795 .. 1893 at 1024, 2550 and 2074 ..
-// 2147 at 2048, 3985 and 2810 at 4096.  So up to kWideExactRows picks an expert
-// (768 tokens here) all products are summed in fp32.  Above, the shared
-// expert's gate and up still are, its weight being 1 (4096 tokens 2810 -> 2880
-// us, the error 0.0020 -> 0.0017), and the rest is the FP8 MFMA's.
+// numbers they are, sums in fp32, at twice the time a product and with 192
+// conversions a step of 128 rows.  While the weights' bytes set the time that
+// costs little: of 256 experts and a shared one of 6144 x 2048, with the routed
+// experts in fp32 and by the FP8 MFMA, 545 and 542 us at 16 tokens, 1560 and
+// 1557 at 300, 1705 and 1700 at 512, 1842 and 1810 at 768, 1969 and 1909 at 1024,
+// 2545 and 2201 at 2048, 3954 and 2915 at 4096; of 240 experts of 6144 x 256 362
+// and 339 at 700.  So up to kWideExactRows picks an expert (512 tokens of 256
+// experts) all products are summed in fp32.  Above, the shared expert's gate and
+// up still are, its weight being 1 (the error at 4096 tokens 0.0020 -> 0.0017, the
+// step 2850 -> 2915 us), and the rest is the FP8 MFMA's.
 #include "wide.h"
 
 #include <type_traits>
@@ -258,27 +258,30 @@ __device__ __forceinline__ void wide_store(const WideArgs& a, const RowTile& til
   }
 }
 
-// The tiles a launch takes: all, or the routed experts' or the shared one's alone
-// (which are the last ones of the list).
-enum : int { kAllTiles, kRoutedTiles, kSharedTiles };
-
-// A block's tile, column block and number of row tiles that hold rows; false:
-// none.  Column blocks (UG: 128 mid columns; down: 256 outputs) first:
-// consecutive blocks go to the 8 XCDs in turn, each with an L2 of its own, and
-// where a multiple of 8 column blocks makes up a row tile, one XCD's L2 serves
-// all the row tiles of a column block, so that an expert's tiles share its
-// weights.
-template <bool UG>
-__device__ __forceinline__ bool wide_place(const WideArgs& a, int part, RowTile* tile, int* nb, int* used) {
+// A block's tile, column block, and number of row tiles that hold rows; false:
+// none.  All of it in scalars: an MFMA runs whatever EXEC says, so that the
+// branches that lead to one have to be scalar.
+//
+// The shared expert's tiles, the last of the list, are taken first: nearly all
+// of them are full, and would outlast the others (90 tokens of 32 experts of
+// 1024 x 1024: 73 -> 60 us).  Column blocks (UG: 128 mid columns; down: 256
+// outputs) before tiles: consecutive blocks go to the 8 XCDs in turn, each with
+// an L2 of its own, and where a multiple of 8 column blocks makes up a row tile,
+// one XCD's L2 serves all the row tiles of a column block, so that an expert's
+// tiles share its weights.
+template <bool UG, bool EXACT>
+__device__ __forceinline__ bool wide_place(const WideArgs& a, RowTile* tile, int* nb, int* used) {
   const uint32_t nbs = UG ? a.I / 128 : (a.H + 255) / 256;
-  const int shared = a.shared ? (a.tokens + kWideTile - 1) / kWideTile : 0;
-  int ti = (int)(blockIdx.x / nbs), end = *a.n_tiles;
-  if (part == kSharedTiles) ti += end - shared;
-  if (part == kRoutedTiles) end -= shared;
+  const int shared = a.shared ? (a.tokens + kWideExactTile - 1) / kWideExactTile : 0;
+  const int ti = (int)(blockIdx.x / nbs), end = __builtin_amdgcn_readfirstlane(*a.n_tiles);
   if (ti >= end) return false;
   *nb = (int)(blockIdx.x % nbs);
-  *tile = a.tiles[ti];
-  *used = __builtin_amdgcn_readfirstlane((tile->end - tile->row + 15) >> 4);
+  const RowTile t = a.tiles[ti < shared ? end - shared + ti : ti - shared];
+  *tile = RowTile{__builtin_amdgcn_readfirstlane(t.group), __builtin_amdgcn_readfirstlane(t.row),
+                  __builtin_amdgcn_readfirstlane(t.end)};
+  const int most = (EXACT || tile->group == a.E ? kWideExactTile : kWideTile) / 16;
+  const int rows = (tile->end - tile->row + 15) >> 4;
+  *used = rows < most ? rows : most;
   return true;
 }
 
@@ -380,9 +383,11 @@ __device__ __forceinline__ void wide_tile(const WideArgs& a, const WideWeights& 
 
   // operands: chunks g and g + 4 of weight row 16 j + col, of sorted row 16 i + col
   const int ow0 = (8 * wn + (col & 3)) * kKilo + (col >> 2) * 128 + 16 * g, oa0 = col * kKilo + 16 * g;
+  auto half_weights = [&](const RingStage& st, int wo, int j, int h) {
+    return ld16(st.w.b + (j >> 1) * (4 * kKilo) + (j & 1) * 512 + wo + 64 * h);
+  };
   auto weights = [&](const RingStage& st, int wo, int j) {
-    const uint8_t* p = st.w.b + (j >> 1) * (4 * kKilo) + (j & 1) * 512 + wo;
-    return cat8(ld16(p), ld16(p + 64));
+    return cat8(half_weights(st, wo, j, 0), half_weights(st, wo, j, 1));
   };
   auto rows_of = [&](const RingStage& st, int ro, int i) {
     const uint8_t* p = st.r.b + i * 128 + ro;
@@ -401,9 +406,25 @@ __device__ __forceinline__ void wide_tile(const WideArgs& a, const WideWeights& 
   // tile on: with 4 row tiles or more their place is loaded again from the
   // second on, before the meeting.
   constexpr bool kAhead = U >= 4;
-  // kExact: sums in fp32 by the bf16 MFMA (top of the file)
+  // kExact: sums in fp32 by the bf16 MFMA (top of the file).  Two vector
+  // operations run beside one of these MFMAs for nothing (18 cycles for 17), each
+  // more takes 6 cycles, so the scaling and the codes' conversion are spread
+  // over them.  A row tile's 16 MFMAs are 4, one a weight tile, for each of 4
+  // pieces of K (8 codes of every lane); a piece's bf16 values are replaced
+  // once used, the rows' by the next row tile's, the weights' from the last row
+  // tile on by the next step's (1623 -> 1558 us at 300 tokens against converting
+  // before a row tile's MFMAs).  One row tile: each piece just before its MFMAs.
+  constexpr bool kSpread = kExact && U > 1;
   v8i op[4], b[3];
-  v8bf opx[4][4], bx[4];  // (kExact) op and b as bf16, 8 codes of every lane an MFMA
+  u32x4 raw[2][4];             // (kExact) the next weights' codes: pieces 2 h, 2 h + 1 of tile j
+  u32x4 opx[4][4], bx[4];      // (kExact) weights and a row tile as bf16, by piece
+  auto weights_pair = [&](int f) {  // pair f % 4 of piece f / 16 of weight tile f / 4 % 4
+    const int p = f >> 4, j = (f >> 2) & 3, r = f & 3;
+    opx[j][p][r] = fp8x2_to_bf16(raw[p >> 1][j][2 * (p & 1) + (r >> 1)], r & 1);
+  };
+  auto rows_pair = [&](const v8i& o, int p, int r) {
+    bx[p][r] = fp8x2_to_bf16((uint32_t)o[2 * p + (r >> 1)], r & 1);
+  };
   float as[3] = {0.f, 0.f, 0.f}, sw[2], sw_last[2] = {0.f, 0.f};
   v4f c[4] = {};  // the products not yet scaled: of the row tile before
   float acc[U][4][4];
@@ -440,33 +461,40 @@ __device__ __forceinline__ void wide_tile(const WideArgs& a, const WideWeights& 
 #pragma unroll
         for (int v = 0; v < 4; v++) acc[t][j][v] = fmaf(c[j][v], s[j >> 1], acc[t][j][v]);
       };
-      if constexpr (kExact) {
-        auto bf16_of = [](const v8i& o, int q) {
-          return fp8x8_to_bf16(uint2{(uint32_t)o[2 * q], (uint32_t)o[2 * q + 1]});
-        };
-        if (i == 0) {
-#pragma unroll
-          for (int j = 0; j < 4; j++)
-#pragma unroll
-            for (int q = 0; q < 4; q++) opx[j][q] = bf16_of(op[j], q);
-        }
-#pragma unroll
-        for (int j = 0; j < 4; j++) {
-          bx[j] = bf16_of(b[(P + i) % 3], j);
-          scale(j);
-          c[j] = v4f{0.f, 0.f, 0.f, 0.f};
-        }
-      }
+      v4f d[4];
 #pragma unroll
       for (int j = 0; j < 4; j++) {
         if constexpr (kExact) {
+          if constexpr (!kSpread) {
 #pragma unroll
-          for (int q = 0; q < 4; q++) c[q] = mfma_bf16(opx[q][j], bx[j], c[q]);
+            for (int f = 0; f < 16; f++) weights_pair(16 * j + f);
+#pragma unroll
+            for (int f = 0; f < 4; f++) rows_pair(b[P % 3], j, f);
+          }
+#pragma unroll
+          for (int q = 0; q < 4; q++) {
+            const int n = 4 * j + q;
+            d[q] = mfma_bf16(__builtin_bit_cast(v8bf, opx[q][j]), __builtin_bit_cast(v8bf, bx[j]),
+                             j ? d[q] : v4f{0.f, 0.f, 0.f, 0.f});
+            acc[t][j][q] = fmaf(c[j][q], s[j >> 1], acc[t][j][q]);
+            if (i == U - 1 && j == (kSpread ? 0 : 1)) raw[0][q] = half_weights(nx, wo, q, 0);
+            if (i == U - 1 && j == 3) raw[1][q] = half_weights(nx, wo, q, 1);
+            if constexpr (kSpread) {
+              rows_pair(b[(P + i + (j > 0)) % 3], (j + 3) & 3, q);  // of the next row tile, once used
+#pragma unroll
+              for (int e = 0; e < 3; e++) {
+                const int f = 3 * n + e;
+                if (i == U - 1 && f >= 12 && f < 44) weights_pair(f - 12);
+                if (i == 0 && f < 32) weights_pair(32 + f);
+              }
+            }
+            __builtin_amdgcn_sched_barrier(0);
+          }
         } else {
           scale(j);
           c[j] = mfma_fp8(op[j], b[(P + i) % 3]);
+          if (i == U - 1) op[j] = weights(nx, wo, j);
         }
-        if (i == U - 1) op[j] = weights(nx, wo, j);
         // step k + 3's loads, evenly over the MFMAs that they may follow
         if constexpr (kAhead) {
           constexpr int QW = 4 * (M - 1), QR = 4 * (U - M);
@@ -489,6 +517,10 @@ __device__ __forceinline__ void wide_tile(const WideArgs& a, const WideWeights& 
         }
         __builtin_amdgcn_sched_barrier(0);
       }
+      if constexpr (kExact) {
+#pragma unroll
+        for (int q = 0; q < 4; q++) c[q] = d[q];
+      }
     }
     sw_last[0] = sw[0];
     sw_last[1] = sw[1];
@@ -505,11 +537,24 @@ __device__ __forceinline__ void wide_tile(const WideArgs& a, const WideWeights& 
   sw[1] = ps1[0];
   wait_and_meet<2 * ND>();  // step 0 has arrived
 #pragma unroll
-  for (int j = 0; j < 4; j++) op[j] = weights(st0, ow0, j);
+  for (int j = 0; j < 4; j++) {
+    if constexpr (kExact) {
+      raw[0][j] = half_weights(st0, ow0, j, 0);
+      raw[1][j] = half_weights(st0, ow0, j, 1);
+    } else {
+      op[j] = weights(st0, ow0, j);
+    }
+  }
 #pragma unroll
   for (int i = 0; i < D; i++) {
     b[i] = rows_of(st0, oa0, i);
     as[i] = scale_of(st0, 4 * col, i);
+  }
+  if constexpr (kSpread) {  // what a step finds of the one before: see there
+#pragma unroll
+    for (int f = 0; f < 32; f++) weights_pair(f);
+#pragma unroll
+    for (int f = 0; f < 12; f++) rows_pair(b[0], f >> 2, f & 3);
   }
   using p0 = std::integral_constant<int, 0>;
   using p1 = std::integral_constant<int, U % 3>;
@@ -539,25 +584,35 @@ __device__ __forceinline__ void wide_tile(const WideArgs& a, const WideWeights& 
 
 // (256 threads a block; the bound of 512 keeps the compiler at 256 registers a
 // thread.  With more it leaves the MFMAs' results in accumulation registers and
-// moves each one before it is scaled: 1857 against 1818 us up/gate.  The bf16
-// operands of the fp32 form need those registers)
+// moves each one before it is scaled: 1857 against 1818 us up/gate by the FP8
+// MFMA.  The bf16 operands leave room for tiles of up to 80 rows; 96 spill
+// registers beside the FP8 form, 16384 tokens 8765 against 8664 us.)
+// EXACT: everything summed in fp32, else the shared expert's gate and up.
 template <bool UG, bool EXACT>
-__global__ __launch_bounds__(EXACT ? 256 : 512) void moe_wide_gemm_kernel(WideArgs a, WideWeights w,
-                                                                               int part) {
+__global__ __launch_bounds__(512) void moe_wide_gemm_kernel(WideArgs a, WideWeights w) {
   __shared__ RingWeights w0, w1, w2;
   __shared__ RingRows r0, r1, r2;
   RowTile tile;
   int nb, used;
-  if (!wide_place<UG>(a, part, &tile, &nb, &used)) return;
+  if (!wide_place<UG, EXACT>(a, &tile, &nb, &used)) return;
   const RingStage s0{w0, r0}, s1{w1, r1}, s2{w2, r2};
-  if (used >= 8) return wide_tile<8, UG, EXACT>(a, w, tile, nb, s0, s1, s2);
-  if (used == 7) return wide_tile<7, UG, EXACT>(a, w, tile, nb, s0, s1, s2);
-  if (used == 6) return wide_tile<6, UG, EXACT>(a, w, tile, nb, s0, s1, s2);
-  if (used == 5) return wide_tile<5, UG, EXACT>(a, w, tile, nb, s0, s1, s2);
-  if (used == 4) return wide_tile<4, UG, EXACT>(a, w, tile, nb, s0, s1, s2);
-  if (used == 3) return wide_tile<3, UG, EXACT>(a, w, tile, nb, s0, s1, s2);
-  if (used == 2) return wide_tile<2, UG, EXACT>(a, w, tile, nb, s0, s1, s2);
-  wide_tile<1, UG, EXACT>(a, w, tile, nb, s0, s1, s2);
+  if (EXACT || (UG && tile.group == a.E)) {
+    if (used >= 5) return wide_tile<5, UG, true>(a, w, tile, nb, s0, s1, s2);
+    if (used == 4) return wide_tile<4, UG, true>(a, w, tile, nb, s0, s1, s2);
+    if (used == 3) return wide_tile<3, UG, true>(a, w, tile, nb, s0, s1, s2);
+    if (used == 2) return wide_tile<2, UG, true>(a, w, tile, nb, s0, s1, s2);
+    return wide_tile<1, UG, true>(a, w, tile, nb, s0, s1, s2);
+  }
+  if constexpr (!EXACT) {
+    if (used >= 8) return wide_tile<8, UG, false>(a, w, tile, nb, s0, s1, s2);
+    if (used == 7) return wide_tile<7, UG, false>(a, w, tile, nb, s0, s1, s2);
+    if (used == 6) return wide_tile<6, UG, false>(a, w, tile, nb, s0, s1, s2);
+    if (used == 5) return wide_tile<5, UG, false>(a, w, tile, nb, s0, s1, s2);
+    if (used == 4) return wide_tile<4, UG, false>(a, w, tile, nb, s0, s1, s2);
+    if (used == 3) return wide_tile<3, UG, false>(a, w, tile, nb, s0, s1, s2);
+    if (used == 2) return wide_tile<2, UG, false>(a, w, tile, nb, s0, s1, s2);
+    wide_tile<1, UG, false>(a, w, tile, nb, s0, s1, s2);
+  }
 }
 
 // out[t] = bf16( sum_j g[t,j] y[pos[t,j]] + y[picks + t] ), in pick order.
@@ -593,14 +648,20 @@ __global__ __launch_bounds__(256) void moe_wide_combine_kernel(WideArgs a,
 
 // Picks an expert up to which a batch's products are all summed in fp32 (top of
 // the file).
-constexpr int kWideExactRows = 24;
+constexpr int kWideExactRows = 16;
+
+static bool wide_exact(int64_t picks, int experts) {
+  return picks <= (int64_t)kWideExactRows * experts;
+}
 
 int wide_max_tiles(int64_t picks, int experts, int shared_rows) {
-  return (int)(sort_max_tiles(picks, experts, kWideTile) + (shared_rows + kWideTile - 1) / kWideTile);
+  const int rows = wide_exact(picks, experts) ? kWideExactTile : kWideTile;
+  return (int)(sort_max_tiles(picks, experts, rows) + (shared_rows + kWideExactTile - 1) / kWideExactTile);
 }
 
 hipError_t launch_wide(const WideArgs& a, const WideWeights& w, const uint16_t* x,
                        const int32_t* ids, const float* gates, uint16_t* out, hipStream_t stream) {
+  const bool exact = wide_exact(a.picks, a.E);
   hipLaunchKernelGGL(moe_wide_act_kernel, dim3(a.tokens), dim3(256), 0, stream, a, x, w.gamma);
   SortArgs s = {};
   s.ids = ids;
@@ -612,27 +673,20 @@ hipError_t launch_wide(const WideArgs& a, const WideWeights& w, const uint16_t* 
   s.counts = a.counts;
   s.tiles = a.tiles;
   s.n_tiles = a.n_tiles;
-  s.tile_rows = kWideTile;
+  s.tile_rows = exact ? kWideExactTile : kWideTile;
+  s.extra_rows = kWideExactTile;
   s.extra = a.shared ? a.tokens : 0;
   hipError_t e = launch_sort(s, stream);
   if (e != hipSuccess) return e;
-  const int nu = a.I / 128, shared = (s.extra + kWideTile - 1) / kWideTile;
-  const dim3 gu(a.max_tiles * nu), gd(a.max_tiles * ((a.H + 255) / 256));
+  const dim3 gu(a.max_tiles * (a.I / 128)), gd(a.max_tiles * ((a.H + 255) / 256));
   hipLaunchKernelGGL(moe_wide_sorted_scales_kernel,
                      dim3((uint32_t)((a.rows + 255) / 256), (a.H / 128 + 3) / 4), dim3(256), 0, stream, a);
-  if (a.picks <= (int64_t)kWideExactRows * a.E) {
-    hipLaunchKernelGGL((moe_wide_gemm_kernel<true, true>), gu, dim3(256), 0, stream, a, w,
-                       kAllTiles);
-    hipLaunchKernelGGL((moe_wide_gemm_kernel<false, true>), gd, dim3(256), 0, stream, a, w,
-                       kAllTiles);
+  if (exact) {
+    hipLaunchKernelGGL((moe_wide_gemm_kernel<true, true>), gu, dim3(256), 0, stream, a, w);
+    hipLaunchKernelGGL((moe_wide_gemm_kernel<false, true>), gd, dim3(256), 0, stream, a, w);
   } else {
-    hipLaunchKernelGGL((moe_wide_gemm_kernel<true, false>), gu, dim3(256), 0, stream, a, w,
-                       kRoutedTiles);
-    if (shared > 0)
-      hipLaunchKernelGGL((moe_wide_gemm_kernel<true, true>), dim3(shared * nu), dim3(256), 0, stream, a, w,
-                         kSharedTiles);
-    hipLaunchKernelGGL((moe_wide_gemm_kernel<false, false>), gd, dim3(256), 0, stream, a, w,
-                       kAllTiles);
+    hipLaunchKernelGGL((moe_wide_gemm_kernel<true, false>), gu, dim3(256), 0, stream, a, w);
+    hipLaunchKernelGGL((moe_wide_gemm_kernel<false, false>), gd, dim3(256), 0, stream, a, w);
   }
   hipLaunchKernelGGL(moe_wide_combine_kernel, dim3(a.tokens, (a.H + 1023) / 1024), dim3(256), 0,
                      stream, a, gates, out);

@@ -1,4 +1,4 @@
-"""How the experts' step of many rows (moe_wide_step) adds: in fp32 up to 24
+"""How the experts' step of many rows (moe_wide_step) adds: in fp32 up to 16
 picks an expert, and for the shared expert's gate and up in every batch; by the
 FP8 MFMA for the rest of wider batches.
 
@@ -67,11 +67,11 @@ def _apart(out, ref):
 
 
 @pytest.mark.parametrize("t,hidden,inter,experts,shared,mode", [
-    (16, 2048, 1024, 32, True, "top"), (96, 2048, 1024, 32, True, "skewed"),
-    (96, 1024, 512, 32, False, "skewed"), (48, 512, 256, 16, True, "dropped")])
+    (16, 2048, 1024, 32, True, "top"), (96, 2048, 1024, 64, True, "skewed"),
+    (96, 1024, 512, 64, False, "skewed"), (32, 512, 256, 16, True, "dropped")])
 def test_few_picks_an_expert(exact_codes, monkeypatch, t, hidden, inter, experts, shared, mode):
     print("wide sums", t, hidden, inter, experts, shared, mode, flush=True)
-    assert t * 8 <= 24 * experts
+    assert t * 8 <= 16 * experts
     monkeypatch.setattr(W, "_product", _fp32_product)
     layer, x, ids, gates = _case(t, hidden, inter, experts, shared, mode, t + hidden)
     out = W._run(layer, x, ids, gates)
@@ -89,11 +89,11 @@ def test_few_picks_an_expert(exact_codes, monkeypatch, t, hidden, inter, experts
 @pytest.mark.parametrize("t", [130, 300])
 def test_the_shared_expert_of_any_batch(exact_codes, t):
     """No pick is in a group: the outputs are the shared expert's, whose gate
-    and up are summed in fp32 in batches of more than 24 picks an expert too.
+    and up are summed in fp32 in batches of more than 16 picks an expert too.
     Its down is the FP8 MFMA's, 1.33e-5 off: sqrt(2 * 1.33e-5 * 2^-7) = 4.6e-4
     from the output's rounding instead of 0.9e-4, twice that in quadrature with
     twice 3.5e-4."""
-    assert t * 8 > 24 * 16
+    assert t * 8 > 16 * 16
     layer, x, ids, gates = _case(t, 2048, 1024, 16, True, "none", t)
     out = W._run(layer, x, ids, gates)
     torch.cuda.synchronize()
@@ -114,9 +114,9 @@ def test_many_picks_an_expert(exact_codes, t, shared):
     assert apart <= FP8_LIMIT
 
 
-@pytest.mark.parametrize("t,more,experts", [(20, 37, 32), (150, 333, 16)])
+@pytest.mark.parametrize("t,more,experts", [(20, 37, 32), (150, 333, 16), (31, 97, 64)])
 def test_a_tokens_bits_in_two_batches(t, more, experts):
-    """Batches on the same side of 24 picks an expert: the first tokens' results
+    """Batches on the same side of 16 picks an expert: the first tokens' results
     are the same bits alone and among others, at other places in the sorted
     order and in tiles of other sizes."""
     layer, x, ids, gates = _case(t + more, 512, 384, experts, True, "top", 7 * t)
@@ -128,3 +128,34 @@ def test_a_tokens_bits_in_two_batches(t, more, experts):
     as_bits = lambda v: v.view(torch.int16)  # noqa: E731
     assert torch.equal(as_bits(both[:t]), as_bits(alone))
     assert torch.equal(as_bits(both[at]), as_bits(moved))
+
+
+@pytest.mark.parametrize("hidden,inter,shared", [(128, 128, False), (256, 128, True), (384, 256, True),
+                                                 (640, 384, False)])
+def test_every_number_of_rows_an_expert_in_fp32(exact_codes, monkeypatch, hidden, inter, shared):
+    """Experts of 0 to 257 rows, every number of row tiles of 16 of a tile of 80,
+    full, one short and one over, in a batch of few picks an expert."""
+    print("wide fp32 rows", hidden, inter, shared, flush=True)
+    monkeypatch.setattr(W, "_product", _fp32_product)
+    counts = W.COUNTS + [159, 160, 161]
+    experts = -(-sum(counts) // 256) * 16
+    flat = torch.repeat_interleave(torch.arange(len(counts)) * 5 % experts, torch.tensor(counts))
+    flat = torch.cat([flat, torch.full((-flat.numel() % 8,), -1)])
+    flat = flat[torch.randperm(flat.numel(), generator=torch.Generator().manual_seed(hidden))]
+    ids = flat.view(-1, 8).to(torch.int32).cuda()
+    assert ids.numel() <= 16 * experts
+    assert torch.bincount(flat[flat >= 0]).max() == max(counts)
+    layer = W._layer(hidden, inter, experts, shared, inter)
+    x = W.S.make_x(ids.shape[0], hidden, seed=inter + 1).cuda()
+    gates = torch.softmax(torch.randn(ids.shape, device="cuda",
+                                      generator=torch.Generator("cuda").manual_seed(3)), 1)
+    gates = torch.where(ids >= 0, gates, torch.zeros_like(gates))
+    out = W._run(layer, x, ids, gates)
+    torch.cuda.synchronize()
+    ref, tol = W._reference(layer, x, ids, gates)
+    bound = tol + 2.0 ** -8 * (ref.abs() + tol)
+    err = (out.double() - ref).abs()
+    assert bool((err <= bound).all()), (int((err > bound).sum()), float((err - bound).max()))
+    apart = _apart(out, ref)
+    print("apart", apart, flush=True)
+    assert apart <= FP32_LIMIT
