@@ -216,6 +216,12 @@ __device__ __forceinline__ void wide_store(const WideArgs& a, const RowTile& til
     for (int i = 0; i < U; i++) {
       const int m = i * 16 + col;
       const float s = __uint_as_float(max(max(mx[m], mx[16 * U + m]), max(mx[32 * U + m], mx[48 * U + m]))) / 448.0f;
+      if (s < 0x1p-126f) {  // a rounded subnormal: values up to 1.5 * 448 of them
+#pragma unroll
+        for (int j = 0; j < 2; j++)
+#pragma unroll
+          for (int v = 0; v < 4; v++) acc[i][j][v] = fminf(fmaxf(acc[i][j][v], -448.f * s), 448.f * s);
+      }
 #pragma unroll
       for (int j = 0; j < 2; j++) {
         uint32_t q = 0u;

@@ -159,3 +159,20 @@ def test_every_number_of_rows_an_expert_in_fp32(exact_codes, monkeypatch, hidden
     apart = _apart(out, ref)
     print("apart", apart, flush=True)
     assert apart <= FP32_LIMIT
+
+
+@pytest.mark.parametrize("t,experts", [(40, 32), (70, 16)])
+def test_tokens_of_tiny_values(t, experts):
+    """Values whose products lie where a block's scale, a 448th of its largest
+    mid, is a rounded subnormal: finite outputs, of the products' size.  With x up
+    to 2^(e + 2), weights up to 2^3 and rstd 2^10 (1 / sqrt(eps)), sums of 256
+    N(0, 1) products give gate and up below 2^(e + 21), mid below 2^(2 e + 41),
+    sums of 128 of them and of 9 experts below 2^(2 e + 52)."""
+    layer = W._layer(256, 128, experts, True, t)
+    x0 = W.S.make_x(t, 256, seed=t + 1).cuda().float()
+    ids, gates = W._routing(t, experts, "top", t + 2)
+    for e in range(-92, -78):
+        out = W._run(layer, (x0 * 2.0 ** e).to(torch.bfloat16), ids, gates)
+        torch.cuda.synchronize()
+        assert bool(torch.isfinite(out).all()), e
+        assert float(out.float().abs().max()) <= 2.0 ** (2 * e + 52), e
