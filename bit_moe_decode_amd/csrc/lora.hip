@@ -117,10 +117,11 @@ __device__ __forceinline__ void k_range(int k, int w, int waves, int* s0, int* s
 
 // A x of a tile over one part of K; the block's 4 waves split the part
 // further and add their sums through LDS in wave order.  RT: rank tiles of 16.
-// 6001 rows of 6144, 24 adapters: 22 us at rank 16, 32 at rank 64 (x alone is
-// 74 MB, 11 us of memory; every tile reads its adapter again, from L2).  Bound
-// by latency: a wave has 6 to 12 steps of 32, 4 of them under way.  Tiles of 64
-// rows halve A's traffic: 32 us here, but 85 against 48 in the expand.
+// 6001 rows of 6144, 24 adapters: 22 us at rank 16, 33 at rank 64 (x alone is
+// 74 MB, 11 us of memory; every tile reads its adapter again, from L2).  Its
+// waves wait for loads: a wave has 6 to 12 steps of 32, 4 of them under way (no
+// other depth was measured).  Tiles of 64 rows halve A's traffic: 32 us here, but
+// 85 against 48 in the expand.
 template <int RT>
 __global__ __launch_bounds__(256, 2) void lora_shrink_tile_kernel(
     LoraArgs l, const uint16_t* __restrict__ x) {
@@ -234,8 +235,8 @@ __device__ __forceinline__ void split_bf16(float v, uint16_t* hi, uint16_t* lo) 
 // MFMAs for one.  The products go back through
 // the wave's LDS area to lanes that hold 8 outputs of one row.  RS: K steps of 32 ranks; the ranks
 // past the adapter's are zero in both operands.
-// 6001 rows of 6144, 24 adapters: 38 us at rank 16, 50 at rank 64; base and y
-// are 148 MB, 29 us of memory at the rate of a copy, which bounds it.
+// 6001 rows of 6144, 24 adapters: 38 us at rank 16, 52 at rank 64; base and y
+// are 148 MB, 29 us of memory at the rate of a copy.
 constexpr int kOutStride = 68;  // floats of a row of products in LDS (64 used)
 
 template <int RS>
@@ -388,7 +389,8 @@ __global__ __launch_bounds__(256, 2) void lora_expand_tile_kernel(
   }
 }
 
-// Above rows * max_rank = 2048 the rows are grouped.  Kernels of one call at n
+// Above rows * max_rank = 2048 the rows are grouped (measured at this n and k
+// alone; more distinct adapters move the crossing up).  Kernels of one call at n
 // = k = 6144, one by one and grouped, with 128 adapters and with 4: 16 rows at
 // rank 128 18.5 and 25.6, 18.1 and 21.2 us; 64 rows at rank 32 15.1 and 21.6,
 // 12.9 and 13.5; 128 at rank 16 15.0 and 23.4, 12.0 and 14.1; 256 at rank 16

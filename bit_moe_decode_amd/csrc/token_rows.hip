@@ -28,7 +28,10 @@ namespace moe {
 // order).  The exclusive sums over the waves' counts, group by group, then
 // turn the ranks into places.  Bound by the latency of that chain, not by its
 // bytes (4 read and 8 written a pick): 128 picks of 256 groups 3.8 us, 6001 of
-// 25 groups 7.6 us in one block, 65536 of 256 in two launches 4.8 + 8.1 us.
+// 25 groups 7.6 us in one block, 65536 of 256 in two launches 4.7 + 8 us.  Every
+// block of the second reads all chunks' counts: little up to some 2^20 picks (31
+// us of 256 groups), most of the time at the 2^24 that it takes (0.8 ms of 256
+// groups, 1.7 of 1024).
 constexpr int kSortWaves = kSortThreads / kWave;
 
 struct SortShared {
@@ -275,8 +278,9 @@ hipError_t launch_sort(SortArgs a, hipStream_t stream) {
 // a row is read once and written once, several rows under way a lane, a row's
 // blocks next to each other so that its lines are used while they are open.
 // At 6144 columns: gather of 8192 tokens to 65536 rows of bf16 170 us, 5.3
-// TB/s; combine of 8191 tokens' 4 of 8 picks in fp32 107 us; combine's gradient
-// of 4096 tokens in bf16 168 us, gather's 111 us.  A few rows take the launch
+// TB/s; combine of 8191 tokens' 2 of 8 picks (those of a quarter of the experts)
+// in fp32 109 us, 5.5 TB/s; combine's gradient of 4096 tokens in bf16 168 us,
+// gather's 110 us.  A few rows take the launch
 // and one pass of latency: 16 tokens gathered 3.5 us, 32 combined 4.3 us.
 typedef uint32_t u32x4_a4 __attribute__((ext_vector_type(4), aligned(4)));
 
@@ -467,8 +471,8 @@ static int row_threads(RowArgs* a, int vec) {
   return threads;
 }
 
-// Calls launch(blocks) for tokens from a->first on: one launch, or several
-// where the grid would pass 2^32 threads.
+// Calls launch(blocks) for tokens from a->first on: one launch, or several of
+// at most 2^23 blocks (2^31 threads) each.
 template <typename F>
 static hipError_t for_tokens(RowArgs* a, F launch) {
   const int64_t most = ((int64_t)1 << 23) / a->parts > 0 ? ((int64_t)1 << 23) / a->parts : 1;

@@ -119,16 +119,18 @@ __global__ __launch_bounds__(256) void moe_wide_sorted_scales_kernel(WideArgs a)
 // next loads are spread between the MFMAs (in one go they stall the wave that
 // issues them: up/gate of 4096 tokens 1790 against 1740 us).
 //
-// Measured at 256 experts of 6144 x 2048 and a shared one.  300 tokens: the
-// weights' 9.7 GB at 6.2 TB/s, which bounds it.  4096 tokens: up/gate 1630 us,
-// down 914, 1.1 PFLOP/s.  Without any loads the up/gate takes 955 us, with half
-// the weights' 1352, and a loop of the loads and LDS reads without any MFMA
-// 1690 (with row scales read from 128 places a step, 1740 instead of 1630 in
-// all): bound by the loads, 14 GB a launch from L2 to the CUs.  A form with the
-// next step in registers and two blocks a CU took 1830 and 920 us, and 4 to 10%
-// more time from 16 tokens on; other orders of tiles over the XCDs, tiles of
-// even size and K started at other places were no faster (1760 .. 1890 where
-// this order took 1760).
+// Measured at 256 experts of 6144 x 2048 and a shared one.  300 tokens: up/gate
+// 950 us, down 524: the bytes of the weights in use (5.8 and 2.9 GB, counted as
+// 5.87 and 2.92) at 6.2 and 5.6 TB/s, which bounds it.  4096 tokens: up/gate 1726
+// us, down 938, 1.1 PFLOP/s; the matrix units of the up/gate are busy for 28% of
+// the time.  Before the shared expert's fp32 sums it took 1630 .. 1680; then
+// without any loads 955, with half the weights' 1352, and a loop of the loads
+// and LDS reads without any MFMA 1690: bound by the loads, 16.1 GB a launch from
+// L2 to the CUs, 8.8 of them from memory.  A form with the next step in
+// registers and two blocks a CU took 1830 and 920 us, and 4 to 10% more time
+// from 16 tokens on; other orders of tiles over the XCDs, tiles of even size and
+// K started at other places were no faster (1760 .. 1890 where this order took
+// 1760), nor were row scales read from 128 places a step (1740 for 1630).
 
 // Loads at a 32-bit offset from a block-uniform base: the base, the uniform
 // part of the offset and the bound stay in scalar registers.
