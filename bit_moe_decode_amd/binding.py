@@ -482,8 +482,11 @@ def _wide_weights(cfg: Config, weights: Weights, device):
     """Weights from make_weights are cfg's FP8 matrices, on `device`."""
     if not hasattr(weights, "tensors") or cfg.routed_fmt != FMT_FP8:
         return
-    gamma, _, routed, shared = weights.tensors
     h = cfg.hidden
+    wanted = (h, cfg.inter, cfg.n_experts, cfg.shared_inter, device)
+    if getattr(weights, "found", None) == wanted:  # by an earlier call: the struct's own tensors
+        return
+    gamma, _, routed, shared = weights.tensors
     _laid_out("moe_wide_step", ("gamma", gamma, _torch.bfloat16, (h,)))
     if cfg.shared_inter > 0 and shared is None:
         _refuse("moe_wide_step", "the weights have no shared expert")
@@ -501,6 +504,7 @@ def _wide_weights(cfg: Config, weights: Weights, device):
                 tensors.append(t)
     if any(t.get_device() != device for t in tensors):
         _refuse("moe_wide_step", f"the weights are not on device {device}")
+    weights.found = wanted
 
 
 def moe_wide_step(cfg: Config, x, ids, gates, weights: Weights, out, workspace, stream=None):

@@ -102,6 +102,14 @@ def test_wide_weights_that_are_refused(name, t):
         assert ONLY_DEVICE not in e and "is not a contiguous" in e
 
 
+def test_wide_weights_of_two_configurations():
+    w = weights()
+    for _ in range(2):  # a call that found them right does not speak for another configuration's
+        assert ONLY_DEVICE in wide(w)
+        assert ONLY_DEVICE not in wide(w, n_experts=32)
+        assert ONLY_DEVICE in wide(w, shared=0)
+
+
 def test_wide_weights_of_another_layer():
     assert ONLY_DEVICE not in wide(weights(), n_experts=32)
     assert ONLY_DEVICE not in wide(weights(), hidden=512)

@@ -86,7 +86,7 @@ def test_few_picks_an_expert(exact_codes, monkeypatch, t, hidden, inter, experts
     assert apart <= FP32_LIMIT
 
 
-@pytest.mark.parametrize("t", [130, 300])
+@pytest.mark.parametrize("t", [33, 80, 81, 130, 160, 161, 300])
 def test_the_shared_expert_of_any_batch(exact_codes, t):
     """No pick is in a group: the outputs are the shared expert's, whose gate
     and up are summed in fp32 in batches of more than 16 picks an expert too.
@@ -176,3 +176,35 @@ def test_tokens_of_tiny_values(t, experts):
         torch.cuda.synchronize()
         assert bool(torch.isfinite(out).all()), e
         assert float(out.float().abs().max()) <= 2.0 ** (2 * e + 52), e
+
+
+def test_two_batches_in_a_graph():
+    """A batch of few picks an expert and one of many, each with its workspace,
+    captured into one graph: every replay on other inputs gives the eager bits."""
+    few, many = W._layer(256, 384, 32, True, 5), W._layer(384, 256, 16, True, 6)
+    sizes = ((few, 60), (many, 200))
+    sets = [[(W.S.make_x(t, l.hidden, seed=9 * s + i).cuda(), *W._routing(t, l.n_experts, "top", 20 * s + i))
+             for i, (l, t) in enumerate(sizes)] for s in range(3)]
+    want = [[W._run(l, *x) for (l, _), x in zip(sizes, one)] for one in sets]
+    torch.cuda.synchronize()
+    cur = [[v.clone() for v in x] for x in sets[0]]
+    outs = [torch.empty_like(x[0]) for x in cur]
+    cfgs = [W._cfg(l) for l, _ in sizes]
+    weights = [W.B.LayerRunner.weights_for(l) for l, _ in sizes]
+    spaces = [torch.empty(W.B.moe_wide_workspace_size(c, t), dtype=torch.uint8, device="cuda")
+              for c, (_, t) in zip(cfgs, sizes)]
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        for i in range(2):
+            W.B.moe_wide_step(cfgs[i], *cur[i], weights[i], outs[i], spaces[i], torch.cuda.current_stream())
+    for rep in range(6):
+        for c, x in zip(cur, sets[rep % 3]):
+            for d, v in zip(c, x):
+                d.copy_(v)
+        g.replay()
+        torch.cuda.synchronize()
+        for i in range(2):
+            assert torch.equal(outs[i], want[rep % 3][i]), (rep, i)
+        W._run(few, *sets[rep % 3][0])
+        torch.cuda.synchronize()
+    del g
