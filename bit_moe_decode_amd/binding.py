@@ -80,6 +80,10 @@ class RowShape(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in ("dtype", "tokens", "top_k", "hidden", "rows")]
 
 
+class ProductShape(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("dtype", "n_experts", "rows", "n", "k")]
+
+
 class LoraSet(ctypes.Structure):
     _fields_ = [("n_adapters", ctypes.c_int32), ("max_rank", ctypes.c_int32),
                 ("n", ctypes.c_int32), ("k", ctypes.c_int32), ("a", ctypes.c_void_p),
@@ -131,6 +135,7 @@ def lib():
         p, i32, size = ctypes.c_void_p, ctypes.c_int32, ctypes.c_size_t
         shape = ctypes.POINTER(RowShape)
         lora = ctypes.POINTER(LoraSet)
+        product = ctypes.POINTER(ProductShape)
         for name, restype, args in (
                 ("moe_sort_workspace_size", size, [i32, i32, i32]),
                 ("moe_sort", ctypes.c_int, [p, i32, i32, i32, p, p, p, p, size, p]),
@@ -141,6 +146,10 @@ def lib():
                 ("moe_wide_workspace_size", size, [ctypes.POINTER(Config), i32]),
                 ("moe_wide_step", ctypes.c_int, [ctypes.POINTER(Config), p, i32, p, p,
                                                  ctypes.POINTER(Weights), p, p, size, p]),
+                ("moe_product_workspace_size", size, [product]),
+                ("moe_product", ctypes.c_int, [product, p, p, p, p, p, size, p]),
+                ("moe_product_backward_workspace_size", size, [product]),
+                ("moe_product_backward", ctypes.c_int, [product, p, p, p, p, p, p, i32, p, size, p]),
                 ("lora_workspace_size", size, [lora, i32]),
                 ("lora_apply", ctypes.c_int, [lora, p, p, i32, p, p, p, size, p]),
                 ("lowbit_gemv_lora", ctypes.c_int, [ctypes.POINTER(LowbitMatrix), lora, p, p, i32,
@@ -520,6 +529,62 @@ def moe_wide_step(cfg: Config, x, ids, gates, weights: Weights, out, workspace, 
     _done(lib().moe_wide_step(ctypes.byref(cfg), x.data_ptr(), t, ids.data_ptr(), gates.data_ptr(),
                               ctypes.byref(weights), out.data_ptr(), ws, n, _stream(stream)),
           "moe_wide_step")
+
+
+# ------------------------------------------ products of rows grouped by expert
+def _moe_dtype(what, dtype):
+    n = {_torch.bfloat16: 0, _torch.float32: 1}.get(dtype)  # moe_dtype
+    if n is None:
+        _refuse(what, f"results of {dtype}")
+    return n
+
+
+def moe_product_workspace_size(rows, n_experts, n, k) -> int:
+    return lib().moe_product_workspace_size(ctypes.byref(ProductShape(0, int(n_experts), int(rows), int(n), int(k))))
+
+
+def moe_product_backward_workspace_size(rows, n_experts, n, k) -> int:
+    return lib().moe_product_backward_workspace_size(
+        ctypes.byref(ProductShape(0, int(n_experts), int(rows), int(n), int(k))))
+
+
+def moe_product(x, w, offsets, y, workspace=None, stream=None):
+    """y[r] = w[e] x[r] for the rows r = offsets[e] .. offsets[e + 1] - 1 of every
+    expert e: x bf16 [rows, k], w bf16 [n_experts, n, k], offsets int32
+    [n_experts + 1] (moe_sort's), y bf16 or float32 [rows, n]; workspace: a device
+    tensor of moe_product_workspace_size bytes (None where that is 0)."""
+    bf = _torch.bfloat16
+    (r, k), (e, n, _) = x.shape, w.shape
+    dtype = _moe_dtype("moe_product", y.dtype)
+    _check("moe_product", x.get_device(), ("x", x, bf, (r, k)), ("w", w, bf, (e, n, k)),
+           ("offsets", offsets, _torch.int32, (e + 1,)), ("y", y, y.dtype, (r, n)))
+    ws, nbytes = _space("moe_product", workspace, x.get_device())
+    _done(lib().moe_product(ctypes.byref(ProductShape(dtype, e, r, n, k)), x.data_ptr(), w.data_ptr(),
+                            offsets.data_ptr(), y.data_ptr(), ws, nbytes, _stream(stream)), "moe_product")
+
+
+def moe_product_backward(dy, x, w, offsets, dx=None, dw=None, workspace=None, add=False, stream=None):
+    """dx[r] = w[e]^T dy[r] and dw[e] = sum_r dy[r] x[r]^T (added to dw with add)
+    over the rows r of every expert e: dy bf16 [rows, n], x bf16 [rows, k] (may
+    be None without dw), w bf16 [n_experts, n, k] (may be None without dx), dx
+    bf16 [rows, k], dw bf16 or float32 [n_experts, n, k]; either may be None."""
+    bf = _torch.bfloat16
+    r, n = dy.shape
+    e = offsets.shape[0] - 1
+    if (dx is not None and w is None) or (dw is not None and x is None):
+        _refuse("moe_product_backward", "dx needs w, and dw needs x")
+    known = next((t for t in (x, dx, w, dw) if t is not None), None)
+    if known is None:
+        return
+    k = known.shape[-1]
+    dtype = 0 if dw is None else _moe_dtype("moe_product_backward", dw.dtype)
+    _check("moe_product_backward", dy.get_device(), ("dy", dy, bf, (r, n)), ("x", x, bf, (r, k)),
+           ("w", w, bf, (e, n, k)), ("offsets", offsets, _torch.int32, (e + 1,)), ("dx", dx, bf, (r, k)),
+           ("dw", dw, None if dw is None else dw.dtype, (e, n, k)))
+    ws, nbytes = _space("moe_product_backward", workspace, dy.get_device())
+    _done(lib().moe_product_backward(ctypes.byref(ProductShape(dtype, e, r, n, k)), dy.data_ptr(), _address(x),
+                                     _address(w), offsets.data_ptr(), _address(dx), _address(dw), int(add), ws,
+                                     nbytes, _stream(stream)), "moe_product_backward")
 
 
 # ----------------------------------------------------------- low-rank adapters

@@ -8,6 +8,7 @@
 
 #include "device_common.h"
 #include "lora.h"
+#include "products.h"
 #include "token_rows.h"
 #include "wide.h"
 
@@ -583,6 +584,37 @@ moe_status plan_wide(const moe_decode_config* cfg, int32_t tokens, Plan* p, Wide
   return MOE_OK;
 }
 
+// ---- products of rows grouped by expert
+
+moe_status check_product(const moe_product_shape* s) {
+  if (!s) return MOE_ERR_INVALID_ARG;
+  if (s->dtype != MOE_BF16 && s->dtype != MOE_F32) return MOE_ERR_UNSUPPORTED;
+  if (s->n_experts < 1 || s->rows < 0 || s->n < 1 || s->k < 1) return MOE_ERR_INVALID_ARG;
+  if (s->n_experts > kProductMaxExperts || s->rows > kProductMaxRows || s->n % 8 || s->k % 8 ||
+      s->n > MOE_MAX_PRODUCT_SIDE || s->k > MOE_MAX_PRODUCT_SIDE)
+    return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+ProductArgs product_args(const moe_product_shape* s, const int32_t* offsets) {
+  ProductArgs a = {};
+  a.offsets = offsets;
+  a.experts = s->n_experts;
+  a.rows = s->rows;
+  a.n = s->n;
+  a.k = s->k;
+  a.f32 = s->dtype == MOE_F32;
+  return a;
+}
+
+struct ProductBytes {
+  size_t x, y, w, offsets;  // [rows, k] and [rows, n] of 2 bytes, [experts, n, k] of 2
+};
+ProductBytes product_bytes(const moe_product_shape* s) {
+  return {(size_t)s->rows * s->k * 2, (size_t)s->rows * s->n * 2, (size_t)s->n_experts * s->n * s->k * 2,
+          ((size_t)s->n_experts + 1) * 4};
+}
+
 // ---- adapters
 
 moe_status check_lora_set(const lora_set* l) {
@@ -791,6 +823,72 @@ moe_status moe_wide_step(const moe_decode_config* cfg, const uint16_t* x, int32_
                          (const float*)wt.up_s, (const float*)wt.down_s, wt.sg_c, wt.su_c, wt.sd_c,
                          wt.sg_s, wt.su_s, wt.sd_s};
   return launch_wide(a, v, x, ids, gates, out, stream) == hipSuccess ? MOE_OK : MOE_ERR_DEVICE;
+}
+
+size_t moe_product_workspace_size(const moe_product_shape* shape) {
+  return check_product(shape) == MOE_OK ? product_workspace(product_args(shape, nullptr)) : 0;
+}
+
+moe_status moe_product(const moe_product_shape* shape, const uint16_t* x, const uint16_t* w,
+                       const int32_t* offsets, void* y, void* workspace, size_t ws_bytes,
+                       hipStream_t stream) {
+  const moe_status st = check_product(shape);
+  if (st != MOE_OK) return st;
+  if (shape->rows == 0) return MOE_OK;
+  if (!x || !w || !offsets || !y || !aligned16(x) || !aligned16(w) || !aligned4(offsets) || !aligned16(y))
+    return MOE_ERR_INVALID_ARG;
+  ProductArgs a = product_args(shape, offsets);
+  const size_t need = product_workspace(a);
+  if (need && (!workspace || ws_bytes < need || !aligned16(workspace))) return MOE_ERR_WORKSPACE;
+  const ProductBytes b = product_bytes(shape);
+  const void* buf[] = {x, w, offsets, workspace, y};
+  const size_t len[] = {b.x, b.w, b.offsets, need, a.f32 ? 2 * b.y : b.y};
+  for (int i = 0; i < 4; i++)
+    for (int j = i + 1; j < 5; j++)
+      if (j >= 3 && len[i] && len[j] && overlap(buf[i], len[i], buf[j], len[j])) return MOE_ERR_INVALID_ARG;
+  a.x = x;
+  a.w = w;
+  a.y = y;
+  a.space = static_cast<float*>(workspace);
+  return launch_product(a, stream) == hipSuccess ? MOE_OK : MOE_ERR_DEVICE;
+}
+
+size_t moe_product_backward_workspace_size(const moe_product_shape* shape) {
+  return check_product(shape) == MOE_OK ? product_backward_workspace(product_args(shape, nullptr)) : 0;
+}
+
+moe_status moe_product_backward(const moe_product_shape* shape, const uint16_t* dy,
+                                const uint16_t* x, const uint16_t* w, const int32_t* offsets,
+                                uint16_t* dx, void* dw, int32_t add, void* workspace,
+                                size_t ws_bytes, hipStream_t stream) {
+  const moe_status st = check_product(shape);
+  if (st != MOE_OK) return st;
+  if (!dx && !dw) return MOE_OK;
+  // without rows dw is all there is, and 0 (x and dy are not read)
+  const bool rows = shape->rows > 0;
+  if (!offsets || !aligned4(offsets) || (rows && (!dy || !aligned16(dy)))) return MOE_ERR_INVALID_ARG;
+  if (dx && rows && (!w || !aligned16(w) || !aligned16(dx))) return MOE_ERR_INVALID_ARG;
+  if (dw && (!aligned16(dw) || (rows && (!x || !aligned16(x))))) return MOE_ERR_INVALID_ARG;
+  ProductArgs a = product_args(shape, offsets);
+  const size_t need = product_backward_workspace(a);
+  if (need && (!workspace || ws_bytes < need || !aligned16(workspace))) return MOE_ERR_WORKSPACE;
+  const ProductBytes b = product_bytes(shape);
+  const void* buf[] = {dy, dw ? x : nullptr, dx ? w : nullptr, offsets, workspace, dx, dw};
+  const size_t len[] = {b.y, dw ? b.x : 0, dx ? b.w : 0, b.offsets, need, dx ? b.x : 0,
+                        dw ? (a.f32 ? 2 * b.w : b.w) : 0};
+  for (int i = 0; i < 6; i++)
+    for (int j = i + 1; j < 7; j++)
+      if (j >= 4 && len[i] && len[j] && overlap(buf[i], len[i], buf[j], len[j])) return MOE_ERR_INVALID_ARG;
+  a.dy = dy;
+  a.x = x;
+  a.w = w;
+  a.dx = dx;
+  a.dw = dw;
+  a.add = add != 0;
+  a.space = static_cast<float*>(workspace);
+  if (dx && rows && launch_product_dx(a, stream) != hipSuccess) return MOE_ERR_DEVICE;
+  if (dw && launch_product_dw(a, stream) != hipSuccess) return MOE_ERR_DEVICE;
+  return MOE_OK;
 }
 
 size_t lora_workspace_size(const lora_set* l, int32_t rows) {

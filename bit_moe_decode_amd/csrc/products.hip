@@ -1,0 +1,272 @@
+// products.hip -- matrix products of rows grouped by expert, for batches whose
+// rows token_rows.hip has sorted: with rows offsets[e] .. offsets[e+1] of the
+// buffers expert e's,
+//   y[r]  = W_e x[r]                      (W_e [n, k])
+//   dx[r] = W_e^T dy[r]
+//   dW_e  = sum_r dy[r] x[r]^T            (0 for an expert without rows)
+// bf16 operands, sums in fp32, rounded once.
+#include "products.h"
+
+#include "device_common.h"
+#include "tile_product.h"
+
+namespace moe {
+
+// Expert e's rows, from offsets that may be anything: none reach out of the
+// buffers.
+__device__ __forceinline__ void rows_of_expert(const ProductArgs& a, int e, int64_t* lo, int64_t* hi) {
+  const int64_t i = a.offsets[e], j = a.offsets[e + 1];
+  *lo = i < 0 ? 0 : (i < a.rows ? i : a.rows);
+  *hi = j < *lo ? *lo : (j < a.rows ? j : a.rows);
+}
+
+// first[e]: row tiles of the experts before e, and of all in first[experts].
+// (A group of 4 experts a thread.)
+struct ProductPlaces {
+  int first[kProductMaxExperts + 1];
+  int wave[4];
+};
+template <int TILE>
+__device__ __forceinline__ void count_tiles(const ProductArgs& a, ProductPlaces& p) {
+  const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
+  int n[4], sum = 0;
+#pragma unroll
+  for (int i = 0; i < 4; i++) {
+    const int e = 4 * tid + i;
+    n[i] = 0;
+    if (e < a.experts) {
+      int64_t lo, hi;
+      rows_of_expert(a, e, &lo, &hi);
+      n[i] = (int)((hi - lo + TILE - 1) / TILE);
+    }
+    sum += n[i];
+  }
+  int upto = sum;
+#pragma unroll
+  for (int o = 1; o < kWave; o <<= 1) {
+    const int t = __shfl_up(upto, o, kWave);
+    if (lane >= o) upto += t;
+  }
+  if (lane == 63) p.wave[wv] = upto;
+  __syncthreads();
+  int at = upto - sum;
+  for (int w = 0; w < wv; w++) at += p.wave[w];
+#pragma unroll
+  for (int i = 0; i < 4; i++) {
+    if (4 * tid + i <= a.experts) p.first[4 * tid + i] = at;
+    at += n[i];
+  }
+  if (tid == 255 && a.experts == kProductMaxExperts) p.first[kProductMaxExperts] = at;
+  __syncthreads();
+}
+// The expert whose row tile i is: the last e with first[e] <= i (16 experts a
+// lane, then one of 16 a lane).
+__device__ __forceinline__ int expert_of_tile(const ProductArgs& a, const ProductPlaces& p, int i) {
+  const int lane = threadIdx.x & 63;
+  const bool big = 16 * lane < a.experts && p.first[16 * lane] <= i;
+  const int e0 = 16 * (__popcll(__ballot(big)) - 1);
+  const int e = e0 + (lane & 15);
+  const bool below = e < a.experts && p.first[e] <= i;
+  return __builtin_amdgcn_readfirstlane(e0 + __popcll(__ballot(below) & 0xFFFFu) - 1);
+}
+
+// The place of tile t of m_tiles x j_tiles: four row tiles in a run, then the
+// next column tile, so that the 32 blocks of an XCD share few rows and columns.
+__device__ __forceinline__ void place_of(int t, int m_tiles, int j_tiles, int* mt, int* jt) {
+  const int band = t / (4 * j_tiles), m0 = 4 * band;
+  const int high = m_tiles - m0 < 4 ? m_tiles - m0 : 4;
+  const int r = t - band * 4 * j_tiles;
+  *jt = r / high;
+  *mt = m0 + (r - *jt * high);
+}
+
+// Blocks go to the 8 XCDs in turn, each with an L2 of its own: of every
+// gridDim.x tiles (a multiple of 8) an XCD takes neighbouring ones.
+__device__ __forceinline__ int first_tile() {
+  return (int)(blockIdx.x & 7) * (int)(gridDim.x >> 3) + (int)(blockIdx.x >> 3);
+}
+
+// Stores a wave's sums as rows m0 + .. of out, of `cols` columns; rows from
+// m_end and columns from j_end on are not there.
+template <int U, int V, typename T, bool ADD>
+__device__ __forceinline__ void store_tile(TileSums<U, V>& sums, T* out, int64_t m0, int64_t m_end, int j0, int cols) {
+  const int tid = threadIdx.x, lane = tid & 63, wv = tile_wave(tid);
+  const int col = lane & 15, g = lane >> 4;
+  auto& acc = sums.s;
+  m0 += (wv & 1) * 16 * U + col;
+  j0 += (wv >> 1) * 16 * V;
+#pragma unroll
+  for (int u = 0; u < U; u++) {
+    tile_hold(acc[u]);
+    const int64_t m = m0 + 16 * u;
+    T* row = out + m * cols;
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+      for (int v = 0; v < V; v++) {
+        const int j = j0 + 16 * v + 4 * g;
+        if (m < m_end && j < cols) {
+          v4f s = acc[u][v];
+          if constexpr (ADD) s += *reinterpret_cast<const v4f*>(row + j);
+          *reinterpret_cast<v4f*>(row + j) = s;
+        }
+      }
+    } else {
+#pragma unroll
+      for (int v = 0; v < V; v += 2) {
+        if constexpr (ADD) {  // in place of the sums: a lane's own 4 columns
+#pragma unroll
+          for (int h = 0; h < 2; h++) {
+            const int j = j0 + 16 * (v + h) + 4 * g;
+            if (m < m_end && j < cols) {
+              const uint2 o = *reinterpret_cast<const uint2*>(row + j);
+              acc[u][v + h] += v4f{__uint_as_float(o.x << 16), __uint_as_float(o.x & 0xFFFF0000u),
+                                   __uint_as_float(o.y << 16), __uint_as_float(o.y & 0xFFFF0000u)};
+            }
+          }
+        }
+        const u32x4 o = tile_pair(acc[u][v], acc[u][v + 1]);
+        const int j = j0 + 16 * v + tile_pair_at(lane);
+        if (m < m_end && j < cols) *reinterpret_cast<u32x4*>(row + j) = o;
+      }
+    }
+  }
+}
+
+template <int U, int V, bool DX, typename Stage, typename T>
+__device__ __forceinline__ void product_tile(const TileOperand& om, const TileOperand& oj, Stage& s0, Stage& s1,
+                                             Stage& s2, Stage& s3, T* out, int64_t lo, int64_t hi, int j0, int cols) {
+  TileSums<U, V> acc;
+  tile_product<U, V, false, DX>(om, oj, s0, s1, s2, s3, acc);
+  store_tile<U, V, T, false>(acc, out, lo, hi, j0, cols);
+}
+
+// y, or with DX dx, of tiles of 32 U rows at most (fewer where a group's last
+// tile holds fewer) and 32 V columns.
+template <int UMAX, int V, bool DX, typename T>
+__global__ __launch_bounds__(256) void moe_product_kernel(ProductArgs a) {
+  constexpr int TM = 32 * UMAX, TJ = 32 * V, KILOS = 2 * UMAX + 2 * V;
+  __shared__ TileStage<KILOS> s0, s1, s2, s3;
+  __shared__ ProductPlaces places;
+  count_tiles<TM>(a, places);
+  const int cols = DX ? a.k : a.n, len = DX ? a.n : a.k;
+  const int j_tiles = (cols + TJ - 1) / TJ;
+  const int64_t total = (int64_t)places.first[a.experts] * j_tiles;
+  const uint16_t* in = DX ? a.dy : a.x;
+  T* out = reinterpret_cast<T*>(DX ? (void*)a.dx : a.y);
+  for (int64_t t = first_tile(); t < total; t += gridDim.x) {
+    const int e = expert_of_tile(a, places, (int)(t / j_tiles));
+    const int before = __builtin_amdgcn_readfirstlane(places.first[e]);
+    const int mine = __builtin_amdgcn_readfirstlane(places.first[e + 1]) - before;
+    int mt, jt;
+    place_of((int)(t - (int64_t)before * j_tiles), mine, j_tiles, &mt, &jt);
+    int64_t lo, hi;
+    rows_of_expert(a, e, &lo, &hi);
+    lo += (int64_t)mt * TM;
+    const int rows = __builtin_amdgcn_readfirstlane((int)(hi - lo < TM ? hi - lo : TM));
+    const int j0 = jt * TJ;
+    const int own = cols - j0 < TJ ? cols - j0 : TJ;
+    const TileOperand om = {in + lo * len, (uint32_t)len * 2u, rows, len};
+    const uint16_t* w = a.w + (int64_t)e * a.n * a.k;
+    const TileOperand oj = {w + (DX ? (int64_t)j0 : (int64_t)j0 * a.k), (uint32_t)a.k * 2u, own, len};
+    if (UMAX == 8 && rows > 128)
+      product_tile<UMAX, V, DX>(om, oj, s0, s1, s2, s3, out, lo, hi, j0, cols);
+    else if (UMAX >= 4 && rows > 64)
+      product_tile<UMAX < 4 ? UMAX : 4, V, DX>(om, oj, s0, s1, s2, s3, out, lo, hi, j0, cols);
+    else if (rows > 32)
+      product_tile<2, V, DX>(om, oj, s0, s1, s2, s3, out, lo, hi, j0, cols);
+    else
+      product_tile<1, V, DX>(om, oj, s0, s1, s2, s3, out, lo, hi, j0, cols);
+  }
+}
+
+// dW of tiles of 32 U rows (of n) and 32 V columns (of k).
+template <int U, int V, typename T, bool ADD>
+__global__ __launch_bounds__(256) void moe_product_dw_kernel(ProductArgs a) {
+  constexpr int TM = 32 * U, TJ = 32 * V, KILOS = 2 * U + 2 * V;
+  __shared__ TileStage<KILOS> s0, s1, s2, s3;
+  const int m_tiles = (a.n + TM - 1) / TM, j_tiles = (a.k + TJ - 1) / TJ;
+  const int per = m_tiles * j_tiles;
+  const int64_t total = (int64_t)a.experts * per;
+  for (int64_t t = first_tile(); t < total; t += gridDim.x) {
+    const int e = (int)(t / per);
+    int mt, jt;
+    place_of((int)(t - (int64_t)e * per), m_tiles, j_tiles, &mt, &jt);
+    int64_t lo, hi;
+    rows_of_expert(a, e, &lo, &hi);
+    const int c = __builtin_amdgcn_readfirstlane((int)(hi - lo));
+    const int m0 = mt * TM, j0 = jt * TJ;
+    const TileOperand om = {a.dy + lo * a.n + m0, (uint32_t)a.n * 2u, a.n - m0 < TM ? a.n - m0 : TM, c};
+    const TileOperand oj = {a.x + lo * a.k + j0, (uint32_t)a.k * 2u, a.k - j0 < TJ ? a.k - j0 : TJ, c};
+    TileSums<U, V> acc;
+    tile_product<U, V, true, true>(om, oj, s0, s1, s2, s3, acc);
+    T* out = reinterpret_cast<T*>(a.dw) + (int64_t)e * a.n * a.k;
+    if (!ADD || c > 0) store_tile<U, V, T, ADD>(acc, out, m0, a.n, j0, a.k);
+  }
+}
+
+static hipError_t product_blocks(int64_t tiles, int a_cu, int* blocks) {
+  int dev = 0, cus = 0;
+  hipError_t e = hipGetDevice(&dev);
+  if (e == hipSuccess) e = hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev);
+  if (e != hipSuccess) return e;
+  const int64_t most = (int64_t)(cus / 8 > 0 ? cus / 8 : 1) * 8 * a_cu;
+  const int64_t want = (tiles + 7) / 8 * 8;
+  *blocks = (int)(want < most ? want : most);
+  return hipSuccess;
+}
+
+// Upper bound of the tiles of `tm` rows by `tj` columns.
+static int64_t most_tiles(const ProductArgs& a, int cols, int tm, int tj) {
+  const int64_t m = a.rows / tm + (a.rows < a.experts ? a.rows : a.experts);
+  return m * ((cols + tj - 1) / tj);
+}
+
+template <bool DX, typename T>
+static hipError_t launch_rows(const ProductArgs& a, hipStream_t stream) {
+  const int cols = DX ? a.k : a.n;
+  int blocks;
+  const bool large = a.rows > (int64_t)48 * a.experts && most_tiles(a, cols, 256, 256) >= 256;
+  if (large) {
+    const hipError_t e = product_blocks(most_tiles(a, cols, 256, 256), 1, &blocks);
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL((moe_product_kernel<8, 8, DX, T>), dim3(blocks), dim3(256), 0, stream, a);
+  } else {
+    const hipError_t e = product_blocks(most_tiles(a, cols, 64, 128), 2, &blocks);
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL((moe_product_kernel<2, 4, DX, T>), dim3(blocks), dim3(256), 0, stream, a);
+  }
+  return hipGetLastError();
+}
+
+size_t product_workspace(const ProductArgs&) { return 0; }
+size_t product_backward_workspace(const ProductArgs&) { return 0; }
+
+hipError_t launch_product(const ProductArgs& a, hipStream_t stream) {
+  return a.f32 ? launch_rows<false, float>(a, stream) : launch_rows<false, uint16_t>(a, stream);
+}
+hipError_t launch_product_dx(const ProductArgs& a, hipStream_t stream) {
+  return launch_rows<true, uint16_t>(a, stream);
+}
+
+template <typename T, bool ADD>
+static hipError_t launch_dw(const ProductArgs& a, hipStream_t stream) {
+  const int64_t large = (int64_t)a.experts * ((a.n + 255) / 256) * ((a.k + 255) / 256);
+  int blocks;
+  if (large >= 256) {
+    const hipError_t e = product_blocks(large, 1, &blocks);
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL((moe_product_dw_kernel<8, 8, T, ADD>), dim3(blocks), dim3(256), 0, stream, a);
+  } else {
+    const hipError_t e = product_blocks((int64_t)a.experts * ((a.n + 127) / 128) * ((a.k + 127) / 128), 2, &blocks);
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL((moe_product_dw_kernel<4, 4, T, ADD>), dim3(blocks), dim3(256), 0, stream, a);
+  }
+  return hipGetLastError();
+}
+
+hipError_t launch_product_dw(const ProductArgs& a, hipStream_t stream) {
+  if (a.f32) return a.add ? launch_dw<float, true>(a, stream) : launch_dw<float, false>(a, stream);
+  return a.add ? launch_dw<uint16_t, true>(a, stream) : launch_dw<uint16_t, false>(a, stream);
+}
+
+}  // namespace moe

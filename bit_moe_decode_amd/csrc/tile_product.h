@@ -1,0 +1,290 @@
+// tile_product.h -- the tile of a bf16 matrix product that products.hip and
+// lm_loss.hip build on: sum_c M(m, c) J(j, c) for a block's m and j, by
+// 16x16x32 bf16 MFMAs with fp32 sums.
+//
+// Either operand lies in memory with c contiguous in a row of each m (j), or
+// transposed, with m (j) contiguous in a row of each c.
+//
+// A block's four waves hold the tile as 2 x 2 parts of 16 U x 16 V sums a wave.
+// c runs in steps of 32 through a ring of four LDS stages that loads fill
+// directly.  While the MFMAs of a step run, the wave reads the next step's
+// operands into registers and refills the stage that this step was read from,
+// one load or LDS read between MFMAs; the waves meet once a step.  At 8 x 8 a
+// step is 64 MFMAs of 16 cycles beside 64 KB read from LDS and 32 KB written to
+// it, 768 cycles of its 128 bytes a cycle: one wave a SIMD with 256 sums a lane
+// keeps the LDS below the MFMAs, where 8 waves of half the width would read 96
+// KB, as long as the MFMAs take.
+#pragma once
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include <type_traits>
+
+#include "device_common.h"
+
+namespace moe {
+
+// One operand: `own` rows (transposed: columns) of the tile that exist and `c`
+// contraction entries, in rows of `pitch` bytes from base on.  Where own or c
+// end the operand is 0: a load past an end reads nothing and fills its place
+// with zeros.  Not transposed: c
+// a multiple of 8, own * pitch below 2^32; transposed: own a multiple of 8.
+struct TileOperand {
+  const uint16_t* base;
+  uint32_t pitch;
+  int own, c;
+};
+
+constexpr int kStepC = 32;
+// A load to LDS puts 16 bytes a lane at consecutive places, 1 KB in all, and
+// reads memory a line at a time only where neighbouring lanes read ascending
+// addresses: a kilobyte holds whole pieces of rows, each of another row.  The
+// next one starts 1056 bytes on, so that the 16 lanes whose LDS reads go
+// together find their rows in distinct banks.
+constexpr int kPiecesAt = 1056;
+
+template <int KILOS>
+struct TileStage {
+  __align__(16) uint8_t b[KILOS * kPiecesAt];
+};
+
+typedef __attribute__((address_space(3))) void tile_lds_void;
+typedef short v4s __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) v4s tile_lds_v4s;
+
+// Waits for this wave's LDS operations, and until at most VM of its loads are
+// under way, then for the other waves.  No memory operation moves across.
+template <int VM>
+__device__ __forceinline__ void tile_meet() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt((VM & 15) | (7 << 4) | ((VM >> 4) << 14));
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
+// How an operand of P tiles of 16 (own) x 32 (c) lies in a stage: P kilobytes.
+//
+// Not transposed: a piece is the 64 bytes of one row; kilobyte q of row tile i
+// holds rows q, q + P, .. of it in its pieces i, i + P, ...  A lane's operand is
+// 16 bytes of row lane % 16: one read.
+// Transposed: a piece is 128 bytes, 64 columns of one c; with 128 columns or
+// more kilobyte q holds c = q % 8 + 8 p in its pieces p, of the first and
+// second 64 of its 128 columns (64 columns: c = q + 4 p).  A lane's operand is
+// the 8 c of column lane % 16: two transposing reads of 4 (in each, lane i of 16
+// names 8 bytes of c = i / 4, columns 4 (i % 4) .., and gets the 4 c of column i).
+template <int P, bool T>
+struct TileLoader {
+  static constexpr int kLoads = P >= 4 ? P / 4 : 1;  // a wave's a step
+  static constexpr int kKilos = 4 * kLoads;          // that they fill
+  static_assert(!T || P >= 4, "64 columns at least");
+  static constexpr uint32_t kNothing = 0xFFFFFF00u;  // an offset behind every buffer's end
+  __amdgpu_buffer_rsrc_t whole;  // not transposed: the tile's rows
+  const uint8_t* base;
+  uint32_t pitch, at[kLoads];    // this lane's offsets in a step
+  int c, kc, q0;                 // entries, this lane's first of a step, the wave's first kilobyte
+  int read;                      // this lane's operands in a stage
+
+  __device__ __forceinline__ void set(const TileOperand& o, int lane, int wv) {
+    pitch = o.pitch;
+    c = o.c;
+    base = reinterpret_cast<const uint8_t*>(o.base);
+    q0 = wv * kLoads;  // (a wave without one loads nothing, zeros, behind the operand)
+    const int col = lane & 15, g = lane >> 4;
+    if constexpr (T) {
+      const int p = lane >> 3;
+      const int cl = P >= 8 ? 8 * (p & 3) : 4 * p, block = P >= 8 ? p >> 2 : 0;
+      const int own0 = (P >= 8 ? (q0 >> 3) * 128 : 0) + block * 64 + (lane & 7) * 8;
+#pragma unroll
+      for (int n = 0; n < kLoads; n++)
+        at[n] = own0 < o.own ? (uint32_t)(cl + (P >= 8 ? (q0 + n) & 7 : q0 + n)) * pitch + (uint32_t)own0 * 2u : kNothing;
+      kc = 0;
+      read = (col >> 2) * kPiecesAt + g * (P >= 8 ? 128 : 256) + (col & 3) * 8;
+    } else {
+      const int p = lane >> 2;
+      const int row = 16 * (p % P) + P * (p / P);
+      whole = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(base), 0, (uint32_t)o.own * pitch, 0x00027000);
+#pragma unroll
+      for (int n = 0; n < kLoads; n++)
+        at[n] = P >= 4 || wv < P ? (uint32_t)(row + q0 + n) * pitch + 16u * (uint32_t)(lane & 3) : kNothing;
+      kc = 8 * (lane & 3);
+      read = (col % P) * kPiecesAt + (col / P) * P * 64 + 16 * g;
+    }
+  }
+  // Load n of the wave's of step k; lds: where the operand starts in the stage.
+  // Past the last step it reads nothing (the part of an offset that is the same
+  // for all lanes is kept inside the buffer: the check of its end subtracts it).
+  __device__ __forceinline__ void issue(uint8_t* lds, int k, int n) const {
+    const int c0 = k * kStepC;
+    tile_lds_void* to = (tile_lds_void*)(lds + (q0 + n) * kPiecesAt);
+    if constexpr (T) {
+      const int left = c - c0 < kStepC ? c - c0 : kStepC;
+      const auto r = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(base + (int64_t)(left > 0 ? c0 : 0) * pitch),
+                                                       0, left > 0 ? (uint32_t)left * pitch : 0u, 0x00027000);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(r, to, 16, at[n], 0, 0, 0);
+    } else {
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(whole, to, 16, c0 + kc < c ? at[n] : kNothing,
+                                               c0 < c ? (uint32_t)c0 * 2u : 0u, 0, 0);
+    }
+  }
+  // Tile i's operand.
+  __device__ __forceinline__ v8bf operand(const uint8_t* lds, int i) const {
+    if constexpr (T) {
+      const uint8_t* p = lds + read + (P >= 8 ? (i >> 3) * (8 * kPiecesAt) + ((i >> 2) & 1) * 512 : 0) + (i & 3) * 32;
+      const v4s a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((tile_lds_v4s*)p);
+      const v4s b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((tile_lds_v4s*)(p + (P >= 8 ? 4 * kPiecesAt : 128)));
+      return __builtin_bit_cast(v8bf, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
+    } else {
+      return *reinterpret_cast<const v8bf*>(lds + read + i * 64);
+    }
+  }
+};
+
+// sums += j m by one MFMA, in place: left to the compiler, 256 sums in 256
+// accumulation registers are moved between them, 600 moves for 256 MFMAs.  Its
+// hazards: the operands come from LDS reads (waited for as any use is) and are
+// not written again before the next step; the sums are read again by the same
+// MFMA of the next step, or, where a basic block ends and the compiler may copy
+// them, behind tile_settle().
+__device__ __forceinline__ void mfma_bf16_into(v4f& sums, const v8bf& j, const v8bf& m) {
+  asm volatile("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(sums) : "v"(j), "v"(m));
+}
+__device__ __forceinline__ void tile_settle() { asm volatile("s_nop 15\n\ts_nop 15" ::: "memory"); }
+
+// Holds sums in accumulation registers up to this point: a store of one row tile
+// at a time takes them from there, where the compiler would move all 256 first.
+template <int V>
+__device__ __forceinline__ void tile_hold(v4f (&sums)[V]) {
+#pragma unroll
+  for (int v = 0; v < V; v++) asm volatile("" : "+a"(sums[v]));
+}
+
+// The wave of a thread, as the scalar it is: an MFMA runs whatever EXEC says,
+// so a branch around one has to be a scalar branch.
+__device__ __forceinline__ int tile_wave(int tid) { return __builtin_amdgcn_readfirstlane(tid >> 6); }
+
+template <int U, int V>
+struct TileSums {
+  v4f s[U][V];
+};
+
+// sums.s[u][v]: this wave's sums, of m tile wm U + u and j tile wj V + v (wm, wj:
+// the wave's bits 0 and 1): a lane holds j = 4 (lane / 16) + 0..3 of m = lane %
+// 16.  All of the block's threads call it, with the same arguments.
+template <int U, int V, bool MT, bool JT, typename Stage>
+__device__ __forceinline__ void tile_product(const TileOperand& om, const TileOperand& oj, Stage& s0, Stage& s1,
+                                             Stage& s2, Stage& s3, TileSums<U, V>& sums) {
+#ifdef __HIP_DEVICE_COMPILE__  // (the host's pass of the compiler refuses the body and needs none)
+  auto& acc = sums.s;
+  constexpr int PM = 2 * U, PJ = 2 * V;
+  static_assert(sizeof(Stage) >= (TileLoader<PM, MT>::kKilos + TileLoader<PJ, JT>::kKilos) * kPiecesAt,
+                "both operands fit a stage");
+  const int tid = threadIdx.x, lane = tid & 63, wv = tile_wave(tid);
+  const int wm = wv & 1, wj = wv >> 1;
+  TileLoader<PM, MT> m;
+  TileLoader<PJ, JT> j;
+  m.set(om, lane, wv);
+  j.set(oj, lane, wv);
+  constexpr int NM = TileLoader<PM, MT>::kLoads, NJ = TileLoader<PJ, JT>::kLoads, NL = NM + NJ;
+  constexpr int kJ = TileLoader<PM, MT>::kKilos * kPiecesAt;  // where J starts in a stage
+  const int steps = (om.c + kStepC - 1) / kStepC;
+#pragma unroll
+  for (int u = 0; u < U; u++)
+#pragma unroll
+    for (int v = 0; v < V; v++) acc[u][v] = v4f{0.f, 0.f, 0.f, 0.f};
+  if (steps <= 0) return;
+  auto issue = [&](Stage& s, int k, int n) {
+    if (n < NM)
+      m.issue(s.b, k, n);
+    else
+      j.issue(s.b + kJ, k, n - NM);
+  };
+  auto issue_all = [&](Stage& s, int k) {
+#pragma unroll
+    for (int n = 0; n < NL; n++) issue(s, k, n);
+  };
+  struct Operands {
+    v8bf m[U], j[V];
+  };
+  auto read = [&](Operands& o, Stage& s, int n) {
+    if (n < V)
+      o.j[n] = j.operand(s.b + kJ, wj * V + n);
+    else
+      o.m[n - V] = m.operand(s.b, wm * U + n - V);
+  };
+  // step k: its operands in `now`; the next's are read from nx, and cur is
+  // filled with step k + 4
+  auto step = [&](Operands& now, Operands& then, Stage& cur, Stage& nx, int k) {
+    // the next step has arrived when the two behind it are under way at most;
+    // and all waves have read all of this one
+    tile_meet<2 * NL>();
+    constexpr int N = U * V, NR = U + V;
+    constexpr int kRead = N >= 16 ? N * 3 / 4 : N;  // reads end early: the next meeting waits for them
+#pragma unroll
+    for (int v = 0; v < V; v++)
+#pragma unroll
+      for (int u = 0; u < U; u++) {
+        const int n = v * U + u;
+#pragma unroll
+        for (int q = 0; q < NR; q++)
+          if (q * kRead / NR == n) read(then, nx, q);
+#pragma unroll
+        for (int q = 0; q < NL; q++)
+          if (q * N / NL == n) issue(cur, k + 4, q);
+        mfma_bf16_into(acc[u][v], now.j[v], now.m[u]);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+  };
+  Operands a, b;
+  issue_all(s0, 0);
+  issue_all(s1, 1);
+  issue_all(s2, 2);
+  issue_all(s3, 3);
+  tile_meet<3 * NL>();
+#pragma unroll
+  for (int q = 0; q < U + V; q++) read(a, s0, q);
+  int k = 0;
+  for (; k + 4 <= steps; k += 4) {
+    step(a, b, s0, s1, k);
+    step(b, a, s1, s2, k + 1);
+    step(a, b, s2, s3, k + 2);
+    step(b, a, s3, s0, k + 3);
+    tile_settle();
+  }
+  if (k < steps) {
+    step(a, b, s0, s1, k);
+    tile_settle();
+  }
+  if (k + 1 < steps) {
+    step(b, a, s1, s2, k + 1);
+    tile_settle();
+  }
+  if (k + 2 < steps) {
+    step(a, b, s2, s3, k + 2);
+    tile_settle();
+  }
+  tile_meet<0>();  // nothing under way into a stage, and no wave reads one
+  // (a branch that the lanes do not share may not draw the last MFMAs into it)
+#pragma unroll
+  for (int u = 0; u < U; u++) tile_hold(acc[u]);
+#endif
+}
+
+// Two neighbouring j tiles' sums of one m as bf16: 16 bytes, the 8 values at
+// tile_pair_at() of the pair's first column.  (The lanes of j 4 .. 7 and 0 .. 3
+// trade halves, so that four lanes store 64 bytes of a row.)
+__device__ __forceinline__ u32x4 tile_pair(const v4f& x, const v4f& y) {
+  u32x4 o;
+#pragma unroll
+  for (int h = 0; h < 2; h++) {
+    const uint32_t a = (uint32_t)f32_to_bf16(x[2 * h]) | ((uint32_t)f32_to_bf16(x[2 * h + 1]) << 16);
+    const uint32_t b = (uint32_t)f32_to_bf16(y[2 * h]) | ((uint32_t)f32_to_bf16(y[2 * h + 1]) << 16);
+    const auto t = __builtin_amdgcn_permlane16_swap(a, b, false, false);
+    o[h] = t[0];
+    o[2 + h] = t[1];
+  }
+  return o;
+}
+__device__ __forceinline__ int tile_pair_at(int lane) { return 16 * ((lane >> 4) & 1) + 8 * (lane >> 5); }
+
+}  // namespace moe

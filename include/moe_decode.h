@@ -12,8 +12,9 @@
  * group-128 weights or, for the LM head after the last layer, FP8 weights.
  * Beside them stand the operators on rows grouped by an index: tokens sorted
  * by expert and back, with gradients (moe_sort, moe_gather, moe_combine), the
- * experts' step for any number of tokens (moe_wide_step), and low-rank
- * adapters of many requests (lora_apply, lowbit_gemv_lora).
+ * experts' step for any number of tokens (moe_wide_step), low-rank adapters of
+ * many requests (lora_apply, lowbit_gemv_lora), and matrix products of the
+ * sorted rows in bf16, with gradients (moe_product).
  *
  * Sources.  The operations follow the body of sgl-amd-mono PR #85 ("...MoE
  * expert dedup and weight loads, kernarg reload, LM-head loads"), quoted on the
@@ -392,6 +393,49 @@ size_t moe_wide_workspace_size(const moe_decode_config* cfg, int32_t tokens);
 moe_status moe_wide_step(const moe_decode_config* cfg, const uint16_t* x, int32_t tokens,
                          const int32_t* ids, const float* gates, const moe_decode_weights* w,
                          uint16_t* out, void* workspace, size_t ws_bytes, hipStream_t stream);
+
+/* ---- Matrix products of rows grouped by expert, between moe_gather and
+ * moe_combine: with expert e's rows offsets[e] .. offsets[e+1] - 1 of the sorted
+ * buffers (moe_sort's offsets),
+ *   y[r] = W_e x[r].
+ * bf16 operands, every sum in fp32, rounded once. */
+#define MOE_MAX_PRODUCT_SIDE 32768
+typedef struct {
+  int32_t dtype;      /* moe_dtype of y (moe_product), of dw (moe_product_backward) */
+  int32_t n_experts;  /* 1..1024 */
+  int32_t rows;       /* rows of the sorted buffers, 0..2^24 */
+  int32_t n, k;       /* an expert's matrix: multiples of 8, 8..MOE_MAX_PRODUCT_SIDE */
+} moe_product_shape;
+
+/* Bytes of workspace the two calls below need (0 for most shapes), or 0 when
+ * the shape is not supported. */
+size_t moe_product_workspace_size(const moe_product_shape* shape);
+size_t moe_product_backward_workspace_size(const moe_product_shape* shape);
+
+/* y[r] = W_e x[r] for the rows r of every expert e:
+ *  x        bf16 [rows, k], w bf16 [n_experts, n, k]
+ *  offsets  int32 [n_experts + 1], ascending, at most rows (no access leaves
+ *           the buffers where they are not; what the rows hold is then not
+ *           defined)
+ *  y        [rows, n]; rows of no expert are left as they were
+ * The buffers must not overlap.  `workspace` may be NULL where the size above is
+ * 0; it is scratch, 16-byte aligned, and calls that overlap in time need one
+ * each. */
+moe_status moe_product(const moe_product_shape* shape, const uint16_t* x, const uint16_t* w,
+                       const int32_t* offsets, void* y, void* workspace, size_t ws_bytes,
+                       hipStream_t stream);
+
+/* Its gradients, of dy bf16 [rows, n] (each may be NULL, and is then not
+ * computed):
+ *  dx   bf16 [rows, k]: dx[r] = W_e^T dy[r]; rows of no expert are left as they
+ *       were.  (x may be NULL without dw.)
+ *  dw   [n_experts, n, k]: dw[e] = sum_r dy[r] x[r]^T over e's rows, 0 without
+ *       any; with add != 0 it is added to dw, in fp32 before the rounding.
+ *       (w may be NULL without dx.) */
+moe_status moe_product_backward(const moe_product_shape* shape, const uint16_t* dy,
+                                const uint16_t* x, const uint16_t* w, const int32_t* offsets,
+                                uint16_t* dx, void* dw, int32_t add, void* workspace,
+                                size_t ws_bytes, hipStream_t stream);
 
 /* ---- Low-rank adapters of many requests beside a projection they share.
  *
