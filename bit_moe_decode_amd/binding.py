@@ -84,6 +84,10 @@ class ProductShape(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in ("dtype", "n_experts", "rows", "n", "k")]
 
 
+class HeadShape(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("dtype", "rows", "vocab", "hidden")]
+
+
 class LoraSet(ctypes.Structure):
     _fields_ = [("n_adapters", ctypes.c_int32), ("max_rank", ctypes.c_int32),
                 ("n", ctypes.c_int32), ("k", ctypes.c_int32), ("a", ctypes.c_void_p),
@@ -135,7 +139,7 @@ def lib():
         p, i32, size = ctypes.c_void_p, ctypes.c_int32, ctypes.c_size_t
         shape = ctypes.POINTER(RowShape)
         lora = ctypes.POINTER(LoraSet)
-        product = ctypes.POINTER(ProductShape)
+        product, head = ctypes.POINTER(ProductShape), ctypes.POINTER(HeadShape)
         for name, restype, args in (
                 ("moe_sort_workspace_size", size, [i32, i32, i32]),
                 ("moe_sort", ctypes.c_int, [p, i32, i32, i32, p, p, p, p, size, p]),
@@ -150,6 +154,10 @@ def lib():
                 ("moe_product", ctypes.c_int, [product, p, p, p, p, p, size, p]),
                 ("moe_product_backward_workspace_size", size, [product]),
                 ("moe_product_backward", ctypes.c_int, [product, p, p, p, p, p, p, i32, p, size, p]),
+                ("lm_head_loss_workspace_size", size, [head]),
+                ("lm_head_loss", ctypes.c_int, [head, p, p, p, p, p, p, size, p]),
+                ("lm_head_loss_backward_workspace_size", size, [head]),
+                ("lm_head_loss_backward", ctypes.c_int, [head, p, p, p, p, p, p, p, i32, p, size, p]),
                 ("lora_workspace_size", size, [lora, i32]),
                 ("lora_apply", ctypes.c_int, [lora, p, p, i32, p, p, p, size, p]),
                 ("lowbit_gemv_lora", ctypes.c_int, [ctypes.POINTER(LowbitMatrix), lora, p, p, i32,
@@ -585,6 +593,50 @@ def moe_product_backward(dy, x, w, offsets, dx=None, dw=None, workspace=None, ad
     _done(lib().moe_product_backward(ctypes.byref(ProductShape(dtype, e, r, n, k)), dy.data_ptr(), _address(x),
                                      _address(w), offsets.data_ptr(), _address(dx), _address(dw), int(add), ws,
                                      nbytes, _stream(stream)), "moe_product_backward")
+
+
+# ---------------------------------------------------------- the LM head's loss
+LOSS_MAX_ROWS = 1 << 20   # MOE_LOSS_MAX_ROWS
+LOSS_MAX_VOCAB = 1 << 20  # MOE_LOSS_MAX_VOCAB
+
+
+def lm_head_loss_workspace_size(rows, vocab, hidden) -> int:
+    return lib().lm_head_loss_workspace_size(ctypes.byref(HeadShape(0, int(rows), int(vocab), int(hidden))))
+
+
+def lm_head_loss_backward_workspace_size(rows, vocab, hidden) -> int:
+    return lib().lm_head_loss_backward_workspace_size(
+        ctypes.byref(HeadShape(0, int(rows), int(vocab), int(hidden))))
+
+
+def lm_head_loss(h, w, targets, loss, lse, workspace, stream=None):
+    """lse[r] = log sum_v exp(w[v] . h[r]) and loss[r] = lse[r] - w[targets[r]] .
+    h[r] (0 for a target outside the vocabulary): h bf16 [rows, hidden], w bf16
+    [vocab, hidden], targets int32 [rows], loss and lse float32 [rows];
+    workspace: a device tensor of lm_head_loss_workspace_size bytes."""
+    bf, f32 = _torch.bfloat16, _torch.float32
+    (r, k), v = h.shape, w.shape[0]
+    _check("lm_head_loss", h.get_device(), ("h", h, bf, (r, k)), ("w", w, bf, (v, k)),
+           ("targets", targets, _torch.int32, (r,)), ("loss", loss, f32, (r,)), ("lse", lse, f32, (r,)))
+    ws, nbytes = _space("lm_head_loss", workspace, h.get_device())
+    _done(lib().lm_head_loss(ctypes.byref(HeadShape(0, r, v, k)), h.data_ptr(), w.data_ptr(), targets.data_ptr(),
+                             loss.data_ptr(), lse.data_ptr(), ws, nbytes, _stream(stream)), "lm_head_loss")
+
+
+def lm_head_loss_backward(h, w, targets, lse, dloss, dh=None, dw=None, workspace=None, add=False, stream=None):
+    """The gradients of lm_head_loss for dloss float32 [rows], of the same h, w
+    and targets and the lse it gave: dh bf16 [rows, hidden], dw bf16 or float32
+    [vocab, hidden] (added to with add); either may be None."""
+    bf, f32 = _torch.bfloat16, _torch.float32
+    (r, k), v = h.shape, w.shape[0]
+    dtype = 0 if dw is None else _moe_dtype("lm_head_loss_backward", dw.dtype)
+    _check("lm_head_loss_backward", h.get_device(), ("h", h, bf, (r, k)), ("w", w, bf, (v, k)),
+           ("targets", targets, _torch.int32, (r,)), ("lse", lse, f32, (r,)), ("dloss", dloss, f32, (r,)),
+           ("dh", dh, bf, (r, k)), ("dw", dw, None if dw is None else dw.dtype, (v, k)))
+    ws, nbytes = _space("lm_head_loss_backward", workspace, h.get_device())
+    _done(lib().lm_head_loss_backward(ctypes.byref(HeadShape(dtype, r, v, k)), h.data_ptr(), w.data_ptr(),
+                                      targets.data_ptr(), lse.data_ptr(), dloss.data_ptr(), _address(dh),
+                                      _address(dw), int(add), ws, nbytes, _stream(stream)), "lm_head_loss_backward")
 
 
 # ----------------------------------------------------------- low-rank adapters

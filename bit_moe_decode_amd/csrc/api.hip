@@ -7,6 +7,7 @@
 #include <new>
 
 #include "device_common.h"
+#include "lm_loss.h"
 #include "lora.h"
 #include "products.h"
 #include "token_rows.h"
@@ -615,6 +616,27 @@ ProductBytes product_bytes(const moe_product_shape* s) {
           ((size_t)s->n_experts + 1) * 4};
 }
 
+// ---- the LM head's loss
+
+moe_status check_head(const lm_head_shape* s) {
+  if (!s) return MOE_ERR_INVALID_ARG;
+  if (s->dtype != MOE_BF16 && s->dtype != MOE_F32) return MOE_ERR_UNSUPPORTED;
+  if (s->rows < 0 || s->vocab < 1 || s->hidden < 1) return MOE_ERR_INVALID_ARG;
+  if (s->rows > MOE_LOSS_MAX_ROWS || s->vocab > MOE_LOSS_MAX_VOCAB || s->hidden % 8 ||
+      s->hidden > kLossMaxHidden)
+    return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+// Whether one of the outputs buf[first] .. overlaps another buffer (null or
+// empty ones overlap nothing).
+bool any_overlap(const void* const* buf, const size_t* len, int first, int n) {
+  for (int i = first; i < n; i++)
+    for (int j = 0; j < i; j++)
+      if (buf[i] && buf[j] && len[i] && len[j] && overlap(buf[i], len[i], buf[j], len[j])) return true;
+  return false;
+}
+
 // ---- adapters
 
 moe_status check_lora_set(const lora_set* l) {
@@ -843,9 +865,7 @@ moe_status moe_product(const moe_product_shape* shape, const uint16_t* x, const 
   const ProductBytes b = product_bytes(shape);
   const void* buf[] = {x, w, offsets, workspace, y};
   const size_t len[] = {b.x, b.w, b.offsets, need, a.f32 ? 2 * b.y : b.y};
-  for (int i = 0; i < 4; i++)
-    for (int j = i + 1; j < 5; j++)
-      if (j >= 3 && len[i] && len[j] && overlap(buf[i], len[i], buf[j], len[j])) return MOE_ERR_INVALID_ARG;
+  if (any_overlap(buf, len, 3, 5)) return MOE_ERR_INVALID_ARG;
   a.x = x;
   a.w = w;
   a.y = y;
@@ -876,9 +896,7 @@ moe_status moe_product_backward(const moe_product_shape* shape, const uint16_t* 
   const void* buf[] = {dy, dw ? x : nullptr, dx ? w : nullptr, offsets, workspace, dx, dw};
   const size_t len[] = {b.y, dw ? b.x : 0, dx ? b.w : 0, b.offsets, need, dx ? b.x : 0,
                         dw ? (a.f32 ? 2 * b.w : b.w) : 0};
-  for (int i = 0; i < 6; i++)
-    for (int j = i + 1; j < 7; j++)
-      if (j >= 4 && len[i] && len[j] && overlap(buf[i], len[i], buf[j], len[j])) return MOE_ERR_INVALID_ARG;
+  if (any_overlap(buf, len, 4, 7)) return MOE_ERR_INVALID_ARG;
   a.dy = dy;
   a.x = x;
   a.w = w;
@@ -889,6 +907,65 @@ moe_status moe_product_backward(const moe_product_shape* shape, const uint16_t* 
   if (dx && rows && launch_product_dx(a, stream) != hipSuccess) return MOE_ERR_DEVICE;
   if (dw && launch_product_dw(a, stream) != hipSuccess) return MOE_ERR_DEVICE;
   return MOE_OK;
+}
+
+size_t lm_head_loss_workspace_size(const lm_head_shape* s) {
+  return check_head(s) == MOE_OK && s->rows > 0 ? loss_workspace(s->rows, s->vocab, s->hidden) : 0;
+}
+
+moe_status lm_head_loss(const lm_head_shape* shape, const uint16_t* h, const uint16_t* w,
+                        const int32_t* targets, float* loss, float* lse, void* workspace,
+                        size_t ws_bytes, hipStream_t stream) {
+  const moe_status st = check_head(shape);
+  if (st != MOE_OK) return st;
+  if (shape->rows == 0) return MOE_OK;
+  if (!h || !w || !targets || !loss || !lse || !aligned16(h) || !aligned16(w) || !aligned4(targets) ||
+      !aligned4(loss) || !aligned4(lse))
+    return MOE_ERR_INVALID_ARG;
+  const size_t need = loss_workspace(shape->rows, shape->vocab, shape->hidden);
+  if (!workspace || ws_bytes < need || !aligned16(workspace)) return MOE_ERR_WORKSPACE;
+  const size_t rb = (size_t)shape->rows * 4;
+  const void* buf[] = {h, w, targets, workspace, loss, lse};
+  const size_t len[] = {(size_t)shape->rows * shape->hidden * 2, (size_t)shape->vocab * shape->hidden * 2, rb,
+                        need, rb, rb};
+  if (any_overlap(buf, len, 3, 6)) return MOE_ERR_INVALID_ARG;
+  const LossArgs a = {h, w, targets, shape->rows, shape->vocab, shape->hidden, loss, lse};
+  return launch_loss(a, workspace, stream) == hipSuccess ? MOE_OK : MOE_ERR_DEVICE;
+}
+
+size_t lm_head_loss_backward_workspace_size(const lm_head_shape* s) {
+  return check_head(s) == MOE_OK && s->rows > 0 ? loss_backward_workspace(s->rows, s->vocab, s->hidden) : 0;
+}
+
+moe_status lm_head_loss_backward(const lm_head_shape* shape, const uint16_t* h, const uint16_t* w,
+                                 const int32_t* targets, const float* lse, const float* dloss,
+                                 uint16_t* dh, void* dw, int32_t add, void* workspace,
+                                 size_t ws_bytes, hipStream_t stream) {
+  const moe_status st = check_head(shape);
+  if (st != MOE_OK) return st;
+  if (!dh && !dw) return MOE_OK;
+  if (!aligned16(dh) || !aligned16(dw)) return MOE_ERR_INVALID_ARG;
+  const bool f32 = shape->dtype == MOE_F32;
+  const size_t wb = (size_t)shape->vocab * shape->hidden * 2;
+  if (shape->rows == 0) {  // a dw of 0
+    if (!dw || add) return MOE_OK;
+    const size_t words = (f32 ? 2 * wb : wb) / 4;
+    const size_t blocks = (words + 1023) / 1024;
+    hipLaunchKernelGGL(moe_fill_u32_kernel, dim3((uint32_t)(blocks < 4096 ? blocks : 4096)), dim3(256), 0, stream,
+                       static_cast<uint32_t*>(dw), words, 0u);
+    return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ERR_DEVICE;
+  }
+  if (!h || !w || !targets || !lse || !dloss || !aligned16(h) || !aligned16(w) || !aligned4(targets) ||
+      !aligned4(lse) || !aligned4(dloss))
+    return MOE_ERR_INVALID_ARG;
+  const size_t need = loss_backward_workspace(shape->rows, shape->vocab, shape->hidden);
+  if (!workspace || ws_bytes < need || !aligned16(workspace)) return MOE_ERR_WORKSPACE;
+  const size_t rb = (size_t)shape->rows * 4, hb = (size_t)shape->rows * shape->hidden * 2;
+  const void* buf[] = {h, w, targets, lse, dloss, workspace, dh, dw};
+  const size_t len[] = {hb, wb, rb, rb, rb, need, hb, f32 ? 2 * wb : wb};
+  if (any_overlap(buf, len, 5, 8)) return MOE_ERR_INVALID_ARG;
+  const LossGradArgs a = {h, w, targets, lse, dloss, shape->rows, shape->vocab, shape->hidden, dh, dw, f32, add != 0};
+  return launch_loss_backward(a, workspace, stream) == hipSuccess ? MOE_OK : MOE_ERR_DEVICE;
 }
 
 size_t lora_workspace_size(const lora_set* l, int32_t rows) {

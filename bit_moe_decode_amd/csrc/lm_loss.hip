@@ -1,0 +1,498 @@
+// lm_loss.hip -- the LM head's softmax cross entropy over a large vocabulary and
+// its gradients, without keeping the logits: with z[r, v] = w[v] . h[r],
+//   lse[r]  = log sum_v exp z[r, v]
+//   loss[r] = lse[r] - z[r, t_r]             (0 for a row without a target)
+//   d[r, v] = (exp(z[r, v] - lse[r]) - [v = t_r]) dloss[r]     (0 without one)
+//   dh[r]   = sum_v d[r, v] w[v],   dw[v] = sum_r d[r, v] h[r]
+// bf16 operands; logits, exponentials and sums in fp32.
+#include "lm_loss.h"
+
+#include <math.h>
+
+#include "device_common.h"
+#include "tile_product.h"
+
+namespace moe {
+
+constexpr float kLog2e = 1.44269504088896340736f;
+
+__device__ __forceinline__ float exp_of(float x) { return __builtin_amdgcn_exp2f(x * kLog2e); }
+
+// The largest and the sum of a value over the four lanes of a row of sums.
+__device__ __forceinline__ float over_lanes_max(float v) {
+  v = fmaxf(v, __shfl_xor(v, 16, kWave));
+  return fmaxf(v, __shfl_xor(v, 32, kWave));
+}
+__device__ __forceinline__ float over_lanes_sum(float v) {
+  v += __shfl_xor(v, 16, kWave);
+  return v + __shfl_xor(v, 32, kWave);
+}
+
+// ------------------------------------------------------------------- the loss
+// A tile's logits stay in its sums: each wave leaves a row's largest logit of
+// its columns and the sum of the exponentials below it, [rows][parts] of
+// float2, and the logit of the row's target where it is among them.
+struct LossTiles {
+  LossArgs a;
+  int first, count;  // rows of this launch
+  int parts;         // a row's: two a column tile
+  float2* part;      // [count][parts]
+  float* at_target;  // [count]
+};
+
+template <int U, int V>
+__device__ __forceinline__ void loss_epilogue(const LossTiles& l, TileSums<U, V>& sums, int m0, int j0, int part) {
+  const int tid = threadIdx.x, lane = tid & 63, wv = tile_wave(tid);
+  const int col = lane & 15, g = lane >> 4;
+  m0 += (wv & 1) * 16 * U + col;
+  j0 += (wv >> 1) * 16 * V;
+  part += wv >> 1;
+  const bool edge = j0 + 16 * V > l.a.vocab;  // columns of the tile that are not there
+#pragma unroll
+  for (int u = 0; u < U; u++) {
+    tile_hold(sums.s[u]);
+    float z[V][4];
+#pragma unroll
+    for (int v = 0; v < V; v++)
+#pragma unroll
+      for (int i = 0; i < 4; i++) {
+        z[v][i] = sums.s[u][v][i];
+        if (edge && j0 + 16 * v + 4 * g + i >= l.a.vocab) z[v][i] = -INFINITY;
+      }
+    float big = -INFINITY;
+#pragma unroll
+    for (int v = 0; v < V; v++) big = fmaxf(big, fmaxf(fmaxf(z[v][0], z[v][1]), fmaxf(z[v][2], z[v][3])));
+    big = over_lanes_max(big);
+    float sum = 0.f;
+    if (__ballot(fabsf(big) == INFINITY)) {  // a largest of +-inf is not subtracted from itself
+#pragma unroll
+      for (int v = 0; v < V; v++)
+#pragma unroll
+        for (int i = 0; i < 4; i++) sum += z[v][i] == big ? 1.f : exp_of(z[v][i] - big);
+    } else {
+#pragma unroll
+      for (int v = 0; v < V; v++)
+#pragma unroll
+        for (int i = 0; i < 4; i++) sum += exp_of(z[v][i] - big);
+    }
+    sum = over_lanes_sum(sum);
+    const int m = m0 + 16 * u;
+    const bool live = m < l.count;
+    if (live && g == 0) l.part[(size_t)m * l.parts + part] = float2{big, sum};
+    const int t = live ? l.a.targets[l.first + m] : -1;
+    const int at = t - j0;  // the target's column here
+    if (__ballot((uint32_t)t < (uint32_t)l.a.vocab && (uint32_t)at < 16u * V)) {
+      if ((uint32_t)t < (uint32_t)l.a.vocab && (uint32_t)at < 16u * V && ((at >> 2) & 3) == g) {
+        float f = 0.f;
+#pragma unroll
+        for (int v = 0; v < V; v++)
+#pragma unroll
+          for (int i = 0; i < 4; i++)
+            if (16 * v + 4 * g + i == at) f = z[v][i];
+        l.at_target[m] = f;
+      }
+    }
+  }
+}
+
+template <int U, int V, typename Stage>
+__device__ __forceinline__ void loss_tile(const LossTiles& l, const TileOperand& om, const TileOperand& oj, Stage& s0,
+                                          Stage& s1, Stage& s2, Stage& s3, int m0, int j0, int part) {
+  TileSums<U, V> sums;
+  tile_product<U, V, false, false>(om, oj, s0, s1, s2, s3, sums);
+  loss_epilogue<U, V>(l, sums, m0, j0, part);
+}
+
+template <int UMAX, int V>
+__global__ __launch_bounds__(256) void lm_loss_kernel(LossTiles l) {
+  constexpr int TM = 32 * UMAX, TJ = 32 * V, KILOS = 2 * UMAX + 2 * V;
+  __shared__ TileStage<KILOS> s0, s1, s2, s3;
+  const int m_tiles = (l.count + TM - 1) / TM, j_tiles = (l.a.vocab + TJ - 1) / TJ;
+  const uint32_t pitch = (uint32_t)l.a.hidden * 2u;
+  for (int t = first_tile(); t < m_tiles * j_tiles; t += gridDim.x) {
+    int mt, jt;
+    place_of(t, m_tiles, j_tiles, &mt, &jt);
+    const int m0 = mt * TM, j0 = jt * TJ;
+    const int rows = l.count - m0 < TM ? l.count - m0 : TM;
+    const TileOperand om = {l.a.h + (int64_t)(l.first + m0) * l.a.hidden, pitch, rows, l.a.hidden};
+    const TileOperand oj = {l.a.w + (int64_t)j0 * l.a.hidden, pitch, l.a.vocab - j0 < TJ ? l.a.vocab - j0 : TJ,
+                            l.a.hidden};
+    if (UMAX == 8 && rows > 128)
+      loss_tile<UMAX, V>(l, om, oj, s0, s1, s2, s3, m0, j0, 2 * jt);
+    else if (UMAX >= 4 && rows > 64)
+      loss_tile<UMAX < 4 ? UMAX : 4, V>(l, om, oj, s0, s1, s2, s3, m0, j0, 2 * jt);
+    else if (rows > 32)
+      loss_tile<2, V>(l, om, oj, s0, s1, s2, s3, m0, j0, 2 * jt);
+    else
+      loss_tile<1, V>(l, om, oj, s0, s1, s2, s3, m0, j0, 2 * jt);
+  }
+}
+
+// A row's parts joined, a block a row: the largest, then the sums below it.
+__global__ __launch_bounds__(256) void lm_loss_join_kernel(LossTiles l) {
+  __shared__ float s_big[4], s_sum[4];
+  const int m = blockIdx.x, tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
+  const float2* p = l.part + (size_t)m * l.parts;
+  float big = -INFINITY, sum = 0.f;
+  for (int i = tid; i < l.parts; i += 256) {
+    const float2 q = p[i];
+    const float b = fmaxf(big, q.x);
+    sum = (big == b ? sum : sum * exp_of(big - b)) + (q.x == b ? q.y : q.y * exp_of(q.x - b));
+    big = b;
+  }
+  const float mine = big;
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) big = fmaxf(big, __shfl_xor(big, o, kWave));
+  if (lane == 0) s_big[wv] = big;
+  __syncthreads();
+  big = fmaxf(fmaxf(s_big[0], s_big[1]), fmaxf(s_big[2], s_big[3]));
+  sum = mine == big ? sum : sum * exp_of(mine - big);
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) sum += __shfl_xor(sum, o, kWave);
+  if (lane == 0) s_sum[wv] = sum;
+  __syncthreads();
+  if (tid == 0) {
+    const float lse = big + logf(s_sum[0] + s_sum[1] + s_sum[2] + s_sum[3]);
+    const int r = l.first + m;
+    l.a.lse[r] = lse;
+    l.a.loss[r] = (uint32_t)l.a.targets[r] < (uint32_t)l.a.vocab ? lse - l.at_target[m] : 0.f;
+  }
+}
+
+// -------------------------------------------------------------- its gradients
+// The rows that have a target, in order, one behind the other: the rest take no
+// part, whatever they hold.  Then, for one piece of the vocabulary after the
+// other: d of the piece, in bf16 (its rounding is as that of a layer's gradient),
+// and from it the piece's dw and its part of dh, which is kept in fp32.
+struct LossGrad {
+  LossGradArgs a;
+  uint16_t* h;       // [rows][hidden] of the rows with a target
+  float2* row;       // their lse and dloss,
+  int32_t* target;   // target,
+  int32_t* place;    // [rows] each row's place among them, or -1
+  int32_t* live;     // [1] their number
+  int32_t* next;     // [8] an XCD's next tile of the second products
+  uint16_t* d;       // [rows][pitch]
+  float* acc;        // [splits][rows][hidden] of dh
+  int pitch, pieces, splits;
+  int first, count;  // this piece's part of the vocabulary
+};
+
+__global__ __launch_bounds__(1024) void lm_loss_rows_kernel(LossGrad l) {
+  __shared__ int s_sum[16];
+  const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
+  int base = 0;
+  for (int r0 = 0; r0 < l.a.rows; r0 += 1024) {
+    const int r = r0 + tid;
+    const int t = r < l.a.rows ? l.a.targets[r] : -1;
+    const bool in = (uint32_t)t < (uint32_t)l.a.vocab;
+    const uint64_t m = __ballot(in);
+    if (lane == 0) s_sum[wv] = __popcll(m);
+    __syncthreads();
+    int at = base + lanes_below(m), all = 0;
+#pragma unroll
+    for (int w = 0; w < 16; w++) {
+      at += w < wv ? s_sum[w] : 0;
+      all += s_sum[w];
+    }
+    if (r < l.a.rows) l.place[r] = in ? at : -1;
+    if (in) {
+      l.target[at] = t;
+      l.row[at] = float2{l.a.lse[r], l.a.dloss[r]};
+    }
+    base += all;
+    __syncthreads();
+  }
+  if (tid == 0) *l.live = base;
+}
+
+__global__ __launch_bounds__(256) void lm_loss_gather_kernel(LossGrad l) {
+  const int r = blockIdx.x, at = l.place[r];
+  if (at < 0) return;
+  const u32x4* from = reinterpret_cast<const u32x4*>(l.a.h + (size_t)r * l.a.hidden);
+  u32x4* to = reinterpret_cast<u32x4*>(l.h + (size_t)at * l.a.hidden);
+  for (int i = threadIdx.x; i < l.a.hidden / 8; i += 256) to[i] = from[i];
+}
+
+// d of a tile; columns past the vocabulary are 0.
+template <int U, int V>
+__device__ __forceinline__ void grad_epilogue(const LossGrad& l, TileSums<U, V>& sums, int live, int m0, int j0) {
+  const int tid = threadIdx.x, lane = tid & 63, wv = tile_wave(tid);
+  const int col = lane & 15, g = lane >> 4;
+  m0 += (wv & 1) * 16 * U + col;
+  j0 += (wv >> 1) * 16 * V;
+  const bool edge = j0 + 16 * V > l.count;
+#pragma unroll
+  for (int u = 0; u < U; u++) {
+    tile_hold(sums.s[u]);
+    const int m = m0 + 16 * u, row = m < live ? m : live - 1;
+    const float2 q = l.row[row];
+    const int at = l.target[row] - l.first - j0;
+    const bool hit = __ballot((uint32_t)at < 16u * V) != 0;
+#pragma unroll
+    for (int v = 0; v < V; v++)
+#pragma unroll
+      for (int i = 0; i < 4; i++) {
+        float p = exp_of(sums.s[u][v][i] - q.x);
+        if (hit && 16 * v + 4 * g + i == at) p -= 1.f;
+        p *= q.y;
+        if (edge && j0 + 16 * v + 4 * g + i >= l.count) p = 0.f;
+        sums.s[u][v][i] = p;
+      }
+#pragma unroll
+    for (int v = 0; v < V; v += 2) {
+      const u32x4 o = tile_pair(sums.s[u][v], sums.s[u][v + 1]);
+      if (m < live) *reinterpret_cast<u32x4*>(l.d + (size_t)m * l.pitch + j0 + 16 * v + tile_pair_at(lane)) = o;
+    }
+  }
+}
+
+template <int U, int V, typename Stage>
+__device__ __forceinline__ void grad_tile(const LossGrad& l, const TileOperand& om, const TileOperand& oj, Stage& s0,
+                                          Stage& s1, Stage& s2, Stage& s3, int live, int m0, int j0) {
+  TileSums<U, V> sums;
+  tile_product<U, V, false, false>(om, oj, s0, s1, s2, s3, sums);
+  grad_epilogue<U, V>(l, sums, live, m0, j0);
+}
+
+template <int UMAX, int V>
+__global__ __launch_bounds__(256) void lm_loss_d_kernel(LossGrad l) {
+  constexpr int TM = 32 * UMAX, TJ = 32 * V, KILOS = 2 * UMAX + 2 * V;
+  __shared__ TileStage<KILOS> s0, s1, s2, s3;
+  if (blockIdx.x == 0 && threadIdx.x < 8) l.next[threadIdx.x] = 0;
+  const int live = __builtin_amdgcn_readfirstlane(*l.live);
+  const int m_tiles = (live + TM - 1) / TM, j_tiles = (l.count + TJ - 1) / TJ;
+  const uint32_t pitch = (uint32_t)l.a.hidden * 2u;
+  for (int t = first_tile(); t < m_tiles * j_tiles; t += gridDim.x) {
+    int mt, jt;
+    place_of(t, m_tiles, j_tiles, &mt, &jt);
+    const int m0 = mt * TM, j0 = jt * TJ;
+    const int rows = live - m0 < TM ? live - m0 : TM;
+    const TileOperand om = {l.h + (int64_t)m0 * l.a.hidden, pitch, rows, l.a.hidden};
+    const TileOperand oj = {l.a.w + (int64_t)(l.first + j0) * l.a.hidden, pitch,
+                            l.count - j0 < TJ ? l.count - j0 : TJ, l.a.hidden};
+    if (UMAX == 8 && rows > 128)
+      grad_tile<UMAX, V>(l, om, oj, s0, s1, s2, s3, live, m0, j0);
+    else if (UMAX >= 4 && rows > 64)
+      grad_tile<UMAX < 4 ? UMAX : 4, V>(l, om, oj, s0, s1, s2, s3, live, m0, j0);
+    else if (rows > 32)
+      grad_tile<2, V>(l, om, oj, s0, s1, s2, s3, live, m0, j0);
+    else
+      grad_tile<1, V>(l, om, oj, s0, s1, s2, s3, live, m0, j0);
+  }
+}
+
+// A tile's part of dh: kept, or added to what earlier pieces left.
+template <int U, typename Stage>
+__device__ __forceinline__ void dh_tile(const LossGrad& l, const TileOperand& om, const TileOperand& oj, Stage& s0,
+                                        Stage& s1, Stage& s2, Stage& s3, float* acc, int live, int m0, int j0) {
+  TileSums<U, 8> sums;
+  tile_product<U, 8, false, true>(om, oj, s0, s1, s2, s3, sums);
+  if (l.first == 0)
+    store_tile<U, 8, float, false>(sums, acc, m0, live, j0, l.a.hidden);
+  else
+    store_tile<U, 8, float, true>(sums, acc, m0, live, j0, l.a.hidden);
+}
+
+// The two products of a piece's d, in one launch: the tiles of dh, which are
+// long (the piece's columns), first, then those of dw (the rows).  Each XCD has
+// its eighth of either, whose tiles its blocks take one after the other, so that
+// tiles under way at once share operands in its L2; then those left of others.
+template <typename T, bool ADD>
+__global__ __launch_bounds__(256) void lm_loss_products_kernel(LossGrad l) {
+  __shared__ TileStage<32> s0, s1, s2, s3;
+  __shared__ int s_next;
+  const int live = __builtin_amdgcn_readfirstlane(*l.live);
+  const int H = l.a.hidden, tid = threadIdx.x;
+  const int h_tiles = (H + 255) / 256, v_tiles = (l.count + 255) / 256, m_tiles = (live + 255) / 256;
+  const int dh_tiles = l.a.dh ? m_tiles * h_tiles * l.splits : 0;
+  const int dw_tiles = l.a.dw ? v_tiles * h_tiles : 0;
+  const int steps = (l.count + kStepC - 1) / kStepC;
+  const int part = (steps + l.splits - 1) / l.splits * kStepC;  // columns of a split
+  const uint32_t pitch_h = (uint32_t)H * 2u, pitch_d = (uint32_t)l.pitch * 2u;
+  for (int x = 0; x < 8; x++) {
+    const int xcd = (blockIdx.x + x) & 7;
+    const int dh0 = (int)((int64_t)dh_tiles * xcd / 8), dh_n = (int)((int64_t)dh_tiles * (xcd + 1) / 8) - dh0;
+    const int dw0 = (int)((int64_t)dw_tiles * xcd / 8), dw_n = (int)((int64_t)dw_tiles * (xcd + 1) / 8) - dw0;
+    for (;;) {
+      __syncthreads();
+      if (tid == 0) s_next = atomicAdd(l.next + xcd, 1);
+      __syncthreads();
+      const int i = __builtin_amdgcn_readfirstlane(s_next);
+      if (i >= dh_n + dw_n) break;
+      int mt, jt;
+      if (i < dh_n) {
+        const int t = dh0 + i, split = t / (m_tiles * h_tiles);
+        place_of(t - split * (m_tiles * h_tiles), m_tiles, h_tiles, &mt, &jt);
+        const int m0 = mt * 256, j0 = jt * 256, c0 = split * part;
+        const int c = l.count - c0 < part ? l.count - c0 : part;
+        if (c <= 0 && l.first > 0) continue;
+        const int rows = live - m0 < 256 ? live - m0 : 256;
+        // (d's columns past the vocabulary are 0, to a multiple of 8)
+        const TileOperand om = {l.d + (int64_t)m0 * l.pitch + c0, pitch_d, rows, c > 0 ? (c + 7) / 8 * 8 : 0};
+        const TileOperand oj = {l.a.w + (int64_t)(l.first + (c > 0 ? c0 : 0)) * H + j0, pitch_h,
+                                H - j0 < 256 ? H - j0 : 256, c > 0 ? c : 0};
+        float* acc = l.acc + (int64_t)split * l.a.rows * H;
+        if (rows > 128)
+          dh_tile<8>(l, om, oj, s0, s1, s2, s3, acc, live, m0, j0);
+        else if (rows > 64)
+          dh_tile<4>(l, om, oj, s0, s1, s2, s3, acc, live, m0, j0);
+        else if (rows > 32)
+          dh_tile<2>(l, om, oj, s0, s1, s2, s3, acc, live, m0, j0);
+        else
+          dh_tile<1>(l, om, oj, s0, s1, s2, s3, acc, live, m0, j0);
+      } else {
+        place_of(dw0 + i - dh_n, v_tiles, h_tiles, &mt, &jt);
+        const int m0 = mt * 256, j0 = jt * 256;
+        const int own = l.count - m0 < 256 ? (l.count - m0 + 7) / 8 * 8 : 256;
+        const TileOperand om = {l.d + m0, pitch_d, own, live};
+        const TileOperand oj = {l.h + j0, pitch_h, H - j0 < 256 ? H - j0 : 256, live};
+        TileSums<8, 8> sums;
+        tile_product<8, 8, true, true>(om, oj, s0, s1, s2, s3, sums);
+        T* out = reinterpret_cast<T*>(l.a.dw) + (int64_t)l.first * H;
+        store_tile<8, 8, T, ADD>(sums, out, m0, l.count, j0, H);
+      }
+    }
+  }
+}
+
+// dh from its parts, in order; 0 for a row without a target.
+__global__ __launch_bounds__(256) void lm_loss_dh_kernel(LossGrad l) {
+  const int r = blockIdx.x, at = l.place[r], H = l.a.hidden;
+  const int c = (blockIdx.y * 256 + threadIdx.x) * 4;
+  if (c >= H) return;
+  v4f s = {0.f, 0.f, 0.f, 0.f};
+  if (at >= 0)
+    for (int i = 0; i < l.splits; i++)
+      s += *reinterpret_cast<const v4f*>(l.acc + ((size_t)i * l.a.rows + at) * H + c);
+  uint2 o;
+  o.x = (uint32_t)f32_to_bf16(s[0]) | ((uint32_t)f32_to_bf16(s[1]) << 16);
+  o.y = (uint32_t)f32_to_bf16(s[2]) | ((uint32_t)f32_to_bf16(s[3]) << 16);
+  *reinterpret_cast<uint2*>(l.a.dh + (size_t)r * H + c) = o;
+}
+
+// --------------------------------------------------------------------- launches
+// Rows of a launch of the loss, for its parts' memory.
+constexpr int kLossRows = 16384;
+// Tiles of 256 x 256 above this many rows, else of 64 x 128.
+constexpr int kLossFew = 64;
+
+static int loss_parts(int rows, int vocab) {
+  return rows > kLossFew ? 2 * ((vocab + 255) / 256) : 2 * ((vocab + 127) / 128);
+}
+static size_t up256(size_t n) { return (n + 255) / 256 * 256; }
+
+size_t loss_workspace(int rows, int vocab, int) {
+  const size_t r = rows < kLossRows ? rows : kLossRows;
+  // (the last of several launches may take the other tiles)
+  const size_t parts = rows > kLossRows ? loss_parts(1, vocab) : loss_parts(rows, vocab);
+  return up256(r * parts * sizeof(float2)) + up256(r * sizeof(float));
+}
+
+hipError_t launch_loss(const LossArgs& a, void* workspace, hipStream_t stream) {
+  LossTiles l = {};
+  l.a = a;
+  const size_t r = a.rows < kLossRows ? a.rows : kLossRows;
+  const size_t parts = a.rows > kLossRows ? loss_parts(1, a.vocab) : loss_parts(a.rows, a.vocab);
+  l.part = static_cast<float2*>(workspace);
+  l.at_target = reinterpret_cast<float*>(static_cast<char*>(workspace) + up256(r * parts * sizeof(float2)));
+  for (l.first = 0; l.first < a.rows; l.first += kLossRows) {
+    l.count = a.rows - l.first < kLossRows ? a.rows - l.first : kLossRows;
+    l.parts = loss_parts(l.count, a.vocab);
+    int blocks;
+    const bool few = l.count <= kLossFew;
+    const int64_t tiles = few ? (int64_t)(a.vocab + 127) / 128
+                              : (int64_t)((l.count + 255) / 256) * ((a.vocab + 255) / 256);
+    hipError_t e = tile_blocks(tiles, few ? 2 : 1, &blocks);
+    if (e != hipSuccess) return e;
+    if (few)
+      hipLaunchKernelGGL((lm_loss_kernel<2, 4>), dim3(blocks), dim3(256), 0, stream, l);
+    else
+      hipLaunchKernelGGL((lm_loss_kernel<8, 8>), dim3(blocks), dim3(256), 0, stream, l);
+    hipLaunchKernelGGL(lm_loss_join_kernel, dim3(l.count), dim3(256), 0, stream, l);
+    e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
+// Columns of a piece: d of at most 128 MB, in multiples of 256.
+constexpr size_t kLossPieceBytes = (size_t)128 << 20;
+
+static size_t loss_grad_plan(LossGrad* l, char* base) {
+  const LossGradArgs& a = l->a;
+  const int whole = (a.vocab + 255) / 256;
+  int64_t most = (int64_t)(kLossPieceBytes / ((size_t)a.rows * 512));
+  most = most < 1 ? 1 : (most < whole ? most : whole);
+  l->pieces = (int)((whole + most - 1) / most);
+  l->pitch = (whole + l->pieces - 1) / l->pieces * 256;
+  // dh's products split over a piece's columns where its tiles are fewer than the
+  // CUs: parts of at least 32 steps, 32 of them at most
+  const int64_t tiles = (int64_t)((a.rows + 255) / 256) * ((a.hidden + 255) / 256);
+  int64_t splits = 256 / tiles;
+  const int64_t by_steps = l->pitch / (32 * kStepC);
+  if (splits > by_steps) splits = by_steps;
+  l->splits = splits < 1 ? 1 : (splits > 32 ? 32 : (int)splits);
+  size_t o = 0;
+  auto take = [&](size_t bytes) {
+    char* p = base + o;
+    o += up256(bytes);
+    return p;
+  };
+  const size_t R = a.rows;
+  l->h = reinterpret_cast<uint16_t*>(take(R * a.hidden * 2));
+  l->row = reinterpret_cast<float2*>(take(R * sizeof(float2)));
+  l->target = reinterpret_cast<int32_t*>(take(R * 4));
+  l->place = reinterpret_cast<int32_t*>(take(R * 4));
+  l->live = reinterpret_cast<int32_t*>(take(4));
+  l->next = reinterpret_cast<int32_t*>(take(8 * 4));
+  l->d = reinterpret_cast<uint16_t*>(take(R * l->pitch * 2));
+  l->acc = reinterpret_cast<float*>(take((size_t)l->splits * R * a.hidden * 4));
+  return o;
+}
+
+size_t loss_backward_workspace(int rows, int vocab, int hidden) {
+  LossGrad l = {};
+  l.a.rows = rows;
+  l.a.vocab = vocab;
+  l.a.hidden = hidden;
+  return loss_grad_plan(&l, nullptr);
+}
+
+hipError_t launch_loss_backward(const LossGradArgs& a, void* workspace, hipStream_t stream) {
+  LossGrad l = {};
+  l.a = a;
+  loss_grad_plan(&l, static_cast<char*>(workspace));
+  hipLaunchKernelGGL(lm_loss_rows_kernel, dim3(1), dim3(1024), 0, stream, l);
+  hipLaunchKernelGGL(lm_loss_gather_kernel, dim3(a.rows), dim3(256), 0, stream, l);
+  for (l.first = 0; l.first < a.vocab; l.first += l.pitch) {
+    l.count = a.vocab - l.first < l.pitch ? a.vocab - l.first : l.pitch;
+    int blocks;
+    const bool few = a.rows <= kLossFew;
+    const int64_t tiles = few ? (int64_t)(l.count + 127) / 128
+                              : (int64_t)((a.rows + 255) / 256) * ((l.count + 255) / 256);
+    hipError_t e = tile_blocks(tiles, few ? 2 : 1, &blocks);
+    if (e != hipSuccess) return e;
+    if (few)
+      hipLaunchKernelGGL((lm_loss_d_kernel<2, 4>), dim3(blocks), dim3(256), 0, stream, l);
+    else
+      hipLaunchKernelGGL((lm_loss_d_kernel<8, 8>), dim3(blocks), dim3(256), 0, stream, l);
+    const int64_t products = ((int64_t)((a.rows + 255) / 256) * l.splits + (l.count + 255) / 256) *
+                             ((a.hidden + 255) / 256);
+    e = tile_blocks(products, 1, &blocks);
+    if (e != hipSuccess) return e;
+    if (a.f32 && a.add)
+      hipLaunchKernelGGL((lm_loss_products_kernel<float, true>), dim3(blocks), dim3(256), 0, stream, l);
+    else if (a.f32)
+      hipLaunchKernelGGL((lm_loss_products_kernel<float, false>), dim3(blocks), dim3(256), 0, stream, l);
+    else if (a.add)
+      hipLaunchKernelGGL((lm_loss_products_kernel<uint16_t, true>), dim3(blocks), dim3(256), 0, stream, l);
+    else
+      hipLaunchKernelGGL((lm_loss_products_kernel<uint16_t, false>), dim3(blocks), dim3(256), 0, stream, l);
+  }
+  if (a.dh)
+    hipLaunchKernelGGL(lm_loss_dh_kernel, dim3(a.rows, (a.hidden + 1023) / 1024), dim3(256), 0, stream, l);
+  return hipGetLastError();
+}
+
+}  // namespace moe

@@ -70,68 +70,6 @@ __device__ __forceinline__ int expert_of_tile(const ProductArgs& a, const Produc
   return __builtin_amdgcn_readfirstlane(e0 + __popcll(__ballot(below) & 0xFFFFu) - 1);
 }
 
-// The place of tile t of m_tiles x j_tiles: four row tiles in a run, then the
-// next column tile, so that the 32 blocks of an XCD share few rows and columns.
-__device__ __forceinline__ void place_of(int t, int m_tiles, int j_tiles, int* mt, int* jt) {
-  const int band = t / (4 * j_tiles), m0 = 4 * band;
-  const int high = m_tiles - m0 < 4 ? m_tiles - m0 : 4;
-  const int r = t - band * 4 * j_tiles;
-  *jt = r / high;
-  *mt = m0 + (r - *jt * high);
-}
-
-// Blocks go to the 8 XCDs in turn, each with an L2 of its own: of every
-// gridDim.x tiles (a multiple of 8) an XCD takes neighbouring ones.
-__device__ __forceinline__ int first_tile() {
-  return (int)(blockIdx.x & 7) * (int)(gridDim.x >> 3) + (int)(blockIdx.x >> 3);
-}
-
-// Stores a wave's sums as rows m0 + .. of out, of `cols` columns; rows from
-// m_end and columns from j_end on are not there.
-template <int U, int V, typename T, bool ADD>
-__device__ __forceinline__ void store_tile(TileSums<U, V>& sums, T* out, int64_t m0, int64_t m_end, int j0, int cols) {
-  const int tid = threadIdx.x, lane = tid & 63, wv = tile_wave(tid);
-  const int col = lane & 15, g = lane >> 4;
-  auto& acc = sums.s;
-  m0 += (wv & 1) * 16 * U + col;
-  j0 += (wv >> 1) * 16 * V;
-#pragma unroll
-  for (int u = 0; u < U; u++) {
-    tile_hold(acc[u]);
-    const int64_t m = m0 + 16 * u;
-    T* row = out + m * cols;
-    if constexpr (sizeof(T) == 4) {
-#pragma unroll
-      for (int v = 0; v < V; v++) {
-        const int j = j0 + 16 * v + 4 * g;
-        if (m < m_end && j < cols) {
-          v4f s = acc[u][v];
-          if constexpr (ADD) s += *reinterpret_cast<const v4f*>(row + j);
-          *reinterpret_cast<v4f*>(row + j) = s;
-        }
-      }
-    } else {
-#pragma unroll
-      for (int v = 0; v < V; v += 2) {
-        if constexpr (ADD) {  // in place of the sums: a lane's own 4 columns
-#pragma unroll
-          for (int h = 0; h < 2; h++) {
-            const int j = j0 + 16 * (v + h) + 4 * g;
-            if (m < m_end && j < cols) {
-              const uint2 o = *reinterpret_cast<const uint2*>(row + j);
-              acc[u][v + h] += v4f{__uint_as_float(o.x << 16), __uint_as_float(o.x & 0xFFFF0000u),
-                                   __uint_as_float(o.y << 16), __uint_as_float(o.y & 0xFFFF0000u)};
-            }
-          }
-        }
-        const u32x4 o = tile_pair(acc[u][v], acc[u][v + 1]);
-        const int j = j0 + 16 * v + tile_pair_at(lane);
-        if (m < m_end && j < cols) *reinterpret_cast<u32x4*>(row + j) = o;
-      }
-    }
-  }
-}
-
 template <int U, int V, bool DX, typename Stage, typename T>
 __device__ __forceinline__ void product_tile(const TileOperand& om, const TileOperand& oj, Stage& s0, Stage& s1,
                                              Stage& s2, Stage& s3, T* out, int64_t lo, int64_t hi, int j0, int cols) {
@@ -204,17 +142,6 @@ __global__ __launch_bounds__(256) void moe_product_dw_kernel(ProductArgs a) {
   }
 }
 
-static hipError_t product_blocks(int64_t tiles, int a_cu, int* blocks) {
-  int dev = 0, cus = 0;
-  hipError_t e = hipGetDevice(&dev);
-  if (e == hipSuccess) e = hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev);
-  if (e != hipSuccess) return e;
-  const int64_t most = (int64_t)(cus / 8 > 0 ? cus / 8 : 1) * 8 * a_cu;
-  const int64_t want = (tiles + 7) / 8 * 8;
-  *blocks = (int)(want < most ? want : most);
-  return hipSuccess;
-}
-
 // Upper bound of the tiles of `tm` rows by `tj` columns.
 static int64_t most_tiles(const ProductArgs& a, int cols, int tm, int tj) {
   const int64_t m = a.rows / tm + (a.rows < a.experts ? a.rows : a.experts);
@@ -227,11 +154,11 @@ static hipError_t launch_rows(const ProductArgs& a, hipStream_t stream) {
   int blocks;
   const bool large = a.rows > (int64_t)48 * a.experts && most_tiles(a, cols, 256, 256) >= 256;
   if (large) {
-    const hipError_t e = product_blocks(most_tiles(a, cols, 256, 256), 1, &blocks);
+    const hipError_t e = tile_blocks(most_tiles(a, cols, 256, 256), 1, &blocks);
     if (e != hipSuccess) return e;
     hipLaunchKernelGGL((moe_product_kernel<8, 8, DX, T>), dim3(blocks), dim3(256), 0, stream, a);
   } else {
-    const hipError_t e = product_blocks(most_tiles(a, cols, 64, 128), 2, &blocks);
+    const hipError_t e = tile_blocks(most_tiles(a, cols, 64, 128), 2, &blocks);
     if (e != hipSuccess) return e;
     hipLaunchKernelGGL((moe_product_kernel<2, 4, DX, T>), dim3(blocks), dim3(256), 0, stream, a);
   }
@@ -253,11 +180,11 @@ static hipError_t launch_dw(const ProductArgs& a, hipStream_t stream) {
   const int64_t large = (int64_t)a.experts * ((a.n + 255) / 256) * ((a.k + 255) / 256);
   int blocks;
   if (large >= 256) {
-    const hipError_t e = product_blocks(large, 1, &blocks);
+    const hipError_t e = tile_blocks(large, 1, &blocks);
     if (e != hipSuccess) return e;
     hipLaunchKernelGGL((moe_product_dw_kernel<8, 8, T, ADD>), dim3(blocks), dim3(256), 0, stream, a);
   } else {
-    const hipError_t e = product_blocks((int64_t)a.experts * ((a.n + 127) / 128) * ((a.k + 127) / 128), 2, &blocks);
+    const hipError_t e = tile_blocks((int64_t)a.experts * ((a.n + 127) / 128) * ((a.k + 127) / 128), 2, &blocks);
     if (e != hipSuccess) return e;
     hipLaunchKernelGGL((moe_product_dw_kernel<4, 4, T, ADD>), dim3(blocks), dim3(256), 0, stream, a);
   }

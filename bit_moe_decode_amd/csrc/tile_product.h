@@ -287,4 +287,79 @@ __device__ __forceinline__ u32x4 tile_pair(const v4f& x, const v4f& y) {
 }
 __device__ __forceinline__ int tile_pair_at(int lane) { return 16 * ((lane >> 4) & 1) + 8 * (lane >> 5); }
 
+// The place of tile t of m_tiles x j_tiles: four row tiles in a run, then the
+// next column tile, so that the 32 blocks of an XCD share few rows and columns.
+__device__ __forceinline__ void place_of(int t, int m_tiles, int j_tiles, int* mt, int* jt) {
+  const int band = t / (4 * j_tiles), m0 = 4 * band;
+  const int high = m_tiles - m0 < 4 ? m_tiles - m0 : 4;
+  const int r = t - band * 4 * j_tiles;
+  *jt = r / high;
+  *mt = m0 + (r - *jt * high);
+}
+
+// Blocks go to the 8 XCDs in turn, each with an L2 of its own: of every
+// gridDim.x tiles (a multiple of 8) an XCD takes neighbouring ones.
+__device__ __forceinline__ int first_tile() {
+  return (int)(blockIdx.x & 7) * (int)(gridDim.x >> 3) + (int)(blockIdx.x >> 3);
+}
+
+// Stores a wave's sums as rows m0 + .. of out, of `cols` columns; rows from
+// m_end and columns from j_end on are not there.
+template <int U, int V, typename T, bool ADD>
+__device__ __forceinline__ void store_tile(TileSums<U, V>& sums, T* out, int64_t m0, int64_t m_end, int j0, int cols) {
+  const int tid = threadIdx.x, lane = tid & 63, wv = tile_wave(tid);
+  const int col = lane & 15, g = lane >> 4;
+  auto& acc = sums.s;
+  m0 += (wv & 1) * 16 * U + col;
+  j0 += (wv >> 1) * 16 * V;
+#pragma unroll
+  for (int u = 0; u < U; u++) {
+    tile_hold(acc[u]);
+    const int64_t m = m0 + 16 * u;
+    T* row = out + m * cols;
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+      for (int v = 0; v < V; v++) {
+        const int j = j0 + 16 * v + 4 * g;
+        if (m < m_end && j < cols) {
+          v4f s = acc[u][v];
+          if constexpr (ADD) s += *reinterpret_cast<const v4f*>(row + j);
+          *reinterpret_cast<v4f*>(row + j) = s;
+        }
+      }
+    } else {
+#pragma unroll
+      for (int v = 0; v < V; v += 2) {
+        if constexpr (ADD) {  // in place of the sums: a lane's own 4 columns
+#pragma unroll
+          for (int h = 0; h < 2; h++) {
+            const int j = j0 + 16 * (v + h) + 4 * g;
+            if (m < m_end && j < cols) {
+              const uint2 o = *reinterpret_cast<const uint2*>(row + j);
+              acc[u][v + h] += v4f{__uint_as_float(o.x << 16), __uint_as_float(o.x & 0xFFFF0000u),
+                                   __uint_as_float(o.y << 16), __uint_as_float(o.y & 0xFFFF0000u)};
+            }
+          }
+        }
+        const u32x4 o = tile_pair(acc[u][v], acc[u][v + 1]);
+        const int j = j0 + 16 * v + tile_pair_at(lane);
+        if (m < m_end && j < cols) *reinterpret_cast<u32x4*>(row + j) = o;
+      }
+    }
+  }
+}
+
+// Blocks of a launch over `tiles` tiles: `a_cu` for each CU of the current device
+// at most, a multiple of 8.
+inline hipError_t tile_blocks(int64_t tiles, int a_cu, int* blocks) {
+  int dev = 0, cus = 0;
+  hipError_t e = hipGetDevice(&dev);
+  if (e == hipSuccess) e = hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev);
+  if (e != hipSuccess) return e;
+  const int64_t most = (int64_t)(cus / 8 > 0 ? cus / 8 : 1) * 8 * a_cu;
+  const int64_t want = (tiles + 7) / 8 * 8;
+  *blocks = (int)(want < most ? want : most);
+  return hipSuccess;
+}
+
 }  // namespace moe

@@ -14,7 +14,8 @@
  * by expert and back, with gradients (moe_sort, moe_gather, moe_combine), the
  * experts' step for any number of tokens (moe_wide_step), low-rank adapters of
  * many requests (lora_apply, lowbit_gemv_lora), and matrix products of the
- * sorted rows in bf16, with gradients (moe_product).
+ * sorted rows in bf16, with gradients (moe_product).  At the model's other end
+ * stands the LM head's loss with its gradients (lm_head_loss).
  *
  * Sources.  The operations follow the body of sgl-amd-mono PR #85 ("...MoE
  * expert dedup and weight loads, kernarg reload, LM-head loads"), quoted on the
@@ -436,6 +437,48 @@ moe_status moe_product_backward(const moe_product_shape* shape, const uint16_t* 
                                 const uint16_t* x, const uint16_t* w, const int32_t* offsets,
                                 uint16_t* dx, void* dw, int32_t add, void* workspace,
                                 size_t ws_bytes, hipStream_t stream);
+
+/* ---- Softmax cross entropy of the LM head: with the logits z[r, v] = w[v] . h[r]
+ * of bf16 rows and weights (lowbit_gemv's bf16 head, for any number of rows),
+ * which no call keeps.  Logits, exponentials and sums are fp32's. */
+#define MOE_LOSS_MAX_ROWS (1 << 20)
+#define MOE_LOSS_MAX_VOCAB (1 << 20)
+typedef struct {
+  int32_t dtype;   /* moe_dtype of dw (lm_head_loss_backward) */
+  int32_t rows;    /* 0..MOE_LOSS_MAX_ROWS */
+  int32_t vocab;   /* 1..MOE_LOSS_MAX_VOCAB */
+  int32_t hidden;  /* a multiple of 8, 8..32768 */
+} lm_head_shape;
+
+/* Bytes of workspace the two calls below need, or 0 when the shape is not
+ * supported (or has no rows). */
+size_t lm_head_loss_workspace_size(const lm_head_shape* shape);
+size_t lm_head_loss_backward_workspace_size(const lm_head_shape* shape);
+
+/* lse[r] = log sum_v exp z[r, v] and loss[r] = lse[r] - z[r, targets[r]], the
+ * loss 0 where the target is outside [0, vocab) (a padded row):
+ *  h        bf16 [rows, hidden], w bf16 [vocab, hidden]
+ *  targets  int32 [rows]
+ *  loss, lse  fp32 [rows]
+ * The buffers must not overlap.  The workspace is scratch of this call, 16-byte
+ * aligned; calls that overlap in time need one each. */
+moe_status lm_head_loss(const lm_head_shape* shape, const uint16_t* h, const uint16_t* w,
+                        const int32_t* targets, float* loss, float* lse, void* workspace,
+                        size_t ws_bytes, hipStream_t stream);
+
+/* Its gradients: with d[r, v] = (exp(z[r, v] - lse[r]) - [v = targets[r]])
+ * dloss[r], rounded to bf16 once and then used in both,
+ *  dh  bf16 [rows, hidden]: dh[r] = sum_v d[r, v] w[v]
+ *  dw  [vocab, hidden]: dw[v] = sum_r d[r, v] h[r]; with add != 0 it is added to
+ *      dw, in fp32 before the rounding
+ * of which either may be NULL, and is then not computed.  lse is lm_head_loss's
+ * of the same h and w, dloss fp32 [rows].  A row whose target is outside [0,
+ * vocab) has a dh of 0 and adds nothing to dw, whatever its h, lse and dloss
+ * hold. */
+moe_status lm_head_loss_backward(const lm_head_shape* shape, const uint16_t* h, const uint16_t* w,
+                                 const int32_t* targets, const float* lse, const float* dloss,
+                                 uint16_t* dh, void* dw, int32_t add, void* workspace,
+                                 size_t ws_bytes, hipStream_t stream);
 
 /* ---- Low-rank adapters of many requests beside a projection they share.
  *
