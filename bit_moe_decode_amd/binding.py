@@ -88,6 +88,10 @@ class HeadShape(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in ("dtype", "rows", "vocab", "hidden")]
 
 
+class EmbedShape(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("dtype", "rows", "vocab", "hidden")]
+
+
 class LoraSet(ctypes.Structure):
     _fields_ = [("n_adapters", ctypes.c_int32), ("max_rank", ctypes.c_int32),
                 ("n", ctypes.c_int32), ("k", ctypes.c_int32), ("a", ctypes.c_void_p),
@@ -140,6 +144,7 @@ def lib():
         shape = ctypes.POINTER(RowShape)
         lora = ctypes.POINTER(LoraSet)
         product, head = ctypes.POINTER(ProductShape), ctypes.POINTER(HeadShape)
+        rows_of, f32 = ctypes.POINTER(EmbedShape), ctypes.c_float
         for name, restype, args in (
                 ("moe_sort_workspace_size", size, [i32, i32, i32]),
                 ("moe_sort", ctypes.c_int, [p, i32, i32, i32, p, p, p, p, size, p]),
@@ -158,6 +163,9 @@ def lib():
                 ("lm_head_loss", ctypes.c_int, [head, p, p, p, p, p, p, size, p]),
                 ("lm_head_loss_backward_workspace_size", size, [head]),
                 ("lm_head_loss_backward", ctypes.c_int, [head, p, p, p, p, p, p, p, i32, p, size, p]),
+                ("embed", ctypes.c_int, [rows_of, p, p, f32, p, p]),
+                ("embed_backward_workspace_size", size, [rows_of]),
+                ("embed_backward", ctypes.c_int, [rows_of, p, p, f32, i32, p, i32, p, size, p]),
                 ("lora_workspace_size", size, [lora, i32]),
                 ("lora_apply", ctypes.c_int, [lora, p, p, i32, p, p, p, size, p]),
                 ("lowbit_gemv_lora", ctypes.c_int, [ctypes.POINTER(LowbitMatrix), lora, p, p, i32,
@@ -637,6 +645,41 @@ def lm_head_loss_backward(h, w, targets, lse, dloss, dh=None, dw=None, workspace
     _done(lib().lm_head_loss_backward(ctypes.byref(HeadShape(dtype, r, v, k)), h.data_ptr(), w.data_ptr(),
                                       targets.data_ptr(), lse.data_ptr(), dloss.data_ptr(), _address(dh),
                                       _address(dw), int(add), ws, nbytes, _stream(stream)), "lm_head_loss_backward")
+
+
+# ------------------------------------------------------------ embedding lookup
+EMBED_MAX_ROWS = 1 << 24   # MOE_EMBED_MAX_ROWS
+EMBED_MAX_VOCAB = 1 << 20  # MOE_EMBED_MAX_VOCAB
+
+
+def embed(ids, table, out, scale=1.0, stream=None):
+    """out[r] = scale table[ids[r]], 0 for an id outside the table: ids int32
+    [rows], table bf16 or float32 [vocab, hidden], out [rows, hidden] of its type."""
+    (v, h), r = table.shape, ids.shape[0]
+    dtype = _moe_dtype("embed", table.dtype)
+    _check("embed", ids.get_device(), ("ids", ids, _torch.int32, (r,)), ("table", table, table.dtype, (v, h)),
+           ("out", out, table.dtype, (r, h)))
+    _done(lib().embed(ctypes.byref(EmbedShape(dtype, r, v, h)), ids.data_ptr(), table.data_ptr(), float(scale),
+                      out.data_ptr(), _stream(stream)), "embed")
+
+
+def embed_backward_workspace_size(rows, vocab, hidden) -> int:
+    return lib().embed_backward_workspace_size(ctypes.byref(EmbedShape(0, int(rows), int(vocab), int(hidden))))
+
+
+def embed_backward(ids, dout, dtable, workspace=None, scale=1.0, add=False, stream=None):
+    """dtable[v] = scale sum of dout[r] over the rows with ids[r] = v, 0 without
+    any (with add: added to dtable): ids int32 [rows], dout bf16 or float32
+    [rows, hidden], dtable bf16 or float32 [vocab, hidden]; workspace: a device
+    tensor of embed_backward_workspace_size bytes (None where that is 0)."""
+    (v, h), r = dtable.shape, ids.shape[0]
+    dtype, table_dtype = (_moe_dtype("embed_backward", t.dtype) for t in (dout, dtable))
+    _check("embed_backward", ids.get_device(), ("ids", ids, _torch.int32, (r,)), ("dout", dout, dout.dtype, (r, h)),
+           ("dtable", dtable, dtable.dtype, (v, h)))
+    ws, nbytes = _space("embed_backward", workspace, ids.get_device())
+    _done(lib().embed_backward(ctypes.byref(EmbedShape(dtype, r, v, h)), ids.data_ptr(), dout.data_ptr(),
+                               float(scale), table_dtype, dtable.data_ptr(), int(add), ws, nbytes,
+                               _stream(stream)), "embed_backward")
 
 
 # ----------------------------------------------------------- low-rank adapters

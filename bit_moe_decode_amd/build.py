@@ -15,7 +15,7 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libbit_moe_decode.so")
 SOURCES = ["api.hip", "router.hip", "route.hip", "upgate.hip", "down.hip", "lowbit_gemv.hip", "dense_gemv.hip",
-           "token_rows.hip", "wide.hip", "lora.hip", "products.hip", "lm_loss.hip"]
+           "token_rows.hip", "wide.hip", "lora.hip", "products.hip", "lm_loss.hip", "embed.hip"]
 ARCH = "gfx950"
 FLAGS = [
     "-O3", "-std=c++17", "-fPIC", f"--offload-arch={ARCH}",

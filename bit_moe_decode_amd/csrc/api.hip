@@ -7,6 +7,7 @@
 #include <new>
 
 #include "device_common.h"
+#include "embed.h"
 #include "lm_loss.h"
 #include "lora.h"
 #include "products.h"
@@ -637,6 +638,27 @@ bool any_overlap(const void* const* buf, const size_t* len, int first, int n) {
   return false;
 }
 
+// ---- the embedding
+
+moe_status check_embed(const embed_shape* s) {
+  if (!s) return MOE_ERR_INVALID_ARG;
+  if (s->dtype != MOE_BF16 && s->dtype != MOE_F32) return MOE_ERR_UNSUPPORTED;
+  if (s->rows < 0 || s->vocab < 1 || s->hidden < 1) return MOE_ERR_INVALID_ARG;
+  if (s->rows > MOE_EMBED_MAX_ROWS || s->vocab > MOE_EMBED_MAX_VOCAB || s->hidden > MOE_MAX_ROW)
+    return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+EmbedArgs embed_args(const embed_shape* s, const int32_t* ids, float scale) {
+  return {ids, s->rows, s->vocab, s->hidden, scale, s->dtype == MOE_F32};
+}
+
+void launch_zero(void* p, size_t bytes, hipStream_t stream) {  // a multiple of 4
+  const size_t words = bytes / 4, blocks = (words + 1023) / 1024;
+  hipLaunchKernelGGL(moe_fill_u32_kernel, dim3((uint32_t)(blocks < 4096 ? blocks : 4096)), dim3(256), 0, stream,
+                     static_cast<uint32_t*>(p), words, 0u);
+}
+
 // ---- adapters
 
 moe_status check_lora_set(const lora_set* l) {
@@ -949,10 +971,7 @@ moe_status lm_head_loss_backward(const lm_head_shape* shape, const uint16_t* h, 
   const size_t wb = (size_t)shape->vocab * shape->hidden * 2;
   if (shape->rows == 0) {  // a dw of 0
     if (!dw || add) return MOE_OK;
-    const size_t words = (f32 ? 2 * wb : wb) / 4;
-    const size_t blocks = (words + 1023) / 1024;
-    hipLaunchKernelGGL(moe_fill_u32_kernel, dim3((uint32_t)(blocks < 4096 ? blocks : 4096)), dim3(256), 0, stream,
-                       static_cast<uint32_t*>(dw), words, 0u);
+    launch_zero(dw, f32 ? 2 * wb : wb, stream);
     return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ERR_DEVICE;
   }
   if (!h || !w || !targets || !lse || !dloss || !aligned16(h) || !aligned16(w) || !aligned4(targets) ||
@@ -966,6 +985,43 @@ moe_status lm_head_loss_backward(const lm_head_shape* shape, const uint16_t* h, 
   if (any_overlap(buf, len, 5, 8)) return MOE_ERR_INVALID_ARG;
   const LossGradArgs a = {h, w, targets, lse, dloss, shape->rows, shape->vocab, shape->hidden, dh, dw, f32, add != 0};
   return launch_loss_backward(a, workspace, stream) == hipSuccess ? MOE_OK : MOE_ERR_DEVICE;
+}
+
+moe_status embed(const embed_shape* shape, const int32_t* ids, const void* table, float scale,
+                 void* out, hipStream_t stream) {
+  const moe_status st = check_embed(shape);
+  if (st != MOE_OK) return st;
+  if (shape->rows == 0) return MOE_OK;
+  if (!ids || !table || !out || !aligned4(ids) || !aligned16(table) || !aligned16(out)) return MOE_ERR_INVALID_ARG;
+  const size_t rb = (size_t)shape->hidden * (shape->dtype == MOE_F32 ? 4 : 2);
+  const void* buf[] = {ids, table, out};
+  const size_t len[] = {(size_t)shape->rows * 4, shape->vocab * rb, shape->rows * rb};
+  if (any_overlap(buf, len, 2, 3)) return MOE_ERR_INVALID_ARG;
+  return launch_embed(embed_args(shape, ids, scale), table, out, stream) == hipSuccess ? MOE_OK : MOE_ERR_DEVICE;
+}
+
+size_t embed_backward_workspace_size(const embed_shape* shape) {
+  return check_embed(shape) == MOE_OK ? embed_backward_workspace(shape->rows, shape->vocab, shape->hidden) : 0;
+}
+
+moe_status embed_backward(const embed_shape* shape, const int32_t* ids, const void* dout,
+                          float scale, int32_t table_dtype, void* dtable, int32_t add,
+                          void* workspace, size_t ws_bytes, hipStream_t stream) {
+  const moe_status st = check_embed(shape);
+  if (st != MOE_OK) return st;
+  if (table_dtype != MOE_BF16 && table_dtype != MOE_F32) return MOE_ERR_UNSUPPORTED;
+  if (shape->rows == 0 && add) return MOE_OK;
+  if (!dtable || !aligned16(dtable) || (shape->rows > 0 && (!ids || !dout || !aligned4(ids) || !aligned16(dout))))
+    return MOE_ERR_INVALID_ARG;
+  const size_t need = embed_backward_workspace(shape->rows, shape->vocab, shape->hidden);
+  if (need && (!workspace || ws_bytes < need || !aligned16(workspace))) return MOE_ERR_WORKSPACE;
+  const size_t h = shape->hidden, rb = h * (shape->dtype == MOE_F32 ? 4 : 2);
+  const void* buf[] = {ids, dout, need ? workspace : nullptr, dtable};
+  const size_t len[] = {(size_t)shape->rows * 4, shape->rows * rb, need,
+                        shape->vocab * h * (table_dtype == MOE_F32 ? 4 : 2)};
+  if (any_overlap(buf, len, 2, 4)) return MOE_ERR_INVALID_ARG;
+  const EmbedGradArgs a = {embed_args(shape, ids, scale), dout, dtable, table_dtype == MOE_F32, add != 0};
+  return launch_embed_backward(a, workspace, stream) == hipSuccess ? MOE_OK : MOE_ERR_DEVICE;
 }
 
 size_t lora_workspace_size(const lora_set* l, int32_t rows) {

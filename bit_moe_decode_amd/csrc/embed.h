@@ -1,0 +1,30 @@
+// embed.h -- host interface of embed.hip: the embedding lookup and its gradient.
+#pragma once
+#include <hip/hip_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+namespace moe {
+
+constexpr int kEmbedMaxRows = 1 << 24;
+constexpr int kEmbedMaxVocab = 1 << 20;
+
+struct EmbedArgs {
+  const int32_t* ids;  // [rows]
+  int rows, vocab, hidden;
+  float scale;
+  bool f32;            // rows (out or dout) are fp32, else bf16
+};
+
+struct EmbedGradArgs {
+  EmbedArgs e;
+  const void* dout;    // [rows][hidden]
+  void* dtable;        // [vocab][hidden]
+  bool f32, add;       // of dtable
+};
+
+hipError_t launch_embed(const EmbedArgs& a, const void* table, void* out, hipStream_t stream);
+size_t embed_backward_workspace(int rows, int vocab, int hidden);
+hipError_t launch_embed_backward(const EmbedGradArgs& a, void* workspace, hipStream_t stream);
+
+}  // namespace moe

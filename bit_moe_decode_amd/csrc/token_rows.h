@@ -34,8 +34,17 @@ struct SortArgs {
   int32_t* n_tiles;
   int tile_rows, extra, extra_rows;
   int spill;  // 1: picks in no group go to the last one
-  int chunks, bits, steps;  // set by launch_sort: blocks, bits of a group, picks a thread
+  int chunks, bits, steps;  // set by plan_sort: blocks, bits of a group, picks a thread
+  // Of a sort by digits of the id (lower digits first, each pass in the last
+  // one's order; its groups are a digit's values, pos is not written): the digit
+  // is (id >> shift) of `bits` bits, ids from ids_below on are in no group; pick
+  // i is id by[i], and there are *kept of them (kept_here without kept).
+  const int32_t *by, *kept;
+  int shift, ids_below, kept_here;
 };
+
+// Sets chunks, bits and steps.
+void plan_sort(SortArgs* a);
 
 size_t sort_workspace(int64_t picks, int groups);
 // The most tiles of `tile_rows` rows that cover `picks` picks of `groups`

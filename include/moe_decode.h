@@ -14,8 +14,9 @@
  * by expert and back, with gradients (moe_sort, moe_gather, moe_combine), the
  * experts' step for any number of tokens (moe_wide_step), low-rank adapters of
  * many requests (lora_apply, lowbit_gemv_lora), and matrix products of the
- * sorted rows in bf16, with gradients (moe_product).  At the model's other end
- * stands the LM head's loss with its gradients (lm_head_loss).
+ * sorted rows in bf16, with gradients (moe_product).  At the model's ends stand
+ * the embedding lookup (embed) and the LM head's loss (lm_head_loss), with
+ * gradients.
  *
  * Sources.  The operations follow the body of sgl-amd-mono PR #85 ("...MoE
  * expert dedup and weight loads, kernarg reload, LM-head loads"), quoted on the
@@ -479,6 +480,40 @@ moe_status lm_head_loss_backward(const lm_head_shape* shape, const uint16_t* h, 
                                  const int32_t* targets, const float* lse, const float* dloss,
                                  uint16_t* dh, void* dw, int32_t add, void* workspace,
                                  size_t ws_bytes, hipStream_t stream);
+
+/* ---- Embedding lookup, rows of a table by token.  An id outside [0, vocab) is a
+ * row without a token (padding).  Where the table is also the LM head, dtable is
+ * lm_head_loss_backward's dw, which embed_backward adds to. */
+#define MOE_EMBED_MAX_ROWS (1 << 24)
+#define MOE_EMBED_MAX_VOCAB (1 << 20)
+typedef struct {
+  int32_t dtype;   /* moe_dtype of table and out, of dout */
+  int32_t rows;    /* 0..MOE_EMBED_MAX_ROWS */
+  int32_t vocab;   /* 1..MOE_EMBED_MAX_VOCAB */
+  int32_t hidden;  /* 1..MOE_MAX_ROW */
+} embed_shape;
+
+/* out[r] = scale table[ids[r]], in fp32, rounded once; 0 for a row without a
+ * token: ids int32 [rows], table [vocab, hidden], out [rows, hidden]. */
+moe_status embed(const embed_shape* shape, const int32_t* ids, const void* table, float scale,
+                 void* out, hipStream_t stream);
+
+/* Bytes of workspace embed_backward needs (0 for few rows), or 0 when the shape
+ * is not supported. */
+size_t embed_backward_workspace_size(const embed_shape* shape);
+
+/* Its gradient: dtable[v] = scale sum_r dout[r] over the rows r with ids[r] = v,
+ * in fp32, rounded once; 0 for a token without rows.  With add != 0 the sum is
+ * added to dtable, in fp32 before the rounding, and the tokens without rows are
+ * left as they were.
+ *  dout          [rows, hidden] of the shape's dtype
+ *  dtable        [vocab, hidden] of table_dtype (moe_dtype)
+ * The order of a sum depends on the ids alone.  `workspace` may be NULL where
+ * the size above is 0; it is scratch, 16-byte aligned, and calls that overlap in
+ * time need one each.  The buffers must not overlap. */
+moe_status embed_backward(const embed_shape* shape, const int32_t* ids, const void* dout,
+                          float scale, int32_t table_dtype, void* dtable, int32_t add,
+                          void* workspace, size_t ws_bytes, hipStream_t stream);
 
 /* ---- Low-rank adapters of many requests beside a projection they share.
  *
