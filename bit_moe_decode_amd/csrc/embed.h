@@ -27,4 +27,11 @@ hipError_t launch_embed(const EmbedArgs& a, const void* table, void* out, hipStr
 size_t embed_backward_workspace(int rows, int vocab, int hidden);
 hipError_t launch_embed_backward(const EmbedGradArgs& a, void* workspace, hipStream_t stream);
 
+// The rows with an id in [0, vocab), by (id, row): their numbers in *order, how
+// many in *kept, both in the workspace.  `clear` (or null) is filled with zeros
+// beside it.
+size_t id_sort_workspace(int rows, int vocab);
+hipError_t launch_id_sort(const int32_t* ids, int rows, int vocab, void* workspace, void* clear, size_t clear_bytes,
+                          int32_t** order, const int32_t** kept, hipStream_t stream);
+
 }  // namespace moe

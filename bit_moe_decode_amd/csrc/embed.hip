@@ -293,19 +293,13 @@ __global__ __launch_bounds__(256) void embed_grad_join_kernel(EmbedGrad g) {
   put_sum<TO, VEC, ADD>(g, v, c, sum);
 }
 
-// --------------------------------------------------------------------- launches
-// Rows up to which every wave holds all ids.
-constexpr int kEmbedFew = 64 * kEmbedFewK;
-
-struct EmbedPlan {
+struct IdSortPlan {
   int low_bits, low, high;  // digits: values of the low one, of the high one (0: none)
-  int chunk, chunks;
-  size_t order_a, order_b, offsets, counts, part, total;
+  size_t order_a, order_b, offsets, counts, total;
 };
 
-static EmbedPlan embed_plan(int rows, int vocab, int hidden) {
-  EmbedPlan p = {};
-  if (rows <= kEmbedFew) return p;
+static IdSortPlan id_sort_plan(int rows, int vocab) {
+  IdSortPlan p = {};
   int bits = 0;
   while ((1 << bits) < vocab) bits++;
   if (vocab <= kSortMaxGroups) {
@@ -316,11 +310,6 @@ static EmbedPlan embed_plan(int rows, int vocab, int hidden) {
     p.low = 1 << p.low_bits;
     p.high = (vocab + p.low - 1) >> p.low_bits;
   }
-  // chunks of 16 rows, longer ones above 32768 rows, so that a token of most rows
-  // goes through few of them
-  const int want = rows / 2048 / 8 * 8;
-  p.chunk = want < 16 ? 16 : (want > 128 ? 128 : want);
-  p.chunks = (rows + p.chunk - 1) / p.chunk;
   size_t o = 0;
   auto take = [&](size_t bytes) {
     const size_t at = o;
@@ -332,8 +321,76 @@ static EmbedPlan embed_plan(int rows, int vocab, int hidden) {
   p.offsets = take((size_t)(kSortMaxGroups + 1) * 4 * 2);
   const size_t ca = sort_workspace(rows, p.low), cb = p.high ? sort_workspace(rows, p.high) : 0;
   p.counts = take(ca > cb ? ca : cb);
-  p.part = take((size_t)p.chunks * 2 * hidden * 4);
   p.total = o;
+  return p;
+}
+
+size_t id_sort_workspace(int rows, int vocab) { return id_sort_plan(rows, vocab).total; }
+
+hipError_t launch_id_sort(const int32_t* ids, int rows, int vocab, void* workspace, void* clear, size_t clear_bytes,
+                          int32_t** order, const int32_t** kept, hipStream_t stream) {
+  const IdSortPlan p = id_sort_plan(rows, vocab);
+  char* b = static_cast<char*>(workspace);
+  EmbedSort s = {};
+  s.low.ids = ids;
+  s.low.picks = rows;
+  s.low.ids_below = vocab;
+  s.low.counts = reinterpret_cast<int32_t*>(b + p.counts);
+  s.high = s.low;
+  s.low.groups = p.low;
+  s.low.order = reinterpret_cast<int32_t*>(b + p.order_a);
+  s.low.offsets = reinterpret_cast<int32_t*>(b + p.offsets);
+  s.high.groups = p.high;
+  s.high.shift = p.low_bits;
+  s.high.by = s.low.order;
+  s.high.kept = s.low.offsets + p.low;
+  s.high.order = reinterpret_cast<int32_t*>(b + p.order_b);
+  s.high.offsets = s.low.offsets + kSortMaxGroups + 1;
+  *order = p.high ? s.high.order : s.low.order;
+  *kept = s.high.kept;
+  plan_sort(&s.low);
+  if (p.high) plan_sort(&s.high);
+  s.table = clear;
+  s.bytes = clear_bytes;
+  const size_t per = (size_t)kSortThreads * 16 * 4;  // bytes of a clearing block, at least
+  const size_t most = (s.bytes + per - 1) / per;
+  const int fill = clear ? (int)(most < 512 ? most : 512) : 0;
+  const size_t lds_low = (size_t)kSortWaves * p.low * 2, lds_high = (size_t)kSortWaves * p.high * 2;
+  if (s.low.chunks <= 1) {
+    hipLaunchKernelGGL(embed_sort_one_kernel, dim3(1 + fill), dim3(kSortThreads), lds_low > lds_high ? lds_low : lds_high,
+                       stream, s);
+    return hipGetLastError();
+  }
+  hipLaunchKernelGGL(embed_sort_count_kernel, dim3(s.low.chunks + fill), dim3(kSortThreads), lds_low, stream, s.low,
+                     s.table, s.bytes);
+  hipLaunchKernelGGL(embed_sort_place_kernel, dim3(s.low.chunks), dim3(kSortThreads), lds_low, stream, s.low);
+  if (p.high) {
+    hipLaunchKernelGGL(embed_sort_count_kernel, dim3(s.high.chunks), dim3(kSortThreads), lds_high, stream, s.high,
+                       nullptr, (size_t)0);
+    hipLaunchKernelGGL(embed_sort_place_kernel, dim3(s.high.chunks), dim3(kSortThreads), lds_high, stream, s.high);
+  }
+  return hipGetLastError();
+}
+
+// --------------------------------------------------------------------- launches
+// Rows up to which every wave holds all ids.
+constexpr int kEmbedFew = 64 * kEmbedFewK;
+
+struct EmbedPlan {
+  int chunk, chunks;
+  size_t part, total;
+};
+
+static EmbedPlan embed_plan(int rows, int vocab, int hidden) {
+  EmbedPlan p = {};
+  if (rows <= kEmbedFew) return p;
+  // chunks of 16 rows, longer ones above 32768 rows, so that a token of most rows
+  // goes through few of them
+  const int want = rows / 2048 / 8 * 8;
+  p.chunk = want < 16 ? 16 : (want > 128 ? 128 : want);
+  p.chunks = (rows + p.chunk - 1) / p.chunk;
+  p.part = id_sort_workspace(rows, vocab);
+  p.total = p.part + (size_t)p.chunks * 2 * hidden * 4;
   return p;
 }
 
@@ -352,47 +409,6 @@ hipError_t launch_embed(const EmbedArgs& a, const void* table, void* out, hipStr
                       : embed_v<uint16_t, true>(a, table, out, stream);
 }
 
-static hipError_t launch_embed_sort(const EmbedGrad& g, const EmbedPlan& p, char* b, hipStream_t stream) {
-  const EmbedArgs& e = g.a.e;
-  EmbedSort s = {};
-  s.low.ids = e.ids;
-  s.low.picks = e.rows;
-  s.low.ids_below = e.vocab;
-  s.low.counts = reinterpret_cast<int32_t*>(b + p.counts);
-  s.high = s.low;
-  s.low.groups = p.low;
-  s.low.order = reinterpret_cast<int32_t*>(b + p.order_a);
-  s.low.offsets = reinterpret_cast<int32_t*>(b + p.offsets);
-  s.high.groups = p.high;
-  s.high.shift = p.low_bits;
-  s.high.by = s.low.order;
-  s.high.kept = s.low.offsets + p.low;
-  s.high.order = reinterpret_cast<int32_t*>(b + p.order_b);
-  s.high.offsets = s.low.offsets + kSortMaxGroups + 1;
-  plan_sort(&s.low);
-  if (p.high) plan_sort(&s.high);
-  s.bytes = (size_t)e.vocab * e.hidden * (g.a.f32 ? 4 : 2);
-  s.table = g.a.add ? nullptr : g.a.dtable;
-  const size_t per = (size_t)kSortThreads * 16 * 4;  // bytes of a clearing block, at least
-  const size_t most = (s.bytes + per - 1) / per;
-  const int fill = g.a.add ? 0 : (int)(most < 512 ? most : 512);
-  const size_t lds_low = (size_t)kSortWaves * p.low * 2, lds_high = (size_t)kSortWaves * p.high * 2;
-  if (s.low.chunks <= 1) {
-    hipLaunchKernelGGL(embed_sort_one_kernel, dim3(1 + fill), dim3(kSortThreads), lds_low > lds_high ? lds_low : lds_high,
-                       stream, s);
-    return hipGetLastError();
-  }
-  hipLaunchKernelGGL(embed_sort_count_kernel, dim3(s.low.chunks + fill), dim3(kSortThreads), lds_low, stream, s.low,
-                     s.table, s.bytes);
-  hipLaunchKernelGGL(embed_sort_place_kernel, dim3(s.low.chunks), dim3(kSortThreads), lds_low, stream, s.low);
-  if (p.high) {
-    hipLaunchKernelGGL(embed_sort_count_kernel, dim3(s.high.chunks), dim3(kSortThreads), lds_high, stream, s.high,
-                       nullptr, (size_t)0);
-    hipLaunchKernelGGL(embed_sort_place_kernel, dim3(s.high.chunks), dim3(kSortThreads), lds_high, stream, s.high);
-  }
-  return hipGetLastError();
-}
-
 template <typename T, typename TO, bool VEC, bool ADD>
 static hipError_t embed_backward_v(const EmbedGradArgs& a, char* b, hipStream_t stream) {
   const EmbedArgs& e = a.e;
@@ -407,10 +423,9 @@ static hipError_t embed_backward_v(const EmbedGradArgs& a, char* b, hipStream_t 
     return hipGetLastError();
   }
   const EmbedPlan p = embed_plan(e.rows, e.vocab, e.hidden);
-  const hipError_t st = launch_embed_sort(g, p, b, stream);
+  const hipError_t st = launch_id_sort(e.ids, e.rows, e.vocab, b, ADD ? nullptr : a.dtable,
+                                       (size_t)e.vocab * e.hidden * sizeof(TO), &g.order, &g.kept, stream);
   if (st != hipSuccess) return st;
-  g.order = reinterpret_cast<int32_t*>(b + (p.high ? p.order_b : p.order_a));
-  g.kept = reinterpret_cast<int32_t*>(b + p.offsets) + p.low;
   g.part = reinterpret_cast<float*>(b + p.part);
   g.chunk = p.chunk;
   const dim3 grid((p.chunks + 3) / 4, parts);

@@ -10,6 +10,7 @@
 #include <math.h>
 
 #include "device_common.h"
+#include "embed.h"
 #include "tile_product.h"
 
 namespace moe {
@@ -160,58 +161,58 @@ __global__ __launch_bounds__(256) void lm_loss_join_kernel(LossTiles l) {
 }
 
 // -------------------------------------------------------------- its gradients
-// The rows that have a target, in order, one behind the other: the rest take no
-// part, whatever they hold.  Then, for one piece of the vocabulary after the
-// other: d of the piece, in bf16 (its rounding is as that of a layer's gradient),
-// and from it the piece's dw and its part of dh, which is kept in fp32.
+// The rows that have a target, by target: the rest take no part, whatever they
+// hold.  Then, for one piece of the vocabulary after the other: d of the piece in
+// bf16, and from it the piece's dw and its part of dh, which is kept in fp32.
+//
+// d's rounding moves each term of a sum by up to 2^-8 of it.  Where a sum has
+// many terms these go their own ways; but at the targets d is near -dloss, and a
+// mean's dloss is the same for all rows: rounded alike, they moved all of dw and
+// dh by up to 2^-8 (error 0.0026 of the gradients' size for their own rounding's
+// 0.0017).  So what the rounding takes from d at a row's target is kept too, and
+// added: to dh by its last kernel, to dw as more rows of the product.  In the
+// order by target the rows of 256 tokens are neighbours, so that their remainders
+// are a dense [rows][256] matrix of one entry a row.
 struct LossGrad {
   LossGradArgs a;
   uint16_t* h;       // [rows][hidden] of the rows with a target
   float2* row;       // their lse and dloss,
   int32_t* target;   // target,
+  float* rest;       // d at the target less its rounding,
+  uint16_t* rests;   // the same at column target % 256 of [rows][256]
   int32_t* place;    // [rows] each row's place among them, or -1
-  int32_t* live;     // [1] their number
+  const int32_t* order;  // [live] the row at each place
+  const int32_t* live;   // [1] their number
+  int32_t* first_of;     // [vocab / 256 + 2] the first place of each 256 tokens
   int32_t* next;     // [8] an XCD's next tile of the second products
   uint16_t* d;       // [rows][pitch]
   float* acc;        // [splits][rows][hidden] of dh
+  void* sort;
   int pitch, pieces, splits;
   int first, count;  // this piece's part of the vocabulary
 };
 
-__global__ __launch_bounds__(1024) void lm_loss_rows_kernel(LossGrad l) {
-  __shared__ int s_sum[16];
-  const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
-  int base = 0;
-  for (int r0 = 0; r0 < l.a.rows; r0 += 1024) {
-    const int r = r0 + tid;
-    const int t = r < l.a.rows ? l.a.targets[r] : -1;
-    const bool in = (uint32_t)t < (uint32_t)l.a.vocab;
-    const uint64_t m = __ballot(in);
-    if (lane == 0) s_sum[wv] = __popcll(m);
-    __syncthreads();
-    int at = base + lanes_below(m), all = 0;
-#pragma unroll
-    for (int w = 0; w < 16; w++) {
-      at += w < wv ? s_sum[w] : 0;
-      all += s_sum[w];
-    }
-    if (r < l.a.rows) l.place[r] = in ? at : -1;
-    if (in) {
-      l.target[at] = t;
-      l.row[at] = float2{l.a.lse[r], l.a.dloss[r]};
-    }
-    base += all;
-    __syncthreads();
-  }
-  if (tid == 0) *l.live = base;
-}
-
+// Block b: row b, if it has no target, and the row at place b.
 __global__ __launch_bounds__(256) void lm_loss_gather_kernel(LossGrad l) {
-  const int r = blockIdx.x, at = l.place[r];
-  if (at < 0) return;
+  const int b = blockIdx.x, tid = threadIdx.x, live = *l.live;
+  if (tid == 0 && (uint32_t)l.a.targets[b] >= (uint32_t)l.a.vocab) l.place[b] = -1;
+  if (b == 0 && live == 0)
+    for (int i = tid; i <= (l.a.vocab + 255) / 256; i += 256) l.first_of[i] = 0;
+  if (b >= live) return;
+  const int r = l.order[b], t = l.a.targets[r];
   const u32x4* from = reinterpret_cast<const u32x4*>(l.a.h + (size_t)r * l.a.hidden);
-  u32x4* to = reinterpret_cast<u32x4*>(l.h + (size_t)at * l.a.hidden);
-  for (int i = threadIdx.x; i < l.a.hidden / 8; i += 256) to[i] = from[i];
+  u32x4* to = reinterpret_cast<u32x4*>(l.h + (size_t)b * l.a.hidden);
+  for (int i = tid; i < l.a.hidden / 8; i += 256) to[i] = from[i];
+  if (tid < 32) reinterpret_cast<u32x4*>(l.rests + (size_t)b * 256)[tid] = u32x4{0u, 0u, 0u, 0u};
+  const int before = b > 0 ? l.a.targets[l.order[b - 1]] / 256 : -1;
+  for (int i = before + 1 + tid; i <= t / 256; i += 256) l.first_of[i] = b;
+  if (b == live - 1)
+    for (int i = t / 256 + 1 + tid; i <= (l.a.vocab + 255) / 256; i += 256) l.first_of[i] = live;
+  if (tid == 0) {
+    l.place[r] = b;
+    l.target[b] = t;
+    l.row[b] = float2{l.a.lse[r], l.a.dloss[r]};
+  }
 }
 
 // d of a tile; columns past the vocabulary are 0.
@@ -227,15 +228,24 @@ __device__ __forceinline__ void grad_epilogue(const LossGrad& l, TileSums<U, V>&
     tile_hold(sums.s[u]);
     const int m = m0 + 16 * u, row = m < live ? m : live - 1;
     const float2 q = l.row[row];
-    const int at = l.target[row] - l.first - j0;
+    const int t = l.target[row], at = t - l.first - j0;
     const bool hit = __ballot((uint32_t)at < 16u * V) != 0;
 #pragma unroll
     for (int v = 0; v < V; v++)
 #pragma unroll
       for (int i = 0; i < 4; i++) {
         float p = exp_of(sums.s[u][v][i] - q.x);
-        if (hit && 16 * v + 4 * g + i == at) p -= 1.f;
-        p *= q.y;
+        if (hit && 16 * v + 4 * g + i == at) {
+          p = (p - 1.f) * q.y;
+          if (m < live) {
+            const float near = bf16_to_f32(f32_to_bf16(p));
+            const float rest = fabsf(near) < INFINITY ? p - near : 0.f;
+            l.rest[m] = rest;
+            l.rests[(size_t)m * 256 + (t & 255)] = f32_to_bf16(rest);
+          }
+        } else {
+          p *= q.y;
+        }
         if (edge && j0 + 16 * v + 4 * g + i >= l.count) p = 0.f;
         sums.s[u][v][i] = p;
       }
@@ -345,10 +355,13 @@ __global__ __launch_bounds__(256) void lm_loss_products_kernel(LossGrad l) {
         place_of(dw0 + i - dh_n, v_tiles, h_tiles, &mt, &jt);
         const int m0 = mt * 256, j0 = jt * 256;
         const int own = l.count - m0 < 256 ? (l.count - m0 + 7) / 8 * 8 : 256;
-        const TileOperand om = {l.d + m0, pitch_d, own, live};
-        const TileOperand oj = {l.h + j0, pitch_h, H - j0 < 256 ? H - j0 : 256, live};
+        const int r0 = __builtin_amdgcn_readfirstlane(l.first_of[(l.first + m0) / 256]);
+        const int more = __builtin_amdgcn_readfirstlane(l.first_of[(l.first + m0) / 256 + 1]) - r0;
+        const TileOperand om = {l.d + m0, pitch_d, own, live, l.rests + (int64_t)r0 * 256, 512u, more};
+        const TileOperand oj = {l.h + j0, pitch_h, H - j0 < 256 ? H - j0 : 256, live,
+                                l.h + (int64_t)r0 * H + j0, pitch_h, more};
         TileSums<8, 8> sums;
-        tile_product<8, 8, true, true>(om, oj, s0, s1, s2, s3, sums);
+        tile_product<8, 8, true, true, true>(om, oj, s0, s1, s2, s3, sums);
         T* out = reinterpret_cast<T*>(l.a.dw) + (int64_t)l.first * H;
         store_tile<8, 8, T, ADD>(sums, out, m0, l.count, j0, H);
       }
@@ -356,15 +369,23 @@ __global__ __launch_bounds__(256) void lm_loss_products_kernel(LossGrad l) {
   }
 }
 
-// dh from its parts, in order; 0 for a row without a target.
+// dh from its parts, in order, and what d's rounding took at the target; 0 for a
+// row without a target.
 __global__ __launch_bounds__(256) void lm_loss_dh_kernel(LossGrad l) {
   const int r = blockIdx.x, at = l.place[r], H = l.a.hidden;
   const int c = (blockIdx.y * 256 + threadIdx.x) * 4;
   if (c >= H) return;
   v4f s = {0.f, 0.f, 0.f, 0.f};
-  if (at >= 0)
+  if (at >= 0) {
+    const float rest = l.rest[at];
+    const uint2 w = *reinterpret_cast<const uint2*>(l.a.w + (size_t)l.target[at] * H + c);
     for (int i = 0; i < l.splits; i++)
       s += *reinterpret_cast<const v4f*>(l.acc + ((size_t)i * l.a.rows + at) * H + c);
+    s[0] = fmaf(rest, __uint_as_float(w.x << 16), s[0]);
+    s[1] = fmaf(rest, __uint_as_float(w.x & 0xFFFF0000u), s[1]);
+    s[2] = fmaf(rest, __uint_as_float(w.y << 16), s[2]);
+    s[3] = fmaf(rest, __uint_as_float(w.y & 0xFFFF0000u), s[3]);
+  }
   uint2 o;
   o.x = (uint32_t)f32_to_bf16(s[0]) | ((uint32_t)f32_to_bf16(s[1]) << 16);
   o.y = (uint32_t)f32_to_bf16(s[2]) | ((uint32_t)f32_to_bf16(s[3]) << 16);
@@ -444,7 +465,10 @@ static size_t loss_grad_plan(LossGrad* l, char* base) {
   l->row = reinterpret_cast<float2*>(take(R * sizeof(float2)));
   l->target = reinterpret_cast<int32_t*>(take(R * 4));
   l->place = reinterpret_cast<int32_t*>(take(R * 4));
-  l->live = reinterpret_cast<int32_t*>(take(4));
+  l->rest = reinterpret_cast<float*>(take(R * 4));
+  l->rests = reinterpret_cast<uint16_t*>(take(R * 512));
+  l->first_of = reinterpret_cast<int32_t*>(take(((size_t)whole + 1) * 4));
+  l->sort = take(id_sort_workspace(a.rows, a.vocab));
   l->next = reinterpret_cast<int32_t*>(take(8 * 4));
   l->d = reinterpret_cast<uint16_t*>(take(R * l->pitch * 2));
   l->acc = reinterpret_cast<float*>(take((size_t)l->splits * R * a.hidden * 4));
@@ -463,7 +487,10 @@ hipError_t launch_loss_backward(const LossGradArgs& a, void* workspace, hipStrea
   LossGrad l = {};
   l.a = a;
   loss_grad_plan(&l, static_cast<char*>(workspace));
-  hipLaunchKernelGGL(lm_loss_rows_kernel, dim3(1), dim3(1024), 0, stream, l);
+  int32_t* order;
+  hipError_t e = launch_id_sort(a.targets, a.rows, a.vocab, l.sort, nullptr, 0, &order, &l.live, stream);
+  if (e != hipSuccess) return e;
+  l.order = order;
   hipLaunchKernelGGL(lm_loss_gather_kernel, dim3(a.rows), dim3(256), 0, stream, l);
   for (l.first = 0; l.first < a.vocab; l.first += l.pitch) {
     l.count = a.vocab - l.first < l.pitch ? a.vocab - l.first : l.pitch;
@@ -471,7 +498,7 @@ hipError_t launch_loss_backward(const LossGradArgs& a, void* workspace, hipStrea
     const bool few = a.rows <= kLossFew;
     const int64_t tiles = few ? (int64_t)(l.count + 127) / 128
                               : (int64_t)((a.rows + 255) / 256) * ((l.count + 255) / 256);
-    hipError_t e = tile_blocks(tiles, few ? 2 : 1, &blocks);
+    e = tile_blocks(tiles, few ? 2 : 1, &blocks);
     if (e != hipSuccess) return e;
     if (few)
       hipLaunchKernelGGL((lm_loss_d_kernel<2, 4>), dim3(blocks), dim3(256), 0, stream, l);

@@ -33,6 +33,11 @@ struct TileOperand {
   const uint16_t* base;
   uint32_t pitch;
   int own, c;
+  // (tile_product's LONGER, transposed operands) c2 more entries behind them,
+  // from another place
+  const uint16_t* base2 = nullptr;
+  uint32_t pitch2 = 0;
+  int c2 = 0;
 };
 
 constexpr int kStepC = 32;
@@ -73,7 +78,7 @@ __device__ __forceinline__ void tile_meet() {
 // second 64 of its 128 columns (64 columns: c = q + 4 p).  A lane's operand is
 // the 8 c of column lane % 16: two transposing reads of 4 (in each, lane i of 16
 // names 8 bytes of c = i / 4, columns 4 (i % 4) .., and gets the 4 c of column i).
-template <int P, bool T>
+template <int P, bool T, bool LONGER>
 struct TileLoader {
   static constexpr int kLoads = P >= 4 ? P / 4 : 1;  // a wave's a step
   static constexpr int kKilos = 4 * kLoads;          // that they fill
@@ -83,6 +88,9 @@ struct TileLoader {
   const uint8_t* base;
   uint32_t pitch, at[kLoads];    // this lane's offsets in a step
   int c, kc, q0;                 // entries, this lane's first of a step, the wave's first kilobyte
+  const uint8_t* base2;          // LONGER: of the entries behind them
+  uint32_t pitch2, at2[LONGER ? kLoads : 1];
+  int c2, steps;                 // their number, the steps before them
   int read;                      // this lane's operands in a stage
 
   __device__ __forceinline__ void set(const TileOperand& o, int lane, int wv) {
@@ -96,9 +104,18 @@ struct TileLoader {
       const int cl = P >= 8 ? 8 * (p & 3) : 4 * p, block = P >= 8 ? p >> 2 : 0;
       const int own0 = (P >= 8 ? (q0 >> 3) * 128 : 0) + block * 64 + (lane & 7) * 8;
 #pragma unroll
-      for (int n = 0; n < kLoads; n++)
-        at[n] = own0 < o.own ? (uint32_t)(cl + (P >= 8 ? (q0 + n) & 7 : q0 + n)) * pitch + (uint32_t)own0 * 2u : kNothing;
+      for (int n = 0; n < kLoads; n++) {
+        const uint32_t row = (uint32_t)(cl + (P >= 8 ? (q0 + n) & 7 : q0 + n));
+        at[n] = own0 < o.own ? row * pitch + (uint32_t)own0 * 2u : kNothing;
+        if constexpr (LONGER) at2[n] = own0 < o.own ? row * o.pitch2 + (uint32_t)own0 * 2u : kNothing;
+      }
       kc = 0;
+      if constexpr (LONGER) {
+        base2 = reinterpret_cast<const uint8_t*>(o.base2);
+        pitch2 = o.pitch2;
+        c2 = o.c2;
+        steps = (c + kStepC - 1) / kStepC;
+      }
       read = (col >> 2) * kPiecesAt + g * (P >= 8 ? 128 : 256) + (col & 3) * 8;
     } else {
       const int p = lane >> 2;
@@ -118,10 +135,14 @@ struct TileLoader {
     const int c0 = k * kStepC;
     tile_lds_void* to = (tile_lds_void*)(lds + (q0 + n) * kPiecesAt);
     if constexpr (T) {
-      const int left = c - c0 < kStepC ? c - c0 : kStepC;
-      const auto r = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(base + (int64_t)(left > 0 ? c0 : 0) * pitch),
-                                                       0, left > 0 ? (uint32_t)left * pitch : 0u, 0x00027000);
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(r, to, 16, at[n], 0, 0, 0);
+      const bool two = LONGER && k >= steps;
+      const int c1 = two ? c0 - steps * kStepC : c0, most = (two ? c2 : c) - c1;
+      const int left = most < kStepC ? most : kStepC;
+      const uint32_t p = two ? pitch2 : pitch;
+      const uint8_t* from = (two ? base2 : base) + (int64_t)(left > 0 ? c1 : 0) * p;
+      const auto r = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(from), 0, left > 0 ? (uint32_t)left * p : 0u,
+                                                       0x00027000);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(r, to, 16, LONGER && two ? at2[LONGER ? n : 0] : at[n], 0, 0, 0);
     } else {
       __builtin_amdgcn_raw_ptr_buffer_load_lds(whole, to, 16, c0 + kc < c ? at[n] : kNothing,
                                                c0 < c ? (uint32_t)c0 * 2u : 0u, 0, 0);
@@ -171,23 +192,26 @@ struct TileSums {
 // sums.s[u][v]: this wave's sums, of m tile wm U + u and j tile wj V + v (wm, wj:
 // the wave's bits 0 and 1): a lane holds j = 4 (lane / 16) + 0..3 of m = lane %
 // 16.  All of the block's threads call it, with the same arguments.
-template <int U, int V, bool MT, bool JT, typename Stage>
+template <int U, int V, bool MT, bool JT, bool LONGER = false, typename Stage>
 __device__ __forceinline__ void tile_product(const TileOperand& om, const TileOperand& oj, Stage& s0, Stage& s1,
                                              Stage& s2, Stage& s3, TileSums<U, V>& sums) {
 #ifdef __HIP_DEVICE_COMPILE__  // (the host's pass of the compiler refuses the body and needs none)
   auto& acc = sums.s;
   constexpr int PM = 2 * U, PJ = 2 * V;
-  static_assert(sizeof(Stage) >= (TileLoader<PM, MT>::kKilos + TileLoader<PJ, JT>::kKilos) * kPiecesAt,
+  static_assert(sizeof(Stage) >= (TileLoader<PM, MT, LONGER>::kKilos + TileLoader<PJ, JT, LONGER>::kKilos) * kPiecesAt,
                 "both operands fit a stage");
   const int tid = threadIdx.x, lane = tid & 63, wv = tile_wave(tid);
   const int wm = wv & 1, wj = wv >> 1;
-  TileLoader<PM, MT> m;
-  TileLoader<PJ, JT> j;
+  static_assert(!LONGER || (MT && JT), "of transposed operands");
+  using Rows = TileLoader<PM, MT, LONGER>;
+  using Columns = TileLoader<PJ, JT, LONGER>;
+  Rows m;
+  Columns j;
   m.set(om, lane, wv);
   j.set(oj, lane, wv);
-  constexpr int NM = TileLoader<PM, MT>::kLoads, NJ = TileLoader<PJ, JT>::kLoads, NL = NM + NJ;
-  constexpr int kJ = TileLoader<PM, MT>::kKilos * kPiecesAt;  // where J starts in a stage
-  const int steps = (om.c + kStepC - 1) / kStepC;
+  constexpr int NM = Rows::kLoads, NJ = Columns::kLoads, NL = NM + NJ;
+  constexpr int kJ = Rows::kKilos * kPiecesAt;  // where J starts in a stage
+  const int steps = (om.c + kStepC - 1) / kStepC + (LONGER ? (om.c2 + kStepC - 1) / kStepC : 0);
 #pragma unroll
   for (int u = 0; u < U; u++)
 #pragma unroll

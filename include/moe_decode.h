@@ -468,7 +468,7 @@ moe_status lm_head_loss(const lm_head_shape* shape, const uint16_t* h, const uin
                         size_t ws_bytes, hipStream_t stream);
 
 /* Its gradients: with d[r, v] = (exp(z[r, v] - lse[r]) - [v = targets[r]])
- * dloss[r], rounded to bf16 once and then used in both,
+ * dloss[r], which enters both as bf16 (at the target as the sum of two),
  *  dh  bf16 [rows, hidden]: dh[r] = sum_v d[r, v] w[v]
  *  dw  [vocab, hidden]: dw[v] = sum_r d[r, v] h[r]; with add != 0 it is added to
  *      dw, in fp32 before the rounding

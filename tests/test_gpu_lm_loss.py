@@ -10,7 +10,8 @@ most, plus 2^-22 of lse.  The additions' term is for one chain; they run in
 chains of at most 64 and then over the tiles: (64 + vocab / 64) 2^-23.
 
 d is (p - hit) dloss, p off by (e + 2^-22 (2 + |z - lse|)) of it, rounded to bf16
-once: 2^-8 of it (or below 2^-126 maybe 0).  dh and dw add d times w (h) in fp32.
+once: 2^-8 of it (or below 2^-126 maybe 0); at the target it is the sum of two
+bf16, 2^-16.  dh and dw add d times w (h) in fp32.
 """
 import math
 
@@ -89,7 +90,7 @@ def _check_grads(dh, dw, h, w, t, lse, dloss, add=None):
     zero = torch.zeros_like(p)
     d = torch.where(live, (p - hit.double()) * dl, zero)
     off = torch.where(live, p * (e + 2 * U32 * (2 + x.abs())) * dl.abs() + 2 * U32 * d.abs() + 2.0 ** -125, zero)
-    off = off + BF16 * (d.abs() + off)
+    off = off + torch.where(hit, 2.0 ** -16, BF16) * (d.abs() + off)
     hd, wd = torch.where(live, h.double(), torch.zeros((), device="cuda", dtype=torch.float64)), w.double()
     for got, ref, terms, part, c in (
             (dh, d @ wd, d.abs() @ wd.abs(), off @ wd.abs(), vocab + 40),
