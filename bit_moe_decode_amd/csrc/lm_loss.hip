@@ -29,6 +29,45 @@ __device__ __forceinline__ float over_lanes_sum(float v) {
   return v + __shfl_xor(v, 32, kWave);
 }
 
+// A tile of the logits of rows m0 + .. and tokens j0 + ..
+struct HeadTile {
+  TileOperand m, j;
+  int m0, j0;
+};
+
+// Calls done(sums, tile) for this block's tiles of `total`.
+template <int UMAX, int V, typename Stage, typename TileAt, typename Done>
+__device__ __forceinline__ void head_tiles(int total, TileAt tile_at, Stage& s0, Stage& s1, Stage& s2, Stage& s3,
+                                           Done done) {
+  int t = first_tile();
+  if (t >= total) return;
+  TilePipe<UMAX, V, false, false> pipe;
+  HeadTile p = tile_at(t);
+  pipe.start(p.m, p.j, s0, s1, s2, s3);
+  for (;;) {
+    t += gridDim.x;
+    const bool more = t < total;
+    HeadTile next = p;
+    if (more) next = tile_at(t);
+    auto finish = [&](auto u) TILE_INLINE {
+      TileSums<decltype(u)::value, V> sums;
+      pipe.run(s0, s1, s2, s3, sums);
+      if (more) pipe.start(next.m, next.j, s0, s1, s2, s3);
+      done(sums, p);
+    };
+    if (UMAX == 8 && p.m.own > 128)
+      finish(std::integral_constant<int, UMAX>{});
+    else if (UMAX >= 4 && p.m.own > 64)
+      finish(std::integral_constant<int, UMAX < 4 ? UMAX : 4>{});
+    else if (p.m.own > 32)
+      finish(std::integral_constant<int, 2>{});
+    else
+      finish(std::integral_constant<int, 1>{});
+    if (!more) return;
+    p = next;
+  }
+}
+
 // ------------------------------------------------------------------- the loss
 // A tile's logits stay in its sums: each wave leaves a row's largest logit of
 // its columns and the sum of the exponentials below it, [rows][parts] of
@@ -83,50 +122,37 @@ __device__ __forceinline__ void loss_epilogue(const LossTiles& l, TileSums<U, V>
     const int t = live ? l.a.targets[l.first + m] : -1;
     const int at = t - j0;  // the target's column here
     if (__ballot((uint32_t)t < (uint32_t)l.a.vocab && (uint32_t)at < 16u * V)) {
-      if ((uint32_t)t < (uint32_t)l.a.vocab && (uint32_t)at < 16u * V && ((at >> 2) & 3) == g) {
-        float f = 0.f;
+      float f = 0.f;
 #pragma unroll
-        for (int v = 0; v < V; v++)
+      for (int v = 0; v < V; v++)
 #pragma unroll
-          for (int i = 0; i < 4; i++)
-            if (16 * v + 4 * g + i == at) f = z[v][i];
-        l.at_target[m] = f;
-      }
+        for (int i = 0; i < 4; i++)
+          if (16 * v + 4 * g + i == at) f = z[v][i];
+      if ((uint32_t)t < (uint32_t)l.a.vocab && (uint32_t)at < 16u * V && ((at >> 2) & 3) == g) l.at_target[m] = f;
     }
+    __builtin_amdgcn_wave_barrier();
   }
-}
-
-template <int U, int V, typename Stage>
-__device__ __forceinline__ void loss_tile(const LossTiles& l, const TileOperand& om, const TileOperand& oj, Stage& s0,
-                                          Stage& s1, Stage& s2, Stage& s3, int m0, int j0, int part) {
-  TileSums<U, V> sums;
-  tile_product<U, V, false, false>(om, oj, s0, s1, s2, s3, sums);
-  loss_epilogue<U, V>(l, sums, m0, j0, part);
 }
 
 template <int UMAX, int V>
 __global__ __launch_bounds__(256) void lm_loss_kernel(LossTiles l) {
-  constexpr int TM = 32 * UMAX, TJ = 32 * V, KILOS = 2 * UMAX + 2 * V;
-  __shared__ TileStage<KILOS> s0, s1, s2, s3;
-  const int m_tiles = (l.count + TM - 1) / TM, j_tiles = (l.a.vocab + TJ - 1) / TJ;
-  const uint32_t pitch = (uint32_t)l.a.hidden * 2u;
-  for (int t = first_tile(); t < m_tiles * j_tiles; t += gridDim.x) {
+  using Pipe = TilePipe<UMAX, V, false, false>;
+  constexpr int TM = 32 * UMAX, TJ = 32 * V;
+  __shared__ typename Pipe::Stage s0, s1, s2, s3;
+  const int m_tiles = (l.count + TM - 1) / TM, j_tiles = (l.a.vocab + TJ - 1) / TJ, H = l.a.hidden;
+  auto tile_at = [&](int t) TILE_INLINE {
     int mt, jt;
     place_of(t, m_tiles, j_tiles, &mt, &jt);
-    const int m0 = mt * TM, j0 = jt * TJ;
-    const int rows = l.count - m0 < TM ? l.count - m0 : TM;
-    const TileOperand om = {l.a.h + (int64_t)(l.first + m0) * l.a.hidden, pitch, rows, l.a.hidden};
-    const TileOperand oj = {l.a.w + (int64_t)j0 * l.a.hidden, pitch, l.a.vocab - j0 < TJ ? l.a.vocab - j0 : TJ,
-                            l.a.hidden};
-    if (UMAX == 8 && rows > 128)
-      loss_tile<UMAX, V>(l, om, oj, s0, s1, s2, s3, m0, j0, 2 * jt);
-    else if (UMAX >= 4 && rows > 64)
-      loss_tile<UMAX < 4 ? UMAX : 4, V>(l, om, oj, s0, s1, s2, s3, m0, j0, 2 * jt);
-    else if (rows > 32)
-      loss_tile<2, V>(l, om, oj, s0, s1, s2, s3, m0, j0, 2 * jt);
-    else
-      loss_tile<1, V>(l, om, oj, s0, s1, s2, s3, m0, j0, 2 * jt);
-  }
+    HeadTile p;
+    p.m0 = mt * TM;
+    p.j0 = jt * TJ;
+    p.m = {l.a.h + (int64_t)(l.first + p.m0) * H, (uint32_t)H * 2u, l.count - p.m0 < TM ? l.count - p.m0 : TM, H};
+    p.j = {l.a.w + (int64_t)p.j0 * H, (uint32_t)H * 2u, l.a.vocab - p.j0 < TJ ? l.a.vocab - p.j0 : TJ, H};
+    return p;
+  };
+  head_tiles<UMAX, V>(m_tiles * j_tiles, tile_at, s0, s1, s2, s3, [&](auto& sums, const HeadTile& p) TILE_INLINE {
+    loss_epilogue(l, sums, p.m0, p.j0, p.j0 / TJ * 2);
+  });
 }
 
 // A row's parts joined, a block a row: the largest, then the sums below it.
@@ -257,114 +283,161 @@ __device__ __forceinline__ void grad_epilogue(const LossGrad& l, TileSums<U, V>&
   }
 }
 
-template <int U, int V, typename Stage>
-__device__ __forceinline__ void grad_tile(const LossGrad& l, const TileOperand& om, const TileOperand& oj, Stage& s0,
-                                          Stage& s1, Stage& s2, Stage& s3, int live, int m0, int j0) {
-  TileSums<U, V> sums;
-  tile_product<U, V, false, false>(om, oj, s0, s1, s2, s3, sums);
-  grad_epilogue<U, V>(l, sums, live, m0, j0);
-}
-
 template <int UMAX, int V>
 __global__ __launch_bounds__(256) void lm_loss_d_kernel(LossGrad l) {
-  constexpr int TM = 32 * UMAX, TJ = 32 * V, KILOS = 2 * UMAX + 2 * V;
-  __shared__ TileStage<KILOS> s0, s1, s2, s3;
+  using Pipe = TilePipe<UMAX, V, false, false>;
+  constexpr int TM = 32 * UMAX, TJ = 32 * V;
+  __shared__ typename Pipe::Stage s0, s1, s2, s3;
   if (blockIdx.x == 0 && threadIdx.x < 8) l.next[threadIdx.x] = 0;
   const int live = __builtin_amdgcn_readfirstlane(*l.live);
-  const int m_tiles = (live + TM - 1) / TM, j_tiles = (l.count + TJ - 1) / TJ;
-  const uint32_t pitch = (uint32_t)l.a.hidden * 2u;
-  for (int t = first_tile(); t < m_tiles * j_tiles; t += gridDim.x) {
+  const int m_tiles = (live + TM - 1) / TM, j_tiles = (l.count + TJ - 1) / TJ, H = l.a.hidden;
+  auto tile_at = [&](int t) TILE_INLINE {
     int mt, jt;
     place_of(t, m_tiles, j_tiles, &mt, &jt);
-    const int m0 = mt * TM, j0 = jt * TJ;
-    const int rows = live - m0 < TM ? live - m0 : TM;
-    const TileOperand om = {l.h + (int64_t)m0 * l.a.hidden, pitch, rows, l.a.hidden};
-    const TileOperand oj = {l.a.w + (int64_t)(l.first + j0) * l.a.hidden, pitch,
-                            l.count - j0 < TJ ? l.count - j0 : TJ, l.a.hidden};
-    if (UMAX == 8 && rows > 128)
-      grad_tile<UMAX, V>(l, om, oj, s0, s1, s2, s3, live, m0, j0);
-    else if (UMAX >= 4 && rows > 64)
-      grad_tile<UMAX < 4 ? UMAX : 4, V>(l, om, oj, s0, s1, s2, s3, live, m0, j0);
-    else if (rows > 32)
-      grad_tile<2, V>(l, om, oj, s0, s1, s2, s3, live, m0, j0);
-    else
-      grad_tile<1, V>(l, om, oj, s0, s1, s2, s3, live, m0, j0);
-  }
-}
-
-// A tile's part of dh: kept, or added to what earlier pieces left.
-template <int U, typename Stage>
-__device__ __forceinline__ void dh_tile(const LossGrad& l, const TileOperand& om, const TileOperand& oj, Stage& s0,
-                                        Stage& s1, Stage& s2, Stage& s3, float* acc, int live, int m0, int j0) {
-  TileSums<U, 8> sums;
-  tile_product<U, 8, false, true>(om, oj, s0, s1, s2, s3, sums);
-  if (l.first == 0)
-    store_tile<U, 8, float, false>(sums, acc, m0, live, j0, l.a.hidden);
-  else
-    store_tile<U, 8, float, true>(sums, acc, m0, live, j0, l.a.hidden);
+    HeadTile p;
+    p.m0 = mt * TM;
+    p.j0 = jt * TJ;
+    p.m = {l.h + (int64_t)p.m0 * H, (uint32_t)H * 2u, live - p.m0 < TM ? live - p.m0 : TM, H};
+    p.j = {l.a.w + (int64_t)(l.first + p.j0) * H, (uint32_t)H * 2u, l.count - p.j0 < TJ ? l.count - p.j0 : TJ, H};
+    return p;
+  };
+  head_tiles<UMAX, V>(m_tiles * j_tiles, tile_at, s0, s1, s2, s3,
+                      [&](auto& sums, const HeadTile& p) TILE_INLINE { grad_epilogue(l, sums, live, p.m0, p.j0); });
 }
 
 // The two products of a piece's d, in one launch: the tiles of dh, which are
 // long (the piece's columns), first, then those of dw (the rows).  Each XCD has
 // its eighth of either, whose tiles its blocks take one after the other, so that
 // tiles under way at once share operands in its L2; then those left of others.
+struct GradTile {
+  TileOperand m, j;
+  int m0, j0, split;  // split -1: of dw
+};
+
+struct GradTiles {
+  int h_tiles, v_tiles, m_tiles, dh, dw;  // tiles a side, and in all
+  int part;                               // columns of a split
+  __device__ __forceinline__ GradTiles(const LossGrad& l, int live) {
+    h_tiles = (l.a.hidden + 255) / 256;
+    v_tiles = (l.count + 255) / 256;
+    m_tiles = (live + 255) / 256;
+    dh = l.a.dh ? m_tiles * h_tiles * l.splits : 0;
+    dw = l.a.dw ? v_tiles * h_tiles : 0;
+    part = ((l.count + kStepC - 1) / kStepC + l.splits - 1) / l.splits * kStepC;
+  }
+  // The first of n tiles that are XCD x's.
+  static __device__ __forceinline__ int first(int n, int x) { return (int)((int64_t)n * x / 8); }
+
+  __device__ __forceinline__ GradTile dh_at(const LossGrad& l, int live, int t) const {
+    const int H = l.a.hidden;
+    GradTile p;
+    p.split = t / (m_tiles * h_tiles);
+    int mt, jt;
+    place_of(t - p.split * (m_tiles * h_tiles), m_tiles, h_tiles, &mt, &jt);
+    p.m0 = mt * 256;
+    p.j0 = jt * 256;
+    const int c0 = p.split * part, left = l.count - c0, c = left < 0 ? 0 : (left < part ? left : part);
+    // (d's columns past the vocabulary are 0, to a multiple of 8)
+    p.m = {l.d + (int64_t)p.m0 * l.pitch + (c ? c0 : 0), (uint32_t)l.pitch * 2u, live - p.m0 < 256 ? live - p.m0 : 256,
+           (c + 7) / 8 * 8};
+    p.j = {l.a.w + (int64_t)(l.first + (c ? c0 : 0)) * H + p.j0, (uint32_t)H * 2u, H - p.j0 < 256 ? H - p.j0 : 256, c};
+    return p;
+  }
+  __device__ __forceinline__ GradTile dw_at(const LossGrad& l, int live, int t) const {
+    const int H = l.a.hidden;
+    GradTile p;
+    p.split = -1;
+    int mt, jt;
+    place_of(t, v_tiles, h_tiles, &mt, &jt);
+    p.m0 = mt * 256;
+    p.j0 = jt * 256;
+    const int r0 = __builtin_amdgcn_readfirstlane(l.first_of[(l.first + p.m0) / 256]);
+    const int more = __builtin_amdgcn_readfirstlane(l.first_of[(l.first + p.m0) / 256 + 1]) - r0;
+    const int own = l.count - p.m0 < 256 ? (l.count - p.m0 + 7) / 8 * 8 : 256, cols = H - p.j0 < 256 ? H - p.j0 : 256;
+    p.m = {l.d + p.m0, (uint32_t)l.pitch * 2u, own, live, l.rests + (int64_t)r0 * 256, 512u, more};
+    p.j = {l.h + p.j0, (uint32_t)H * 2u, cols, live, l.h + (int64_t)r0 * H + p.j0, (uint32_t)H * 2u, more};
+    return p;
+  }
+};
+
 template <typename T, bool ADD>
 __global__ __launch_bounds__(256) void lm_loss_products_kernel(LossGrad l) {
-  __shared__ TileStage<32> s0, s1, s2, s3;
+  using Long = TilePipe<8, 8, false, true>;
+  using Wide = TilePipe<8, 8, true, true, true>;
+  static_assert(sizeof(Long::Stage) == sizeof(Wide::Stage), "both take the same stages");
+  __shared__ Long::Stage s0, s1, s2, s3;
   __shared__ int s_next;
-  const int live = __builtin_amdgcn_readfirstlane(*l.live);
-  const int H = l.a.hidden, tid = threadIdx.x;
-  const int h_tiles = (H + 255) / 256, v_tiles = (l.count + 255) / 256, m_tiles = (live + 255) / 256;
-  const int dh_tiles = l.a.dh ? m_tiles * h_tiles * l.splits : 0;
-  const int dw_tiles = l.a.dw ? v_tiles * h_tiles : 0;
-  const int steps = (l.count + kStepC - 1) / kStepC;
-  const int part = (steps + l.splits - 1) / l.splits * kStepC;  // columns of a split
-  const uint32_t pitch_h = (uint32_t)H * 2u, pitch_d = (uint32_t)l.pitch * 2u;
-  for (int x = 0; x < 8; x++) {
-    const int xcd = (blockIdx.x + x) & 7;
-    const int dh0 = (int)((int64_t)dh_tiles * xcd / 8), dh_n = (int)((int64_t)dh_tiles * (xcd + 1) / 8) - dh0;
-    const int dw0 = (int)((int64_t)dw_tiles * xcd / 8), dw_n = (int)((int64_t)dw_tiles * (xcd + 1) / 8) - dw0;
-    for (;;) {
-      __syncthreads();
-      if (tid == 0) s_next = atomicAdd(l.next + xcd, 1);
-      __syncthreads();
-      const int i = __builtin_amdgcn_readfirstlane(s_next);
-      if (i >= dh_n + dw_n) break;
-      int mt, jt;
-      if (i < dh_n) {
-        const int t = dh0 + i, split = t / (m_tiles * h_tiles);
-        place_of(t - split * (m_tiles * h_tiles), m_tiles, h_tiles, &mt, &jt);
-        const int m0 = mt * 256, j0 = jt * 256, c0 = split * part;
-        const int c = l.count - c0 < part ? l.count - c0 : part;
-        if (c <= 0 && l.first > 0) continue;
-        const int rows = live - m0 < 256 ? live - m0 : 256;
-        // (d's columns past the vocabulary are 0, to a multiple of 8)
-        const TileOperand om = {l.d + (int64_t)m0 * l.pitch + c0, pitch_d, rows, c > 0 ? (c + 7) / 8 * 8 : 0};
-        const TileOperand oj = {l.a.w + (int64_t)(l.first + (c > 0 ? c0 : 0)) * H + j0, pitch_h,
-                                H - j0 < 256 ? H - j0 : 256, c > 0 ? c : 0};
-        float* acc = l.acc + (int64_t)split * l.a.rows * H;
-        if (rows > 128)
-          dh_tile<8>(l, om, oj, s0, s1, s2, s3, acc, live, m0, j0);
-        else if (rows > 64)
-          dh_tile<4>(l, om, oj, s0, s1, s2, s3, acc, live, m0, j0);
-        else if (rows > 32)
-          dh_tile<2>(l, om, oj, s0, s1, s2, s3, acc, live, m0, j0);
-        else
-          dh_tile<1>(l, om, oj, s0, s1, s2, s3, acc, live, m0, j0);
-      } else {
-        place_of(dw0 + i - dh_n, v_tiles, h_tiles, &mt, &jt);
-        const int m0 = mt * 256, j0 = jt * 256;
-        const int own = l.count - m0 < 256 ? (l.count - m0 + 7) / 8 * 8 : 256;
-        const int r0 = __builtin_amdgcn_readfirstlane(l.first_of[(l.first + m0) / 256]);
-        const int more = __builtin_amdgcn_readfirstlane(l.first_of[(l.first + m0) / 256 + 1]) - r0;
-        const TileOperand om = {l.d + m0, pitch_d, own, live, l.rests + (int64_t)r0 * 256, 512u, more};
-        const TileOperand oj = {l.h + j0, pitch_h, H - j0 < 256 ? H - j0 : 256, live,
-                                l.h + (int64_t)r0 * H + j0, pitch_h, more};
-        TileSums<8, 8> sums;
-        tile_product<8, 8, true, true, true>(om, oj, s0, s1, s2, s3, sums);
-        T* out = reinterpret_cast<T*>(l.a.dw) + (int64_t)l.first * H;
-        store_tile<8, 8, T, ADD>(sums, out, m0, l.count, j0, H);
+  const int live = __builtin_amdgcn_readfirstlane(*l.live), tid = threadIdx.x;
+  const GradTiles g(l, live);
+  // a tile's number behind those of dh: g.dh + i is tile i of dw; -1: none left
+  int x = 0;
+  auto ask = [&]() TILE_INLINE {  // one thread; the others read s_next behind the next meeting
+    int n = -1;
+    for (; x < 8; x++) {
+      const int q = (blockIdx.x + x) & 7;
+      const int dh0 = g.first(g.dh, q), dh_n = g.first(g.dh, q + 1) - dh0;
+      const int dw0 = g.first(g.dw, q), dw_n = g.first(g.dw, q + 1) - dw0;
+      const int i = atomicAdd(l.next + q, 1);
+      if (i < dh_n + dw_n) {
+        n = i < dh_n ? dh0 + i : g.dh + dw0 + i - dh_n;
+        break;
       }
+    }
+    s_next = n;
+  };
+  if (tid == 0) ask();
+  __syncthreads();
+  int t = __builtin_amdgcn_readfirstlane(s_next);
+  if (t < 0) return;
+  Long dh;
+  Wide dw;
+  int m0, j0, split, own;  // the tile that is under way
+  auto begin = [&](int n) TILE_INLINE {
+    const GradTile p = n < g.dh ? g.dh_at(l, live, n) : g.dw_at(l, live, n - g.dh);
+    m0 = __builtin_amdgcn_readfirstlane(p.m0);
+    j0 = __builtin_amdgcn_readfirstlane(p.j0);
+    split = __builtin_amdgcn_readfirstlane(p.split);
+    own = __builtin_amdgcn_readfirstlane(p.m.own);
+    if (n < g.dh)
+      dh.start(p.m, p.j, s0, s1, s2, s3);
+    else
+      dw.start(p.m, p.j, s0, s1, s2, s3);
+  };
+  begin(t);
+  while (t >= 0) {
+    __syncthreads();  // (all have read s_next)
+    if (tid == 0) ask();
+    const int m = m0, j = j0;
+    if (split < 0) {
+      TileSums<8, 8> sums;
+      dw.run(s0, s1, s2, s3, sums);
+      __syncthreads();
+      t = __builtin_amdgcn_readfirstlane(s_next);
+      if (t >= 0) begin(t);
+      store_tile<8, 8, T, ADD>(sums, reinterpret_cast<T*>(l.a.dw) + (int64_t)l.first * l.a.hidden, m, l.count, j,
+                               l.a.hidden);
+    } else {
+      float* acc = l.acc + (int64_t)split * l.a.rows * l.a.hidden;
+      auto finish = [&](auto u) TILE_INLINE {
+        TileSums<decltype(u)::value, 8> sums;
+        dh.run(s0, s1, s2, s3, sums);
+        const bool none = dh.steps == 0;
+        __syncthreads();
+        t = __builtin_amdgcn_readfirstlane(s_next);
+        if (t >= 0) begin(t);
+        if (l.first == 0)  // kept, or added to what earlier pieces left
+          store_tile<decltype(u)::value, 8, float, false>(sums, acc, m, live, j, l.a.hidden);
+        else if (!none)
+          store_tile<decltype(u)::value, 8, float, true>(sums, acc, m, live, j, l.a.hidden);
+      };
+      if (own > 128)
+        finish(std::integral_constant<int, 8>{});
+      else if (own > 64)
+        finish(std::integral_constant<int, 4>{});
+      else if (own > 32)
+        finish(std::integral_constant<int, 2>{});
+      else
+        finish(std::integral_constant<int, 1>{});
     }
   }
 }

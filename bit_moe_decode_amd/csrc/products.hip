@@ -70,75 +70,115 @@ __device__ __forceinline__ int expert_of_tile(const ProductArgs& a, const Produc
   return __builtin_amdgcn_readfirstlane(e0 + __popcll(__ballot(below) & 0xFFFFu) - 1);
 }
 
-template <int U, int V, bool DX, typename Stage, typename T>
-__device__ __forceinline__ void product_tile(const TileOperand& om, const TileOperand& oj, Stage& s0, Stage& s1,
-                                             Stage& s2, Stage& s3, T* out, int64_t lo, int64_t hi, int j0, int cols) {
-  TileSums<U, V> acc;
-  tile_product<U, V, false, DX>(om, oj, s0, s1, s2, s3, acc);
-  store_tile<U, V, T, false>(acc, out, lo, hi, j0, cols);
-}
+// A tile: rows lo + .. to hi, columns j0 + .. of the output.
+struct ProductTile {
+  TileOperand m, j;
+  int64_t lo, hi;
+  int j0;
+};
 
-// y, or with DX dx, of tiles of 32 U rows at most (fewer where a group's last
+// y, or with DX dx, of tiles of 32 UMAX rows at most (fewer where a group's last
 // tile holds fewer) and 32 V columns.
 template <int UMAX, int V, bool DX, typename T>
 __global__ __launch_bounds__(256) void moe_product_kernel(ProductArgs a) {
-  constexpr int TM = 32 * UMAX, TJ = 32 * V, KILOS = 2 * UMAX + 2 * V;
-  __shared__ TileStage<KILOS> s0, s1, s2, s3;
+  using Pipe = TilePipe<UMAX, V, false, DX>;
+  constexpr int TM = 32 * UMAX, TJ = 32 * V;
+  __shared__ typename Pipe::Stage s0, s1, s2, s3;
   __shared__ ProductPlaces places;
   count_tiles<TM>(a, places);
   const int cols = DX ? a.k : a.n, len = DX ? a.n : a.k;
   const int j_tiles = (cols + TJ - 1) / TJ;
   const int64_t total = (int64_t)places.first[a.experts] * j_tiles;
-  const uint16_t* in = DX ? a.dy : a.x;
   T* out = reinterpret_cast<T*>(DX ? (void*)a.dx : a.y);
-  for (int64_t t = first_tile(); t < total; t += gridDim.x) {
+  auto tile_at = [&](int64_t t) TILE_INLINE {
     const int e = expert_of_tile(a, places, (int)(t / j_tiles));
     const int before = __builtin_amdgcn_readfirstlane(places.first[e]);
     const int mine = __builtin_amdgcn_readfirstlane(places.first[e + 1]) - before;
     int mt, jt;
     place_of((int)(t - (int64_t)before * j_tiles), mine, j_tiles, &mt, &jt);
-    int64_t lo, hi;
-    rows_of_expert(a, e, &lo, &hi);
-    lo += (int64_t)mt * TM;
-    const int rows = __builtin_amdgcn_readfirstlane((int)(hi - lo < TM ? hi - lo : TM));
-    const int j0 = jt * TJ;
-    const int own = cols - j0 < TJ ? cols - j0 : TJ;
-    const TileOperand om = {in + lo * len, (uint32_t)len * 2u, rows, len};
-    const uint16_t* w = a.w + (int64_t)e * a.n * a.k;
-    const TileOperand oj = {w + (DX ? (int64_t)j0 : (int64_t)j0 * a.k), (uint32_t)a.k * 2u, own, len};
-    if (UMAX == 8 && rows > 128)
-      product_tile<UMAX, V, DX>(om, oj, s0, s1, s2, s3, out, lo, hi, j0, cols);
-    else if (UMAX >= 4 && rows > 64)
-      product_tile<UMAX < 4 ? UMAX : 4, V, DX>(om, oj, s0, s1, s2, s3, out, lo, hi, j0, cols);
-    else if (rows > 32)
-      product_tile<2, V, DX>(om, oj, s0, s1, s2, s3, out, lo, hi, j0, cols);
+    ProductTile p;
+    rows_of_expert(a, e, &p.lo, &p.hi);
+    p.lo += (int64_t)mt * TM;
+    p.j0 = jt * TJ;
+    const int rows = __builtin_amdgcn_readfirstlane((int)(p.hi - p.lo < TM ? p.hi - p.lo : TM));
+    p.m = {(DX ? a.dy : a.x) + p.lo * len, (uint32_t)len * 2u, rows, len};
+    p.j = {a.w + (int64_t)e * a.n * a.k + (DX ? (int64_t)p.j0 : (int64_t)p.j0 * a.k), (uint32_t)a.k * 2u,
+           cols - p.j0 < TJ ? cols - p.j0 : TJ, len};
+    return p;
+  };
+  int64_t t = first_tile();
+  if (t >= total) return;
+  Pipe pipe;
+  ProductTile p = tile_at(t);
+  pipe.start(p.m, p.j, s0, s1, s2, s3);
+  for (;;) {
+    t += gridDim.x;
+    const bool more = t < total;
+    ProductTile next = p;
+    if (more) next = tile_at(t);
+    auto finish = [&](auto u) TILE_INLINE {
+      TileSums<decltype(u)::value, V> sums;
+      pipe.run(s0, s1, s2, s3, sums);
+      if (more) pipe.start(next.m, next.j, s0, s1, s2, s3);
+      store_tile<decltype(u)::value, V, T, false>(sums, out, p.lo, p.hi, p.j0, cols);
+    };
+    if (UMAX == 8 && p.m.own > 128)
+      finish(std::integral_constant<int, UMAX>{});
+    else if (UMAX >= 4 && p.m.own > 64)
+      finish(std::integral_constant<int, UMAX < 4 ? UMAX : 4>{});
+    else if (p.m.own > 32)
+      finish(std::integral_constant<int, 2>{});
     else
-      product_tile<1, V, DX>(om, oj, s0, s1, s2, s3, out, lo, hi, j0, cols);
+      finish(std::integral_constant<int, 1>{});
+    if (!more) return;
+    p = next;
   }
 }
 
 // dW of tiles of 32 U rows (of n) and 32 V columns (of k).
 template <int U, int V, typename T, bool ADD>
 __global__ __launch_bounds__(256) void moe_product_dw_kernel(ProductArgs a) {
-  constexpr int TM = 32 * U, TJ = 32 * V, KILOS = 2 * U + 2 * V;
-  __shared__ TileStage<KILOS> s0, s1, s2, s3;
+  using Pipe = TilePipe<U, V, true, true>;
+  constexpr int TM = 32 * U, TJ = 32 * V;
+  __shared__ typename Pipe::Stage s0, s1, s2, s3;
   const int m_tiles = (a.n + TM - 1) / TM, j_tiles = (a.k + TJ - 1) / TJ;
   const int per = m_tiles * j_tiles;
   const int64_t total = (int64_t)a.experts * per;
-  for (int64_t t = first_tile(); t < total; t += gridDim.x) {
-    const int e = (int)(t / per);
+  struct Tile {
+    TileOperand m, j;
+    int e, m0, j0;
+  };
+  auto tile_at = [&](int64_t t) TILE_INLINE {
+    Tile p;
+    p.e = (int)(t / per);
     int mt, jt;
-    place_of((int)(t - (int64_t)e * per), m_tiles, j_tiles, &mt, &jt);
+    place_of((int)(t - (int64_t)p.e * per), m_tiles, j_tiles, &mt, &jt);
     int64_t lo, hi;
-    rows_of_expert(a, e, &lo, &hi);
+    rows_of_expert(a, p.e, &lo, &hi);
     const int c = __builtin_amdgcn_readfirstlane((int)(hi - lo));
-    const int m0 = mt * TM, j0 = jt * TJ;
-    const TileOperand om = {a.dy + lo * a.n + m0, (uint32_t)a.n * 2u, a.n - m0 < TM ? a.n - m0 : TM, c};
-    const TileOperand oj = {a.x + lo * a.k + j0, (uint32_t)a.k * 2u, a.k - j0 < TJ ? a.k - j0 : TJ, c};
-    TileSums<U, V> acc;
-    tile_product<U, V, true, true>(om, oj, s0, s1, s2, s3, acc);
-    T* out = reinterpret_cast<T*>(a.dw) + (int64_t)e * a.n * a.k;
-    if (!ADD || c > 0) store_tile<U, V, T, ADD>(acc, out, m0, a.n, j0, a.k);
+    p.m0 = mt * TM;
+    p.j0 = jt * TJ;
+    p.m = {a.dy + lo * a.n + p.m0, (uint32_t)a.n * 2u, a.n - p.m0 < TM ? a.n - p.m0 : TM, c};
+    p.j = {a.x + lo * a.k + p.j0, (uint32_t)a.k * 2u, a.k - p.j0 < TJ ? a.k - p.j0 : TJ, c};
+    return p;
+  };
+  int64_t t = first_tile();
+  if (t >= total) return;
+  Pipe pipe;
+  Tile p = tile_at(t);
+  pipe.start(p.m, p.j, s0, s1, s2, s3);
+  for (;;) {
+    t += gridDim.x;
+    const bool more = t < total;
+    Tile next = p;
+    if (more) next = tile_at(t);
+    TileSums<U, V> sums;
+    pipe.run(s0, s1, s2, s3, sums);
+    if (more) pipe.start(next.m, next.j, s0, s1, s2, s3);
+    T* out = reinterpret_cast<T*>(a.dw) + (int64_t)p.e * a.n * a.k;
+    if (!ADD || p.m.c > 0) store_tile<U, V, T, ADD>(sums, out, p.m0, a.n, p.j0, a.k);
+    if (!more) return;
+    p = next;
   }
 }
 

@@ -40,6 +40,10 @@ struct TileOperand {
   int c2 = 0;
 };
 
+// (on a lambda: a tile of it that is called and not inlined keeps its registers in
+// memory)
+#define TILE_INLINE __attribute__((always_inline))
+
 constexpr int kStepC = 32;
 // A load to LDS puts 16 bytes a lane at consecutive places, 1 KB in all, and
 // reads memory a line at a time only where neighbouring lanes read ascending
@@ -68,6 +72,15 @@ __device__ __forceinline__ void tile_meet() {
   asm volatile("" ::: "memory");
 }
 
+// An address that is the same in all lanes, as the scalar it is (a buffer whose
+// base the compiler takes for a lane's own is read lane by lane).
+__device__ __forceinline__ const uint8_t* tile_scalar(const void* p) {
+  const uint64_t a = (uint64_t)p;
+  return reinterpret_cast<const uint8_t*>(
+      (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)a) |
+      (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(a >> 32)) << 32);
+}
+
 // How an operand of P tiles of 16 (own) x 32 (c) lies in a stage: P kilobytes.
 //
 // Not transposed: a piece is the 64 bytes of one row; kilobyte q of row tile i
@@ -94,9 +107,9 @@ struct TileLoader {
   int read;                      // this lane's operands in a stage
 
   __device__ __forceinline__ void set(const TileOperand& o, int lane, int wv) {
-    pitch = o.pitch;
-    c = o.c;
-    base = reinterpret_cast<const uint8_t*>(o.base);
+    pitch = (uint32_t)__builtin_amdgcn_readfirstlane((int)o.pitch);
+    c = __builtin_amdgcn_readfirstlane(o.c);
+    base = tile_scalar(o.base);
     q0 = wv * kLoads;  // (a wave without one loads nothing, zeros, behind the operand)
     const int col = lane & 15, g = lane >> 4;
     if constexpr (T) {
@@ -111,16 +124,17 @@ struct TileLoader {
       }
       kc = 0;
       if constexpr (LONGER) {
-        base2 = reinterpret_cast<const uint8_t*>(o.base2);
-        pitch2 = o.pitch2;
-        c2 = o.c2;
+        base2 = tile_scalar(o.base2);
+        pitch2 = (uint32_t)__builtin_amdgcn_readfirstlane((int)o.pitch2);
+        c2 = __builtin_amdgcn_readfirstlane(o.c2);
         steps = (c + kStepC - 1) / kStepC;
       }
       read = (col >> 2) * kPiecesAt + g * (P >= 8 ? 128 : 256) + (col & 3) * 8;
     } else {
       const int p = lane >> 2;
       const int row = 16 * (p % P) + P * (p / P);
-      whole = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(base), 0, (uint32_t)o.own * pitch, 0x00027000);
+      whole = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(base), 0,
+                                                (uint32_t)__builtin_amdgcn_readfirstlane(o.own) * pitch, 0x00027000);
 #pragma unroll
       for (int n = 0; n < kLoads; n++)
         at[n] = P >= 4 || wv < P ? (uint32_t)(row + q0 + n) * pitch + 16u * (uint32_t)(lane & 3) : kNothing;
@@ -184,115 +198,134 @@ __device__ __forceinline__ void tile_hold(v4f (&sums)[V]) {
 // so a branch around one has to be a scalar branch.
 __device__ __forceinline__ int tile_wave(int tid) { return __builtin_amdgcn_readfirstlane(tid >> 6); }
 
+// One wave's sums: s[u][v] of m tile wm U + u and j tile wj V + v (wm, wj: the
+// wave's bits 0 and 1); a lane holds j = 4 (lane / 16) + 0..3 of m = lane % 16.
 template <int U, int V>
 struct TileSums {
   v4f s[U][V];
 };
 
-// sums.s[u][v]: this wave's sums, of m tile wm U + u and j tile wj V + v (wm, wj:
-// the wave's bits 0 and 1): a lane holds j = 4 (lane / 16) + 0..3 of m = lane %
-// 16.  All of the block's threads call it, with the same arguments.
-template <int U, int V, bool MT, bool JT, bool LONGER = false, typename Stage>
-__device__ __forceinline__ void tile_product(const TileOperand& om, const TileOperand& oj, Stage& s0, Stage& s1,
-                                             Stage& s2, Stage& s3, TileSums<U, V>& sums) {
-#ifdef __HIP_DEVICE_COMPILE__  // (the host's pass of the compiler refuses the body and needs none)
-  auto& acc = sums.s;
-  constexpr int PM = 2 * U, PJ = 2 * V;
-  static_assert(sizeof(Stage) >= (TileLoader<PM, MT, LONGER>::kKilos + TileLoader<PJ, JT, LONGER>::kKilos) * kPiecesAt,
-                "both operands fit a stage");
-  const int tid = threadIdx.x, lane = tid & 63, wv = tile_wave(tid);
-  const int wm = wv & 1, wj = wv >> 1;
+// The products of tiles of 32 UMAX m at most by 32 V j, one after the other:
+//   pipe.start(..) the first tile's loads
+//   for each tile: pipe.run<U>(.., sums) for its sums, U = UMAX or fewer row tiles
+//     a wave where the tile's m are; then pipe.start(..) the next tile, whose
+//     first loads run while the sums are stored.
+// All of the block's threads call them, with the same arguments.  A tile lies in
+// the stages as one of UMAX does.
+template <int UMAX, int V, bool MT, bool JT, bool LONGER = false>
+struct TilePipe {
+  static constexpr int PM = 2 * UMAX, PJ = 2 * V;
   static_assert(!LONGER || (MT && JT), "of transposed operands");
   using Rows = TileLoader<PM, MT, LONGER>;
   using Columns = TileLoader<PJ, JT, LONGER>;
+  static constexpr int NM = Rows::kLoads, NJ = Columns::kLoads, NL = NM + NJ;
+  static constexpr int kJ = Rows::kKilos * kPiecesAt;  // where J starts in a stage
+  static constexpr int kKilos = Rows::kKilos + Columns::kKilos;
+  using Stage = TileStage<kKilos>;
   Rows m;
   Columns j;
-  m.set(om, lane, wv);
-  j.set(oj, lane, wv);
-  constexpr int NM = Rows::kLoads, NJ = Columns::kLoads, NL = NM + NJ;
-  constexpr int kJ = Rows::kKilos * kPiecesAt;  // where J starts in a stage
-  const int steps = (om.c + kStepC - 1) / kStepC + (LONGER ? (om.c2 + kStepC - 1) / kStepC : 0);
-#pragma unroll
-  for (int u = 0; u < U; u++)
-#pragma unroll
-    for (int v = 0; v < V; v++) acc[u][v] = v4f{0.f, 0.f, 0.f, 0.f};
-  if (steps <= 0) return;
-  auto issue = [&](Stage& s, int k, int n) {
+  int steps;
+
+#ifdef __HIP_DEVICE_COMPILE__  // (the host's pass of the compiler refuses the bodies and needs none)
+  __device__ __forceinline__ void issue(uint8_t* b, int k, int n) const {
     if (n < NM)
-      m.issue(s.b, k, n);
+      m.issue(b, k, n);
     else
-      j.issue(s.b + kJ, k, n - NM);
-  };
-  auto issue_all = [&](Stage& s, int k) {
-#pragma unroll
-    for (int n = 0; n < NL; n++) issue(s, k, n);
-  };
-  struct Operands {
-    v8bf m[U], j[V];
-  };
-  auto read = [&](Operands& o, Stage& s, int n) {
-    if (n < V)
-      o.j[n] = j.operand(s.b + kJ, wj * V + n);
-    else
-      o.m[n - V] = m.operand(s.b, wm * U + n - V);
-  };
-  // step k: its operands in `now`; the next's are read from nx, and cur is
-  // filled with step k + 4
-  auto step = [&](Operands& now, Operands& then, Stage& cur, Stage& nx, int k) {
-    // the next step has arrived when the two behind it are under way at most;
-    // and all waves have read all of this one
-    tile_meet<2 * NL>();
-    constexpr int N = U * V, NR = U + V;
-    constexpr int kRead = N >= 16 ? N * 3 / 4 : N;  // reads end early: the next meeting waits for them
-#pragma unroll
-    for (int v = 0; v < V; v++)
-#pragma unroll
-      for (int u = 0; u < U; u++) {
-        const int n = v * U + u;
-#pragma unroll
-        for (int q = 0; q < NR; q++)
-          if (q * kRead / NR == n) read(then, nx, q);
-#pragma unroll
-        for (int q = 0; q < NL; q++)
-          if (q * N / NL == n) issue(cur, k + 4, q);
-        mfma_bf16_into(acc[u][v], now.j[v], now.m[u]);
-        __builtin_amdgcn_sched_barrier(0);
-      }
-  };
-  Operands a, b;
-  issue_all(s0, 0);
-  issue_all(s1, 1);
-  issue_all(s2, 2);
-  issue_all(s3, 3);
-  tile_meet<3 * NL>();
-#pragma unroll
-  for (int q = 0; q < U + V; q++) read(a, s0, q);
-  int k = 0;
-  for (; k + 4 <= steps; k += 4) {
-    step(a, b, s0, s1, k);
-    step(b, a, s1, s2, k + 1);
-    step(a, b, s2, s3, k + 2);
-    step(b, a, s3, s0, k + 3);
-    tile_settle();
+      j.issue(b + kJ, k, n - NM);
   }
-  if (k < steps) {
-    step(a, b, s0, s1, k);
-    tile_settle();
-  }
-  if (k + 1 < steps) {
-    step(b, a, s1, s2, k + 1);
-    tile_settle();
-  }
-  if (k + 2 < steps) {
-    step(a, b, s2, s3, k + 2);
-    tile_settle();
-  }
-  tile_meet<0>();  // nothing under way into a stage, and no wave reads one
-  // (a branch that the lanes do not share may not draw the last MFMAs into it)
+  __device__ __forceinline__ void start(const TileOperand& om, const TileOperand& oj, Stage& s0, Stage& s1, Stage& s2,
+                                        Stage& s3) {
+    const int tid = threadIdx.x, lane = tid & 63, wv = tile_wave(tid);
+    m.set(om, lane, wv);
+    j.set(oj, lane, wv);
+    steps = (m.c + kStepC - 1) / kStepC + (LONGER ? (m.c2 + kStepC - 1) / kStepC : 0);
+    if (steps <= 0) return;
 #pragma unroll
-  for (int u = 0; u < U; u++) tile_hold(acc[u]);
+    for (int n = 0; n < NL; n++) issue(s0.b, 0, n);
+#pragma unroll
+    for (int n = 0; n < NL; n++) issue(s1.b, 1, n);
+#pragma unroll
+    for (int n = 0; n < NL; n++) issue(s2.b, 2, n);
+#pragma unroll
+    for (int n = 0; n < NL; n++) issue(s3.b, 3, n);
+  }
+
+  template <int U>
+  __device__ __forceinline__ void run(Stage& s0, Stage& s1, Stage& s2, Stage& s3, TileSums<U, V>& sums) const {
+    const int wv = tile_wave(threadIdx.x), wm = wv & 1, wj = wv >> 1;
+    auto& acc = sums.s;
+#pragma unroll
+    for (int u = 0; u < U; u++)
+#pragma unroll
+      for (int v = 0; v < V; v++) acc[u][v] = v4f{0.f, 0.f, 0.f, 0.f};
+    if (steps <= 0) return;
+    struct Operands {
+      v8bf m[U], j[V];
+    };
+    auto read = [&](Operands& o, Stage& s, int n) TILE_INLINE {
+      if (n < V)
+        o.j[n] = j.operand(s.b + kJ, wj * V + n);
+      else
+        o.m[n - V] = m.operand(s.b, wm * U + n - V);
+    };
+    // step k: its operands in `now`; the next's are read from nx, and cur is
+    // filled with step k + 4
+    auto step = [&](Operands& now, Operands& then, Stage& cur, Stage& nx, int k) TILE_INLINE {
+      // the next step has arrived when the two behind it are under way at most;
+      // and all waves have read all of this one
+      tile_meet<2 * NL>();
+      constexpr int N = U * V, NR = U + V;
+      constexpr int kRead = N >= 16 ? N * 3 / 4 : N;  // reads end early: the next meeting waits for them
+#pragma unroll
+      for (int v = 0; v < V; v++)
+#pragma unroll
+        for (int u = 0; u < U; u++) {
+          const int n = v * U + u;
+#pragma unroll
+          for (int q = 0; q < NR; q++)
+            if (q * kRead / NR == n) read(then, nx, q);
+#pragma unroll
+          for (int q = 0; q < NL; q++)
+            if (q * N / NL == n) issue(cur.b, k + 4, q);
+          mfma_bf16_into(acc[u][v], now.j[v], now.m[u]);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+    };
+    Operands a, b;
+    tile_meet<3 * NL>();
+#pragma unroll
+    for (int q = 0; q < U + V; q++) read(a, s0, q);
+    int k = 0;
+    for (; k + 4 <= steps; k += 4) {
+      step(a, b, s0, s1, k);
+      step(b, a, s1, s2, k + 1);
+      step(a, b, s2, s3, k + 2);
+      step(b, a, s3, s0, k + 3);
+      tile_settle();
+    }
+    if (k < steps) {
+      step(a, b, s0, s1, k);
+      tile_settle();
+    }
+    if (k + 1 < steps) {
+      step(b, a, s1, s2, k + 1);
+      tile_settle();
+    }
+    if (k + 2 < steps) {
+      step(a, b, s2, s3, k + 2);
+      tile_settle();
+    }
+    tile_meet<0>();  // nothing under way into a stage, and no wave reads one
+    // (a branch that the lanes do not share may not draw the last MFMAs into it)
+#pragma unroll
+    for (int u = 0; u < U; u++) tile_hold(acc[u]);
+  }
+#else
+  __device__ void start(const TileOperand&, const TileOperand&, Stage&, Stage&, Stage&, Stage&) {}
+  template <int U>
+  __device__ void run(Stage&, Stage&, Stage&, Stage&, TileSums<U, V>&) const {}
 #endif
-}
+};
 
 // Two neighbouring j tiles' sums of one m as bf16: 16 bytes, the 8 values at
 // tile_pair_at() of the pair's first column.  (The lanes of j 4 .. 7 and 0 .. 3
