@@ -36,14 +36,14 @@ struct HeadTile {
 };
 
 // Calls done(sums, tile) for this block's tiles of `total`.
-template <int UMAX, int V, typename Stage, typename TileAt, typename Done>
-__device__ __forceinline__ void head_tiles(int total, TileAt tile_at, Stage& s0, Stage& s1, Stage& s2, Stage& s3,
+template <int UMAX, int V, typename Stage, typename Last, typename TileAt, typename Done>
+__device__ __forceinline__ void head_tiles(int total, TileAt tile_at, Stage& s0, Stage& s1, Last& s2,
                                            Done done) {
   int t = first_tile();
   if (t >= total) return;
   TilePipe<UMAX, V, false, false> pipe;
   HeadTile p = tile_at(t);
-  pipe.start(p.m, p.j, s0, s1, s2, s3);
+  pipe.start(p.m, p.j, s0, s1, s2);
   for (;;) {
     t += gridDim.x;
     const bool more = t < total;
@@ -51,8 +51,8 @@ __device__ __forceinline__ void head_tiles(int total, TileAt tile_at, Stage& s0,
     if (more) next = tile_at(t);
     auto finish = [&](auto u) TILE_INLINE {
       TileSums<decltype(u)::value, V> sums;
-      pipe.run(s0, s1, s2, s3, sums);
-      if (more) pipe.start(next.m, next.j, s0, s1, s2, s3);
+      pipe.template run<0>(s0, s1, s2, sums, false);
+      if (more) pipe.start(next.m, next.j, s0, s1, s2);
       done(sums, p);
     };
     if (UMAX == 8 && p.m.own > 128)
@@ -138,7 +138,8 @@ template <int UMAX, int V>
 __global__ __launch_bounds__(256) void lm_loss_kernel(LossTiles l) {
   using Pipe = TilePipe<UMAX, V, false, false>;
   constexpr int TM = 32 * UMAX, TJ = 32 * V;
-  __shared__ typename Pipe::Stage s0, s1, s2, s3;
+  __shared__ typename Pipe::Stage s0, s1;
+  __shared__ typename Pipe::Last s2;
   const int m_tiles = (l.count + TM - 1) / TM, j_tiles = (l.a.vocab + TJ - 1) / TJ, H = l.a.hidden;
   auto tile_at = [&](int t) TILE_INLINE {
     int mt, jt;
@@ -150,7 +151,7 @@ __global__ __launch_bounds__(256) void lm_loss_kernel(LossTiles l) {
     p.j = {l.a.w + (int64_t)p.j0 * H, (uint32_t)H * 2u, l.a.vocab - p.j0 < TJ ? l.a.vocab - p.j0 : TJ, H};
     return p;
   };
-  head_tiles<UMAX, V>(m_tiles * j_tiles, tile_at, s0, s1, s2, s3, [&](auto& sums, const HeadTile& p) TILE_INLINE {
+  head_tiles<UMAX, V>(m_tiles * j_tiles, tile_at, s0, s1, s2, [&](auto& sums, const HeadTile& p) TILE_INLINE {
     loss_epilogue(l, sums, p.m0, p.j0, p.j0 / TJ * 2);
   });
 }
@@ -287,7 +288,8 @@ template <int UMAX, int V>
 __global__ __launch_bounds__(256) void lm_loss_d_kernel(LossGrad l) {
   using Pipe = TilePipe<UMAX, V, false, false>;
   constexpr int TM = 32 * UMAX, TJ = 32 * V;
-  __shared__ typename Pipe::Stage s0, s1, s2, s3;
+  __shared__ typename Pipe::Stage s0, s1;
+  __shared__ typename Pipe::Last s2;
   if (blockIdx.x == 0 && threadIdx.x < 8) l.next[threadIdx.x] = 0;
   const int live = __builtin_amdgcn_readfirstlane(*l.live);
   const int m_tiles = (live + TM - 1) / TM, j_tiles = (l.count + TJ - 1) / TJ, H = l.a.hidden;
@@ -301,7 +303,7 @@ __global__ __launch_bounds__(256) void lm_loss_d_kernel(LossGrad l) {
     p.j = {l.a.w + (int64_t)(l.first + p.j0) * H, (uint32_t)H * 2u, l.count - p.j0 < TJ ? l.count - p.j0 : TJ, H};
     return p;
   };
-  head_tiles<UMAX, V>(m_tiles * j_tiles, tile_at, s0, s1, s2, s3,
+  head_tiles<UMAX, V>(m_tiles * j_tiles, tile_at, s0, s1, s2,
                       [&](auto& sums, const HeadTile& p) TILE_INLINE { grad_epilogue(l, sums, live, p.m0, p.j0); });
 }
 
@@ -365,7 +367,8 @@ __global__ __launch_bounds__(256) void lm_loss_products_kernel(LossGrad l) {
   using Long = TilePipe<8, 8, false, true>;
   using Wide = TilePipe<8, 8, true, true, true>;
   static_assert(sizeof(Long::Stage) == sizeof(Wide::Stage), "both take the same stages");
-  __shared__ Long::Stage s0, s1, s2, s3;
+  __shared__ Long::Stage s0, s1;
+  __shared__ Long::Last s2;
   __shared__ int s_next;
   const int live = __builtin_amdgcn_readfirstlane(*l.live), tid = threadIdx.x;
   const GradTiles g(l, live);
@@ -399,9 +402,9 @@ __global__ __launch_bounds__(256) void lm_loss_products_kernel(LossGrad l) {
     split = __builtin_amdgcn_readfirstlane(p.split);
     own = __builtin_amdgcn_readfirstlane(p.m.own);
     if (n < g.dh)
-      dh.start(p.m, p.j, s0, s1, s2, s3);
+      dh.start(p.m, p.j, s0, s1, s2);
     else
-      dw.start(p.m, p.j, s0, s1, s2, s3);
+      dw.start(p.m, p.j, s0, s1, s2);
   };
   begin(t);
   while (t >= 0) {
@@ -410,7 +413,7 @@ __global__ __launch_bounds__(256) void lm_loss_products_kernel(LossGrad l) {
     const int m = m0, j = j0;
     if (split < 0) {
       TileSums<8, 8> sums;
-      dw.run(s0, s1, s2, s3, sums);
+      dw.run<0>(s0, s1, s2, sums, false);
       __syncthreads();
       t = __builtin_amdgcn_readfirstlane(s_next);
       if (t >= 0) begin(t);
@@ -420,8 +423,8 @@ __global__ __launch_bounds__(256) void lm_loss_products_kernel(LossGrad l) {
       float* acc = l.acc + (int64_t)split * l.a.rows * l.a.hidden;
       auto finish = [&](auto u) TILE_INLINE {
         TileSums<decltype(u)::value, 8> sums;
-        dh.run(s0, s1, s2, s3, sums);
-        const bool none = dh.steps == 0;
+        dh.run<0>(s0, s1, s2, sums, false);
+        const bool none = dh.halves == 0;
         __syncthreads();
         t = __builtin_amdgcn_readfirstlane(s_next);
         if (t >= 0) begin(t);

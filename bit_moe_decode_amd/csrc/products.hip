@@ -83,7 +83,8 @@ template <int UMAX, int V, bool DX, typename T>
 __global__ __launch_bounds__(256) void moe_product_kernel(ProductArgs a) {
   using Pipe = TilePipe<UMAX, V, false, DX>;
   constexpr int TM = 32 * UMAX, TJ = 32 * V;
-  __shared__ typename Pipe::Stage s0, s1, s2, s3;
+  __shared__ typename Pipe::Stage s0, s1;
+  __shared__ typename Pipe::Last s2;
   __shared__ ProductPlaces places;
   count_tiles<TM>(a, places);
   const int cols = DX ? a.k : a.n, len = DX ? a.n : a.k;
@@ -110,7 +111,8 @@ __global__ __launch_bounds__(256) void moe_product_kernel(ProductArgs a) {
   if (t >= total) return;
   Pipe pipe;
   ProductTile p = tile_at(t);
-  pipe.start(p.m, p.j, s0, s1, s2, s3);
+  pipe.start(p.m, p.j, s0, s1, s2);
+  bool stored = false;
   for (;;) {
     t += gridDim.x;
     const bool more = t < total;
@@ -118,8 +120,8 @@ __global__ __launch_bounds__(256) void moe_product_kernel(ProductArgs a) {
     if (more) next = tile_at(t);
     auto finish = [&](auto u) TILE_INLINE {
       TileSums<decltype(u)::value, V> sums;
-      pipe.run(s0, s1, s2, s3, sums);
-      if (more) pipe.start(next.m, next.j, s0, s1, s2, s3);
+      pipe.template run<kTileStores<UMAX, V, T>>(s0, s1, s2, sums, stored);
+      if (more) pipe.start(next.m, next.j, s0, s1, s2);
       store_tile<decltype(u)::value, V, T, false>(sums, out, p.lo, p.hi, p.j0, cols);
     };
     if (UMAX == 8 && p.m.own > 128)
@@ -131,6 +133,7 @@ __global__ __launch_bounds__(256) void moe_product_kernel(ProductArgs a) {
     else
       finish(std::integral_constant<int, 1>{});
     if (!more) return;
+    stored = p.m.own > 16 * UMAX;  // (fewer stores of a tile of fewer rows)
     p = next;
   }
 }
@@ -140,7 +143,8 @@ template <int U, int V, typename T, bool ADD>
 __global__ __launch_bounds__(256) void moe_product_dw_kernel(ProductArgs a) {
   using Pipe = TilePipe<U, V, true, true>;
   constexpr int TM = 32 * U, TJ = 32 * V;
-  __shared__ typename Pipe::Stage s0, s1, s2, s3;
+  __shared__ typename Pipe::Stage s0, s1;
+  __shared__ typename Pipe::Last s2;
   const int m_tiles = (a.n + TM - 1) / TM, j_tiles = (a.k + TJ - 1) / TJ;
   const int per = m_tiles * j_tiles;
   const int64_t total = (int64_t)a.experts * per;
@@ -166,19 +170,21 @@ __global__ __launch_bounds__(256) void moe_product_dw_kernel(ProductArgs a) {
   if (t >= total) return;
   Pipe pipe;
   Tile p = tile_at(t);
-  pipe.start(p.m, p.j, s0, s1, s2, s3);
+  pipe.start(p.m, p.j, s0, s1, s2);
+  bool stored = false;
   for (;;) {
     t += gridDim.x;
     const bool more = t < total;
     Tile next = p;
     if (more) next = tile_at(t);
     TileSums<U, V> sums;
-    pipe.run(s0, s1, s2, s3, sums);
-    if (more) pipe.start(next.m, next.j, s0, s1, s2, s3);
+    pipe.template run<ADD ? 0 : kTileStores<U, V, T>>(s0, s1, s2, sums, stored);
+    if (more) pipe.start(next.m, next.j, s0, s1, s2);
     T* out = reinterpret_cast<T*>(a.dw) + (int64_t)p.e * a.n * a.k;
     if (!ADD || p.m.c > 0) store_tile<U, V, T, ADD>(sums, out, p.m0, a.n, p.j0, a.k);
     if (!more) return;
     p = next;
+    stored = true;
   }
 }
 

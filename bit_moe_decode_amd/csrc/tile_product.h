@@ -6,14 +6,19 @@
 // transposed, with m (j) contiguous in a row of each c.
 //
 // A block's four waves hold the tile as 2 x 2 parts of 16 U x 16 V sums a wave.
-// c runs in steps of 32 through a ring of four LDS stages that loads fill
-// directly.  While the MFMAs of a step run, the wave reads the next step's
-// operands into registers and refills the stage that this step was read from,
-// one load or LDS read between MFMAs; the waves meet once a step.  At 8 x 8 a
-// step is 64 MFMAs of 16 cycles beside 64 KB read from LDS and 32 KB written to
-// it, 768 cycles of its 128 bytes a cycle: one wave a SIMD with 256 sums a lane
-// keeps the LDS below the MFMAs, where 8 waves of half the width would read 96
-// KB, as long as the MFMAs take.
+// c runs in steps of 64 through a ring of LDS stages that loads fill directly,
+// and in halves of 32 through the MFMAs: while those of one half run, the wave
+// reads the next half's operands into registers, and in a step's second half,
+// when all waves have read its stage, the stage's next loads go out, one load or
+// LDS read between MFMAs.  At 8 x 8 a half is 64 MFMAs of 16 cycles beside 64 KB
+// read from LDS and 32 KB written to it, 768 cycles of its 128 bytes a cycle: one
+// wave a SIMD with 256 sums a lane keeps the LDS below the MFMAs, where 8 waves of
+// half the width would read 96 KB, as long as the MFMAs take.
+//
+// Loads take 128 bytes of a row, a line, in all cases: the L2 serves 64 bytes in
+// the time of 128 (loads to LDS alone of 256 blocks that share their rows as these
+// do, 15 against 25 TB/s; with steps of 32, which took a line in two halves, two
+// steps apart, the loss of 4096 rows took 2717 us, 2400 of them without the MFMAs).
 #pragma once
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -44,7 +49,7 @@ struct TileOperand {
 // memory)
 #define TILE_INLINE __attribute__((always_inline))
 
-constexpr int kStepC = 32;
+constexpr int kStepC = 64, kHalfC = 32;
 // A load to LDS puts 16 bytes a lane at consecutive places, 1 KB in all, and
 // reads memory a line at a time only where neighbouring lanes read ascending
 // addresses: a kilobyte holds whole pieces of rows, each of another row.  The
@@ -54,7 +59,7 @@ constexpr int kPiecesAt = 1056;
 
 template <int KILOS>
 struct TileStage {
-  __align__(16) uint8_t b[KILOS * kPiecesAt];
+  __align__(16) uint8_t b[KILOS > 0 ? KILOS * kPiecesAt : 16];
 };
 
 typedef __attribute__((address_space(3))) void tile_lds_void;
@@ -64,10 +69,15 @@ typedef __attribute__((address_space(3))) v4s tile_lds_v4s;
 // Waits for this wave's LDS operations, and until at most VM of its loads are
 // under way, then for the other waves.  No memory operation moves across.
 template <int VM>
+__device__ __forceinline__ void tile_wait() {
+  constexpr int N = VM < 63 ? VM : 63;
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt((N & 15) | (7 << 4) | ((N >> 4) << 14));
+  asm volatile("" ::: "memory");
+}
+template <int VM>
 __device__ __forceinline__ void tile_meet() {
-  asm volatile("" ::: "memory");
-  __builtin_amdgcn_s_waitcnt((VM & 15) | (7 << 4) | ((VM >> 4) << 14));
-  asm volatile("" ::: "memory");
+  tile_wait<VM>();
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
 }
@@ -81,20 +91,21 @@ __device__ __forceinline__ const uint8_t* tile_scalar(const void* p) {
       (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(a >> 32)) << 32);
 }
 
-// How an operand of P tiles of 16 (own) x 32 (c) lies in a stage: P kilobytes.
+// How an operand of P tiles of 16 (own) x 64 (c) lies in a stage: 2 P kilobytes of
+// 8 pieces of 128 bytes.
 //
-// Not transposed: a piece is the 64 bytes of one row; kilobyte q of row tile i
-// holds rows q, q + P, .. of it in its pieces i, i + P, ...  A lane's operand is
-// 16 bytes of row lane % 16: one read.
-// Transposed: a piece is 128 bytes, 64 columns of one c; with 128 columns or
-// more kilobyte q holds c = q % 8 + 8 p in its pieces p, of the first and
-// second 64 of its 128 columns (64 columns: c = q + 4 p).  A lane's operand is
-// the 8 c of column lane % 16: two transposing reads of 4 (in each, lane i of 16
-// names 8 bytes of c = i / 4, columns 4 (i % 4) .., and gets the 4 c of column i).
+// Not transposed: a piece is 64 c of one row.  Kilobyte r holds row r of each of 8
+// row tiles (P = 16: 16 + r of the second 8); with P below 8 kilobyte q holds rows
+// q, q + 2 P, .. of tile i in its pieces i, i + P, ..  A lane's operand of a half
+// is 16 bytes of row lane % 16: one read.
+// Transposed: a piece is 64 columns of one c: kilobyte 8 b + q holds c = q + 8 p of
+// the b-th 64 columns in its pieces p.  A lane's operand of a half is the 8 c of
+// column lane % 16: two transposing reads of 4 (in each, lane i of 16 names 8 bytes
+// of c = i / 4, columns 4 (i % 4) .., and gets the 4 c of column i).
 template <int P, bool T, bool LONGER>
 struct TileLoader {
-  static constexpr int kLoads = P >= 4 ? P / 4 : 1;  // a wave's a step
-  static constexpr int kKilos = 4 * kLoads;          // that they fill
+  static constexpr int kKilos = 2 * P, kLoads = kKilos / 4;  // of a stage, a wave's of them
+  static_assert(P == 2 || P == 4 || P == 8 || P == 16, "tiles of an operand");
   static_assert(!T || P >= 4, "64 columns at least");
   static constexpr uint32_t kNothing = 0xFFFFFF00u;  // an offset behind every buffer's end
   __amdgpu_buffer_rsrc_t whole;  // not transposed: the tile's rows
@@ -110,15 +121,13 @@ struct TileLoader {
     pitch = (uint32_t)__builtin_amdgcn_readfirstlane((int)o.pitch);
     c = __builtin_amdgcn_readfirstlane(o.c);
     base = tile_scalar(o.base);
-    q0 = wv * kLoads;  // (a wave without one loads nothing, zeros, behind the operand)
-    const int col = lane & 15, g = lane >> 4;
+    q0 = wv * kLoads;
+    const int col = lane & 15, g = lane >> 4, p = lane >> 3;
     if constexpr (T) {
-      const int p = lane >> 3;
-      const int cl = P >= 8 ? 8 * (p & 3) : 4 * p, block = P >= 8 ? p >> 2 : 0;
-      const int own0 = (P >= 8 ? (q0 >> 3) * 128 : 0) + block * 64 + (lane & 7) * 8;
 #pragma unroll
       for (int n = 0; n < kLoads; n++) {
-        const uint32_t row = (uint32_t)(cl + (P >= 8 ? (q0 + n) & 7 : q0 + n));
+        const int q = q0 + n, own0 = (q >> 3) * 64 + (lane & 7) * 8;
+        const uint32_t row = (uint32_t)((q & 7) + 8 * p);
         at[n] = own0 < o.own ? row * pitch + (uint32_t)own0 * 2u : kNothing;
         if constexpr (LONGER) at2[n] = own0 < o.own ? row * o.pitch2 + (uint32_t)own0 * 2u : kNothing;
       }
@@ -129,17 +138,18 @@ struct TileLoader {
         c2 = __builtin_amdgcn_readfirstlane(o.c2);
         steps = (c + kStepC - 1) / kStepC;
       }
-      read = (col >> 2) * kPiecesAt + g * (P >= 8 ? 128 : 256) + (col & 3) * 8;
+      read = (col >> 2) * kPiecesAt + g * 128 + (col & 3) * 8;
     } else {
-      const int p = lane >> 2;
-      const int row = 16 * (p % P) + P * (p / P);
       whole = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(base), 0,
                                                 (uint32_t)__builtin_amdgcn_readfirstlane(o.own) * pitch, 0x00027000);
 #pragma unroll
-      for (int n = 0; n < kLoads; n++)
-        at[n] = P >= 4 || wv < P ? (uint32_t)(row + q0 + n) * pitch + 16u * (uint32_t)(lane & 3) : kNothing;
-      kc = 8 * (lane & 3);
-      read = (col % P) * kPiecesAt + (col / P) * P * 64 + 16 * g;
+      for (int n = 0; n < kLoads; n++) {
+        const int q = q0 + n;
+        const int row = P >= 8 ? ((q >> 4) * 8 + p) * 16 + (q & 15) : (p % P) * 16 + q + 2 * P * (p / P);
+        at[n] = (uint32_t)row * pitch + 16u * (uint32_t)(lane & 7);
+      }
+      kc = 8 * (lane & 7);
+      read = P >= 8 ? col * kPiecesAt + 16 * g : (col % kKilos) * kPiecesAt + (col / kKilos) * P * 128 + 16 * g;
     }
   }
   // Load n of the wave's of step k; lds: where the operand starts in the stage.
@@ -162,15 +172,15 @@ struct TileLoader {
                                                c0 < c ? (uint32_t)c0 * 2u : 0u, 0, 0);
     }
   }
-  // Tile i's operand.
-  __device__ __forceinline__ v8bf operand(const uint8_t* lds, int i) const {
+  // Tile i's operand of half h.
+  __device__ __forceinline__ v8bf operand(const uint8_t* lds, int i, int h) const {
     if constexpr (T) {
-      const uint8_t* p = lds + read + (P >= 8 ? (i >> 3) * (8 * kPiecesAt) + ((i >> 2) & 1) * 512 : 0) + (i & 3) * 32;
+      const uint8_t* p = lds + read + (i >> 2) * (8 * kPiecesAt) + (i & 3) * 32 + h * 512;
       const v4s a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((tile_lds_v4s*)p);
-      const v4s b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((tile_lds_v4s*)(p + (P >= 8 ? 4 * kPiecesAt : 128)));
+      const v4s b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((tile_lds_v4s*)(p + 4 * kPiecesAt));
       return __builtin_bit_cast(v8bf, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
     } else {
-      return *reinterpret_cast<const v8bf*>(lds + read + i * 64);
+      return *reinterpret_cast<const v8bf*>(lds + read + (i >> 3) * (16 * kPiecesAt) + (i & 7) * 128 + h * 64);
     }
   }
 };
@@ -211,8 +221,9 @@ struct TileSums {
 //     a wave where the tile's m are; then pipe.start(..) the next tile, whose
 //     first loads run while the sums are stored.
 // All of the block's threads call them, with the same arguments.  A tile lies in
-// the stages as one of UMAX does.
-template <int UMAX, int V, bool MT, bool JT, bool LONGER = false>
+// the stages as one of UMAX does.  The ring has two stages where they are large
+// (67 KB), or three.
+template <int UMAX, int V, bool MT, bool JT, bool LONGER = false, int STAGES = 0>
 struct TilePipe {
   static constexpr int PM = 2 * UMAX, PJ = 2 * V;
   static_assert(!LONGER || (MT && JT), "of transposed operands");
@@ -221,10 +232,14 @@ struct TilePipe {
   static constexpr int NM = Rows::kLoads, NJ = Columns::kLoads, NL = NM + NJ;
   static constexpr int kJ = Rows::kKilos * kPiecesAt;  // where J starts in a stage
   static constexpr int kKilos = Rows::kKilos + Columns::kKilos;
+  static constexpr int kStages = STAGES ? STAGES : kKilos > 48 ? 2 : 3;
+  // (one LDS object a stage: while a load to an object is under way, the compiler
+  // lets reads of that object wait for all loads)
   using Stage = TileStage<kKilos>;
+  using Last = TileStage<kStages == 3 ? kKilos : 0>;
   Rows m;
   Columns j;
-  int steps;
+  int halves;
 
 #ifdef __HIP_DEVICE_COMPILE__  // (the host's pass of the compiler refuses the bodies and needs none)
   __device__ __forceinline__ void issue(uint8_t* b, int k, int n) const {
@@ -233,49 +248,52 @@ struct TilePipe {
     else
       j.issue(b + kJ, k, n - NM);
   }
-  __device__ __forceinline__ void start(const TileOperand& om, const TileOperand& oj, Stage& s0, Stage& s1, Stage& s2,
-                                        Stage& s3) {
+  __device__ __forceinline__ void start(const TileOperand& om, const TileOperand& oj, Stage& s0, Stage& s1, Last& s2) {
     const int tid = threadIdx.x, lane = tid & 63, wv = tile_wave(tid);
     m.set(om, lane, wv);
     j.set(oj, lane, wv);
-    steps = (m.c + kStepC - 1) / kStepC + (LONGER ? (m.c2 + kStepC - 1) / kStepC : 0);
-    if (steps <= 0) return;
+    // (a step of the second part of LONGER begins where one of the first ends)
+    halves = LONGER && m.c2 > 0 ? 2 * m.steps + (m.c2 + kHalfC - 1) / kHalfC : (m.c + kHalfC - 1) / kHalfC;
+    if (halves <= 0) return;
 #pragma unroll
     for (int n = 0; n < NL; n++) issue(s0.b, 0, n);
 #pragma unroll
     for (int n = 0; n < NL; n++) issue(s1.b, 1, n);
+    if constexpr (kStages == 3) {
 #pragma unroll
-    for (int n = 0; n < NL; n++) issue(s2.b, 2, n);
-#pragma unroll
-    for (int n = 0; n < NL; n++) issue(s3.b, 3, n);
+      for (int n = 0; n < NL; n++) issue(s2.b, 2, n);
+    }
   }
 
-  template <int U>
-  __device__ __forceinline__ void run(Stage& s0, Stage& s1, Stage& s2, Stage& s3, TileSums<U, V>& sums) const {
+  // STORES: stores that every wave has issued behind the tile's first loads, at
+  // least, where `stored`: they count among what is under way, and are not waited
+  // for before the second step.
+  template <int STORES, int U>
+  __device__ __forceinline__ void run(Stage& s0, Stage& s1, Last& s2, TileSums<U, V>& sums, bool stored) const {
     const int wv = tile_wave(threadIdx.x), wm = wv & 1, wj = wv >> 1;
     auto& acc = sums.s;
 #pragma unroll
     for (int u = 0; u < U; u++)
 #pragma unroll
       for (int v = 0; v < V; v++) acc[u][v] = v4f{0.f, 0.f, 0.f, 0.f};
-    if (steps <= 0) return;
+    if (halves <= 0) return;
+    constexpr int N = U * V, NR = U + V;
     struct Operands {
       v8bf m[U], j[V];
     };
-    auto read = [&](Operands& o, Stage& s, int n) TILE_INLINE {
+    auto read = [&](Operands& o, const uint8_t* s, int h, int n) TILE_INLINE {
       if (n < V)
-        o.j[n] = j.operand(s.b + kJ, wj * V + n);
+        o.j[n] = j.operand(s + kJ, wj * V + n, h);
       else
-        o.m[n - V] = m.operand(s.b, wm * U + n - V);
+        o.m[n - V] = m.operand(s, wm * U + n - V, h);
     };
-    // step k: its operands in `now`; the next's are read from nx, and cur is
-    // filled with step k + 4
-    auto step = [&](Operands& now, Operands& then, Stage& cur, Stage& nx, int k) TILE_INLINE {
-      // the next step has arrived when the two behind it are under way at most;
-      // and all waves have read all of this one
-      tile_meet<2 * NL>();
-      constexpr int N = U * V, NR = U + V;
-      constexpr int kRead = N >= 16 ? N * 3 / 4 : N;  // reads end early: the next meeting waits for them
+    // A half's MFMAs, of the operands in `now`.  READ: beside them the half h of
+    // `from` is read into `then`; LOAD: and `to` is filled with step k.
+    auto half = [&](auto read_too, auto load_too, Operands& now, Operands& then, const uint8_t* from, int h, uint8_t* to,
+                    int k) TILE_INLINE {
+      constexpr bool READ = decltype(read_too)::value, LOAD = decltype(load_too)::value;
+      constexpr int kRead = N >= 16 ? N * 3 / 4 : N;  // reads end early: the next half waits for them
+      constexpr int kLoad = N >= 16 ? N / 2 : N;      // and loads have the more time to arrive
 #pragma unroll
       for (int v = 0; v < V; v++)
 #pragma unroll
@@ -283,36 +301,61 @@ struct TilePipe {
           const int n = v * U + u;
 #pragma unroll
           for (int q = 0; q < NR; q++)
-            if (q * kRead / NR == n) read(then, nx, q);
+            if (READ && q * kRead / NR == n) read(then, from, h, q);
 #pragma unroll
           for (int q = 0; q < NL; q++)
-            if (q * N / NL == n) issue(cur.b, k + 4, q);
+            if (LOAD && q * kLoad / NL == n) issue(to, k, q);
           mfma_bf16_into(acc[u][v], now.j[v], now.m[u]);
           __builtin_amdgcn_sched_barrier(0);
         }
     };
+    using yes = std::true_type;
+    using no = std::false_type;
     Operands a, b;
-    tile_meet<3 * NL>();
+    // step k in stage cur, the next in nx
+    auto step = [&](uint8_t* cur, uint8_t* nx, int k) TILE_INLINE {
+      half(yes{}, no{}, a, b, cur, 1, nullptr, 0);
+      // the next step has arrived when at most the one behind it is under way, and
+      // all waves have read all of this one
+      if (STORES > 0 && stored && k == 0)
+        tile_wait<(kStages - 2) * NL + STORES>();
+      else
+        tile_wait<(kStages - 2) * NL>();
+      tile_meet<63>();
+      half(yes{}, yes{}, b, a, nx, 0, cur, k + kStages);
+    };
+    if (STORES > 0 && stored)
+      tile_wait<(kStages - 1) * NL + STORES>();
+    else
+      tile_wait<(kStages - 1) * NL>();
+    tile_meet<63>();
 #pragma unroll
-    for (int q = 0; q < U + V; q++) read(a, s0, q);
+    for (int q = 0; q < NR; q++) read(a, s0.b, 0, q);
+    const int steps = halves >> 1;
     int k = 0;
-    for (; k + 4 <= steps; k += 4) {
-      step(a, b, s0, s1, k);
-      step(b, a, s1, s2, k + 1);
-      step(a, b, s2, s3, k + 2);
-      step(b, a, s3, s0, k + 3);
+    for (; k + kStages <= steps; k += kStages) {
+      if constexpr (kStages == 3) {
+        step(s0.b, s1.b, k);
+        step(s1.b, s2.b, k + 1);
+        step(s2.b, s0.b, k + 2);
+      } else {
+        step(s0.b, s1.b, k);
+        step(s1.b, s0.b, k + 1);
+      }
       tile_settle();
     }
     if (k < steps) {
-      step(a, b, s0, s1, k);
+      step(s0.b, s1.b, k);
       tile_settle();
     }
-    if (k + 1 < steps) {
-      step(b, a, s1, s2, k + 1);
-      tile_settle();
+    if constexpr (kStages == 3) {
+      if (k + 1 < steps) {
+        step(s1.b, s2.b, k + 1);
+        tile_settle();
+      }
     }
-    if (k + 2 < steps) {
-      step(a, b, s2, s3, k + 2);
+    if (halves & 1) {
+      half(no{}, no{}, a, b, nullptr, 0, nullptr, 0);
       tile_settle();
     }
     tile_meet<0>();  // nothing under way into a stage, and no wave reads one
@@ -321,9 +364,9 @@ struct TilePipe {
     for (int u = 0; u < U; u++) tile_hold(acc[u]);
   }
 #else
-  __device__ void start(const TileOperand&, const TileOperand&, Stage&, Stage&, Stage&, Stage&) {}
-  template <int U>
-  __device__ void run(Stage&, Stage&, Stage&, Stage&, TileSums<U, V>&) const {}
+  __device__ void start(const TileOperand&, const TileOperand&, Stage&, Stage&, Last&) {}
+  template <int STORES, int U>
+  __device__ void run(Stage&, Stage&, Last&, TileSums<U, V>&, bool) const {}
 #endif
 };
 
@@ -360,29 +403,42 @@ __device__ __forceinline__ int first_tile() {
   return (int)(blockIdx.x & 7) * (int)(gridDim.x >> 3) + (int)(blockIdx.x >> 3);
 }
 
-// Stores a wave's sums as rows m0 + .. of out, of `cols` columns; rows from
-// m_end and columns from j_end on are not there.
+// Stores a wave's sums as rows m0 + .. of out, of `cols` columns (a multiple of
+// 8); rows from m_end on and columns from cols on are not there.  Without ADD
+// every wave issues kTileStores stores, whose own bounds keep them inside.
+template <int U, int V, typename T>
+constexpr int kTileStores = sizeof(T) == 4 ? U * V : U * V / 2;
+
 template <int U, int V, typename T, bool ADD>
 __device__ __forceinline__ void store_tile(TileSums<U, V>& sums, T* out, int64_t m0, int64_t m_end, int j0, int cols) {
   const int tid = threadIdx.x, lane = tid & 63, wv = tile_wave(tid);
   const int col = lane & 15, g = lane >> 4;
   auto& acc = sums.s;
-  m0 += (wv & 1) * 16 * U + col;
+  m0 += (wv & 1) * 16 * U;
   j0 += (wv >> 1) * 16 * V;
+  // this wave's rows, from column j0 on
+  const int64_t rows = m_end - m0;
+  const uint32_t pitch = (uint32_t)cols * (uint32_t)sizeof(T);
+  const uint8_t* base = tile_scalar(out + (rows > 0 ? m0 : 0) * cols);
+  const auto whole = __builtin_amdgcn_make_buffer_rsrc(
+      const_cast<uint8_t*>(base), 0,
+      rows > 0 ? (uint32_t)__builtin_amdgcn_readfirstlane((int)(rows < 16 * U ? rows : 16 * U)) * pitch : 0u, 0x00027000);
+  constexpr uint32_t kNothing = 0xFFFFFF00u;
 #pragma unroll
   for (int u = 0; u < U; u++) {
     tile_hold(acc[u]);
-    const int64_t m = m0 + 16 * u;
-    T* row = out + m * cols;
+    const uint32_t row = (uint32_t)(16 * u + col) * pitch;
+    const bool there = 16 * u + col < rows;
     if constexpr (sizeof(T) == 4) {
 #pragma unroll
       for (int v = 0; v < V; v++) {
         const int j = j0 + 16 * v + 4 * g;
-        if (m < m_end && j < cols) {
-          v4f s = acc[u][v];
-          if constexpr (ADD) s += *reinterpret_cast<const v4f*>(row + j);
-          *reinterpret_cast<v4f*>(row + j) = s;
+        v4f s = acc[u][v];
+        if constexpr (ADD) {
+          if (there && j < cols) s += *reinterpret_cast<const v4f*>(base + row + 4u * (uint32_t)j);
         }
+        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, s), whole,
+                                               j < cols ? row + 4u * (uint32_t)j : kNothing, 0, 0);
       }
     } else {
 #pragma unroll
@@ -391,8 +447,8 @@ __device__ __forceinline__ void store_tile(TileSums<U, V>& sums, T* out, int64_t
 #pragma unroll
           for (int h = 0; h < 2; h++) {
             const int j = j0 + 16 * (v + h) + 4 * g;
-            if (m < m_end && j < cols) {
-              const uint2 o = *reinterpret_cast<const uint2*>(row + j);
+            if (there && j < cols) {
+              const uint2 o = *reinterpret_cast<const uint2*>(base + row + 2u * (uint32_t)j);
               acc[u][v + h] += v4f{__uint_as_float(o.x << 16), __uint_as_float(o.x & 0xFFFF0000u),
                                    __uint_as_float(o.y << 16), __uint_as_float(o.y & 0xFFFF0000u)};
             }
@@ -400,7 +456,7 @@ __device__ __forceinline__ void store_tile(TileSums<U, V>& sums, T* out, int64_t
         }
         const u32x4 o = tile_pair(acc[u][v], acc[u][v + 1]);
         const int j = j0 + 16 * v + tile_pair_at(lane);
-        if (m < m_end && j < cols) *reinterpret_cast<u32x4*>(row + j) = o;
+        __builtin_amdgcn_raw_buffer_store_b128(o, whole, j < cols ? row + 2u * (uint32_t)j : kNothing, 0, 0);
       }
     }
   }
