@@ -11,6 +11,7 @@
 
 #include "device_common.h"
 #include "embed.h"
+#include "stream_product.h"
 #include "tile_product.h"
 
 namespace moe {
@@ -36,12 +37,12 @@ struct HeadTile {
 };
 
 // Calls done(sums, tile) for this block's tiles of `total`.
-template <int UMAX, int V, typename Stage, typename Last, typename TileAt, typename Done>
+template <typename Stage, typename Last, typename TileAt, typename Done>
 __device__ __forceinline__ void head_tiles(int total, TileAt tile_at, Stage& s0, Stage& s1, Last& s2,
                                            Done done) {
   int t = first_tile();
   if (t >= total) return;
-  TilePipe<UMAX, V, false, false> pipe;
+  TilePipe<8, 8, false, false> pipe;
   HeadTile p = tile_at(t);
   pipe.start(p.m, p.j, s0, s1, s2);
   for (;;) {
@@ -50,21 +51,50 @@ __device__ __forceinline__ void head_tiles(int total, TileAt tile_at, Stage& s0,
     HeadTile next = p;
     if (more) next = tile_at(t);
     auto finish = [&](auto u) TILE_INLINE {
-      TileSums<decltype(u)::value, V> sums;
+      TileSums<decltype(u)::value, 8> sums;
       pipe.template run<0>(s0, s1, s2, sums, false);
       if (more) pipe.start(next.m, next.j, s0, s1, s2);
       done(sums, p);
     };
-    if (UMAX == 8 && p.m.own > 128)
-      finish(std::integral_constant<int, UMAX>{});
-    else if (UMAX >= 4 && p.m.own > 64)
-      finish(std::integral_constant<int, UMAX < 4 ? UMAX : 4>{});
+    if (p.m.own > 128)
+      finish(std::integral_constant<int, 8>{});
+    else if (p.m.own > 64)
+      finish(std::integral_constant<int, 4>{});
     else if (p.m.own > 32)
       finish(std::integral_constant<int, 2>{});
     else
       finish(std::integral_constant<int, 1>{});
     if (!more) return;
     p = next;
+  }
+}
+
+// Few rows h [rows][hidden] against `columns` rows of w: calls done(m, j, part, z)
+// with the logits of row m and columns j .. j + 3, of the part-th 16 columns.
+template <int U, typename Done>
+__device__ __forceinline__ void few_tiles(const uint16_t* h, int rows, const uint16_t* w, int columns, int hidden,
+                                          uint8_t* lds, Done done) {
+  const int lane = threadIdx.x & 63, col = lane & 15, g = lane >> 4;
+  const int tiles = (columns + kStreamJ - 1) / kStreamJ;
+  const uint32_t pitch = (uint32_t)hidden * 2u;
+  const TileOperand om = {h, pitch, rows, hidden};
+  auto columns_of = [&](int jt) TILE_INLINE {
+    const int j0 = jt * kStreamJ;
+    return TileOperand{w + (int64_t)j0 * hidden, pitch, columns - j0 < kStreamJ ? columns - j0 : kStreamJ, hidden};
+  };
+  int jt = blockIdx.x;
+  if (jt >= tiles) return;
+  StreamPipe<U> pipe;
+  pipe.start(om, columns_of(jt));
+  for (;;) {
+    const int now = jt;
+    jt += gridDim.x;
+    pipe.run(lds);
+    if (jt < tiles) pipe.start(om, columns_of(jt));
+    pipe.add(lds, [&](int u, int v, const v4f& z) TILE_INLINE {
+      done(16 * u + col, now * kStreamJ + 16 * v + 4 * g, now * kStreamV + v, z);
+    });
+    if (jt >= tiles) return;
   }
 }
 
@@ -134,10 +164,9 @@ __device__ __forceinline__ void loss_epilogue(const LossTiles& l, TileSums<U, V>
   }
 }
 
-template <int UMAX, int V>
 __global__ __launch_bounds__(256) void lm_loss_kernel(LossTiles l) {
-  using Pipe = TilePipe<UMAX, V, false, false>;
-  constexpr int TM = 32 * UMAX, TJ = 32 * V;
+  using Pipe = TilePipe<8, 8, false, false>;
+  constexpr int TM = 256, TJ = 256;
   __shared__ typename Pipe::Stage s0, s1;
   __shared__ typename Pipe::Last s2;
   const int m_tiles = (l.count + TM - 1) / TM, j_tiles = (l.a.vocab + TJ - 1) / TJ, H = l.a.hidden;
@@ -151,36 +180,73 @@ __global__ __launch_bounds__(256) void lm_loss_kernel(LossTiles l) {
     p.j = {l.a.w + (int64_t)p.j0 * H, (uint32_t)H * 2u, l.a.vocab - p.j0 < TJ ? l.a.vocab - p.j0 : TJ, H};
     return p;
   };
-  head_tiles<UMAX, V>(m_tiles * j_tiles, tile_at, s0, s1, s2, [&](auto& sums, const HeadTile& p) TILE_INLINE {
+  head_tiles(m_tiles * j_tiles, tile_at, s0, s1, s2, [&](auto& sums, const HeadTile& p) TILE_INLINE {
     loss_epilogue(l, sums, p.m0, p.j0, p.j0 / TJ * 2);
   });
 }
 
+// Few rows (up to 16 U): a part is 16 columns of a row.
+template <int U>
+__global__ __launch_bounds__(256, 2) void lm_loss_few_kernel(LossTiles l) {
+  __shared__ __align__(16) uint8_t lds[StreamPipe<U>::kLds];
+  few_tiles<U>(l.a.h + (int64_t)l.first * l.a.hidden, l.count, l.a.w, l.a.vocab, l.a.hidden, lds,
+               [&](int m, int j, int part, v4f z) TILE_INLINE {
+    float big = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+      if (j + i >= l.a.vocab) z[i] = -INFINITY;
+      big = fmaxf(big, z[i]);
+    }
+    big = over_lanes_max(big);
+    float sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; i++) sum += z[i] == big ? 1.f : exp_of(z[i] - big);
+    sum = over_lanes_sum(sum);
+    if (m >= l.count) return;
+    if ((threadIdx.x & 63) < 16) l.part[(size_t)m * l.parts + part] = float2{big, sum};
+    const int t = l.a.targets[l.first + m];
+    if ((uint32_t)t < (uint32_t)l.a.vocab && (uint32_t)(t - j) < 4u)
+      l.at_target[m] = t - j == 0 ? z[0] : (t - j == 1 ? z[1] : (t - j == 2 ? z[2] : z[3]));
+  });
+}
+
 // A row's parts joined, a block a row: the largest, then the sums below it.
-__global__ __launch_bounds__(256) void lm_loss_join_kernel(LossTiles l) {
-  __shared__ float s_big[4], s_sum[4];
-  const int m = blockIdx.x, tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
+__global__ __launch_bounds__(1024) void lm_loss_join_kernel(LossTiles l) {
+  __shared__ float s_big[16], s_sum[16];
+  const int m = blockIdx.x, tid = threadIdx.x, lane = tid & 63, wv = tid >> 6, waves = blockDim.x >> 6;
   const float2* p = l.part + (size_t)m * l.parts;
   float big = -INFINITY, sum = 0.f;
-  for (int i = tid; i < l.parts; i += 256) {
-    const float2 q = p[i];
-    const float b = fmaxf(big, q.x);
-    sum = (big == b ? sum : sum * exp_of(big - b)) + (q.x == b ? q.y : q.y * exp_of(q.x - b));
-    big = b;
+  for (int i0 = tid; i0 < l.parts; i0 += 4 * blockDim.x) {
+    float2 q[4];
+#pragma unroll
+    for (int n = 0; n < 4; n++) {
+      const int i = i0 + n * (int)blockDim.x;
+      q[n] = p[i < l.parts ? i : l.parts - 1];
+      if (i >= l.parts) q[n] = float2{-INFINITY, 0.f};
+    }
+#pragma unroll
+    for (int n = 0; n < 4; n++) {
+      const float b = fmaxf(big, q[n].x);
+      sum = (big == b ? sum : sum * exp_of(big - b)) + (q[n].x == b ? q[n].y : q[n].y * exp_of(q[n].x - b));
+      big = b;
+    }
   }
   const float mine = big;
 #pragma unroll
   for (int o = 32; o > 0; o >>= 1) big = fmaxf(big, __shfl_xor(big, o, kWave));
   if (lane == 0) s_big[wv] = big;
   __syncthreads();
-  big = fmaxf(fmaxf(s_big[0], s_big[1]), fmaxf(s_big[2], s_big[3]));
+  big = s_big[0];
+  for (int w = 1; w < waves; w++) big = fmaxf(big, s_big[w]);
   sum = mine == big ? sum : sum * exp_of(mine - big);
 #pragma unroll
   for (int o = 32; o > 0; o >>= 1) sum += __shfl_xor(sum, o, kWave);
   if (lane == 0) s_sum[wv] = sum;
   __syncthreads();
   if (tid == 0) {
-    const float lse = big + logf(s_sum[0] + s_sum[1] + s_sum[2] + s_sum[3]);
+    sum = s_sum[0];
+    for (int w = 1; w < waves; w++) sum += s_sum[w];
+    const float lse = big + logf(sum);
     const int r = l.first + m;
     l.a.lse[r] = lse;
     l.a.loss[r] = (uint32_t)l.a.targets[r] < (uint32_t)l.a.vocab ? lse - l.at_target[m] : 0.f;
@@ -242,6 +308,22 @@ __global__ __launch_bounds__(256) void lm_loss_gather_kernel(LossGrad l) {
   }
 }
 
+// d at a logit z of the row at place m, whose lse and dloss are q and target t;
+// what its rounding takes at the target is kept.  0 past the vocabulary.
+__device__ __forceinline__ float d_of(const LossGrad& l, float z, const float2& q, int m, int t, bool hit, bool past) {
+  float p = exp_of(z - q.x);
+  if (hit) {
+    p = (p - 1.f) * q.y;
+    const float near = bf16_to_f32(f32_to_bf16(p));
+    const float rest = fabsf(near) < INFINITY ? p - near : 0.f;
+    l.rest[m] = rest;
+    l.rests[(size_t)m * 256 + (t & 255)] = f32_to_bf16(rest);
+  } else {
+    p *= q.y;
+  }
+  return past ? 0.f : p;
+}
+
 // d of a tile; columns past the vocabulary are 0.
 template <int U, int V>
 __device__ __forceinline__ void grad_epilogue(const LossGrad& l, TileSums<U, V>& sums, int live, int m0, int j0) {
@@ -261,20 +343,8 @@ __device__ __forceinline__ void grad_epilogue(const LossGrad& l, TileSums<U, V>&
     for (int v = 0; v < V; v++)
 #pragma unroll
       for (int i = 0; i < 4; i++) {
-        float p = exp_of(sums.s[u][v][i] - q.x);
-        if (hit && 16 * v + 4 * g + i == at) {
-          p = (p - 1.f) * q.y;
-          if (m < live) {
-            const float near = bf16_to_f32(f32_to_bf16(p));
-            const float rest = fabsf(near) < INFINITY ? p - near : 0.f;
-            l.rest[m] = rest;
-            l.rests[(size_t)m * 256 + (t & 255)] = f32_to_bf16(rest);
-          }
-        } else {
-          p *= q.y;
-        }
-        if (edge && j0 + 16 * v + 4 * g + i >= l.count) p = 0.f;
-        sums.s[u][v][i] = p;
+        const int c = 16 * v + 4 * g + i;
+        sums.s[u][v][i] = d_of(l, sums.s[u][v][i], q, m, t, hit && c == at && m < live, edge && j0 + c >= l.count);
       }
 #pragma unroll
     for (int v = 0; v < V; v += 2) {
@@ -284,10 +354,9 @@ __device__ __forceinline__ void grad_epilogue(const LossGrad& l, TileSums<U, V>&
   }
 }
 
-template <int UMAX, int V>
 __global__ __launch_bounds__(256) void lm_loss_d_kernel(LossGrad l) {
-  using Pipe = TilePipe<UMAX, V, false, false>;
-  constexpr int TM = 32 * UMAX, TJ = 32 * V;
+  using Pipe = TilePipe<8, 8, false, false>;
+  constexpr int TM = 256, TJ = 256;
   __shared__ typename Pipe::Stage s0, s1;
   __shared__ typename Pipe::Last s2;
   if (blockIdx.x == 0 && threadIdx.x < 8) l.next[threadIdx.x] = 0;
@@ -303,8 +372,28 @@ __global__ __launch_bounds__(256) void lm_loss_d_kernel(LossGrad l) {
     p.j = {l.a.w + (int64_t)(l.first + p.j0) * H, (uint32_t)H * 2u, l.count - p.j0 < TJ ? l.count - p.j0 : TJ, H};
     return p;
   };
-  head_tiles<UMAX, V>(m_tiles * j_tiles, tile_at, s0, s1, s2,
+  head_tiles(m_tiles * j_tiles, tile_at, s0, s1, s2,
                       [&](auto& sums, const HeadTile& p) TILE_INLINE { grad_epilogue(l, sums, live, p.m0, p.j0); });
+}
+
+// d of few rows (up to 16 U).
+template <int U>
+__global__ __launch_bounds__(256, 2) void lm_loss_d_few_kernel(LossGrad l) {
+  __shared__ __align__(16) uint8_t lds[StreamPipe<U>::kLds];
+  if (blockIdx.x == 0 && threadIdx.x < 8) l.next[threadIdx.x] = 0;
+  const int live = __builtin_amdgcn_readfirstlane(*l.live);
+  if (live == 0) return;
+  few_tiles<U>(l.h, live, l.a.w + (int64_t)l.first * l.a.hidden, l.count, l.a.hidden, lds,
+               [&](int m, int j, int, v4f z) TILE_INLINE {
+    if (m >= live) return;
+    const float2 q = l.row[m];
+    const int t = l.target[m];
+#pragma unroll
+    for (int i = 0; i < 4; i++) z[i] = d_of(l, z[i], q, m, t, t - l.first == j + i, j + i >= l.count);
+    *reinterpret_cast<uint2*>(l.d + (size_t)m * l.pitch + j) =
+        uint2{(uint32_t)f32_to_bf16(z[0]) | ((uint32_t)f32_to_bf16(z[1]) << 16),
+              (uint32_t)f32_to_bf16(z[2]) | ((uint32_t)f32_to_bf16(z[3]) << 16)};
+  });
 }
 
 // The two products of a piece's d, in one launch: the tiles of dh, which are
@@ -471,11 +560,17 @@ __global__ __launch_bounds__(256) void lm_loss_dh_kernel(LossGrad l) {
 // --------------------------------------------------------------------- launches
 // Rows of a launch of the loss, for its parts' memory.
 constexpr int kLossRows = 16384;
-// Tiles of 256 x 256 above this many rows, else of 64 x 128.
-constexpr int kLossFew = 64;
+// Tiles of 256 x 256 above this many rows, else of 64 x 64.
+constexpr int kLossFew = kStreamM;
+
+template <typename Args>
+static void launch_few(void (*u1)(Args), void (*u2)(Args), void (*u4)(Args), int rows, int blocks, const Args& l,
+                       hipStream_t stream) {
+  hipLaunchKernelGGL((rows > 32 ? u4 : rows > 16 ? u2 : u1), dim3(blocks), dim3(256), 0, stream, l);
+}
 
 static int loss_parts(int rows, int vocab) {
-  return rows > kLossFew ? 2 * ((vocab + 255) / 256) : 2 * ((vocab + 127) / 128);
+  return rows > kLossFew ? 2 * ((vocab + 255) / 256) : kStreamV * ((vocab + kStreamJ - 1) / kStreamJ);
 }
 static size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 
@@ -498,15 +593,15 @@ hipError_t launch_loss(const LossArgs& a, void* workspace, hipStream_t stream) {
     l.parts = loss_parts(l.count, a.vocab);
     int blocks;
     const bool few = l.count <= kLossFew;
-    const int64_t tiles = few ? (int64_t)(a.vocab + 127) / 128
+    const int64_t tiles = few ? (int64_t)(a.vocab + kStreamJ - 1) / kStreamJ
                               : (int64_t)((l.count + 255) / 256) * ((a.vocab + 255) / 256);
     hipError_t e = tile_blocks(tiles, few ? 2 : 1, &blocks);
     if (e != hipSuccess) return e;
     if (few)
-      hipLaunchKernelGGL((lm_loss_kernel<2, 4>), dim3(blocks), dim3(256), 0, stream, l);
+      launch_few(lm_loss_few_kernel<1>, lm_loss_few_kernel<2>, lm_loss_few_kernel<4>, l.count, blocks, l, stream);
     else
-      hipLaunchKernelGGL((lm_loss_kernel<8, 8>), dim3(blocks), dim3(256), 0, stream, l);
-    hipLaunchKernelGGL(lm_loss_join_kernel, dim3(l.count), dim3(256), 0, stream, l);
+      hipLaunchKernelGGL(lm_loss_kernel, dim3(blocks), dim3(256), 0, stream, l);
+    hipLaunchKernelGGL(lm_loss_join_kernel, dim3(l.count), dim3(few ? 1024 : 256), 0, stream, l);
     e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
@@ -572,14 +667,14 @@ hipError_t launch_loss_backward(const LossGradArgs& a, void* workspace, hipStrea
     l.count = a.vocab - l.first < l.pitch ? a.vocab - l.first : l.pitch;
     int blocks;
     const bool few = a.rows <= kLossFew;
-    const int64_t tiles = few ? (int64_t)(l.count + 127) / 128
+    const int64_t tiles = few ? (int64_t)(l.count + kStreamJ - 1) / kStreamJ
                               : (int64_t)((a.rows + 255) / 256) * ((l.count + 255) / 256);
     e = tile_blocks(tiles, few ? 2 : 1, &blocks);
     if (e != hipSuccess) return e;
     if (few)
-      hipLaunchKernelGGL((lm_loss_d_kernel<2, 4>), dim3(blocks), dim3(256), 0, stream, l);
+      launch_few(lm_loss_d_few_kernel<1>, lm_loss_d_few_kernel<2>, lm_loss_d_few_kernel<4>, a.rows, blocks, l, stream);
     else
-      hipLaunchKernelGGL((lm_loss_d_kernel<8, 8>), dim3(blocks), dim3(256), 0, stream, l);
+      hipLaunchKernelGGL(lm_loss_d_kernel, dim3(blocks), dim3(256), 0, stream, l);
     const int64_t products = ((int64_t)((a.rows + 255) / 256) * l.splits + (l.count + 255) / 256) *
                              ((a.hidden + 255) / 256);
     e = tile_blocks(products, 1, &blocks);

@@ -8,6 +8,7 @@
 #include "products.h"
 
 #include "device_common.h"
+#include "stream_product.h"
 #include "tile_product.h"
 
 namespace moe {
@@ -138,6 +139,55 @@ __global__ __launch_bounds__(256) void moe_product_kernel(ProductArgs a) {
   }
 }
 
+// y of tiles of few rows: 64 rows and 64 columns.
+template <typename T>
+__global__ __launch_bounds__(256, 2) void moe_product_few_kernel(ProductArgs a) {
+  __shared__ __align__(16) uint8_t lds[StreamPipe<kStreamU>::kLds];
+  __shared__ ProductPlaces places;
+  count_tiles<kStreamM>(a, places);
+  const int j_tiles = (a.n + kStreamJ - 1) / kStreamJ;
+  const int64_t total = (int64_t)places.first[a.experts] * j_tiles;
+  T* out = reinterpret_cast<T*>(a.y);
+  const int lane = threadIdx.x & 63, col = lane & 15, g = lane >> 4;
+  for (int64_t t = blockIdx.x; t < total; t += gridDim.x) {
+    const int rt = (int)(t / j_tiles), e = expert_of_tile(a, places, rt);
+    int64_t lo, hi;
+    rows_of_expert(a, e, &lo, &hi);
+    lo += (int64_t)(rt - __builtin_amdgcn_readfirstlane(places.first[e])) * kStreamM;
+    const int j0 = (int)(t - (int64_t)rt * j_tiles) * kStreamJ;
+    const int rows = __builtin_amdgcn_readfirstlane((int)(hi - lo < kStreamM ? hi - lo : kStreamM));
+    const TileOperand om = {a.x + lo * a.k, (uint32_t)a.k * 2u, rows, a.k};
+    const TileOperand oj = {a.w + ((int64_t)e * a.n + j0) * a.k, (uint32_t)a.k * 2u,
+                            a.n - j0 < kStreamJ ? a.n - j0 : kStreamJ, a.k};
+    auto done = [&](int u, int v, const v4f& s) TILE_INLINE {
+      const int m = 16 * u + col, j = j0 + 16 * v + 4 * g;
+      if (m >= rows || j >= a.n) return;
+      T* to = out + (lo + m) * a.n + j;
+      if constexpr (sizeof(T) == 4)
+        *reinterpret_cast<v4f*>(to) = s;
+      else
+        *reinterpret_cast<uint2*>(to) = uint2{(uint32_t)f32_to_bf16(s[0]) | ((uint32_t)f32_to_bf16(s[1]) << 16),
+                                              (uint32_t)f32_to_bf16(s[2]) | ((uint32_t)f32_to_bf16(s[3]) << 16)};
+    };
+    if (rows > 32) {
+      StreamPipe<4> pipe;
+      pipe.start(om, oj);
+      pipe.run(lds);
+      pipe.add(lds, done);
+    } else if (rows > 16) {
+      StreamPipe<2> pipe;
+      pipe.start(om, oj);
+      pipe.run(lds);
+      pipe.add(lds, done);
+    } else {
+      StreamPipe<1> pipe;
+      pipe.start(om, oj);
+      pipe.run(lds);
+      pipe.add(lds, done);
+    }
+  }
+}
+
 // dW of tiles of 32 U rows (of n) and 32 V columns (of k).
 template <int U, int V, typename T, bool ADD>
 __global__ __launch_bounds__(256) void moe_product_dw_kernel(ProductArgs a) {
@@ -203,6 +253,10 @@ static hipError_t launch_rows(const ProductArgs& a, hipStream_t stream) {
     const hipError_t e = tile_blocks(most_tiles(a, cols, 256, 256), 1, &blocks);
     if (e != hipSuccess) return e;
     hipLaunchKernelGGL((moe_product_kernel<8, 8, DX, T>), dim3(blocks), dim3(256), 0, stream, a);
+  } else if constexpr (!DX) {
+    const hipError_t e = tile_blocks(most_tiles(a, cols, kStreamM, kStreamJ), 2, &blocks);
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL(moe_product_few_kernel<T>, dim3(blocks), dim3(256), 0, stream, a);
   } else {
     const hipError_t e = tile_blocks(most_tiles(a, cols, 64, 128), 2, &blocks);
     if (e != hipSuccess) return e;
