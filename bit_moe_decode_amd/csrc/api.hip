@@ -912,7 +912,7 @@ moe_status moe_product_backward(const moe_product_shape* shape, const uint16_t* 
   if (dx && rows && (!w || !aligned16(w) || !aligned16(dx))) return MOE_ERR_INVALID_ARG;
   if (dw && (!aligned16(dw) || (rows && (!x || !aligned16(x))))) return MOE_ERR_INVALID_ARG;
   ProductArgs a = product_args(shape, offsets);
-  const size_t need = product_backward_workspace(a);
+  const size_t need = dw ? product_backward_workspace(a) : 0;
   if (need && (!workspace || ws_bytes < need || !aligned16(workspace))) return MOE_ERR_WORKSPACE;
   const ProductBytes b = product_bytes(shape);
   const void* buf[] = {dy, dw ? x : nullptr, dx ? w : nullptr, offsets, workspace, dx, dw};

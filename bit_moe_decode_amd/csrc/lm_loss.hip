@@ -285,27 +285,78 @@ struct LossGrad {
   int first, count;  // this piece's part of the vocabulary
 };
 
-// Block b: row b, if it has no target, and the row at place b.
-__global__ __launch_bounds__(256) void lm_loss_gather_kernel(LossGrad l) {
-  const int b = blockIdx.x, tid = threadIdx.x, live = *l.live;
-  if (tid == 0 && (uint32_t)l.a.targets[b] >= (uint32_t)l.a.vocab) l.place[b] = -1;
-  if (b == 0 && live == 0)
-    for (int i = tid; i <= (l.a.vocab + 255) / 256; i += 256) l.first_of[i] = 0;
-  if (b >= live) return;
-  const int r = l.order[b], t = l.a.targets[r];
+// The row r of place b, from h: its part in all that the places hold.
+// `before`: the target at the place before, -1 without one; `live`: all places.
+__device__ __forceinline__ void take_place(const LossGrad& l, int r, int b, int t, int before, int live) {
+  const int tid = threadIdx.x, last = (l.a.vocab + 255) / 256;
   const u32x4* from = reinterpret_cast<const u32x4*>(l.a.h + (size_t)r * l.a.hidden);
   u32x4* to = reinterpret_cast<u32x4*>(l.h + (size_t)b * l.a.hidden);
   for (int i = tid; i < l.a.hidden / 8; i += 256) to[i] = from[i];
   if (tid < 32) reinterpret_cast<u32x4*>(l.rests + (size_t)b * 256)[tid] = u32x4{0u, 0u, 0u, 0u};
-  const int before = b > 0 ? l.a.targets[l.order[b - 1]] / 256 : -1;
-  for (int i = before + 1 + tid; i <= t / 256; i += 256) l.first_of[i] = b;
+  for (int i = (before < 0 ? 0 : before / 256 + 1) + tid; i <= t / 256; i += 256) l.first_of[i] = b;
   if (b == live - 1)
-    for (int i = t / 256 + 1 + tid; i <= (l.a.vocab + 255) / 256; i += 256) l.first_of[i] = live;
+    for (int i = t / 256 + 1 + tid; i <= last; i += 256) l.first_of[i] = live;
   if (tid == 0) {
     l.place[r] = b;
     l.target[b] = t;
     l.row[b] = float2{l.a.lse[r], l.a.dloss[r]};
   }
+}
+__device__ __forceinline__ void take_no_place(const LossGrad& l, int r, int live) {
+  if (threadIdx.x == 0) l.place[r] = -1;
+  if (r == 0 && live == 0)
+    for (int i = threadIdx.x; i <= (l.a.vocab + 255) / 256; i += 256) l.first_of[i] = 0;
+}
+
+// Up to kLossRanked rows, without a sort: a block counts what its row comes
+// behind, reading all targets.
+__global__ __launch_bounds__(256) void lm_loss_rank_kernel(LossGrad l, int32_t* count) {
+  __shared__ int s_behind[4], s_live[4], s_before[4];
+  const int r = blockIdx.x, tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
+  const uint32_t t = (uint32_t)l.a.targets[r];
+  int behind = 0, live = 0, before = -1;
+  for (int i0 = tid; i0 < l.a.rows; i0 += 4 * 256) {
+    uint32_t o[4];
+#pragma unroll
+    for (int n = 0; n < 4; n++) {
+      const int i = i0 + 256 * n;
+      o[n] = (uint32_t)l.a.targets[i < l.a.rows ? i : l.a.rows - 1];
+      if (i >= l.a.rows) o[n] = ~0u;
+    }
+#pragma unroll
+    for (int n = 0; n < 4; n++) {
+      const bool in = o[n] < (uint32_t)l.a.vocab, less = in && (o[n] < t || (o[n] == t && i0 + 256 * n < r));
+      live += in;
+      behind += less;
+      if (less) before = max(before, (int)o[n]);
+    }
+  }
+#pragma unroll
+  for (int s = 32; s > 0; s >>= 1) {
+    live += __shfl_xor(live, s, kWave);
+    behind += __shfl_xor(behind, s, kWave);
+    before = max(before, __shfl_xor(before, s, kWave));
+  }
+  if (lane == 0) s_behind[wv] = behind, s_live[wv] = live, s_before[wv] = before;
+  __syncthreads();
+  live = s_live[0] + s_live[1] + s_live[2] + s_live[3];
+  behind = s_behind[0] + s_behind[1] + s_behind[2] + s_behind[3];
+  before = max(max(s_before[0], s_before[1]), max(s_before[2], s_before[3]));
+  if (r == 0 && tid == 0) *count = live;
+  if (t < (uint32_t)l.a.vocab)
+    take_place(l, r, behind, (int)t, before, live);
+  else
+    take_no_place(l, r, live);
+}
+
+// More rows, sorted: block b takes row b, if it has no target, and the row at
+// place b.
+__global__ __launch_bounds__(256) void lm_loss_gather_kernel(LossGrad l) {
+  const int b = blockIdx.x, live = *l.live;
+  if ((uint32_t)l.a.targets[b] >= (uint32_t)l.a.vocab) take_no_place(l, b, live);
+  if (b >= live) return;
+  const int r = l.order[b];
+  take_place(l, r, b, l.a.targets[r], b > 0 ? l.a.targets[l.order[b - 1]] : -1, live);
 }
 
 // d at a logit z of the row at place m, whose lse and dloss are q and target t;
@@ -416,9 +467,6 @@ struct GradTiles {
     dw = l.a.dw ? v_tiles * h_tiles : 0;
     part = ((l.count + kStepC - 1) / kStepC + l.splits - 1) / l.splits * kStepC;
   }
-  // The first of n tiles that are XCD x's.
-  static __device__ __forceinline__ int first(int n, int x) { return (int)((int64_t)n * x / 8); }
-
   __device__ __forceinline__ GradTile dh_at(const LossGrad& l, int live, int t) const {
     const int H = l.a.hidden;
     GradTile p;
@@ -461,25 +509,18 @@ __global__ __launch_bounds__(256) void lm_loss_products_kernel(LossGrad l) {
   __shared__ int s_next;
   const int live = __builtin_amdgcn_readfirstlane(*l.live), tid = threadIdx.x;
   const GradTiles g(l, live);
-  // a tile's number behind those of dh: g.dh + i is tile i of dw; -1: none left
-  int x = 0;
-  auto ask = [&]() TILE_INLINE {  // one thread; the others read s_next behind the next meeting
-    int n = -1;
-    for (; x < 8; x++) {
-      const int q = (blockIdx.x + x) & 7;
-      const int dh0 = g.first(g.dh, q), dh_n = g.first(g.dh, q + 1) - dh0;
-      const int dw0 = g.first(g.dw, q), dw_n = g.first(g.dw, q + 1) - dw0;
-      const int i = atomicAdd(l.next + q, 1);
-      if (i < dh_n + dw_n) {
-        n = i < dh_n ? dh0 + i : g.dh + dw0 + i - dh_n;
-        break;
-      }
-    }
-    s_next = n;
+  // a tile's number: those of dh, then those of dw; each XCD has an eighth of either
+  TileQueues queues{l.next};
+  auto redeem = [&](int ticket) TILE_INLINE {
+    return queues.redeem(
+        ticket, &s_next,
+        [&](int q) TILE_INLINE { return eighth(g.dh, q + 1) - eighth(g.dh, q) + eighth(g.dw, q + 1) - eighth(g.dw, q); },
+        [&](int q, int i) TILE_INLINE {
+          const int n = eighth(g.dh, q + 1) - eighth(g.dh, q);
+          return i < n ? eighth(g.dh, q) + i : g.dh + eighth(g.dw, q) + i - n;
+        });
   };
-  if (tid == 0) ask();
-  __syncthreads();
-  int t = __builtin_amdgcn_readfirstlane(s_next);
+  int t = redeem(tid == 0 ? queues.ticket() : 0);
   if (t < 0) return;
   Long dh;
   Wide dw;
@@ -497,14 +538,12 @@ __global__ __launch_bounds__(256) void lm_loss_products_kernel(LossGrad l) {
   };
   begin(t);
   while (t >= 0) {
-    __syncthreads();  // (all have read s_next)
-    if (tid == 0) ask();
+    const int ticket = tid == 0 ? queues.ticket() : 0;
     const int m = m0, j = j0;
     if (split < 0) {
       TileSums<8, 8> sums;
       dw.run<0>(s0, s1, s2, sums, false);
-      __syncthreads();
-      t = __builtin_amdgcn_readfirstlane(s_next);
+      t = redeem(ticket);
       if (t >= 0) begin(t);
       store_tile<8, 8, T, ADD>(sums, reinterpret_cast<T*>(l.a.dw) + (int64_t)l.first * l.a.hidden, m, l.count, j,
                                l.a.hidden);
@@ -514,8 +553,7 @@ __global__ __launch_bounds__(256) void lm_loss_products_kernel(LossGrad l) {
         TileSums<decltype(u)::value, 8> sums;
         dh.run<0>(s0, s1, s2, sums, false);
         const bool none = dh.halves == 0;
-        __syncthreads();
-        t = __builtin_amdgcn_readfirstlane(s_next);
+        t = redeem(ticket);
         if (t >= 0) begin(t);
         if (l.first == 0)  // kept, or added to what earlier pieces left
           store_tile<decltype(u)::value, 8, float, false>(sums, acc, m, live, j, l.a.hidden);
@@ -608,6 +646,10 @@ hipError_t launch_loss(const LossArgs& a, void* workspace, hipStream_t stream) {
   return hipSuccess;
 }
 
+// Rows up to which each one's place is counted (4096 rows of 2560 17.8 us, sorted
+// and gathered 33; 333 of 1000 4.9 and 17).
+constexpr int kLossRanked = 4096;
+
 // Columns of a piece: d of at most 128 MB, in multiples of 256.
 constexpr size_t kLossPieceBytes = (size_t)128 << 20;
 
@@ -639,7 +681,7 @@ static size_t loss_grad_plan(LossGrad* l, char* base) {
   l->rest = reinterpret_cast<float*>(take(R * 4));
   l->rests = reinterpret_cast<uint16_t*>(take(R * 512));
   l->first_of = reinterpret_cast<int32_t*>(take(((size_t)whole + 1) * 4));
-  l->sort = take(id_sort_workspace(a.rows, a.vocab));
+  l->sort = take(a.rows <= kLossRanked ? 4 : id_sort_workspace(a.rows, a.vocab));
   l->next = reinterpret_cast<int32_t*>(take(8 * 4));
   l->d = reinterpret_cast<uint16_t*>(take(R * l->pitch * 2));
   l->acc = reinterpret_cast<float*>(take((size_t)l->splits * R * a.hidden * 4));
@@ -658,11 +700,18 @@ hipError_t launch_loss_backward(const LossGradArgs& a, void* workspace, hipStrea
   LossGrad l = {};
   l.a = a;
   loss_grad_plan(&l, static_cast<char*>(workspace));
-  int32_t* order;
-  hipError_t e = launch_id_sort(a.targets, a.rows, a.vocab, l.sort, nullptr, 0, &order, &l.live, stream);
-  if (e != hipSuccess) return e;
-  l.order = order;
-  hipLaunchKernelGGL(lm_loss_gather_kernel, dim3(a.rows), dim3(256), 0, stream, l);
+  hipError_t e = hipSuccess;
+  if (a.rows <= kLossRanked) {
+    int32_t* count = static_cast<int32_t*>(l.sort);
+    l.live = count;
+    hipLaunchKernelGGL(lm_loss_rank_kernel, dim3(a.rows), dim3(256), 0, stream, l, count);
+  } else {
+    int32_t* order;
+    e = launch_id_sort(a.targets, a.rows, a.vocab, l.sort, nullptr, 0, &order, &l.live, stream);
+    if (e != hipSuccess) return e;
+    l.order = order;
+    hipLaunchKernelGGL(lm_loss_gather_kernel, dim3(a.rows), dim3(256), 0, stream, l);
+  }
   for (l.first = 0; l.first < a.vocab; l.first += l.pitch) {
     l.count = a.vocab - l.first < l.pitch ? a.vocab - l.first : l.pitch;
     int blocks;

@@ -21,7 +21,8 @@ struct ProductArgs {
   void* dw;                // [experts][n][k]
   bool f32;                // y or dw is fp32, else bf16
   bool add;                // dw is added to
-  float* space;            // the workspace
+  float* space;            // the workspace: sums of parts, where there are several
+  int parts, part;         // set by the launches: parts of the contraction, entries of one
 };
 
 size_t product_workspace(const ProductArgs& a);           // of y

@@ -139,7 +139,15 @@ __global__ __launch_bounds__(256) void moe_product_kernel(ProductArgs a) {
   }
 }
 
-// y of tiles of few rows: 64 rows and 64 columns.
+__device__ __forceinline__ void put4(float* to, const v4f& s) { *reinterpret_cast<v4f*>(to) = s; }
+__device__ __forceinline__ void put4(uint16_t* to, const v4f& s) {
+  *reinterpret_cast<uint2*>(to) = uint2{(uint32_t)f32_to_bf16(s[0]) | ((uint32_t)f32_to_bf16(s[1]) << 16),
+                                        (uint32_t)f32_to_bf16(s[2]) | ((uint32_t)f32_to_bf16(s[3]) << 16)};
+}
+
+// y of tiles of few rows: 64 rows and 64 columns.  Where these are fewer than the
+// CUs, of parts of k, whose sums [parts][rows][n] of float are T's; they are then
+// added in order.
 template <typename T>
 __global__ __launch_bounds__(256, 2) void moe_product_few_kernel(ProductArgs a) {
   __shared__ __align__(16) uint8_t lds[StreamPipe<kStreamU>::kLds];
@@ -147,27 +155,24 @@ __global__ __launch_bounds__(256, 2) void moe_product_few_kernel(ProductArgs a) 
   count_tiles<kStreamM>(a, places);
   const int j_tiles = (a.n + kStreamJ - 1) / kStreamJ;
   const int64_t total = (int64_t)places.first[a.experts] * j_tiles;
-  T* out = reinterpret_cast<T*>(a.y);
   const int lane = threadIdx.x & 63, col = lane & 15, g = lane >> 4;
-  for (int64_t t = blockIdx.x; t < total; t += gridDim.x) {
+  for (int64_t i = blockIdx.x; i < total * a.parts; i += gridDim.x) {
+    const int part = (int)(i / total), k0 = part * a.part, c = a.k - k0 < a.part ? a.k - k0 : a.part;
+    const int64_t t = i - part * total;
+    T* out = a.parts > 1 ? reinterpret_cast<T*>(a.space) + (int64_t)part * a.rows * a.n : reinterpret_cast<T*>(a.y);
     const int rt = (int)(t / j_tiles), e = expert_of_tile(a, places, rt);
     int64_t lo, hi;
     rows_of_expert(a, e, &lo, &hi);
     lo += (int64_t)(rt - __builtin_amdgcn_readfirstlane(places.first[e])) * kStreamM;
     const int j0 = (int)(t - (int64_t)rt * j_tiles) * kStreamJ;
     const int rows = __builtin_amdgcn_readfirstlane((int)(hi - lo < kStreamM ? hi - lo : kStreamM));
-    const TileOperand om = {a.x + lo * a.k, (uint32_t)a.k * 2u, rows, a.k};
-    const TileOperand oj = {a.w + ((int64_t)e * a.n + j0) * a.k, (uint32_t)a.k * 2u,
-                            a.n - j0 < kStreamJ ? a.n - j0 : kStreamJ, a.k};
+    const TileOperand om = {a.x + lo * a.k + k0, (uint32_t)a.k * 2u, rows, c};
+    const TileOperand oj = {a.w + ((int64_t)e * a.n + j0) * a.k + k0, (uint32_t)a.k * 2u,
+                            a.n - j0 < kStreamJ ? a.n - j0 : kStreamJ, c};
     auto done = [&](int u, int v, const v4f& s) TILE_INLINE {
       const int m = 16 * u + col, j = j0 + 16 * v + 4 * g;
       if (m >= rows || j >= a.n) return;
-      T* to = out + (lo + m) * a.n + j;
-      if constexpr (sizeof(T) == 4)
-        *reinterpret_cast<v4f*>(to) = s;
-      else
-        *reinterpret_cast<uint2*>(to) = uint2{(uint32_t)f32_to_bf16(s[0]) | ((uint32_t)f32_to_bf16(s[1]) << 16),
-                                              (uint32_t)f32_to_bf16(s[2]) | ((uint32_t)f32_to_bf16(s[3]) << 16)};
+      put4(out + (lo + m) * a.n + j, s);
     };
     if (rows > 32) {
       StreamPipe<4> pipe;
@@ -188,7 +193,21 @@ __global__ __launch_bounds__(256, 2) void moe_product_few_kernel(ProductArgs a) 
   }
 }
 
-// dW of tiles of 32 U rows (of n) and 32 V columns (of k).
+// y from the sums of k's parts.
+template <typename T>
+__global__ __launch_bounds__(256) void moe_product_add_kernel(ProductArgs a) {
+  int64_t first, last, unused;
+  rows_of_expert(a, 0, &first, &unused);
+  rows_of_expert(a, a.experts - 1, &unused, &last);
+  const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4, r = i / a.n;
+  if (r < first || r >= last) return;
+  v4f s = *reinterpret_cast<const v4f*>(a.space + i);
+  for (int p = 1; p < a.parts; p++) s += *reinterpret_cast<const v4f*>(a.space + p * a.rows * a.n + i);
+  put4(reinterpret_cast<T*>(a.y) + i, s);
+}
+
+// dW of tiles of 32 U rows (of n) and 32 V columns (of k); where these are fewer
+// than the CUs, of parts of the expert's rows, as above.
 template <int U, int V, typename T, bool ADD>
 __global__ __launch_bounds__(256) void moe_product_dw_kernel(ProductArgs a) {
   using Pipe = TilePipe<U, V, true, true>;
@@ -197,10 +216,10 @@ __global__ __launch_bounds__(256) void moe_product_dw_kernel(ProductArgs a) {
   __shared__ typename Pipe::Last s2;
   const int m_tiles = (a.n + TM - 1) / TM, j_tiles = (a.k + TJ - 1) / TJ;
   const int per = m_tiles * j_tiles;
-  const int64_t total = (int64_t)a.experts * per;
+  const int64_t total = (int64_t)a.experts * per * a.parts;
   struct Tile {
     TileOperand m, j;
-    int e, m0, j0;
+    int e, m0, j0;  // e: behind the experts, part by part, where there are several
   };
   auto tile_at = [&](int64_t t) TILE_INLINE {
     Tile p;
@@ -208,7 +227,13 @@ __global__ __launch_bounds__(256) void moe_product_dw_kernel(ProductArgs a) {
     int mt, jt;
     place_of((int)(t - (int64_t)p.e * per), m_tiles, j_tiles, &mt, &jt);
     int64_t lo, hi;
-    rows_of_expert(a, p.e, &lo, &hi);
+    const int part = p.e / a.experts;
+    rows_of_expert(a, p.e - part * a.experts, &lo, &hi);
+    if (a.parts > 1) {  // an expert's rows, in equal parts
+      const int64_t one = ((hi - lo + a.parts - 1) / a.parts + kStepC - 1) / kStepC * kStepC;
+      lo = lo + part * one < hi ? lo + part * one : hi;
+      hi = hi - lo < one ? hi : lo + one;
+    }
     const int c = __builtin_amdgcn_readfirstlane((int)(hi - lo));
     p.m0 = mt * TM;
     p.j0 = jt * TJ;
@@ -230,12 +255,35 @@ __global__ __launch_bounds__(256) void moe_product_dw_kernel(ProductArgs a) {
     TileSums<U, V> sums;
     pipe.template run<ADD ? 0 : kTileStores<U, V, T>>(s0, s1, s2, sums, stored);
     if (more) pipe.start(next.m, next.j, s0, s1, s2);
-    T* out = reinterpret_cast<T*>(a.dw) + (int64_t)p.e * a.n * a.k;
+    T* out = reinterpret_cast<T*>(a.parts > 1 ? (void*)a.space : a.dw) + (int64_t)p.e * a.n * a.k;
     if (!ADD || p.m.c > 0) store_tile<U, V, T, ADD>(sums, out, p.m0, a.n, p.j0, a.k);
     if (!more) return;
     p = next;
     stored = true;
   }
+}
+
+// dW from the sums of the rows' parts.
+template <typename T, bool ADD>
+__global__ __launch_bounds__(256) void moe_product_dw_add_kernel(ProductArgs a) {
+  const int64_t one = (int64_t)a.n * a.k, all = one * a.experts, i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
+  if (i >= all) return;
+  T* to = reinterpret_cast<T*>(a.dw) + i;
+  v4f s = *reinterpret_cast<const v4f*>(a.space + i);
+  for (int p = 1; p < a.parts; p++) s += *reinterpret_cast<const v4f*>(a.space + p * all + i);
+  if constexpr (ADD) {
+    int64_t lo, hi;
+    rows_of_expert(a, (int)(i / one), &lo, &hi);
+    if (lo == hi) return;  // (no rows: left as it was)
+    if constexpr (sizeof(T) == 4) {
+      s += *reinterpret_cast<const v4f*>(to);
+    } else {
+      const uint2 o = *reinterpret_cast<const uint2*>(to);
+      s += v4f{__uint_as_float(o.x << 16), __uint_as_float(o.x & 0xFFFF0000u), __uint_as_float(o.y << 16),
+               __uint_as_float(o.y & 0xFFFF0000u)};
+    }
+  }
+  put4(to, s);
 }
 
 // Upper bound of the tiles of `tm` rows by `tj` columns.
@@ -244,50 +292,110 @@ static int64_t most_tiles(const ProductArgs& a, int cols, int tm, int tj) {
   return m * ((cols + tj - 1) / tj);
 }
 
+// Large tiles where there are enough of them, and rows for half of one an expert.
+static bool rows_large(const ProductArgs& a, int cols) {
+  return a.rows > (int64_t)48 * a.experts && most_tiles(a, cols, 256, 256) >= 256;
+}
+// Parts of k of the small tiles, up to a block a CU, of 16 steps of 64 at least (8
+// rows of 4 experts [512, 6144] 15.8 -> 10.2 us; two blocks a CU: 64 rows of 8
+// experts [1024, 4096] 17.7 us, not split 14.5).
+static void split_rows(ProductArgs* a) {
+  const int64_t tiles = most_tiles(*a, a->n, kStreamM, kStreamJ), steps = (a->k + 63) / 64;
+  int64_t parts = rows_large(*a, a->n) || tiles < 1 ? 1 : 256 / tiles;
+  if (parts > steps / 16) parts = steps / 16;
+  if (parts > 16) parts = 16;
+  a->parts = parts < 2 ? 1 : (int)parts;
+  a->part = (int)((steps + a->parts - 1) / a->parts) * 64;
+}
+// Tiles of dW, and parts of the rows up to two blocks a CU, of 512 rows at least
+// if they are spread evenly (60000 rows of 8 experts, dW [128, 128] 51.7 -> 16.6
+// us; 16384 of 4 experts [512, 512] 32.8 -> 29.7).
+static int64_t dw_tiles(const ProductArgs& a, int side) {
+  return (int64_t)a.experts * ((a.n + side - 1) / side) * ((a.k + side - 1) / side);
+}
+static void split_dw(ProductArgs* a) {
+  int64_t parts = dw_tiles(*a, 256) >= 256 ? 1 : 512 / dw_tiles(*a, 128);
+  const int64_t by_rows = a->rows / ((int64_t)a->experts * 512);
+  if (parts > by_rows) parts = by_rows;
+  if (parts > 32) parts = 32;
+  a->parts = parts < 2 ? 1 : (int)parts;
+}
+
+size_t product_workspace(const ProductArgs& args) {
+  ProductArgs a = args;
+  split_rows(&a);
+  return a.parts > 1 ? (size_t)a.parts * a.rows * a.n * 4 : 0;
+}
+size_t product_backward_workspace(const ProductArgs& args) {
+  ProductArgs a = args;
+  split_dw(&a);
+  return a.parts > 1 ? (size_t)a.parts * a.experts * a.n * a.k * 4 : 0;
+}
+
 template <bool DX, typename T>
-static hipError_t launch_rows(const ProductArgs& a, hipStream_t stream) {
-  const int cols = DX ? a.k : a.n;
+static hipError_t launch_large(const ProductArgs& a, hipStream_t stream) {
   int blocks;
-  const bool large = a.rows > (int64_t)48 * a.experts && most_tiles(a, cols, 256, 256) >= 256;
-  if (large) {
-    const hipError_t e = tile_blocks(most_tiles(a, cols, 256, 256), 1, &blocks);
-    if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((moe_product_kernel<8, 8, DX, T>), dim3(blocks), dim3(256), 0, stream, a);
-  } else if constexpr (!DX) {
-    const hipError_t e = tile_blocks(most_tiles(a, cols, kStreamM, kStreamJ), 2, &blocks);
-    if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(moe_product_few_kernel<T>, dim3(blocks), dim3(256), 0, stream, a);
-  } else {
-    const hipError_t e = tile_blocks(most_tiles(a, cols, 64, 128), 2, &blocks);
-    if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((moe_product_kernel<2, 4, DX, T>), dim3(blocks), dim3(256), 0, stream, a);
-  }
+  const hipError_t e = tile_blocks(most_tiles(a, DX ? a.k : a.n, 256, 256), 1, &blocks);
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL((moe_product_kernel<8, 8, DX, T>), dim3(blocks), dim3(256), 0, stream, a);
   return hipGetLastError();
 }
 
-size_t product_workspace(const ProductArgs&) { return 0; }
-size_t product_backward_workspace(const ProductArgs&) { return 0; }
-
-hipError_t launch_product(const ProductArgs& a, hipStream_t stream) {
-  return a.f32 ? launch_rows<false, float>(a, stream) : launch_rows<false, uint16_t>(a, stream);
+template <typename T>
+static hipError_t launch_few(const ProductArgs& a, hipStream_t stream) {
+  int blocks;
+  const hipError_t e = tile_blocks(most_tiles(a, a.n, kStreamM, kStreamJ) * a.parts, 2, &blocks);
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(moe_product_few_kernel<T>, dim3(blocks), dim3(256), 0, stream, a);
+  return hipGetLastError();
 }
+
+hipError_t launch_product(const ProductArgs& args, hipStream_t stream) {
+  ProductArgs a = args;
+  if (rows_large(a, a.n)) return a.f32 ? launch_large<false, float>(a, stream) : launch_large<false, uint16_t>(a, stream);
+  split_rows(&a);
+  if (a.parts == 1) return a.f32 ? launch_few<float>(a, stream) : launch_few<uint16_t>(a, stream);
+  const hipError_t e = launch_few<float>(a, stream);
+  if (e != hipSuccess) return e;
+  const dim3 grid((uint32_t)((a.rows * a.n / 4 + 255) / 256));
+  if (a.f32)
+    hipLaunchKernelGGL(moe_product_add_kernel<float>, grid, dim3(256), 0, stream, a);
+  else
+    hipLaunchKernelGGL(moe_product_add_kernel<uint16_t>, grid, dim3(256), 0, stream, a);
+  return hipGetLastError();
+}
+
 hipError_t launch_product_dx(const ProductArgs& a, hipStream_t stream) {
-  return launch_rows<true, uint16_t>(a, stream);
+  if (rows_large(a, a.k)) return launch_large<true, uint16_t>(a, stream);
+  int blocks;
+  const hipError_t e = tile_blocks(most_tiles(a, a.k, 64, 128), 2, &blocks);
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL((moe_product_kernel<2, 4, true, uint16_t>), dim3(blocks), dim3(256), 0, stream, a);
+  return hipGetLastError();
 }
 
 template <typename T, bool ADD>
-static hipError_t launch_dw(const ProductArgs& a, hipStream_t stream) {
-  const int64_t large = (int64_t)a.experts * ((a.n + 255) / 256) * ((a.k + 255) / 256);
+static hipError_t launch_dw(const ProductArgs& args, hipStream_t stream) {
+  ProductArgs a = args;
+  a.parts = 1;
+  const int64_t large = dw_tiles(a, 256), small = dw_tiles(a, 128);
   int blocks;
   if (large >= 256) {
     const hipError_t e = tile_blocks(large, 1, &blocks);
     if (e != hipSuccess) return e;
     hipLaunchKernelGGL((moe_product_dw_kernel<8, 8, T, ADD>), dim3(blocks), dim3(256), 0, stream, a);
-  } else {
-    const hipError_t e = tile_blocks((int64_t)a.experts * ((a.n + 127) / 128) * ((a.k + 127) / 128), 2, &blocks);
-    if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((moe_product_dw_kernel<4, 4, T, ADD>), dim3(blocks), dim3(256), 0, stream, a);
+    return hipGetLastError();
   }
+  split_dw(&a);
+  const hipError_t e = tile_blocks(small * a.parts, 1, &blocks);
+  if (e != hipSuccess) return e;
+  if (a.parts == 1) {
+    hipLaunchKernelGGL((moe_product_dw_kernel<4, 4, T, ADD>), dim3(blocks), dim3(256), 0, stream, a);
+    return hipGetLastError();
+  }
+  hipLaunchKernelGGL((moe_product_dw_kernel<4, 4, float, false>), dim3(blocks), dim3(256), 0, stream, a);
+  const int64_t n = (int64_t)a.experts * a.n * a.k / 4;
+  hipLaunchKernelGGL((moe_product_dw_add_kernel<T, ADD>), dim3((uint32_t)((n + 255) / 256)), dim3(256), 0, stream, a);
   return hipGetLastError();
 }
 

@@ -403,6 +403,39 @@ __device__ __forceinline__ int first_tile() {
   return (int)(blockIdx.x & 7) * (int)(gridDim.x >> 3) + (int)(blockIdx.x >> 3);
 }
 
+// Tiles of unequal length, taken as blocks come free: XCD x's blocks take the
+// tiles of queue x one after the other, then those left in the others.  Which
+// block computes a tile changes no result.  A ticket is asked for before the tile
+// that runs meanwhile, and looked at behind it.
+struct TileQueues {
+  int32_t* next;  // [8], zeros at the start
+  int empty = 0;  // queues known to be (thread 0's)
+  __device__ __forceinline__ int queue() const { return (int)(blockIdx.x + empty) & 7; }
+  __device__ __forceinline__ int ticket() const { return atomicAdd(next + queue(), 1); }  // thread 0
+  // The tile of thread 0's ticket, for all threads; -1: none is left.  size(q):
+  // tiles of queue q; tile(q, i): its i-th.
+  template <typename Size, typename Tile>
+  __device__ __forceinline__ int redeem(int ticket_, int* shared, Size size, Tile tile) {
+    if (threadIdx.x == 0) {
+      int t = -1;
+      while (empty < 8) {
+        if (ticket_ < size(queue())) {
+          t = tile(queue(), ticket_);
+          break;
+        }
+        if (++empty < 8) ticket_ = ticket();
+      }
+      *shared = t;
+    }
+    tile_meet<63>();
+    const int t = __builtin_amdgcn_readfirstlane(*shared);
+    tile_meet<63>();
+    return t;
+  }
+};
+// An eighth of n tiles, in their order.
+__device__ __forceinline__ int eighth(int n, int q) { return (int)((int64_t)n * q / 8); }
+
 // Stores a wave's sums as rows m0 + .. of out, of `cols` columns (a multiple of
 // 8); rows from m_end on and columns from cols on are not there.  Without ADD
 // every wave issues kTileStores stores, whose own bounds keep them inside.

@@ -409,8 +409,9 @@ typedef struct {
   int32_t n, k;       /* an expert's matrix: multiples of 8, 8..MOE_MAX_PRODUCT_SIDE */
 } moe_product_shape;
 
-/* Bytes of workspace the two calls below need (0 for most shapes), or 0 when
- * the shape is not supported. */
+/* Bytes of workspace the two calls below need, or 0 when the shape is not
+ * supported; 0 for most shapes, not where a few small tiles have long sums, whose
+ * parts it holds.  The second is dw's: without dw none is needed. */
 size_t moe_product_workspace_size(const moe_product_shape* shape);
 size_t moe_product_backward_workspace_size(const moe_product_shape* shape);
 

@@ -161,6 +161,33 @@ def test_product_of_every_number_of_steps(k):
     del dy
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("counts,more,n,k", [([3, 0, 5], 4, 72, 8200), ([40], 0, 8, 32768), ([1], 0, 200, 4104)])
+def test_product_of_long_sums(counts, more, n, k, dtype):
+    """A few tiles, whose sums are split."""
+    _say("long sums", counts, n, k, dtype)
+    rows = sum(counts) + more
+    assert B.moe_product_workspace_size(rows, len(counts), n, k) > 0
+    x, w = _normal(1, rows, k), _normal(2, len(counts), n, k)
+    y = _product(x, w, _offsets(counts), dtype)
+    torch.cuda.synchronize()
+    _check_product(y, x, w, counts)
+
+
+@pytest.mark.parametrize("add", [False, True])
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("counts,n,k", [([2500, 0, 3, 1601], 72, 136), ([5000], 264, 8), ([1, 8000], 40, 296)])
+def test_gradients_of_many_rows_of_small_experts(counts, n, k, dtype, add):
+    _say("many rows", counts, n, k, dtype, add)
+    rows = sum(counts)
+    assert B.moe_product_backward_workspace_size(rows, len(counts), n, k) > 0
+    x, w, dy = _normal(1, rows, k), _normal(2, len(counts), n, k), _normal(3, rows, n)
+    base = _normal(4, len(counts), n, k).to(dtype) if add else None
+    dx, dw = _backward(dy, x, w, _offsets(counts), dtype, base)
+    torch.cuda.synchronize()
+    _check_backward(dx, dw, dy, x, w, counts, base)
+
+
 def test_product_of_no_rows():
     w = _normal(1, 3, 16, 24)
     offsets = _offsets([0, 0, 0])
