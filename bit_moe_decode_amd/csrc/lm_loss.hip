@@ -69,32 +69,34 @@ __device__ __forceinline__ void head_tiles(int total, TileAt tile_at, Stage& s0,
   }
 }
 
-// Few rows h [rows][hidden] against `columns` rows of w: calls done(m, j, part, z)
-// with the logits of row m and columns j .. j + 3, of the part-th 16 columns.
+// Rows h [rows][hidden] against `columns` rows of w in tiles of 16 U x 64: calls
+// done(m, j, part, z) with the logits of row m and columns j .. j + 3, of the
+// part-th 16 columns.
 template <int U, typename Done>
 __device__ __forceinline__ void few_tiles(const uint16_t* h, int rows, const uint16_t* w, int columns, int hidden,
                                           uint8_t* lds, Done done) {
   const int lane = threadIdx.x & 63, col = lane & 15, g = lane >> 4;
-  const int tiles = (columns + kStreamJ - 1) / kStreamJ;
+  const int m_tiles = (rows + 16 * U - 1) / (16 * U), j_tiles = (columns + kStreamJ - 1) / kStreamJ;
+  const int tiles = m_tiles * j_tiles;
   const uint32_t pitch = (uint32_t)hidden * 2u;
-  const TileOperand om = {h, pitch, rows, hidden};
-  auto columns_of = [&](int jt) TILE_INLINE {
-    const int j0 = jt * kStreamJ;
-    return TileOperand{w + (int64_t)j0 * hidden, pitch, columns - j0 < kStreamJ ? columns - j0 : kStreamJ, hidden};
+  auto start = [&](StreamPipe<U>& pipe, int t) TILE_INLINE {
+    const int jt = t / m_tiles, m0 = (t - jt * m_tiles) * 16 * U, j0 = jt * kStreamJ;
+    pipe.start(TileOperand{h + (int64_t)m0 * hidden, pitch, rows - m0 < 16 * U ? rows - m0 : 16 * U, hidden},
+               TileOperand{w + (int64_t)j0 * hidden, pitch, columns - j0 < kStreamJ ? columns - j0 : kStreamJ, hidden});
   };
-  int jt = blockIdx.x;
-  if (jt >= tiles) return;
+  int t = blockIdx.x;
+  if (t >= tiles) return;
   StreamPipe<U> pipe;
-  pipe.start(om, columns_of(jt));
+  start(pipe, t);
   for (;;) {
-    const int now = jt;
-    jt += gridDim.x;
+    const int jt = t / m_tiles, m0 = (t - jt * m_tiles) * 16 * U;
+    t += gridDim.x;
     pipe.run(lds);
-    if (jt < tiles) pipe.start(om, columns_of(jt));
+    if (t < tiles) start(pipe, t);
     pipe.add(lds, [&](int u, int v, const v4f& z) TILE_INLINE {
-      done(16 * u + col, now * kStreamJ + 16 * v + 4 * g, now * kStreamV + v, z);
+      done(m0 + 16 * u + col, jt * kStreamJ + 16 * v + 4 * g, jt * kStreamV + v, z);
     });
-    if (jt >= tiles) return;
+    if (t >= tiles) return;
   }
 }
 
@@ -185,7 +187,7 @@ __global__ __launch_bounds__(256) void lm_loss_kernel(LossTiles l) {
   });
 }
 
-// Few rows (up to 16 U): a part is 16 columns of a row.
+// In small tiles: a part is 16 columns of a row.
 template <int U>
 __global__ __launch_bounds__(256, 2) void lm_loss_few_kernel(LossTiles l) {
   __shared__ __align__(16) uint8_t lds[StreamPipe<U>::kLds];
@@ -427,7 +429,7 @@ __global__ __launch_bounds__(256) void lm_loss_d_kernel(LossGrad l) {
                       [&](auto& sums, const HeadTile& p) TILE_INLINE { grad_epilogue(l, sums, live, p.m0, p.j0); });
 }
 
-// d of few rows (up to 16 U).
+// d in small tiles.
 template <int U>
 __global__ __launch_bounds__(256, 2) void lm_loss_d_few_kernel(LossGrad l) {
   __shared__ __align__(16) uint8_t lds[StreamPipe<U>::kLds];
@@ -456,13 +458,14 @@ struct GradTile {
   int m0, j0, split;  // split -1: of dw
 };
 
+template <int SIDE>
 struct GradTiles {
   int h_tiles, v_tiles, m_tiles, dh, dw;  // tiles a side, and in all
   int part;                               // columns of a split
   __device__ __forceinline__ GradTiles(const LossGrad& l, int live) {
-    h_tiles = (l.a.hidden + 255) / 256;
-    v_tiles = (l.count + 255) / 256;
-    m_tiles = (live + 255) / 256;
+    h_tiles = (l.a.hidden + SIDE - 1) / SIDE;
+    v_tiles = (l.count + SIDE - 1) / SIDE;
+    m_tiles = (live + SIDE - 1) / SIDE;
     dh = l.a.dh ? m_tiles * h_tiles * l.splits : 0;
     dw = l.a.dw ? v_tiles * h_tiles : 0;
     part = ((l.count + kStepC - 1) / kStepC + l.splits - 1) / l.splits * kStepC;
@@ -473,13 +476,13 @@ struct GradTiles {
     p.split = t / (m_tiles * h_tiles);
     int mt, jt;
     place_of(t - p.split * (m_tiles * h_tiles), m_tiles, h_tiles, &mt, &jt);
-    p.m0 = mt * 256;
-    p.j0 = jt * 256;
+    p.m0 = mt * SIDE;
+    p.j0 = jt * SIDE;
     const int c0 = p.split * part, left = l.count - c0, c = left < 0 ? 0 : (left < part ? left : part);
     // (d's columns past the vocabulary are 0, to a multiple of 8)
-    p.m = {l.d + (int64_t)p.m0 * l.pitch + (c ? c0 : 0), (uint32_t)l.pitch * 2u, live - p.m0 < 256 ? live - p.m0 : 256,
+    p.m = {l.d + (int64_t)p.m0 * l.pitch + (c ? c0 : 0), (uint32_t)l.pitch * 2u, live - p.m0 < SIDE ? live - p.m0 : SIDE,
            (c + 7) / 8 * 8};
-    p.j = {l.a.w + (int64_t)(l.first + (c ? c0 : 0)) * H + p.j0, (uint32_t)H * 2u, H - p.j0 < 256 ? H - p.j0 : 256, c};
+    p.j = {l.a.w + (int64_t)(l.first + (c ? c0 : 0)) * H + p.j0, (uint32_t)H * 2u, H - p.j0 < SIDE ? H - p.j0 : SIDE, c};
     return p;
   }
   __device__ __forceinline__ GradTile dw_at(const LossGrad& l, int live, int t) const {
@@ -488,27 +491,27 @@ struct GradTiles {
     p.split = -1;
     int mt, jt;
     place_of(t, v_tiles, h_tiles, &mt, &jt);
-    p.m0 = mt * 256;
-    p.j0 = jt * 256;
+    p.m0 = mt * SIDE;
+    p.j0 = jt * SIDE;
     const int r0 = __builtin_amdgcn_readfirstlane(l.first_of[(l.first + p.m0) / 256]);
     const int more = __builtin_amdgcn_readfirstlane(l.first_of[(l.first + p.m0) / 256 + 1]) - r0;
-    const int own = l.count - p.m0 < 256 ? (l.count - p.m0 + 7) / 8 * 8 : 256, cols = H - p.j0 < 256 ? H - p.j0 : 256;
-    p.m = {l.d + p.m0, (uint32_t)l.pitch * 2u, own, live, l.rests + (int64_t)r0 * 256, 512u, more};
+    const int own = l.count - p.m0 < SIDE ? (l.count - p.m0 + 7) / 8 * 8 : SIDE, cols = H - p.j0 < SIDE ? H - p.j0 : SIDE;
+    p.m = {l.d + p.m0, (uint32_t)l.pitch * 2u, own, live, l.rests + (int64_t)r0 * 256 + p.m0 % 256, 512u, more};
     p.j = {l.h + p.j0, (uint32_t)H * 2u, cols, live, l.h + (int64_t)r0 * H + p.j0, (uint32_t)H * 2u, more};
     return p;
   }
 };
 
-template <typename T, bool ADD>
+template <int U, typename T, bool ADD>
 __global__ __launch_bounds__(256) void lm_loss_products_kernel(LossGrad l) {
-  using Long = TilePipe<8, 8, false, true>;
-  using Wide = TilePipe<8, 8, true, true, true>;
-  static_assert(sizeof(Long::Stage) == sizeof(Wide::Stage), "both take the same stages");
-  __shared__ Long::Stage s0, s1;
-  __shared__ Long::Last s2;
+  using Long = TilePipe<U, U, false, true>;
+  using Wide = TilePipe<U, U, true, true, true>;
+  static_assert(sizeof(typename Long::Stage) == sizeof(typename Wide::Stage), "both take the same stages");
+  __shared__ typename Long::Stage s0, s1;
+  __shared__ typename Long::Last s2;
   __shared__ int s_next;
   const int live = __builtin_amdgcn_readfirstlane(*l.live), tid = threadIdx.x;
-  const GradTiles g(l, live);
+  const GradTiles<32 * U> g(l, live);
   // a tile's number: those of dh, then those of dw; each XCD has an eighth of either
   TileQueues queues{l.next};
   auto redeem = [&](int ticket) TILE_INLINE {
@@ -541,27 +544,27 @@ __global__ __launch_bounds__(256) void lm_loss_products_kernel(LossGrad l) {
     const int ticket = tid == 0 ? queues.ticket() : 0;
     const int m = m0, j = j0;
     if (split < 0) {
-      TileSums<8, 8> sums;
-      dw.run<0>(s0, s1, s2, sums, false);
+      TileSums<U, U> sums;
+      dw.template run<0>(s0, s1, s2, sums, false);
       t = redeem(ticket);
       if (t >= 0) begin(t);
-      store_tile<8, 8, T, ADD>(sums, reinterpret_cast<T*>(l.a.dw) + (int64_t)l.first * l.a.hidden, m, l.count, j,
+      store_tile<U, U, T, ADD>(sums, reinterpret_cast<T*>(l.a.dw) + (int64_t)l.first * l.a.hidden, m, l.count, j,
                                l.a.hidden);
     } else {
       float* acc = l.acc + (int64_t)split * l.a.rows * l.a.hidden;
       auto finish = [&](auto u) TILE_INLINE {
-        TileSums<decltype(u)::value, 8> sums;
-        dh.run<0>(s0, s1, s2, sums, false);
+        TileSums<decltype(u)::value, U> sums;
+        dh.template run<0>(s0, s1, s2, sums, false);
         const bool none = dh.halves == 0;
         t = redeem(ticket);
         if (t >= 0) begin(t);
         if (l.first == 0)  // kept, or added to what earlier pieces left
-          store_tile<decltype(u)::value, 8, float, false>(sums, acc, m, live, j, l.a.hidden);
+          store_tile<decltype(u)::value, U, float, false>(sums, acc, m, live, j, l.a.hidden);
         else if (!none)
-          store_tile<decltype(u)::value, 8, float, true>(sums, acc, m, live, j, l.a.hidden);
+          store_tile<decltype(u)::value, U, float, true>(sums, acc, m, live, j, l.a.hidden);
       };
-      if (own > 128)
-        finish(std::integral_constant<int, 8>{});
+      if (U == 8 && own > 128)
+        finish(std::integral_constant<int, U>{});
       else if (own > 64)
         finish(std::integral_constant<int, 4>{});
       else if (own > 32)
@@ -598,8 +601,15 @@ __global__ __launch_bounds__(256) void lm_loss_dh_kernel(LossGrad l) {
 // --------------------------------------------------------------------- launches
 // Rows of a launch of the loss, for its parts' memory.
 constexpr int kLossRows = 16384;
-// Tiles of 256 x 256 above this many rows, else of 64 x 64.
-constexpr int kLossFew = kStreamM;
+// Tiles of 256 x 256 where three quarters of the CUs or more have one, of 64 x 64
+// else (SMALL_A).
+constexpr int kLossTiles = 192;
+static bool loss_large(int rows, int columns) {
+  return rows > kStreamM && (int64_t)((rows + 255) / 256) * ((columns + 255) / 256) >= kLossTiles;
+}
+static int64_t small_tiles(int rows, int columns) {
+  return (int64_t)((rows + kStreamM - 1) / kStreamM) * ((columns + kStreamJ - 1) / kStreamJ);
+}
 
 template <typename Args>
 static void launch_few(void (*u1)(Args), void (*u2)(Args), void (*u4)(Args), int rows, int blocks, const Args& l,
@@ -608,30 +618,35 @@ static void launch_few(void (*u1)(Args), void (*u2)(Args), void (*u4)(Args), int
 }
 
 static int loss_parts(int rows, int vocab) {
-  return rows > kLossFew ? 2 * ((vocab + 255) / 256) : kStreamV * ((vocab + kStreamJ - 1) / kStreamJ);
+  return loss_large(rows, vocab) ? 2 * ((vocab + 255) / 256) : kStreamV * ((vocab + kStreamJ - 1) / kStreamJ);
 }
 static size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 
+// Parts of all rows of a launch, at most: the last of several may have fewer rows,
+// and take the small tiles.
+static size_t all_parts(int rows, int vocab) {
+  if (rows <= kLossRows) return (size_t)rows * loss_parts(rows, vocab);
+  int few = kLossTiles / ((vocab + 255) / 256) * 256;  // rows that may take the small tiles
+  few = few < kStreamM ? kStreamM : (few < kLossRows ? few : kLossRows);
+  const size_t large = (size_t)kLossRows * loss_parts(kLossRows, vocab), small = (size_t)few * loss_parts(1, vocab);
+  return large > small ? large : small;
+}
+
 size_t loss_workspace(int rows, int vocab, int) {
-  const size_t r = rows < kLossRows ? rows : kLossRows;
-  // (the last of several launches may take the other tiles)
-  const size_t parts = rows > kLossRows ? loss_parts(1, vocab) : loss_parts(rows, vocab);
-  return up256(r * parts * sizeof(float2)) + up256(r * sizeof(float));
+  return up256(all_parts(rows, vocab) * sizeof(float2)) + up256((size_t)(rows < kLossRows ? rows : kLossRows) * 4);
 }
 
 hipError_t launch_loss(const LossArgs& a, void* workspace, hipStream_t stream) {
   LossTiles l = {};
   l.a = a;
-  const size_t r = a.rows < kLossRows ? a.rows : kLossRows;
-  const size_t parts = a.rows > kLossRows ? loss_parts(1, a.vocab) : loss_parts(a.rows, a.vocab);
   l.part = static_cast<float2*>(workspace);
-  l.at_target = reinterpret_cast<float*>(static_cast<char*>(workspace) + up256(r * parts * sizeof(float2)));
+  l.at_target = reinterpret_cast<float*>(static_cast<char*>(workspace) + up256(all_parts(a.rows, a.vocab) * sizeof(float2)));
   for (l.first = 0; l.first < a.rows; l.first += kLossRows) {
     l.count = a.rows - l.first < kLossRows ? a.rows - l.first : kLossRows;
     l.parts = loss_parts(l.count, a.vocab);
     int blocks;
-    const bool few = l.count <= kLossFew;
-    const int64_t tiles = few ? (int64_t)(a.vocab + kStreamJ - 1) / kStreamJ
+    const bool few = !loss_large(l.count, a.vocab);
+    const int64_t tiles = few ? small_tiles(l.count, a.vocab)
                               : (int64_t)((l.count + 255) / 256) * ((a.vocab + 255) / 256);
     hipError_t e = tile_blocks(tiles, few ? 2 : 1, &blocks);
     if (e != hipSuccess) return e;
@@ -639,7 +654,7 @@ hipError_t launch_loss(const LossArgs& a, void* workspace, hipStream_t stream) {
       launch_few(lm_loss_few_kernel<1>, lm_loss_few_kernel<2>, lm_loss_few_kernel<4>, l.count, blocks, l, stream);
     else
       hipLaunchKernelGGL(lm_loss_kernel, dim3(blocks), dim3(256), 0, stream, l);
-    hipLaunchKernelGGL(lm_loss_join_kernel, dim3(l.count), dim3(few ? 1024 : 256), 0, stream, l);
+    hipLaunchKernelGGL(lm_loss_join_kernel, dim3(l.count), dim3(l.parts > 2048 ? 1024 : 256), 0, stream, l);
     e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
@@ -653,6 +668,11 @@ constexpr int kLossRanked = 4096;
 // Columns of a piece: d of at most 128 MB, in multiples of 256.
 constexpr size_t kLossPieceBytes = (size_t)128 << 20;
 
+// Side of the second products' tiles: 256 where dw has one for each CU, 128 else.
+static int grad_side(const LossGradArgs& a) {
+  return (int64_t)((a.vocab + 255) / 256) * ((a.hidden + 255) / 256) >= 256 ? 256 : 128;
+}
+
 static size_t loss_grad_plan(LossGrad* l, char* base) {
   const LossGradArgs& a = l->a;
   const int whole = (a.vocab + 255) / 256;
@@ -661,10 +681,11 @@ static size_t loss_grad_plan(LossGrad* l, char* base) {
   l->pieces = (int)((whole + most - 1) / most);
   l->pitch = (whole + l->pieces - 1) / l->pieces * 256;
   // dh's products split over a piece's columns where its tiles are fewer than the
-  // CUs: parts of at least 32 steps, 32 of them at most
-  const int64_t tiles = (int64_t)((a.rows + 255) / 256) * ((a.hidden + 255) / 256);
+  // CUs: parts of at least 32 steps (16 of small tiles), 32 of them at most
+  const int side = grad_side(a);
+  const int64_t tiles = (int64_t)((a.rows + side - 1) / side) * ((a.hidden + side - 1) / side);
   int64_t splits = 256 / tiles;
-  const int64_t by_steps = l->pitch / (32 * kStepC);
+  const int64_t by_steps = l->pitch / ((side / 8) * kStepC);
   if (splits > by_steps) splits = by_steps;
   l->splits = splits < 1 ? 1 : (splits > 32 ? 32 : (int)splits);
   size_t o = 0;
@@ -696,6 +717,18 @@ size_t loss_backward_workspace(int rows, int vocab, int hidden) {
   return loss_grad_plan(&l, nullptr);
 }
 
+template <int U>
+static void launch_products(const LossGrad& l, int blocks, hipStream_t stream) {
+  if (l.a.f32 && l.a.add)
+    hipLaunchKernelGGL((lm_loss_products_kernel<U, float, true>), dim3(blocks), dim3(256), 0, stream, l);
+  else if (l.a.f32)
+    hipLaunchKernelGGL((lm_loss_products_kernel<U, float, false>), dim3(blocks), dim3(256), 0, stream, l);
+  else if (l.a.add)
+    hipLaunchKernelGGL((lm_loss_products_kernel<U, uint16_t, true>), dim3(blocks), dim3(256), 0, stream, l);
+  else
+    hipLaunchKernelGGL((lm_loss_products_kernel<U, uint16_t, false>), dim3(blocks), dim3(256), 0, stream, l);
+}
+
 hipError_t launch_loss_backward(const LossGradArgs& a, void* workspace, hipStream_t stream) {
   LossGrad l = {};
   l.a = a;
@@ -715,8 +748,8 @@ hipError_t launch_loss_backward(const LossGradArgs& a, void* workspace, hipStrea
   for (l.first = 0; l.first < a.vocab; l.first += l.pitch) {
     l.count = a.vocab - l.first < l.pitch ? a.vocab - l.first : l.pitch;
     int blocks;
-    const bool few = a.rows <= kLossFew;
-    const int64_t tiles = few ? (int64_t)(l.count + kStreamJ - 1) / kStreamJ
+    const bool few = !loss_large(a.rows, l.count);
+    const int64_t tiles = few ? small_tiles(a.rows, l.count)
                               : (int64_t)((a.rows + 255) / 256) * ((l.count + 255) / 256);
     e = tile_blocks(tiles, few ? 2 : 1, &blocks);
     if (e != hipSuccess) return e;
@@ -724,18 +757,15 @@ hipError_t launch_loss_backward(const LossGradArgs& a, void* workspace, hipStrea
       launch_few(lm_loss_d_few_kernel<1>, lm_loss_d_few_kernel<2>, lm_loss_d_few_kernel<4>, a.rows, blocks, l, stream);
     else
       hipLaunchKernelGGL(lm_loss_d_kernel, dim3(blocks), dim3(256), 0, stream, l);
-    const int64_t products = ((int64_t)((a.rows + 255) / 256) * l.splits + (l.count + 255) / 256) *
-                             ((a.hidden + 255) / 256);
+    const int side = grad_side(a);
+    const int64_t products = ((int64_t)((a.rows + side - 1) / side) * l.splits + (l.count + side - 1) / side) *
+                             ((a.hidden + side - 1) / side);
     e = tile_blocks(products, 1, &blocks);
     if (e != hipSuccess) return e;
-    if (a.f32 && a.add)
-      hipLaunchKernelGGL((lm_loss_products_kernel<float, true>), dim3(blocks), dim3(256), 0, stream, l);
-    else if (a.f32)
-      hipLaunchKernelGGL((lm_loss_products_kernel<float, false>), dim3(blocks), dim3(256), 0, stream, l);
-    else if (a.add)
-      hipLaunchKernelGGL((lm_loss_products_kernel<uint16_t, true>), dim3(blocks), dim3(256), 0, stream, l);
+    if (side == 256)
+      launch_products<8>(l, blocks, stream);
     else
-      hipLaunchKernelGGL((lm_loss_products_kernel<uint16_t, false>), dim3(blocks), dim3(256), 0, stream, l);
+      launch_products<4>(l, blocks, stream);
   }
   if (a.dh)
     hipLaunchKernelGGL(lm_loss_dh_kernel, dim3(a.rows, (a.hidden + 1023) / 1024), dim3(256), 0, stream, l);

@@ -302,3 +302,28 @@ def test_on_another_stream_and_in_a_graph():
         rh, rw = _grads(h, w, t, re, dloss)
         torch.cuda.synchronize()
         assert torch.equal(loss, rl) and torch.equal(lse, re) and torch.equal(dh, rh) and torch.equal(dw, rw)
+
+
+@pytest.mark.parametrize("rows", [16384 + 40, 16384 + 300])
+def test_several_launches_of_rows(rows):
+    """More rows than a launch takes; the last launch's in small tiles."""
+    vocab, hidden = 4000, 8
+    _say("launches", rows)
+    h, w, t, _ = _inputs(rows, vocab, hidden, rows)
+    loss, lse = _loss(h, w, t)
+    torch.cuda.synchronize()
+    for i in (0, 16384):
+        part = slice(i, min(rows, i + 3000))
+        _check_loss(loss[part], lse[part], h[part], w, t[part])
+
+
+@pytest.mark.parametrize("rows,vocab,hidden", [(5000, 300, 24), (70, 9000, 16), (400, 70000, 264), (4200, 1003, 520)])
+def test_shapes_between_the_tiles(rows, vocab, hidden):
+    """Tiles of either size, rows placed by counting and by a sort, dh split."""
+    _say("between", rows, vocab, hidden)
+    h, w, t, dloss = _inputs(rows, vocab, hidden, rows + vocab)
+    loss, lse = _loss(h, w, t)
+    dh, dw = _grads(h, w, t, lse, dloss)
+    torch.cuda.synchronize()
+    _check_loss(loss, lse, h, w, t)
+    _check_grads(dh, dw, h, w, t, lse, dloss)
