@@ -116,7 +116,8 @@ __global__ __launch_bounds__(256) void embed_grad_few_kernel(EmbedGrad g) {
 #pragma unroll
     for (int k = 0; k < kEmbedFewK; k++)
       if (64 * k < e.rows) hit |= id[k] == v;
-    if (__ballot(hit)) {
+    const bool any = __ballot(hit) != 0;
+    if (any) {
 #pragma unroll
       for (int k = 0; k < kEmbedFewK; k++) {
         if (64 * k >= e.rows) continue;
@@ -146,7 +147,12 @@ __global__ __launch_bounds__(256) void embed_grad_few_kernel(EmbedGrad g) {
         }
       }
     }
-    if (c < e.hidden) put_sum<TO, VEC, ADD>(g, v, c, sum);
+    if (c < e.hidden) {
+      if (any)
+        put_sum<TO, VEC, ADD>(g, v, c, sum);
+      else  // 0, whatever the scale is
+        store8<TO, VEC>(static_cast<TO*>(g.a.dtable) + (int64_t)v * e.hidden, c, e.hidden, sum);
+    }
   next:;
   }
 }

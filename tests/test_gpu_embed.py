@@ -148,6 +148,22 @@ def test_rows_without_a_token_are_not_read_into_others(rows):
     assert torch.equal(got[keep], want[keep]) and bool((got[5] == float("inf")).all())
 
 
+@pytest.mark.parametrize("rows", [30, 2000])
+def test_a_scale_that_is_not_finite(rows):
+    """Tokens without rows have a gradient of 0 all the same, rows without a token
+    an embedding of 0."""
+    ids, dout = _ids(rows, 5000, "outside", 12), _rows(rows, 16, F32, 13)
+    dtable = _grad(ids, dout, 5000, F32, float("inf"))
+    out = torch.empty(rows, 16, dtype=BF, device="cuda")
+    B.embed(ids, _rows(5000, 16, BF, 14), out, float("nan"))
+    torch.cuda.synchronize()
+    live = (ids >= 0) & (ids < 5000)
+    used = torch.zeros(5000, dtype=torch.bool, device="cuda")
+    used[ids[live].long()] = True
+    assert bool((dtable[~used] == 0).all()) and not bool(torch.isfinite(dtable[used]).any())
+    assert bool((out[~live] == 0).all()) and bool(torch.isnan(out[live]).all())
+
+
 def test_no_rows():
     ids = torch.empty(0, dtype=torch.int32, device="cuda")
     table, dout = _rows(50, 7, BF, 1), torch.empty(0, 7, dtype=BF, device="cuda")
