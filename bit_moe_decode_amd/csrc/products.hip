@@ -5,6 +5,17 @@
 //   dx[r] = W_e^T dy[r]
 //   dW_e  = sum_r dy[r] x[r]^T            (0 for an expert without rows)
 // bf16 operands, sums in fp32, rounded once.
+//
+// Rows enough for half a tile of 256 an expert, and such tiles enough for the CUs:
+// tiles of 256 x 256 (tile_product.h), of fewer row tiles where an expert's rows
+// end.  Else y takes tiles of 64 x 64 that stream the weights (stream_product.h),
+// dx of 64 x 128 and dW of 128 x 128.  Measured, of 256 experts [4096, 6144]: 16
+// tokens x 8 picks 630 .. 690 us, the bytes of the 72 .. 84 experts in use at 6 TB/s.
+// Of 64 experts [4096, 6144]: y of 65536 rows 2900 .. 3000 us (1.1 PFLOP/s; 16.8
+// rounds of tiles where full ones would take 16, in 19 rounds of blocks), dx of
+// 32768 1530 us (1.08), dW of 32768 2050 .. 2100 us (0.8 PFLOP/s: of it 600 us are
+// the 3.2 GB of its store, which 8 steps a tile do not hide; without the store
+// 1410).
 #include "products.h"
 
 #include "device_common.h"
@@ -113,7 +124,6 @@ __global__ __launch_bounds__(256) void moe_product_kernel(ProductArgs a) {
   Pipe pipe;
   ProductTile p = tile_at(t);
   pipe.start(p.m, p.j, s0, s1, s2);
-  bool stored = false;
   for (;;) {
     t += gridDim.x;
     const bool more = t < total;
@@ -121,7 +131,7 @@ __global__ __launch_bounds__(256) void moe_product_kernel(ProductArgs a) {
     if (more) next = tile_at(t);
     auto finish = [&](auto u) TILE_INLINE {
       TileSums<decltype(u)::value, V> sums;
-      pipe.template run<kTileStores<UMAX, V, T>>(s0, s1, s2, sums, stored);
+      pipe.run(s0, s1, s2, sums);
       if (more) pipe.start(next.m, next.j, s0, s1, s2);
       store_tile<decltype(u)::value, V, T, false>(sums, out, p.lo, p.hi, p.j0, cols);
     };
@@ -134,7 +144,6 @@ __global__ __launch_bounds__(256) void moe_product_kernel(ProductArgs a) {
     else
       finish(std::integral_constant<int, 1>{});
     if (!more) return;
-    stored = p.m.own > 16 * UMAX;  // (fewer stores of a tile of fewer rows)
     p = next;
   }
 }
@@ -246,20 +255,18 @@ __global__ __launch_bounds__(256) void moe_product_dw_kernel(ProductArgs a) {
   Pipe pipe;
   Tile p = tile_at(t);
   pipe.start(p.m, p.j, s0, s1, s2);
-  bool stored = false;
   for (;;) {
     t += gridDim.x;
     const bool more = t < total;
     Tile next = p;
     if (more) next = tile_at(t);
     TileSums<U, V> sums;
-    pipe.template run<ADD ? 0 : kTileStores<U, V, T>>(s0, s1, s2, sums, stored);
+    pipe.run(s0, s1, s2, sums);
     if (more) pipe.start(next.m, next.j, s0, s1, s2);
     T* out = reinterpret_cast<T*>(a.parts > 1 ? (void*)a.space : a.dw) + (int64_t)p.e * a.n * a.k;
     if (!ADD || p.m.c > 0) store_tile<U, V, T, ADD>(sums, out, p.m0, a.n, p.j0, a.k);
     if (!more) return;
     p = next;
-    stored = true;
   }
 }
 

@@ -9,6 +9,12 @@
 // steps ahead, without meetings: 8 KB a wave and step.  A step then goes through
 // an LDS area of the wave's own into the order of the MFMA's operands.  The waves'
 // sums are added in wave order at the end.
+//
+// 16 tokens x 8 of 256 experts [4096, 6144] 633 us, in halves of lines 738, with
+// loads that the caches are told not to keep, which fetch a line twice, 850, in
+// tiles that share LDS 760 .. 930.  The loss of 8 rows of 151936 x 2560 134 us, 5.8
+// TB/s, where loads alone take 128.  Two steps under way a wave: 4 as good there
+// (633 us), 161 against 153 us in the loss.
 #pragma once
 #include <hip/hip_runtime.h>
 #include <stdint.h>

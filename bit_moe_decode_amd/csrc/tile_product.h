@@ -19,6 +19,13 @@
 // the time of 128 (loads to LDS alone of 256 blocks that share their rows as these
 // do, 15 against 25 TB/s; with steps of 32, which took a line in two halves, two
 // steps apart, the loss of 4096 rows took 2717 us, 2400 of them without the MFMAs).
+//
+// What bounds it at 8 x 8 and long c is the chip's power more than any one path:
+// 1.3 to 1.46 PFLOP/s at a clock that falls to 1.8 GHz, as a large library product
+// does (1.18 to 1.55).  Taking tiles of unequal length from queues, which evens the
+// blocks' ends, took longer (y of 65536 rows 3190 us for 3070), and so did tiles of
+// 256 x 128 and, two blocks a CU, 128 x 128 in dW (with its dx 4005 and 4253 us for
+// 3758).
 #pragma once
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -31,14 +38,14 @@ namespace moe {
 
 // One operand: `own` rows (transposed: columns) of the tile that exist and `c`
 // contraction entries, in rows of `pitch` bytes from base on.  Where own or c
-// end the operand is 0: a load past an end reads nothing and fills its place
-// with zeros.  Not transposed: c
-// a multiple of 8, own * pitch below 2^32; transposed: own a multiple of 8.
+// end the operand is 0: a load past an end reads nothing and fills its place with
+// zeros.  Not transposed: c a multiple of 8, own * pitch below 2^32; transposed:
+// own a multiple of 8.
 struct TileOperand {
   const uint16_t* base;
   uint32_t pitch;
   int own, c;
-  // (tile_product's LONGER, transposed operands) c2 more entries behind them,
+  // (TilePipe's LONGER, transposed operands) c2 more entries behind them,
   // from another place
   const uint16_t* base2 = nullptr;
   uint32_t pitch2 = 0;
@@ -69,15 +76,11 @@ typedef __attribute__((address_space(3))) v4s tile_lds_v4s;
 // Waits for this wave's LDS operations, and until at most VM of its loads are
 // under way, then for the other waves.  No memory operation moves across.
 template <int VM>
-__device__ __forceinline__ void tile_wait() {
-  constexpr int N = VM < 63 ? VM : 63;
-  asm volatile("" ::: "memory");
-  __builtin_amdgcn_s_waitcnt((N & 15) | (7 << 4) | ((N >> 4) << 14));
-  asm volatile("" ::: "memory");
-}
-template <int VM>
 __device__ __forceinline__ void tile_meet() {
-  tile_wait<VM>();
+  static_assert(VM < 64, "what the counter holds");
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt((VM & 15) | (7 << 4) | ((VM >> 4) << 14));
+  asm volatile("" ::: "memory");
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
 }
@@ -105,8 +108,7 @@ __device__ __forceinline__ const uint8_t* tile_scalar(const void* p) {
 template <int P, bool T, bool LONGER>
 struct TileLoader {
   static constexpr int kKilos = 2 * P, kLoads = kKilos / 4;  // of a stage, a wave's of them
-  static_assert(P == 2 || P == 4 || P == 8 || P == 16, "tiles of an operand");
-  static_assert(!T || P >= 4, "64 columns at least");
+  static_assert(P == 4 || P == 8 || P == 16, "tiles of an operand");
   static constexpr uint32_t kNothing = 0xFFFFFF00u;  // an offset behind every buffer's end
   __amdgpu_buffer_rsrc_t whole;  // not transposed: the tile's rows
   const uint8_t* base;
@@ -223,7 +225,7 @@ struct TileSums {
 // All of the block's threads call them, with the same arguments.  A tile lies in
 // the stages as one of UMAX does.  The ring has two stages where they are large
 // (67 KB), or three.
-template <int UMAX, int V, bool MT, bool JT, bool LONGER = false, int STAGES = 0>
+template <int UMAX, int V, bool MT, bool JT, bool LONGER = false>
 struct TilePipe {
   static constexpr int PM = 2 * UMAX, PJ = 2 * V;
   static_assert(!LONGER || (MT && JT), "of transposed operands");
@@ -232,7 +234,7 @@ struct TilePipe {
   static constexpr int NM = Rows::kLoads, NJ = Columns::kLoads, NL = NM + NJ;
   static constexpr int kJ = Rows::kKilos * kPiecesAt;  // where J starts in a stage
   static constexpr int kKilos = Rows::kKilos + Columns::kKilos;
-  static constexpr int kStages = STAGES ? STAGES : kKilos > 48 ? 2 : 3;
+  static constexpr int kStages = kKilos > 48 ? 2 : 3;
   // (one LDS object a stage: while a load to an object is under way, the compiler
   // lets reads of that object wait for all loads)
   using Stage = TileStage<kKilos>;
@@ -265,11 +267,8 @@ struct TilePipe {
     }
   }
 
-  // STORES: stores that every wave has issued behind the tile's first loads, at
-  // least, where `stored`: they count among what is under way, and are not waited
-  // for before the second step.
-  template <int STORES, int U>
-  __device__ __forceinline__ void run(Stage& s0, Stage& s1, Last& s2, TileSums<U, V>& sums, bool stored) const {
+  template <int U>
+  __device__ __forceinline__ void run(Stage& s0, Stage& s1, Last& s2, TileSums<U, V>& sums) const {
     const int wv = tile_wave(threadIdx.x), wm = wv & 1, wj = wv >> 1;
     auto& acc = sums.s;
 #pragma unroll
@@ -317,18 +316,10 @@ struct TilePipe {
       half(yes{}, no{}, a, b, cur, 1, nullptr, 0);
       // the next step has arrived when at most the one behind it is under way, and
       // all waves have read all of this one
-      if (STORES > 0 && stored && k == 0)
-        tile_wait<(kStages - 2) * NL + STORES>();
-      else
-        tile_wait<(kStages - 2) * NL>();
-      tile_meet<63>();
+      tile_meet<(kStages - 2) * NL>();
       half(yes{}, yes{}, b, a, nx, 0, cur, k + kStages);
     };
-    if (STORES > 0 && stored)
-      tile_wait<(kStages - 1) * NL + STORES>();
-    else
-      tile_wait<(kStages - 1) * NL>();
-    tile_meet<63>();
+    tile_meet<(kStages - 1) * NL>();
 #pragma unroll
     for (int q = 0; q < NR; q++) read(a, s0.b, 0, q);
     const int steps = halves >> 1;
@@ -365,8 +356,8 @@ struct TilePipe {
   }
 #else
   __device__ void start(const TileOperand&, const TileOperand&, Stage&, Stage&, Last&) {}
-  template <int STORES, int U>
-  __device__ void run(Stage&, Stage&, Last&, TileSums<U, V>&, bool) const {}
+  template <int U>
+  __device__ void run(Stage&, Stage&, Last&, TileSums<U, V>&) const {}
 #endif
 };
 
@@ -437,11 +428,7 @@ struct TileQueues {
 __device__ __forceinline__ int eighth(int n, int q) { return (int)((int64_t)n * q / 8); }
 
 // Stores a wave's sums as rows m0 + .. of out, of `cols` columns (a multiple of
-// 8); rows from m_end on and columns from cols on are not there.  Without ADD
-// every wave issues kTileStores stores, whose own bounds keep them inside.
-template <int U, int V, typename T>
-constexpr int kTileStores = sizeof(T) == 4 ? U * V : U * V / 2;
-
+// 8); rows from m_end on and columns from cols on are not there.
 template <int U, int V, typename T, bool ADD>
 __device__ __forceinline__ void store_tile(TileSums<U, V>& sums, T* out, int64_t m0, int64_t m_end, int j0, int cols) {
   const int tid = threadIdx.x, lane = tid & 63, wv = tile_wave(tid);
