@@ -375,6 +375,13 @@ def _check(what, device, *tensors):
                           f"{t.dtype} {tuple(t.shape)} with strides {t.stride()} on {t.device}")
 
 
+def _sizes(what, kind, *sizes):
+    """The structure `kind` of these sizes, which its 32 bits hold."""
+    if any(not -(1 << 31) <= int(n) < 1 << 31 for n in sizes):
+        _refuse(what, f"sizes of {tuple(int(n) for n in sizes)}")
+    return ctypes.byref(kind(*(int(n) for n in sizes)))
+
+
 def _byte_types():
     return _torch.uint8, _torch.float8_e4m3fn  # FP8 codes, as either
 
@@ -556,12 +563,13 @@ def _moe_dtype(what, dtype):
 
 
 def moe_product_workspace_size(rows, n_experts, n, k) -> int:
-    return lib().moe_product_workspace_size(ctypes.byref(ProductShape(0, int(n_experts), int(rows), int(n), int(k))))
+    return lib().moe_product_workspace_size(
+        _sizes("moe_product_workspace_size", ProductShape, 0, n_experts, rows, n, k))
 
 
 def moe_product_backward_workspace_size(rows, n_experts, n, k) -> int:
     return lib().moe_product_backward_workspace_size(
-        ctypes.byref(ProductShape(0, int(n_experts), int(rows), int(n), int(k))))
+        _sizes("moe_product_backward_workspace_size", ProductShape, 0, n_experts, rows, n, k))
 
 
 def moe_product(x, w, offsets, y, workspace=None, stream=None):
@@ -572,10 +580,11 @@ def moe_product(x, w, offsets, y, workspace=None, stream=None):
     bf = _torch.bfloat16
     (r, k), (e, n, _) = x.shape, w.shape
     dtype = _moe_dtype("moe_product", y.dtype)
+    shape = _sizes("moe_product", ProductShape, dtype, e, r, n, k)
     _check("moe_product", x.get_device(), ("x", x, bf, (r, k)), ("w", w, bf, (e, n, k)),
            ("offsets", offsets, _torch.int32, (e + 1,)), ("y", y, y.dtype, (r, n)))
     ws, nbytes = _space("moe_product", workspace, x.get_device())
-    _done(lib().moe_product(ctypes.byref(ProductShape(dtype, e, r, n, k)), x.data_ptr(), w.data_ptr(),
+    _done(lib().moe_product(shape, x.data_ptr(), w.data_ptr(),
                             offsets.data_ptr(), y.data_ptr(), ws, nbytes, _stream(stream)), "moe_product")
 
 
@@ -594,11 +603,12 @@ def moe_product_backward(dy, x, w, offsets, dx=None, dw=None, workspace=None, ad
         return
     k = known.shape[-1]
     dtype = 0 if dw is None else _moe_dtype("moe_product_backward", dw.dtype)
+    shape = _sizes("moe_product_backward", ProductShape, dtype, e, r, n, k)
     _check("moe_product_backward", dy.get_device(), ("dy", dy, bf, (r, n)), ("x", x, bf, (r, k)),
            ("w", w, bf, (e, n, k)), ("offsets", offsets, _torch.int32, (e + 1,)), ("dx", dx, bf, (r, k)),
            ("dw", dw, None if dw is None else dw.dtype, (e, n, k)))
     ws, nbytes = _space("moe_product_backward", workspace, dy.get_device())
-    _done(lib().moe_product_backward(ctypes.byref(ProductShape(dtype, e, r, n, k)), dy.data_ptr(), _address(x),
+    _done(lib().moe_product_backward(shape, dy.data_ptr(), _address(x),
                                      _address(w), offsets.data_ptr(), _address(dx), _address(dw), int(add), ws,
                                      nbytes, _stream(stream)), "moe_product_backward")
 
@@ -609,12 +619,13 @@ LOSS_MAX_VOCAB = 1 << 20  # MOE_LOSS_MAX_VOCAB
 
 
 def lm_head_loss_workspace_size(rows, vocab, hidden) -> int:
-    return lib().lm_head_loss_workspace_size(ctypes.byref(HeadShape(0, int(rows), int(vocab), int(hidden))))
+    return lib().lm_head_loss_workspace_size(
+        _sizes("lm_head_loss_workspace_size", HeadShape, 0, rows, vocab, hidden))
 
 
 def lm_head_loss_backward_workspace_size(rows, vocab, hidden) -> int:
     return lib().lm_head_loss_backward_workspace_size(
-        ctypes.byref(HeadShape(0, int(rows), int(vocab), int(hidden))))
+        _sizes("lm_head_loss_backward_workspace_size", HeadShape, 0, rows, vocab, hidden))
 
 
 def lm_head_loss(h, w, targets, loss, lse, workspace, stream=None):
@@ -624,10 +635,11 @@ def lm_head_loss(h, w, targets, loss, lse, workspace, stream=None):
     workspace: a device tensor of lm_head_loss_workspace_size bytes."""
     bf, f32 = _torch.bfloat16, _torch.float32
     (r, k), v = h.shape, w.shape[0]
+    shape = _sizes("lm_head_loss", HeadShape, 0, r, v, k)
     _check("lm_head_loss", h.get_device(), ("h", h, bf, (r, k)), ("w", w, bf, (v, k)),
            ("targets", targets, _torch.int32, (r,)), ("loss", loss, f32, (r,)), ("lse", lse, f32, (r,)))
     ws, nbytes = _space("lm_head_loss", workspace, h.get_device())
-    _done(lib().lm_head_loss(ctypes.byref(HeadShape(0, r, v, k)), h.data_ptr(), w.data_ptr(), targets.data_ptr(),
+    _done(lib().lm_head_loss(shape, h.data_ptr(), w.data_ptr(), targets.data_ptr(),
                              loss.data_ptr(), lse.data_ptr(), ws, nbytes, _stream(stream)), "lm_head_loss")
 
 
@@ -638,11 +650,12 @@ def lm_head_loss_backward(h, w, targets, lse, dloss, dh=None, dw=None, workspace
     bf, f32 = _torch.bfloat16, _torch.float32
     (r, k), v = h.shape, w.shape[0]
     dtype = 0 if dw is None else _moe_dtype("lm_head_loss_backward", dw.dtype)
+    shape = _sizes("lm_head_loss_backward", HeadShape, dtype, r, v, k)
     _check("lm_head_loss_backward", h.get_device(), ("h", h, bf, (r, k)), ("w", w, bf, (v, k)),
            ("targets", targets, _torch.int32, (r,)), ("lse", lse, f32, (r,)), ("dloss", dloss, f32, (r,)),
            ("dh", dh, bf, (r, k)), ("dw", dw, None if dw is None else dw.dtype, (v, k)))
     ws, nbytes = _space("lm_head_loss_backward", workspace, h.get_device())
-    _done(lib().lm_head_loss_backward(ctypes.byref(HeadShape(dtype, r, v, k)), h.data_ptr(), w.data_ptr(),
+    _done(lib().lm_head_loss_backward(shape, h.data_ptr(), w.data_ptr(),
                                       targets.data_ptr(), lse.data_ptr(), dloss.data_ptr(), _address(dh),
                                       _address(dw), int(add), ws, nbytes, _stream(stream)), "lm_head_loss_backward")
 
@@ -657,14 +670,16 @@ def embed(ids, table, out, scale=1.0, stream=None):
     [rows], table bf16 or float32 [vocab, hidden], out [rows, hidden] of its type."""
     (v, h), r = table.shape, ids.shape[0]
     dtype = _moe_dtype("embed", table.dtype)
+    shape = _sizes("embed", EmbedShape, dtype, r, v, h)
     _check("embed", ids.get_device(), ("ids", ids, _torch.int32, (r,)), ("table", table, table.dtype, (v, h)),
            ("out", out, table.dtype, (r, h)))
-    _done(lib().embed(ctypes.byref(EmbedShape(dtype, r, v, h)), ids.data_ptr(), table.data_ptr(), float(scale),
+    _done(lib().embed(shape, ids.data_ptr(), table.data_ptr(), float(scale),
                       out.data_ptr(), _stream(stream)), "embed")
 
 
 def embed_backward_workspace_size(rows, vocab, hidden) -> int:
-    return lib().embed_backward_workspace_size(ctypes.byref(EmbedShape(0, int(rows), int(vocab), int(hidden))))
+    return lib().embed_backward_workspace_size(
+        _sizes("embed_backward_workspace_size", EmbedShape, 0, rows, vocab, hidden))
 
 
 def embed_backward(ids, dout, dtable, workspace=None, scale=1.0, add=False, stream=None):
@@ -674,10 +689,11 @@ def embed_backward(ids, dout, dtable, workspace=None, scale=1.0, add=False, stre
     tensor of embed_backward_workspace_size bytes (None where that is 0)."""
     (v, h), r = dtable.shape, ids.shape[0]
     dtype, table_dtype = (_moe_dtype("embed_backward", t.dtype) for t in (dout, dtable))
+    shape = _sizes("embed_backward", EmbedShape, dtype, r, v, h)
     _check("embed_backward", ids.get_device(), ("ids", ids, _torch.int32, (r,)), ("dout", dout, dout.dtype, (r, h)),
            ("dtable", dtable, dtable.dtype, (v, h)))
     ws, nbytes = _space("embed_backward", workspace, ids.get_device())
-    _done(lib().embed_backward(ctypes.byref(EmbedShape(dtype, r, v, h)), ids.data_ptr(), dout.data_ptr(),
+    _done(lib().embed_backward(shape, ids.data_ptr(), dout.data_ptr(),
                                float(scale), table_dtype, dtable.data_ptr(), int(add), ws, nbytes,
                                _stream(stream)), "embed_backward")
 

@@ -167,3 +167,29 @@ def test_embed_refusals():
     assert embed(embed_shape(rows=0), None, None, None) == OK
     assert embed_backward(embed_shape(rows=0), None, None, None, None, 0, add=1) == OK
     assert B.embed_backward_workspace_size(1024, 1000, 128) == 0 and B.embed_backward_workspace_size(1025, 1000, 128) > 0
+
+
+def _big(*shape, dtype="bfloat16"):
+    import torch
+    return torch.empty(shape, dtype=getattr(torch, dtype), device="meta")
+
+
+@pytest.mark.parametrize("call", [
+    lambda n: B.moe_product_workspace_size(n, 16, 64, 64),
+    lambda n: B.moe_product_backward_workspace_size(n, 16, 64, 64),
+    lambda n: B.lm_head_loss_workspace_size(n, 500, 64),
+    lambda n: B.lm_head_loss_backward_workspace_size(n, 500, 64),
+    lambda n: B.embed_backward_workspace_size(n, 500, 64),
+    lambda n: B.moe_product(_big(n, 8), _big(4, 8, 8), _big(5, dtype="int32"), _big(n, 8)),
+    lambda n: B.moe_product_backward(_big(n, 8), None, _big(4, 8, 8), _big(5, dtype="int32"), dx=_big(n, 8)),
+    lambda n: B.lm_head_loss(_big(n, 8), _big(40, 8), _big(n, dtype="int32"), _big(n, dtype="float32"),
+                             _big(n, dtype="float32"), None),
+    lambda n: B.lm_head_loss_backward(_big(n, 8), _big(40, 8), _big(n, dtype="int32"), _big(n, dtype="float32"),
+                                      _big(n, dtype="float32"), dh=_big(n, 8)),
+    lambda n: B.embed(_big(n, dtype="int32"), _big(40, 1), _big(n, 1)),
+    lambda n: B.embed_backward(_big(n, dtype="int32"), _big(n, 1), _big(40, 1)),
+])
+def test_sizes_past_32_bits_are_not_cut(call):
+    """2^32 + 16 rows are not the 16 of their low bits."""
+    with pytest.raises(B.MoeError, match="sizes of"):
+        call((1 << 32) + 16)
