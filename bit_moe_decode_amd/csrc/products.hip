@@ -10,12 +10,11 @@
 // tiles of 256 x 256 (tile_product.h), of fewer row tiles where an expert's rows
 // end.  Else y takes tiles of 64 x 64 that stream the weights (stream_product.h),
 // dx of 64 x 128 and dW of 128 x 128.  Measured, of 256 experts [4096, 6144]: 16
-// tokens x 8 picks 630 .. 690 us, the bytes of the 72 .. 84 experts in use at 6 TB/s.
-// Of 64 experts [4096, 6144]: y of 65536 rows 2900 .. 3000 us (1.1 PFLOP/s; 16.8
-// rounds of tiles where full ones would take 16, in 19 rounds of blocks), dx of
-// 32768 1530 us (1.08), dW of 32768 2050 .. 2100 us (0.8 PFLOP/s: of it 600 us are
-// the 3.2 GB of its store, which 8 steps a tile do not hide; without the store
-// 1410).
+// tokens x 8 picks 630 .. 720 us, the bytes of the 72 .. 84 experts in use at 5.4 ..
+// 6.2 TB/s.  Of 64 experts [4096, 6144]: y of 65536 rows 2850 .. 3000 us (1.1
+// PFLOP/s; 19 rounds of tiles where even experts would take 16), dx of 32768 1530 ..
+// 1600 us (1.05), dW of 32768 2010 .. 2140 us (0.8 PFLOP/s: of it 600 us are the 3.2
+// GB of its store, which 8 steps a tile do not hide; without the store 1410).
 #include "products.h"
 
 #include "device_common.h"
