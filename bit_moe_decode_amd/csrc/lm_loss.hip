@@ -275,10 +275,13 @@ __global__ __launch_bounds__(1024) void lm_loss_join_kernel(LossTiles l) {
 // 0.0017).  So what the rounding takes from d at a row's target is kept too, and
 // added: to dh by its last kernel, to dw as more rows of the product.  In the
 // order by target the rows of 256 tokens are neighbours, so that their remainders
-// are a dense [rows][256] matrix of one entry a row.
+// are a dense [rows][256] matrix of one entry a row.  Where a weight or a row holds
+// an infinity, d itself has given the infinity or NaN that the result is: it takes
+// no remainder, whose 0 or other sign would make it a NaN.
 struct LossGrad {
   LossGradArgs a;
   uint16_t* h;       // [rows][hidden] of the rows with a target
+  uint16_t* h_rest;  // the same with 0 for what is not finite: the remainders' factor
   float2* row;       // their lse and dloss,
   int32_t* target;   // target,
   float* rest;       // d at the target less its rounding,
@@ -295,13 +298,28 @@ struct LossGrad {
   int first, count;  // this piece's part of the vocabulary
 };
 
+// Eight bf16 with 0 for those that are not finite.
+__device__ __forceinline__ u32x4 finite8(u32x4 v) {
+#pragma unroll
+  for (int i = 0; i < 4; i++) {
+    if ((v[i] & 0x7F80u) == 0x7F80u) v[i] &= 0xFFFF0000u;
+    if ((v[i] & 0x7F800000u) == 0x7F800000u) v[i] &= 0xFFFFu;
+  }
+  return v;
+}
+
 // The row r of place b, from h: its part in all that the places hold.
 // `before`: the target at the place before, -1 without one; `live`: all places.
 __device__ __forceinline__ void take_place(const LossGrad& l, int r, int b, int t, int before, int live) {
   const int tid = threadIdx.x, last = (l.a.vocab + 255) / 256;
   const u32x4* from = reinterpret_cast<const u32x4*>(l.a.h + (size_t)r * l.a.hidden);
   u32x4* to = reinterpret_cast<u32x4*>(l.h + (size_t)b * l.a.hidden);
-  for (int i = tid; i < l.a.hidden / 8; i += 256) to[i] = from[i];
+  u32x4* to_rest = reinterpret_cast<u32x4*>(l.h_rest + (size_t)b * l.a.hidden);
+  for (int i = tid; i < l.a.hidden / 8; i += 256) {
+    const u32x4 v = from[i];
+    to[i] = v;
+    to_rest[i] = finite8(v);
+  }
   if (tid < 32) reinterpret_cast<u32x4*>(l.rests + (size_t)b * 256)[tid] = u32x4{0u, 0u, 0u, 0u};
   for (int i = (before < 0 ? 0 : before / 256 + 1) + tid; i <= t / 256; i += 256) l.first_of[i] = b;
   if (b == live - 1)
@@ -505,7 +523,7 @@ struct GradTiles {
     const int more = __builtin_amdgcn_readfirstlane(l.first_of[(l.first + p.m0) / 256 + 1]) - r0;
     const int own = l.count - p.m0 < SIDE ? (l.count - p.m0 + 7) / 8 * 8 : SIDE, cols = H - p.j0 < SIDE ? H - p.j0 : SIDE;
     p.m = {l.d + p.m0, (uint32_t)l.pitch * 2u, own, live, l.rests + (int64_t)r0 * 256 + p.m0 % 256, 512u, more};
-    p.j = {l.h + p.j0, (uint32_t)H * 2u, cols, live, l.h + (int64_t)r0 * H + p.j0, (uint32_t)H * 2u, more};
+    p.j = {l.h + p.j0, (uint32_t)H * 2u, cols, live, l.h_rest + (int64_t)r0 * H + p.j0, (uint32_t)H * 2u, more};
     return p;
   }
 };
@@ -595,10 +613,10 @@ __global__ __launch_bounds__(256) void lm_loss_dh_kernel(LossGrad l) {
     const uint2 w = *reinterpret_cast<const uint2*>(l.a.w + (size_t)l.target[at] * H + c);
     for (int i = 0; i < l.splits; i++)
       s += *reinterpret_cast<const v4f*>(l.acc + ((size_t)i * l.a.rows + at) * H + c);
-    s[0] = fmaf(rest, __uint_as_float(w.x << 16), s[0]);
-    s[1] = fmaf(rest, __uint_as_float(w.x & 0xFFFF0000u), s[1]);
-    s[2] = fmaf(rest, __uint_as_float(w.y << 16), s[2]);
-    s[3] = fmaf(rest, __uint_as_float(w.y & 0xFFFF0000u), s[3]);
+    const float f[4] = {__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xFFFF0000u), __uint_as_float(w.y << 16),
+                        __uint_as_float(w.y & 0xFFFF0000u)};
+#pragma unroll
+    for (int i = 0; i < 4; i++) s[i] = fabsf(f[i]) < INFINITY ? fmaf(rest, f[i], s[i]) : s[i];
   }
   uint2 o;
   o.x = (uint32_t)f32_to_bf16(s[0]) | ((uint32_t)f32_to_bf16(s[1]) << 16);
@@ -706,6 +724,7 @@ static size_t loss_grad_plan(LossGrad* l, char* base) {
   };
   const size_t R = a.rows;
   l->h = reinterpret_cast<uint16_t*>(take(R * a.hidden * 2));
+  l->h_rest = reinterpret_cast<uint16_t*>(take(R * a.hidden * 2));
   l->row = reinterpret_cast<float2*>(take(R * sizeof(float2)));
   l->target = reinterpret_cast<int32_t*>(take(R * 4));
   l->place = reinterpret_cast<int32_t*>(take(R * 4));
