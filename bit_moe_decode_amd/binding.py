@@ -646,7 +646,8 @@ def lm_head_loss(h, w, targets, loss, lse, workspace, stream=None):
 def lm_head_loss_backward(h, w, targets, lse, dloss, dh=None, dw=None, workspace=None, add=False, stream=None):
     """The gradients of lm_head_loss for dloss float32 [rows], of the same h, w
     and targets and the lse it gave: dh bf16 [rows, hidden], dw bf16 or float32
-    [vocab, hidden] (added to with add); either may be None."""
+    [vocab, hidden] (added to with add; a float32 one is of float32 accuracy, at a
+    third more time); either may be None."""
     bf, f32 = _torch.bfloat16, _torch.float32
     (r, k), v = h.shape, w.shape[0]
     dtype = 0 if dw is None else _moe_dtype("lm_head_loss_backward", dw.dtype)

@@ -275,7 +275,12 @@ __global__ __launch_bounds__(1024) void lm_loss_join_kernel(LossTiles l) {
 // 0.0017).  So what the rounding takes from d at a row's target is kept too, and
 // added: to dh by its last kernel, to dw as more rows of the product.  In the
 // order by target the rows of 256 tokens are neighbours, so that their remainders
-// are a dense [rows][256] matrix of one entry a row.  Where a weight or a row holds
+// are a dense [rows][256] matrix of one entry a row.  An fp32 dw is to be as near
+// as fp32 sums are: there the remainders of all of d are kept, and dw is a product
+// of twice the rows, whose d is within 2^-16 (333 rows of 16000 tokens of 512, those
+// that are no target: error 0.0017 by d in one bf16, 2.6e-6 by two, where sums in
+// fp32 of an fp32 d give 1.4e-6; the gradients of 4096 rows of 151936 x 2560 take
+// 11.4 ms for 8.3).  Where a weight or a row holds
 // an infinity, d itself has given the infinity or NaN that the result is: it takes
 // no remainder, whose 0 or other sign would make it a NaN.
 struct LossGrad {
@@ -284,18 +289,21 @@ struct LossGrad {
   uint16_t* h_rest;  // the same with 0 for what is not finite: the remainders' factor
   float2* row;       // their lse and dloss,
   int32_t* target;   // target,
-  float* rest;       // d at the target less its rounding,
-  uint16_t* rests;   // the same at column target % 256 of [rows][256]
+  float* rest;       // d at the target less its rounding
+  // the same at column target % 256 of [rows][256]; ALL: all of d less its rounding,
+  // [rows][pitch]
+  uint16_t* rests;
   int32_t* place;    // [rows] each row's place among them, or -1
   const int32_t* order;  // [live] the row at each place
   const int32_t* live;   // [1] their number
-  int32_t* first_of;     // [vocab / 256 + 2] the first place of each 256 tokens
+  int32_t* first_of;     // [ceil(vocab / 256) + 1] the first place of each 256 tokens
   int32_t* next;     // [8] an XCD's next tile of the second products
   uint16_t* d;       // [rows][pitch]
   float* acc;        // [splits][rows][hidden] of dh
   void* sort;
-  int pitch, pieces, splits;
+  int pitch, splits;
   int first, count;  // this piece's part of the vocabulary
+  bool all;          // dw is fp32: the kernels' ALL
 };
 
 // Eight bf16 with 0 for those that are not finite.
@@ -320,7 +328,7 @@ __device__ __forceinline__ void take_place(const LossGrad& l, int r, int b, int 
     to[i] = v;
     to_rest[i] = finite8(v);
   }
-  if (tid < 32) reinterpret_cast<u32x4*>(l.rests + (size_t)b * 256)[tid] = u32x4{0u, 0u, 0u, 0u};
+  if (tid < 32 && !l.all) reinterpret_cast<u32x4*>(l.rests + (size_t)b * 256)[tid] = u32x4{0u, 0u, 0u, 0u};
   for (int i = (before < 0 ? 0 : before / 256 + 1) + tid; i <= t / 256; i += 256) l.first_of[i] = b;
   if (b == live - 1)
     for (int i = t / 256 + 1 + tid; i <= last; i += 256) l.first_of[i] = live;
@@ -387,16 +395,22 @@ __global__ __launch_bounds__(256) void lm_loss_gather_kernel(LossGrad l) {
   take_place(l, r, b, l.a.targets[r], b > 0 ? l.a.targets[l.order[b - 1]] : -1, live);
 }
 
+// What d's rounding takes from it (nothing of an infinity or NaN).
+__device__ __forceinline__ float rest_of(float d) {
+  const float near = bf16_to_f32(f32_to_bf16(d));
+  return fabsf(near) < INFINITY ? d - near : 0.f;
+}
+
 // d at a logit z of the row at place m, whose lse and dloss are q and target t;
 // what its rounding takes at the target is kept.  0 past the vocabulary.
+template <bool ALL>
 __device__ __forceinline__ float d_of(const LossGrad& l, float z, const float2& q, int m, int t, bool hit, bool past) {
   float p = exp_of(z - q.x);
   if (hit) {
     p = (p - 1.f) * q.y;
-    const float near = bf16_to_f32(f32_to_bf16(p));
-    const float rest = fabsf(near) < INFINITY ? p - near : 0.f;
+    const float rest = rest_of(p);
     l.rest[m] = rest;
-    l.rests[(size_t)m * 256 + (t & 255)] = f32_to_bf16(rest);
+    if constexpr (!ALL) l.rests[(size_t)m * 256 + (t & 255)] = f32_to_bf16(rest);
   } else {
     p *= q.y;
   }
@@ -404,7 +418,7 @@ __device__ __forceinline__ float d_of(const LossGrad& l, float z, const float2& 
 }
 
 // d of a tile; columns past the vocabulary are 0.
-template <int U, int V>
+template <bool ALL, int U, int V>
 __device__ __forceinline__ void grad_epilogue(const LossGrad& l, TileSums<U, V>& sums, int live, int m0, int j0) {
   const int tid = threadIdx.x, lane = tid & 63, wv = tile_wave(tid);
   const int col = lane & 15, g = lane >> 4;
@@ -423,16 +437,27 @@ __device__ __forceinline__ void grad_epilogue(const LossGrad& l, TileSums<U, V>&
 #pragma unroll
       for (int i = 0; i < 4; i++) {
         const int c = 16 * v + 4 * g + i;
-        sums.s[u][v][i] = d_of(l, sums.s[u][v][i], q, m, t, hit && c == at && m < live, edge && j0 + c >= l.count);
+        sums.s[u][v][i] = d_of<ALL>(l, sums.s[u][v][i], q, m, t, hit && c == at && m < live, edge && j0 + c >= l.count);
       }
 #pragma unroll
     for (int v = 0; v < V; v += 2) {
+      const size_t at_d = (size_t)m * l.pitch + j0 + 16 * v + tile_pair_at(lane);
       const u32x4 o = tile_pair(sums.s[u][v], sums.s[u][v + 1]);
-      if (m < live) *reinterpret_cast<u32x4*>(l.d + (size_t)m * l.pitch + j0 + 16 * v + tile_pair_at(lane)) = o;
+      if (m < live) *reinterpret_cast<u32x4*>(l.d + at_d) = o;
+      if constexpr (ALL) {
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+          sums.s[u][v][i] = rest_of(sums.s[u][v][i]);
+          sums.s[u][v + 1][i] = rest_of(sums.s[u][v + 1][i]);
+        }
+        const u32x4 rest = tile_pair(sums.s[u][v], sums.s[u][v + 1]);
+        if (m < live) *reinterpret_cast<u32x4*>(l.rests + at_d) = rest;
+      }
     }
   }
 }
 
+template <bool ALL>
 __global__ __launch_bounds__(256) void lm_loss_d_kernel(LossGrad l) {
   using Pipe = TilePipe<8, 8, false, false>;
   constexpr int TM = 256, TJ = 256;
@@ -452,11 +477,16 @@ __global__ __launch_bounds__(256) void lm_loss_d_kernel(LossGrad l) {
     return p;
   };
   head_tiles(m_tiles * j_tiles, tile_at, s0, s1, s2,
-                      [&](auto& sums, const HeadTile& p) TILE_INLINE { grad_epilogue(l, sums, live, p.m0, p.j0); });
+             [&](auto& sums, const HeadTile& p) TILE_INLINE { grad_epilogue<ALL>(l, sums, live, p.m0, p.j0); });
+}
+
+__device__ __forceinline__ void put4_bf16(uint16_t* to, const v4f& s) {
+  *reinterpret_cast<uint2*>(to) = uint2{(uint32_t)f32_to_bf16(s[0]) | ((uint32_t)f32_to_bf16(s[1]) << 16),
+                                        (uint32_t)f32_to_bf16(s[2]) | ((uint32_t)f32_to_bf16(s[3]) << 16)};
 }
 
 // d in small tiles.
-template <int U>
+template <int U, bool ALL>
 __global__ __launch_bounds__(256, 2) void lm_loss_d_few_kernel(LossGrad l) {
   __shared__ __align__(16) uint8_t lds[StreamPipe<U>::kLds];
   if (blockIdx.x == 0 && threadIdx.x < 8) l.next[threadIdx.x] = 0;
@@ -468,10 +498,13 @@ __global__ __launch_bounds__(256, 2) void lm_loss_d_few_kernel(LossGrad l) {
     const float2 q = l.row[m];
     const int t = l.target[m];
 #pragma unroll
-    for (int i = 0; i < 4; i++) z[i] = d_of(l, z[i], q, m, t, t - l.first == j + i, j + i >= l.count);
-    *reinterpret_cast<uint2*>(l.d + (size_t)m * l.pitch + j) =
-        uint2{(uint32_t)f32_to_bf16(z[0]) | ((uint32_t)f32_to_bf16(z[1]) << 16),
-              (uint32_t)f32_to_bf16(z[2]) | ((uint32_t)f32_to_bf16(z[3]) << 16)};
+    for (int i = 0; i < 4; i++) z[i] = d_of<ALL>(l, z[i], q, m, t, t - l.first == j + i, j + i >= l.count);
+    put4_bf16(l.d + (size_t)m * l.pitch + j, z);
+    if constexpr (ALL) {
+#pragma unroll
+      for (int i = 0; i < 4; i++) z[i] = rest_of(z[i]);
+      put4_bf16(l.rests + (size_t)m * l.pitch + j, z);
+    }
   });
 }
 
@@ -484,7 +517,7 @@ struct GradTile {
   int m0, j0, split;  // split -1: of dw
 };
 
-template <int SIDE>
+template <int SIDE, bool ALL>
 struct GradTiles {
   int h_tiles, v_tiles, m_tiles, dh, dw;  // tiles a side, and in all
   int part;                               // columns of a split
@@ -519,9 +552,14 @@ struct GradTiles {
     place_of(t, v_tiles, h_tiles, &mt, &jt);
     p.m0 = mt * SIDE;
     p.j0 = jt * SIDE;
+    const int own = l.count - p.m0 < SIDE ? (l.count - p.m0 + 7) / 8 * 8 : SIDE, cols = H - p.j0 < SIDE ? H - p.j0 : SIDE;
+    if constexpr (ALL) {  // all rows, and all of them again with d's remainders
+      p.m = {l.d + p.m0, (uint32_t)l.pitch * 2u, own, live, l.rests + p.m0, (uint32_t)l.pitch * 2u, live};
+      p.j = {l.h + p.j0, (uint32_t)H * 2u, cols, live, l.h_rest + p.j0, (uint32_t)H * 2u, live};
+      return p;
+    }
     const int r0 = __builtin_amdgcn_readfirstlane(l.first_of[(l.first + p.m0) / 256]);
     const int more = __builtin_amdgcn_readfirstlane(l.first_of[(l.first + p.m0) / 256 + 1]) - r0;
-    const int own = l.count - p.m0 < SIDE ? (l.count - p.m0 + 7) / 8 * 8 : SIDE, cols = H - p.j0 < SIDE ? H - p.j0 : SIDE;
     p.m = {l.d + p.m0, (uint32_t)l.pitch * 2u, own, live, l.rests + (int64_t)r0 * 256 + p.m0 % 256, 512u, more};
     p.j = {l.h + p.j0, (uint32_t)H * 2u, cols, live, l.h_rest + (int64_t)r0 * H + p.j0, (uint32_t)H * 2u, more};
     return p;
@@ -537,7 +575,7 @@ __global__ __launch_bounds__(256) void lm_loss_products_kernel(LossGrad l) {
   __shared__ typename Long::Last s2;
   __shared__ int s_next;
   const int live = __builtin_amdgcn_readfirstlane(*l.live), tid = threadIdx.x;
-  const GradTiles<32 * U> g(l, live);
+  const GradTiles<32 * U, sizeof(T) == 4> g(l, live);
   // a tile's number: those of dh, then those of dw; each XCD has an eighth of either
   TileQueues queues{l.next};
   auto redeem = [&](int ticket) TILE_INLINE {
@@ -618,10 +656,7 @@ __global__ __launch_bounds__(256) void lm_loss_dh_kernel(LossGrad l) {
 #pragma unroll
     for (int i = 0; i < 4; i++) s[i] = fabsf(f[i]) < INFINITY ? fmaf(rest, f[i], s[i]) : s[i];
   }
-  uint2 o;
-  o.x = (uint32_t)f32_to_bf16(s[0]) | ((uint32_t)f32_to_bf16(s[1]) << 16);
-  o.y = (uint32_t)f32_to_bf16(s[2]) | ((uint32_t)f32_to_bf16(s[3]) << 16);
-  *reinterpret_cast<uint2*>(l.a.dh + (size_t)r * H + c) = o;
+  put4_bf16(l.a.dh + (size_t)r * H + c, s);
 }
 
 // --------------------------------------------------------------------- launches
@@ -692,7 +727,8 @@ hipError_t launch_loss(const LossArgs& a, void* workspace, hipStream_t stream) {
 // and gathered 33; 333 of 1000 4.9 and 17).
 constexpr int kLossRanked = 4096;
 
-// Columns of a piece: d of at most 128 MB, in multiples of 256.
+// Columns of a piece: d of at most 128 MB, in multiples of 256, and room for as much
+// again, the remainders of an fp32 dw's.
 constexpr size_t kLossPieceBytes = (size_t)128 << 20;
 
 // Side of the second products' tiles: 256 where dw has one for each CU, 128 else
@@ -706,8 +742,9 @@ static size_t loss_grad_plan(LossGrad* l, char* base) {
   const int whole = (a.vocab + 255) / 256;
   int64_t most = (int64_t)(kLossPieceBytes / ((size_t)a.rows * 512));
   most = most < 1 ? 1 : (most < whole ? most : whole);
-  l->pieces = (int)((whole + most - 1) / most);
-  l->pitch = (whole + l->pieces - 1) / l->pieces * 256;
+  const int pieces = (int)((whole + most - 1) / most);
+  l->pitch = (whole + pieces - 1) / pieces * 256;
+  l->all = a.f32 && a.dw;
   // dh's products split over a piece's columns where its tiles are fewer than the
   // CUs: parts of at least 32 steps (16 of small tiles), 32 of them at most
   const int side = grad_side(a);
@@ -729,11 +766,11 @@ static size_t loss_grad_plan(LossGrad* l, char* base) {
   l->target = reinterpret_cast<int32_t*>(take(R * 4));
   l->place = reinterpret_cast<int32_t*>(take(R * 4));
   l->rest = reinterpret_cast<float*>(take(R * 4));
-  l->rests = reinterpret_cast<uint16_t*>(take(R * 512));
   l->first_of = reinterpret_cast<int32_t*>(take(((size_t)whole + 1) * 4));
   l->sort = take(a.rows <= kLossRanked ? 4 : id_sort_workspace(a.rows, a.vocab));
   l->next = reinterpret_cast<int32_t*>(take(8 * 4));
   l->d = reinterpret_cast<uint16_t*>(take(R * l->pitch * 2));
+  l->rests = reinterpret_cast<uint16_t*>(take(R * l->pitch * 2));  // (pitch: 256 or more)
   l->acc = reinterpret_cast<float*>(take((size_t)l->splits * R * a.hidden * 4));
   return o;
 }
@@ -744,6 +781,15 @@ size_t loss_backward_workspace(int rows, int vocab, int hidden) {
   l.a.vocab = vocab;
   l.a.hidden = hidden;
   return loss_grad_plan(&l, nullptr);
+}
+
+template <bool ALL>
+static void launch_d(const LossGrad& l, bool few, int blocks, hipStream_t stream) {
+  if (few)
+    launch_few(lm_loss_d_few_kernel<1, ALL>, lm_loss_d_few_kernel<2, ALL>, lm_loss_d_few_kernel<4, ALL>, l.a.rows, blocks, l,
+               stream);
+  else
+    hipLaunchKernelGGL(lm_loss_d_kernel<ALL>, dim3(blocks), dim3(256), 0, stream, l);
 }
 
 template <int U>
@@ -782,10 +828,10 @@ hipError_t launch_loss_backward(const LossGradArgs& a, void* workspace, hipStrea
                               : (int64_t)((a.rows + 255) / 256) * ((l.count + 255) / 256);
     e = tile_blocks(tiles, few ? 2 : 1, &blocks);
     if (e != hipSuccess) return e;
-    if (few)
-      launch_few(lm_loss_d_few_kernel<1>, lm_loss_d_few_kernel<2>, lm_loss_d_few_kernel<4>, a.rows, blocks, l, stream);
+    if (l.all)
+      launch_d<true>(l, few, blocks, stream);
     else
-      hipLaunchKernelGGL(lm_loss_d_kernel, dim3(blocks), dim3(256), 0, stream, l);
+      launch_d<false>(l, few, blocks, stream);
     const int side = grad_side(a);
     const int64_t products = ((int64_t)((a.rows + side - 1) / side) * l.splits + (l.count + side - 1) / side) *
                              ((a.hidden + side - 1) / side);

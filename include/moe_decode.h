@@ -469,7 +469,8 @@ moe_status lm_head_loss(const lm_head_shape* shape, const uint16_t* h, const uin
                         size_t ws_bytes, hipStream_t stream);
 
 /* Its gradients: with d[r, v] = (exp(z[r, v] - lse[r]) - [v = targets[r]])
- * dloss[r], which enters both as bf16 (at the target as the sum of two),
+ * dloss[r], which enters dh and a bf16 dw as bf16 (at the target as the sum of
+ * two), an fp32 dw as the sum of two bf16 everywhere (within 2^-16 of each term),
  *  dh  bf16 [rows, hidden]: dh[r] = sum_v d[r, v] w[v]
  *  dw  [vocab, hidden]: dw[v] = sum_r d[r, v] h[r]; with add != 0 it is added to
  *      dw, in fp32 before the rounding
