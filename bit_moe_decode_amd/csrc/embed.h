@@ -6,9 +6,6 @@
 
 namespace moe {
 
-constexpr int kEmbedMaxRows = 1 << 24;
-constexpr int kEmbedMaxVocab = 1 << 20;
-
 struct EmbedArgs {
   const int32_t* ids;  // [rows]
   int rows, vocab, hidden;

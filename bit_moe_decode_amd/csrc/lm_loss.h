@@ -7,8 +7,6 @@
 
 namespace moe {
 
-constexpr int kLossMaxRows = 1 << 20;
-constexpr int kLossMaxVocab = 1 << 20;
 constexpr int kLossMaxHidden = 32768;
 
 struct LossArgs {

@@ -8,7 +8,6 @@
 namespace moe {
 
 constexpr int kProductMaxExperts = 1024;
-constexpr int kProductMaxSide = 32768;           // n and k
 constexpr int64_t kProductMaxRows = (int64_t)1 << 24;
 
 struct ProductArgs {
