@@ -382,7 +382,9 @@ hipError_t launch_id_sort(const int32_t* ids, int rows, int vocab, void* workspa
 }
 
 // --------------------------------------------------------------------- launches
-// Rows up to which every wave holds all ids.
+// Rows up to which every wave holds all ids, and one of them sums a token's in 512
+// columns.  bf16 into 1000 x 2560: 1024 rows of different tokens 8.0 us, 1025, by the
+// sort, 18.7; but all of one token 212 (with add 368) and 40.
 constexpr int kEmbedFew = 64 * kEmbedFewK;
 
 struct EmbedPlan {

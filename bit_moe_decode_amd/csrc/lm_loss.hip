@@ -8,7 +8,7 @@
 //
 // Measured at 151936 tokens of 2560: the loss of 4096 rows 2510 .. 2670 us, 1.24
 // PFLOP/s, of 8 rows 140 us (134 of them the weights at 5.8 TB/s).  The gradients
-// of 4096 rows 7.7 .. 8.1 ms, 1.2 PFLOP/s: in ten pieces d 309 us (1.03 PFLOP/s;
+// of 4096 rows 7.7 .. 8.2 ms, 1.2 PFLOP/s: in ten pieces d 306 us (1.04 PFLOP/s;
 // the exponentials of a tile take as long as 5 of its 40 steps and nothing runs
 // beside them), dh and dw 420 .. 470 (1.4).  Of 333 rows of 32003 x 1000 145 us: 5
 // for the places, 55 d, 80 dh and dw, whose tiles of 5 to 35 steps wait for their
@@ -723,8 +723,8 @@ hipError_t launch_loss(const LossArgs& a, void* workspace, hipStream_t stream) {
   return hipSuccess;
 }
 
-// Rows up to which each one's place is counted (4096 rows of 2560 17.8 us, sorted
-// and gathered 33; 333 of 1000 4.9 and 17).
+// Rows up to which each one's place is counted (4096 rows of 2560 21 us, sorted and
+// gathered 38; 333 of 1000 5.1 and 17).
 constexpr int kLossRanked = 4096;
 
 // Columns of a piece: d of at most 128 MB, in multiples of 256, and room for as much

@@ -6,15 +6,16 @@
 //   dW_e  = sum_r dy[r] x[r]^T            (0 for an expert without rows)
 // bf16 operands, sums in fp32, rounded once.
 //
-// Rows enough for half a tile of 256 an expert, and such tiles enough for the CUs:
-// tiles of 256 x 256 (tile_product.h), of fewer row tiles where an expert's rows
-// end.  Else y takes tiles of 64 x 64 that stream the weights (stream_product.h),
+// More than 48 rows of the buffers an expert, and tiles of 256 x 256 enough for the
+// CUs: such tiles (tile_product.h), of fewer row tiles where an expert's rows end.
+// Else y takes tiles of 64 x 64 that stream the weights (stream_product.h),
 // dx of 64 x 128 and dW of 128 x 128.  Measured, of 256 experts [4096, 6144]: 16
 // tokens x 8 picks 630 .. 720 us, the bytes of the 72 .. 84 experts in use at 5.4 ..
 // 6.2 TB/s.  Of 64 experts [4096, 6144]: y of 65536 rows 2850 .. 3000 us (1.1
 // PFLOP/s; 19 rounds of tiles where even experts would take 16), dx of 32768 1530 ..
 // 1600 us (1.05), dW of 32768 2010 .. 2140 us (0.8 PFLOP/s: of it 600 us are the 3.2
-// GB of its store, which 8 steps a tile do not hide; without the store 1410).
+// GB of its store, which 8 steps a tile do not hide; without the store 1410; added to
+// an old dW, which is read behind the sums, 3650 .. 3710).
 #include "products.h"
 
 #include "device_common.h"
@@ -298,7 +299,13 @@ static int64_t most_tiles(const ProductArgs& a, int cols, int tm, int tj) {
   return m * ((cols + tj - 1) / tj);
 }
 
-// Large tiles where there are enough of them, and rows for half of one an expert.
+// Large tiles where there are enough of them and more than 48 rows an expert.  The
+// offsets are the device's, so these are the buffers' rows, those of no expert here
+// (another rank's) among them.  y and dx of 64 experts [4096, 6144], us, in large
+// tiles and in small ones: 32 rows an expert 668, 635 and 589, 601; 48: 679, 644 and
+// 645, 618; 64: 691, 647 and 681, 634; 96: 718 .. 752, 660 and 1245, 866; 128: 748,
+// 677 and 1014, 923.  A quarter of the rows here, 16 of 64 an expert: 656, 630, where
+// small tiles would take 555, 581.
 static bool rows_large(const ProductArgs& a, int cols) {
   return a.rows > (int64_t)48 * a.experts && most_tiles(a, cols, 256, 256) >= 256;
 }

@@ -10,7 +10,8 @@
 // an LDS area of the wave's own into the order of the MFMA's operands.  The waves'
 // sums are added in wave order at the end.
 //
-// 16 tokens x 8 of 256 experts [4096, 6144] 633 us, in halves of lines 738, with
+// 16 tokens x 8 of 256 experts [4096, 6144], one draw of the picks 633 us (several
+// 630 .. 720, by the 72 .. 84 experts that they use), in halves of lines 738, with
 // loads that the caches are told not to keep, which fetch a line twice, 850, in
 // tiles that share LDS 760 .. 930.  The loss of 8 rows of 151936 x 2560 134 us, 5.8
 // TB/s, where loads alone take 128.  Two steps under way a wave: 4 as good there
